@@ -10,6 +10,7 @@
 #include <string>
 
 #include "common.cuh"
+#include "fp4.cuh"
 #include "kernels.h"
 
 namespace csa {
@@ -689,6 +690,245 @@ int csa_quantize_kv_fp8(const void* kv, int64_t rows, int c, int rope_dims, uint
     return CSA_OK;
 }
 
+// ---------------------------------------------------------------- 4-bit KV
+static int check_kv_fp4(int c, int rope_dims, const char* who) {
+    if (c < 128 || c % 128 || c > CSA_MAX_HEAD_DIM || rope_dims < 0 || rope_dims % 32 || c - rope_dims < 32)
+        return fail(CSA_ERR_UNSUPPORTED, "%s: c=%d rope_dims=%d (c a multiple of 128 up to %d, rope_dims a multiple "
+                    "of 32, at least 32 quantised dims)", who, c, rope_dims, CSA_MAX_HEAD_DIM);
+    return CSA_OK;
+}
+
+size_t csa_fp4_row_bytes(int c, int rope_dims) {
+    return check_kv_fp4(c, rope_dims, "csa_fp4_row_bytes") == CSA_OK ? (size_t)fp4_row(c, rope_dims).bytes : 0;
+}
+
+static int check_launch_rows(int64_t rows, const char* who) {
+    if (rows < 0) return fail(CSA_ERR_INVALID_ARG, "%s: rows=%lld", who, (long long)rows);
+    if ((rows + 7) / 8 > INT32_MAX) return fail(CSA_ERR_UNSUPPORTED, "rows beyond one launch");
+    return CSA_OK;
+}
+
+int csa_quantize_kv_fp4(const void* kv, int64_t rows, int c, int rope_dims, uint8_t* out, void* stream) {
+    CSA_TRY(check_kv_fp4(c, rope_dims, "csa_quantize_kv_fp4"));
+    CSA_TRY(check_launch_rows(rows, "csa_quantize_kv_fp4"));
+    if (rows == 0) return CSA_OK;
+    CSA_TRY(check_ptr(kv, "kv"));
+    CSA_TRY(check_ptr(out, "out"));
+    CSA_CUDA(quantize_kv_fp4(kv, rows, c, rope_dims, nullptr, 0, out, (cudaStream_t)stream), "csa_quantize_kv_fp4");
+    return CSA_OK;
+}
+
+int csa_append_kv_fp4(const void* kv, const int32_t* slot, int B, int c, int rope_dims, uint8_t* cache, int64_t Nmax,
+                      void* stream) {
+    CSA_TRY(check_kv_fp4(c, rope_dims, "csa_append_kv_fp4"));
+    if (B < 0 || Nmax < 0) return fail(CSA_ERR_INVALID_ARG, "csa_append_kv_fp4: bad B/Nmax");
+    CSA_TRY(check_cache_rows(B, Nmax));
+    if (B == 0 || Nmax == 0) return CSA_OK;
+    CSA_TRY(check_ptr(kv, "kv"));
+    CSA_TRY(check_ptr(slot, "slot"));
+    CSA_TRY(check_ptr(cache, "cache"));
+    CSA_CUDA(quantize_kv_fp4(kv, B, c, rope_dims, slot, Nmax, cache, (cudaStream_t)stream), "csa_append_kv_fp4");
+    return CSA_OK;
+}
+
+int csa_dequantize_kv_fp4(const uint8_t* kv4, int64_t rows, int c, int rope_dims, void* out, void* stream) {
+    CSA_TRY(check_kv_fp4(c, rope_dims, "csa_dequantize_kv_fp4"));
+    CSA_TRY(check_launch_rows(rows, "csa_dequantize_kv_fp4"));
+    if (rows == 0) return CSA_OK;
+    CSA_TRY(check_ptr(kv4, "kv4"));
+    CSA_TRY(check_ptr(out, "out"));
+    CSA_CUDA(dequantize_kv_fp4(kv4, rows, c, rope_dims, out, (cudaStream_t)stream), "csa_dequantize_kv_fp4");
+    return CSA_OK;
+}
+
+// Outputs written while other CTAs still read the queries.
+static int check_no_alias(const void* out, const void* q, const char* who) {
+    return out == q ? fail(CSA_ERR_INVALID_ARG, "%s: out must not overlap q", who) : CSA_OK;
+}
+
+// Shape and size checks shared by the calls that attend over 4-bit entries.
+static int check_fp4_attn(int nq, int n_seq, int H, int c, int rope_dims, int64_t Nmax, bool identity,
+                          const char* who) {
+    CSA_TRY(check_attn_shape(H, c));
+    CSA_TRY(check_kv_fp4(c, rope_dims, who));
+    CSA_TRY(check_rows(nq, who));
+    if (nq < 0 || Nmax < 0 || n_seq < 1) return fail(CSA_ERR_INVALID_ARG, "%s: bad nq/n_seq/Nmax", who);
+    if (identity && n_seq < nq)
+        return fail(CSA_ERR_INVALID_ARG, "%s: seq_of_q is NULL (query t reads sequence t) but n_seq < nq", who);
+    return check_cache_rows(n_seq, Nmax);
+}
+
+size_t csa_sparse_mqa_fp4kv_workspace_size(int nq, int H, int c, int k) {
+    if (nq < 0 || H < 1 || c < 1 || k < 1) return 0;
+    return mqa_fp4_workspace_bytes(nq, H, c, k);
+}
+
+int csa_sparse_mqa_fp4kv(const void* q, const uint8_t* kv4, const int32_t* idx, const int32_t* seq_of_q, int nq,
+                         int n_seq, int H, int c, int rope_dims, int64_t Nmax, int k, float scale, const float* sink,
+                         void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    CSA_TRY(check_fp4_attn(nq, n_seq, H, c, rope_dims, Nmax, !seq_of_q, "csa_sparse_mqa_fp4kv"));
+    CSA_TRY(check_k(k));
+    if (nq == 0) return CSA_OK;
+    CSA_TRY(check_ptr(q, "q"));
+    CSA_TRY(check_ptr(kv4, "kv4", Nmax > 0));
+    CSA_TRY(check_ptr(idx, "idx"));
+    CSA_TRY(check_ptr(seq_of_q, "seq_of_q", false));
+    CSA_TRY(check_ptr(sink, "sink", false));
+    CSA_TRY(check_ptr(out, "out"));
+    CSA_TRY(check_ptr(lse, "lse", false));
+    CSA_TRY(check_no_alias(out, q, "csa_sparse_mqa_fp4kv"));
+    CSA_TRY(check_ws(ws, ws_bytes, csa_sparse_mqa_fp4kv_workspace_size(nq, H, c, k)));
+    const Fp4MqaArgs a{q, kv4, idx, k, QuerySpec{seq_of_q, nullptr, 0, 0}, 1, nq, n_seq, H, c, rope_dims, Nmax,
+                       default_scale(scale, c), sink, out, lse};
+    CSA_CUDA(mqa_fp4(a, ws, (cudaStream_t)stream), "csa_sparse_mqa_fp4kv");
+    return CSA_OK;
+}
+
+size_t hca_dense_mqa_fp4kv_workspace_size(int nq, int H, int c, int64_t Nmax) {
+    if (nq < 0 || H < 1 || c < 1 || Nmax < 0) return 0;
+    return mqa_fp4_workspace_bytes(nq, H, c, Nmax);
+}
+
+int hca_dense_mqa_fp4kv(const void* q, const uint8_t* kv4, const int32_t* pos, const int32_t* seq_of_q, int nq,
+                        int n_seq, int H, int c, int rope_dims, int64_t Nmax, int mp, float scale, const float* sink,
+                        void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    CSA_TRY(check_fp4_attn(nq, n_seq, H, c, rope_dims, Nmax, !seq_of_q, "hca_dense_mqa_fp4kv"));
+    if (mp < 1) return fail(CSA_ERR_INVALID_ARG, "hca_dense_mqa_fp4kv: mp=%d", mp);
+    if (nq == 0) return CSA_OK;
+    CSA_TRY(check_ptr(q, "q"));
+    CSA_TRY(check_ptr(kv4, "kv4", Nmax > 0));
+    CSA_TRY(check_ptr(pos, "pos"));
+    CSA_TRY(check_ptr(seq_of_q, "seq_of_q", false));
+    CSA_TRY(check_ptr(sink, "sink", false));
+    CSA_TRY(check_ptr(out, "out"));
+    CSA_TRY(check_ptr(lse, "lse", false));
+    CSA_TRY(check_no_alias(out, q, "hca_dense_mqa_fp4kv"));
+    CSA_TRY(check_ws(ws, ws_bytes, hca_dense_mqa_fp4kv_workspace_size(nq, H, c, Nmax)));
+    const Fp4MqaArgs a{q, kv4, nullptr, 0, QuerySpec{seq_of_q, pos, 0, 0}, mp, nq, n_seq, H, c, rope_dims, Nmax,
+                       default_scale(scale, c), sink, out, lse};
+    CSA_CUDA(mqa_fp4(a, ws, (cudaStream_t)stream), "hca_dense_mqa_fp4kv");
+    return CSA_OK;
+}
+
+int csa_entry_weights_fp4kv(const void* q, const float* lse, const uint8_t* kv4, const int32_t* idx,
+                            const int32_t* seq_of_q, int nq, int n_seq, int H, int c, int rope_dims, int64_t Nmax,
+                            int k, float scale, float* weights, float* acc, void* stream) {
+    CSA_TRY(check_fp4_attn(nq, n_seq, H, c, rope_dims, Nmax, !seq_of_q, "csa_entry_weights_fp4kv"));
+    CSA_TRY(check_k(k));
+    if (seq_of_q && acc)
+        return fail(CSA_ERR_INVALID_ARG, "csa_entry_weights_fp4kv: acc needs one query per sequence (seq_of_q NULL): "
+                    "the order in which several queries add to one entry would change the sum");
+    if (!weights && !acc) return fail(CSA_ERR_INVALID_ARG, "csa_entry_weights_fp4kv: neither weights nor acc given");
+    if (nq == 0) return CSA_OK;
+    CSA_TRY(check_ptr(q, "q"));
+    CSA_TRY(check_ptr(lse, "lse"));
+    CSA_TRY(check_ptr(kv4, "kv4", Nmax > 0));
+    CSA_TRY(check_ptr(idx, "idx"));
+    CSA_TRY(check_ptr(seq_of_q, "seq_of_q", false));
+    CSA_TRY(check_ptr(weights, "weights", false));
+    CSA_TRY(check_ptr(acc, "acc", false));
+    const Fp4WeightArgs a{q, lse, kv4, idx, k, seq_of_q, nullptr, nq, 1, n_seq, H, c, rope_dims, Nmax, 1,
+                          default_scale(scale, c), acc, weights};
+    CSA_CUDA(entry_weights_fp4(a, (cudaStream_t)stream), "csa_entry_weights_fp4kv");
+    return CSA_OK;
+}
+
+int hca_entry_weights_fp4kv(const void* q, const float* lse, const uint8_t* kv4, const int32_t* pos, int B, int T,
+                            int H, int c, int rope_dims, int64_t Nmax, int mp, float scale, const float* acc,
+                            float* out, void* stream) {
+    CSA_TRY(check_fp4_attn(B, B > 0 ? B : 1, H, c, rope_dims, Nmax, true, "hca_entry_weights_fp4kv"));
+    if (T < 0 || mp < 1) return fail(CSA_ERR_INVALID_ARG, "hca_entry_weights_fp4kv: T=%d mp=%d", T, mp);
+    if ((int64_t)B * T * H > INT32_MAX) return fail(CSA_ERR_UNSUPPORTED, "query rows B*T*H beyond int32");
+    if (B == 0 || Nmax == 0) return CSA_OK;
+    CSA_TRY(check_ptr(q, "q", T > 0));
+    CSA_TRY(check_ptr(lse, "lse", T > 0));
+    CSA_TRY(check_ptr(kv4, "kv4"));
+    CSA_TRY(check_ptr(pos, "pos", T > 0));
+    CSA_TRY(check_ptr(acc, "acc", false));
+    CSA_TRY(check_ptr(out, "out"));
+    const Fp4WeightArgs a{q, lse, kv4, nullptr, 0, nullptr, pos, B, T, B, H, c, rope_dims, Nmax, mp,
+                          default_scale(scale, c), const_cast<float*>(acc), out};
+    CSA_CUDA(entry_weights_fp4(a, (cudaStream_t)stream), "hca_entry_weights_fp4kv");
+    return CSA_OK;
+}
+
+// ---------------------------------------------------------------- eviction
+static int check_evict(int B, int64_t Nmax, const char* who) {
+    if (B < 0 || Nmax < 0) return fail(CSA_ERR_INVALID_ARG, "%s: bad B/Nmax", who);
+    CSA_TRY(check_rows(B, who));
+    if (Nmax > INT32_MAX) return fail(CSA_ERR_UNSUPPORTED, "Nmax beyond int32 entry indices");
+    return CSA_OK;
+}
+
+size_t csa_evict_plan_workspace_size(int B, int64_t Nmax, int64_t keep) {
+    if (B < 0 || Nmax < 0 || keep < 0 || keep > Nmax) return 0;
+    return evict_plan_workspace_bytes(B, Nmax, keep);
+}
+
+int csa_evict_plan(const float* acc, const int32_t* n_ent, const int32_t* entry_pos, const int32_t* protect_from,
+                   int B, int64_t Nmax, int64_t keep, int32_t* src, int32_t* dst, int32_t* n_moves, int32_t* n_out,
+                   float* acc_out, int32_t* pos_out, void* ws, size_t ws_bytes, void* stream) {
+    CSA_TRY(check_evict(B, Nmax, "csa_evict_plan"));
+    if (keep < 0 || keep > Nmax)
+        return fail(CSA_ERR_INVALID_ARG, "csa_evict_plan: keep=%lld outside [0, Nmax]", (long long)keep);
+    if (protect_from && !entry_pos)
+        return fail(CSA_ERR_INVALID_ARG, "csa_evict_plan: protect_from needs entry_pos");
+    if ((entry_pos == nullptr) != (pos_out == nullptr))
+        return fail(CSA_ERR_INVALID_ARG, "csa_evict_plan: entry_pos and pos_out go together");
+    if (B == 0) return CSA_OK;
+    const int64_t M = keep < Nmax - keep ? keep : Nmax - keep;
+    CSA_TRY(check_ptr(acc, "acc", Nmax > 0));
+    CSA_TRY(check_ptr(n_ent, "n_ent"));
+    CSA_TRY(check_ptr(entry_pos, "entry_pos", false));
+    CSA_TRY(check_ptr(protect_from, "protect_from", false));
+    CSA_TRY(check_ptr(src, "src", M > 0));
+    CSA_TRY(check_ptr(dst, "dst", M > 0));
+    CSA_TRY(check_ptr(n_moves, "n_moves"));
+    CSA_TRY(check_ptr(n_out, "n_out"));
+    CSA_TRY(check_ptr(acc_out, "acc_out", Nmax > 0));
+    CSA_TRY(check_ptr(pos_out, "pos_out", false));
+    CSA_TRY(check_ws(ws, ws_bytes, csa_evict_plan_workspace_size(B, Nmax, keep)));
+    const EvictPlanArgs a{acc, n_ent, entry_pos, protect_from, B, Nmax, keep, M, src, dst, n_moves, n_out, acc_out,
+                          pos_out};
+    CSA_CUDA(evict_plan(a, ws, (cudaStream_t)stream), "csa_evict_plan");
+    return CSA_OK;
+}
+
+int csa_evict_rows(void* cache, int64_t row_bytes, int B, int64_t Nmax, const int32_t* src, const int32_t* dst,
+                   const int32_t* n_moves, int64_t max_moves, void* stream) {
+    CSA_TRY(check_evict(B, Nmax, "csa_evict_rows"));
+    if (row_bytes < 16 || row_bytes % 16)
+        return fail(CSA_ERR_INVALID_ARG, "csa_evict_rows: row_bytes=%lld must be a positive multiple of 16",
+                    (long long)row_bytes);
+    if (max_moves < 0 || max_moves > Nmax) return fail(CSA_ERR_INVALID_ARG, "csa_evict_rows: bad max_moves");
+    if (B == 0 || max_moves == 0) return CSA_OK;
+    CSA_TRY(check_ptr(cache, "cache"));
+    CSA_TRY(check_ptr(src, "src"));
+    CSA_TRY(check_ptr(dst, "dst"));
+    CSA_TRY(check_ptr(n_moves, "n_moves"));
+    CSA_CUDA(evict_rows(cache, row_bytes, B, Nmax, src, dst, n_moves, max_moves, (cudaStream_t)stream),
+             "csa_evict_rows");
+    return CSA_OK;
+}
+
+int csa_evict_slot(float* acc, int32_t* n_ent, int32_t* entry_pos, const int32_t* pos, int B, int64_t Nmax, int m,
+                   int cap, int recent, int32_t* slot, void* stream) {
+    CSA_TRY(check_evict(B, Nmax, "csa_evict_slot"));
+    if (m < 1) return fail(CSA_ERR_INVALID_ARG, "csa_evict_slot: m=%d", m);
+    if (cap < 1 || cap > Nmax) return fail(CSA_ERR_INVALID_ARG, "csa_evict_slot: cap=%d outside [1, Nmax]", cap);
+    if (recent < 0 || (recent > 0 && !entry_pos))
+        return fail(CSA_ERR_INVALID_ARG, "csa_evict_slot: recent=%d needs entry_pos", recent);
+    if (B == 0) return CSA_OK;
+    CSA_TRY(check_ptr(acc, "acc"));
+    CSA_TRY(check_ptr(n_ent, "n_ent"));
+    CSA_TRY(check_ptr(entry_pos, "entry_pos", false));
+    CSA_TRY(check_ptr(pos, "pos"));
+    CSA_TRY(check_ptr(slot, "slot"));
+    const EvictSlotArgs a{acc, n_ent, entry_pos, pos, B, Nmax, m, cap, recent, slot};
+    CSA_CUDA(evict_slot(a, (cudaStream_t)stream), "csa_evict_slot");
+    return CSA_OK;
+}
+
 static int check_index_fp8(int HI, int cI) {
     CSA_TRY(check_index_shape(HI, cI));
     if (!index_tc_supported(HI, cI, 1, true))
@@ -986,6 +1226,61 @@ int csa_decode_fp8kv(const void* qI, const float* w, const void* idx_cache, cons
     CSA_CUDA(mqa(q, rows, slots, k, qs_rows, 1, B, B, H, c, k, default_scale(scale, c), sink, out, lse, mws, t, st),
              "csa_decode_fp8kv: mqa");
     return CSA_OK;
+}
+
+size_t csa_decode_fp4kv_workspace_size(int B, int64_t Nmax, int H, int c, int HI, int cI, int k) {
+    (void)HI; (void)cI;
+    if (B < 0 || Nmax < 0 || k < 1 || H < 1 || c < 1) return 0;
+    return select_bytes(B, Nmax, k) + align256((size_t)B * k * sizeof(int32_t)) + mqa_fp4_workspace_bytes(B, H, c, k);
+}
+
+int csa_decode_fp4kv(const void* qI, const float* w, const void* idx_cache, const void* q, const uint8_t* kv4,
+                     const int32_t* ctx_len, int B, int64_t Nmax, int m, int H, int c, int rope_dims, int HI, int cI,
+                     int k, float scale, const float* sink, void* out, float* lse, int32_t* topk_idx, void* ws,
+                     size_t ws_bytes, void* stream) {
+    CSA_TRY(check_index_shape(HI, cI));
+    CSA_TRY(check_index_mode(HI, cI, ElemType::BF16));
+    CSA_TRY(check_fp4_attn(B, B > 0 ? B : 1, H, c, rope_dims, Nmax, true, "csa_decode_fp4kv"));
+    CSA_TRY(check_k(k));
+    if (m < 1) return fail(CSA_ERR_INVALID_ARG, "csa_decode_fp4kv: m=%d", m);
+    if (B == 0) return CSA_OK;
+    CSA_TRY(check_ptr(qI, "qI"));
+    CSA_TRY(check_ptr(w, "w"));
+    CSA_TRY(check_ptr(idx_cache, "idx_cache", Nmax > 0));
+    CSA_TRY(check_ptr(q, "q"));
+    CSA_TRY(check_ptr(kv4, "kv4", Nmax > 0));
+    CSA_TRY(check_ptr(ctx_len, "ctx_len"));
+    CSA_TRY(check_ptr(sink, "sink", false));
+    CSA_TRY(check_ptr(out, "out"));
+    CSA_TRY(check_ptr(lse, "lse", false));
+    CSA_TRY(check_ptr(topk_idx, "topk_idx", false));
+    CSA_TRY(check_no_alias(out, q, "csa_decode_fp4kv"));
+    CSA_TRY(check_ws(ws, ws_bytes, csa_decode_fp4kv_workspace_size(B, Nmax, H, c, HI, cI, k)));
+    cudaStream_t st = (cudaStream_t)stream;
+    Carve cv(ws);
+    void* blk = cv.take(select_bytes(B, Nmax, k));
+    int32_t* sel = (int32_t*)cv.take((size_t)B * k * sizeof(int32_t));
+    void* mws = cv.take(mqa_fp4_workspace_bytes(B, H, c, k));
+    if (topk_idx) sel = topk_idx;
+    QuerySpec qs{nullptr, ctx_len, 0, 0};
+    const char* step = "indexer";
+    const cudaError_t se = index_then_select(qI, w, idx_cache, qs, B, B, HI, cI, Nmax, m, 1, k, sel, blk,
+                                             ElemType::BF16, st, RowBlocks{0, 0}, step);
+    if (se != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_decode_fp4kv: %s: %s", step, cudaGetErrorString(se));
+    const Fp4MqaArgs a{q, kv4, sel, k, qs, 1, B, B, H, c, rope_dims, Nmax, default_scale(scale, c), sink, out, lse};
+    CSA_CUDA(mqa_fp4(a, mws, st), "csa_decode_fp4kv: mqa");
+    return CSA_OK;
+}
+
+size_t hca_decode_fp4kv_workspace_size(int B, int64_t Nmax, int H, int c) {
+    return hca_dense_mqa_fp4kv_workspace_size(B, H, c, Nmax);
+}
+
+int hca_decode_fp4kv(const void* q, const uint8_t* kv4, const int32_t* ctx_len, int B, int64_t Nmax, int mp, int H,
+                     int c, int rope_dims, float scale, const float* sink, void* out, float* lse, void* ws,
+                     size_t ws_bytes, void* stream) {
+    return hca_dense_mqa_fp4kv(q, kv4, ctx_len, nullptr, B, B > 0 ? B : 1, H, c, rope_dims, Nmax, mp, scale, sink, out,
+                               lse, ws, ws_bytes, stream);
 }
 
 int hca_decode(const void* q, const void* kv_cache, const int32_t* ctx_len, int B, int64_t Nmax,

@@ -195,6 +195,78 @@ cudaError_t quantize_e4m3(const void* x, int64_t rows, int cols, void* out, floa
 cudaError_t gather_kv_fp8(const uint8_t* codes, const float* scales, const void* rope, const int32_t* idx, int nq,
                           int k, int64_t Nmax, int c, int rope_dims, void* out, int32_t* idx_out, cudaStream_t st);
 
+// quant_fp4.cu: 4-bit KV entries (the format: fp4.cuh). quantize: row r of kv
+// [rows, c] bf16 to row r of out, or, with slot, to row slot[r] of sequence
+// r's Nmax rows (skipped outside [0, Nmax)).
+cudaError_t quantize_kv_fp4(const void* kv, int64_t rows, int c, int R, const int32_t* slot, int64_t Nmax,
+                            uint8_t* out, cudaStream_t st);
+cudaError_t dequantize_kv_fp4(const uint8_t* in, int64_t rows, int c, int R, void* out, cudaStream_t st);
+
+// mqa_fp4.cu: shared-KV MQA over 4-bit entries (idx: entry lists [nq, k],
+// entries outside [0, Nmax) empty; otherwise every s < pos / mp).
+struct Fp4MqaArgs {
+    const void* q;
+    const uint8_t* kv4;
+    const int32_t* idx;
+    int k;
+    QuerySpec qs;
+    int mp, nq, n_seq, H, c, R;
+    int64_t Nmax;
+    float scale;
+    const float* sink;
+    void* out;
+    float* lse;
+};
+size_t mqa_fp4_workspace_bytes(int nq, int H, int c, int64_t max_entries);
+cudaError_t mqa_fp4(const Fp4MqaArgs& a, void* ws, cudaStream_t st);
+// The attention weight of entries, summed over heads: of idx[t][i] (B queries,
+// T = 1) into weights [B, k] and added to acc; or of every entry of sequence
+// b over its T queries, weights [B, Nmax] = acc + sum (acc nullable).
+struct Fp4WeightArgs {
+    const void* q;
+    const float* lse;
+    const uint8_t* kv4;
+    const int32_t* idx;
+    int k;
+    const int32_t* seq_of_q;
+    const int32_t* pos;
+    int B, T, n_seq, H, c, R;
+    int64_t Nmax;
+    int mp;
+    float scale;
+    float* acc;
+    float* weights;
+};
+cudaError_t entry_weights_fp4(const Fp4WeightArgs& a, cudaStream_t st);
+
+// evict.cu
+struct EvictPlanArgs {
+    const float* acc;
+    const int32_t* n_ent;
+    const int32_t* entry_pos;      // nullable
+    const int32_t* protect_from;   // nullable
+    int B;
+    int64_t Nmax, keep, M;         // M = min(keep, Nmax - keep)
+    int32_t *src, *dst, *n_moves, *n_out;
+    float* acc_out;
+    int32_t* pos_out;              // nullable
+};
+size_t evict_plan_workspace_bytes(int B, int64_t Nmax, int64_t keep);
+cudaError_t evict_plan(const EvictPlanArgs& a, void* ws, cudaStream_t st);
+cudaError_t evict_rows(void* cache, int64_t row_bytes, int B, int64_t Nmax, const int32_t* src, const int32_t* dst,
+                       const int32_t* n_moves, int64_t M, cudaStream_t st);
+struct EvictSlotArgs {
+    float* acc;
+    int32_t* n_ent;
+    int32_t* entry_pos;            // nullable when recent == 0
+    const int32_t* pos;
+    int B;
+    int64_t Nmax;
+    int m, cap, recent;
+    int32_t* slot;
+};
+cudaError_t evict_slot(const EvictSlotArgs& a, cudaStream_t st);
+
 // api.cu: device address of the status word on the current device
 int* device_status();
 

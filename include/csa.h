@@ -360,6 +360,130 @@ int csa_decode_fp8kv(const void* qI, const float* w, const void* idx_cache, cons
                      float* lse, int32_t* topk_idx, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * 4-bit KV storage with bf16 rotary dims: the step below FP8 entries [Notes
+ * §1.3 and §2.4: low-precision storage of compressed entries, rotary dims
+ * BF16]. An entry of c channels, the last R = rope_dims of them rotary, Q =
+ * c - R, is one row of csa_fp4_row_bytes(c, R) bytes:
+ *   [0, Q/2)           codes, e2m1 (sign, 2 exponent bits, 1 mantissa bit:
+ *                      0 .5 1 1.5 2 3 4 6); a 4-byte word holds 8 channels,
+ *                      channel 2j in nibble j and channel 2j+1 in nibble j+4
+ *   [Q/2, Q/2 + Q/16)  a scale byte s per 16 channels
+ *   Q/2 + Q/16         the row exponent E; zeros up to a multiple of 16
+ *   then               the R rotary channels, bf16, unchanged
+ *   value = e2m1 * (1 + (s & 7)/8) * 2^((s >> 3) - 31 + E - 127)
+ * (384 bytes for c = 512, R = 64: 3/8 of bf16.) Every value is a bf16 number
+ * exactly. Writing: a block's scale is max|x| / 6 rounded to 4 significant
+ * bits (nearest, ties to even; at least 2^-94, at most 1.25 * 2^125), E is
+ * the largest block's exponent plus 127, a block more than 31 binades below
+ * it takes s = 0, and a code is the e2m1 value nearest x / scale (ties to the
+ * even code, magnitudes past 6 saturate). A row with an infinity or NaN among
+ * its quantised channels reads as NaN in all of them. c is a multiple of 128
+ * (<= CSA_MAX_HEAD_DIM), R a multiple of 32, Q >= 32. bf16 in and out.
+ *
+ * csa_fp4_row_bytes: the row size, 0 (and a message) for other c, R.
+ * csa_quantize_kv_fp4: kv [rows, c] bf16 -> out [rows, row_bytes].
+ * csa_append_kv_fp4: kv [B, c], the new entry of each sequence -> row slot[b]
+ *   (device int32) of cache [B, Nmax, row_bytes]; a slot outside [0, Nmax)
+ *   writes nothing for that sequence.
+ * csa_dequantize_kv_fp4: kv4 [rows, row_bytes] -> out [rows, c] bf16, exact.
+ *
+ * csa_sparse_mqa_fp4kv, hca_dense_mqa_fp4kv, csa_decode_fp4kv,
+ * hca_decode_fp4kv: csa_sparse_mqa, hca_dense_mqa, csa_decode and hca_decode
+ * (bf16) over such a cache kv4 [n_seq, Nmax, row_bytes]: the same formulas on
+ * the stored values, which are read as they are (only the softmax weights
+ * are rounded to bf16 for the second product, and the output). idx entries
+ * outside [0, Nmax) are empty slots; an entry listed twice counts twice; rows
+ * that no query sees are not read. Queries without entries give out = 0,
+ * lse = -inf (the sink logit with a sink). csa_decode_fp4kv's index keys are
+ * bf16 and its selection is csa_decode's. out must not overlap an input.
+ * ------------------------------------------------------------------------ */
+size_t csa_fp4_row_bytes(int c, int rope_dims);
+int csa_quantize_kv_fp4(const void* kv, int64_t rows, int c, int rope_dims, uint8_t* out, void* stream);
+int csa_append_kv_fp4(const void* kv, const int32_t* slot, int B, int c, int rope_dims, uint8_t* cache, int64_t Nmax,
+                      void* stream);
+int csa_dequantize_kv_fp4(const uint8_t* kv4, int64_t rows, int c, int rope_dims, void* out, void* stream);
+size_t csa_sparse_mqa_fp4kv_workspace_size(int nq, int H, int c, int k);
+int csa_sparse_mqa_fp4kv(const void* q, const uint8_t* kv4, const int32_t* idx, const int32_t* seq_of_q, int nq,
+                         int n_seq, int H, int c, int rope_dims, int64_t Nmax, int k, float scale, const float* sink,
+                         void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+size_t hca_dense_mqa_fp4kv_workspace_size(int nq, int H, int c, int64_t Nmax);
+int hca_dense_mqa_fp4kv(const void* q, const uint8_t* kv4, const int32_t* pos, const int32_t* seq_of_q, int nq,
+                        int n_seq, int H, int c, int rope_dims, int64_t Nmax, int mp, float scale, const float* sink,
+                        void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+size_t csa_decode_fp4kv_workspace_size(int B, int64_t Nmax, int H, int c, int HI, int cI, int k);
+int csa_decode_fp4kv(const void* qI, const float* w, const void* idx_cache, const void* q, const uint8_t* kv4,
+                     const int32_t* ctx_len, int B, int64_t Nmax, int m, int H, int c, int rope_dims, int HI, int cI,
+                     int k, float scale, const float* sink, void* out, float* lse, int32_t* topk_idx, void* ws,
+                     size_t ws_bytes, void* stream);
+size_t hca_decode_fp4kv_workspace_size(int B, int64_t Nmax, int H, int c);
+int hca_decode_fp4kv(const void* q, const uint8_t* kv4, const int32_t* ctx_len, int B, int64_t Nmax, int mp, int H,
+                     int c, int rope_dims, float scale, const float* sink, void* out, float* lse, void* ws,
+                     size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Bounding a cache: the attention weight its entries receive, and eviction of
+ * those that receive least.
+ *
+ * csa_entry_weights_fp4kv: for query t and slot i of its entry list idx [nq, k]
+ *     weights[t][i] = sum_h exp(scale * q[t][h] . v - lse[t][h])
+ *   (0 for an empty slot; a head with lse = -inf adds 0), lse [nq, H] as the
+ *   attention call over the same list returned it (with a sink, the sink's
+ *   share is in lse and the weights sum to less than H). weights [nq, k] fp32
+ *   or NULL. acc [n_seq, Nmax] fp32 or NULL: each weight is added to its
+ *   entry's, for one query per sequence only (seq_of_q NULL), so that the sum
+ *   does not depend on an order.
+ * hca_entry_weights_fp4kv: for every entry s of sequence b, over its T queries
+ *   (T = 1: a decode step; more: a prompt's)
+ *     out[b][s] = acc[b][s] + sum_{t: s < floor(pos[b][t] / mp)} sum_h
+ *                 exp(scale * q[b][t][h] . v_s - lse[b][t][h])
+ *   q [B, T, H, c], lse [B, T, H], pos [B, T], kv4 [B, Nmax, row_bytes], out
+ *   [B, Nmax] written in full, acc [B, Nmax] or NULL (0); out == acc is
+ *   allowed. Queries are added in order of t.
+ *
+ * csa_evict_plan: cuts the first n_ent[b] entries of every sequence to `keep`.
+ *   Entries are ordered by (protected, acc descending, index ascending), a NaN
+ *   weight counting as -inf; the first `keep` stay (all, when n_ent[b] <=
+ *   keep). Protected: entry_pos[b][i] >= protect_from[b] (both NULL: none).
+ *   The order of a cache's entries does not matter to attention, so rows are
+ *   not shifted: with M = min(keep, Nmax - keep), src [B, M] lists the kept
+ *   rows at or after keep in ascending order, dst [B, M] the evicted rows
+ *   before keep in ascending order (as many), n_moves [B] their number; -1
+ *   past it. n_out [B] = min(n_ent, keep). acc_out [B, Nmax] (and pos_out,
+ *   with entry_pos) are the weights (positions) after the moves, 0 (-1) past
+ *   n_out. In place is allowed: acc_out == acc, pos_out == entry_pos, n_out ==
+ *   n_ent; other overlap is not. n_ent is clipped to [0, Nmax].
+ * csa_evict_rows: carries the moves out on cache [B, Nmax, row_bytes] (any
+ *   cache of the sequences: 4-bit or bf16 entries, index keys), in place;
+ *   row_bytes a multiple of 16, max_moves = M. A move with a row outside
+ *   [0, Nmax) is skipped.
+ * csa_evict_slot: decode time, one new entry per sequence. A token at pos[b]
+ *   closes entry i = (pos+1)/m - 1 when (pos+1) % m == 0 (as
+ *   csa_compress_step); otherwise, or for a negative pos, slot[b] = -1 and
+ *   nothing changes. The entry gets slot n_ent[b] while that is below cap, and
+ *   in a full cache the slot of the entry that comes last in the order above
+ *   among slots [0, cap), protected being those with entry_pos >= i - recent.
+ *   acc of the slot becomes 0, its entry_pos i, n_ent counts up to cap. The
+ *   entry itself is stored with csa_append_kv_fp4 (or a row copy).
+ *
+ * A cache whose entries are no longer in token order is attended with m (or
+ * mp) = 1 and pos = ctx_len = n_ent.
+ * ------------------------------------------------------------------------ */
+int csa_entry_weights_fp4kv(const void* q, const float* lse, const uint8_t* kv4, const int32_t* idx,
+                            const int32_t* seq_of_q, int nq, int n_seq, int H, int c, int rope_dims, int64_t Nmax,
+                            int k, float scale, float* weights, float* acc, void* stream);
+int hca_entry_weights_fp4kv(const void* q, const float* lse, const uint8_t* kv4, const int32_t* pos, int B, int T,
+                            int H, int c, int rope_dims, int64_t Nmax, int mp, float scale, const float* acc,
+                            float* out, void* stream);
+size_t csa_evict_plan_workspace_size(int B, int64_t Nmax, int64_t keep);
+int csa_evict_plan(const float* acc, const int32_t* n_ent, const int32_t* entry_pos, const int32_t* protect_from,
+                   int B, int64_t Nmax, int64_t keep, int32_t* src, int32_t* dst, int32_t* n_moves, int32_t* n_out,
+                   float* acc_out, int32_t* pos_out, void* ws, size_t ws_bytes, void* stream);
+int csa_evict_rows(void* cache, int64_t row_bytes, int B, int64_t Nmax, const int32_t* src, const int32_t* dst,
+                   const int32_t* n_moves, int64_t max_moves, void* stream);
+int csa_evict_slot(float* acc, int32_t* n_ent, int32_t* entry_pos, const int32_t* pos, int B, int64_t Nmax, int m,
+                   int cap, int recent, int32_t* slot, void* stream);
+
+/* ------------------------------------------------------------------------
  * a6. Sparse shared-KV MQA [Notes §1.1 last paragraph: every compressed
  * entry is both key and value, all query heads share it; Walk §2.3.2; sink
  * from Notes §1.3 equation s_{h,i,j}]:

@@ -169,6 +169,109 @@ def dequantize_kv_fp8(codes, scales, rope):
     return np.concatenate([_f64(codes) * _f64(scales)[..., None], _f64(rope)], axis=-1)
 
 
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def fp4_row_bytes(c: int, rope_dims: int) -> int:
+    Q = c - rope_dims
+    return Q // 2 + -(-(Q // 16 + 1) // 16) * 16 + 2 * rope_dims
+
+
+def quantize_kv_fp4(KV, rope_dims: int) -> np.ndarray:
+    """4-bit rows [..., row_bytes] uint8 of bf16 entries (given as float64),
+    written from the format in include/csa.h, one block at a time."""
+    KV = _f64(KV)
+    c = KV.shape[-1]
+    Q = c - rope_dims
+    x = KV.reshape(-1, c)
+    out = np.zeros((x.shape[0], fp4_row_bytes(c, rope_dims)), dtype=np.uint8)
+    grid = np.array(E2M1)
+    for r in range(x.shape[0]):
+        row = x[r, :Q]
+        if not np.isfinite(row).all():
+            out[r, Q // 2:Q // 2 + Q // 16 + 1] = 255
+        else:
+            ex, man = [], []
+            for b in range(Q // 16):
+                t = np.abs(row[16 * b:16 * b + 16]).max() / 6
+                t = min(max(t, 2.0 ** -94), 1.25 * 2.0 ** 125)
+                e = int(np.frexp(t)[1]) - 1
+                n = int(np.rint(t / 2.0 ** e * 8))           # 8 .. 16, ties to even
+                if n == 16:
+                    e, n = e + 1, 8
+                ex.append(e)
+                man.append(n - 8)
+            top = max(ex)
+            for b in range(Q // 16):
+                s = 8 * (ex[b] - top + 31) + man[b] if ex[b] - top >= -31 else 0
+                S = (1 + (s % 8) / 8) * 2.0 ** (s // 8 - 31 + top)
+                out[r, Q // 2 + b] = s
+                for d in range(16 * b, 16 * b + 16):
+                    gap = np.abs(abs(row[d]) / S - grid)
+                    best = np.flatnonzero(gap == gap.min())
+                    code = int(best[0] if len(best) == 1 else best[best % 2 == 0][0])
+                    code += 8 if np.signbit(row[d]) else 0
+                    nib = (d % 8) // 2 + 4 * (d % 2)
+                    out[r, 4 * (d // 8) + nib // 2] |= code << (4 * (nib % 2))
+            out[r, Q // 2 + Q // 16] = top + 127
+        if rope_dims:
+            # (bf16 values: the upper half of their fp32 bits)
+            bits = x[r, Q:].astype(np.float32).view(np.uint32) >> 16
+            out[r, -2 * rope_dims:] = bits.astype(np.uint16).view(np.uint8)
+    return out.reshape(KV.shape[:-1] + (out.shape[1],))
+
+
+def dequantize_kv_fp4(rows, c: int, rope_dims: int) -> np.ndarray:
+    """The values [..., c] (float64) of 4-bit rows [..., row_bytes] uint8."""
+    rows = np.asarray(rows)
+    Q = c - rope_dims
+    d = np.arange(Q)
+    nib = (d % 8) // 2 + 4 * (d % 2)
+    code = (rows[..., 4 * (d // 8) + nib // 2] >> (4 * (nib % 2))) & 15
+    s = rows[..., Q // 2 + d // 16].astype(np.int64)
+    E = rows[..., Q // 2 + Q // 16].astype(np.int64)[..., None]
+    val = np.where(code >= 8, -1.0, 1.0) * np.array(E2M1)[code % 8]
+    val = val * (1 + (s % 8) / 8) * np.exp2((s // 8 - 31 + E - 127).astype(np.float64))
+    val = np.where((E == 255) & (s == 255), np.nan, val)
+    if rope_dims:
+        bits = np.ascontiguousarray(rows[..., -2 * rope_dims:]).view(np.uint16).astype(np.uint32) << 16
+        val = np.concatenate([val, bits.view(np.float32).astype(np.float64)], -1)
+    return val
+
+
+def entry_weights(q, lse, KV, idx, scale: float, seq) -> np.ndarray:
+    """weights [nq, k]: sum over heads of exp(scale q.v - lse) of each listed entry (0: empty slot)."""
+    q, lse, KV = _f64(q), _f64(lse), _f64(KV)
+    out = np.zeros(idx.shape)
+    for t in range(q.shape[0]):
+        for i, s in enumerate(idx[t]):
+            if 0 <= seq[t] < KV.shape[0] and 0 <= s < KV.shape[1]:
+                z = scale * (q[t] @ KV[seq[t], s])
+                live = ~np.isneginf(lse[t])
+                out[t, i] = np.exp(z[live] - lse[t][live]).sum()
+    return out
+
+
+def evict_order(acc, pos=None, protect_from=None) -> np.ndarray:
+    """Entry indices of one sequence from the first to stay to the first to go."""
+    w = np.where(np.isnan(acc), -np.inf, _f64(acc))
+    prot = np.zeros(len(w)) if protect_from is None else (np.asarray(pos) >= protect_from).astype(np.float64)
+    return np.lexsort((np.arange(len(w)), -w, -prot))
+
+
+def evict_plan(acc, n_ent: int, keep: int, pos=None, protect_from=None):
+    """One sequence: (moves as (src, dst) pairs, entries left)."""
+    n = min(max(int(n_ent), 0), len(acc))
+    if n <= keep:
+        return [], n
+    order = evict_order(acc[:n], None if pos is None else pos[:n], protect_from)
+    stay = set(order[:keep].tolist())
+    movers = [i for i in range(keep, n) if i in stay]
+    holes = [i for i in range(keep) if i not in stay]
+    assert len(movers) == len(holes)
+    return list(zip(movers, holes)), keep
+
+
 def topk_recall(idx, ref_idx) -> float:
     """Mean over rows of |idx ∩ ref_idx| / |ref_idx| (entries >= 0 only)."""
     idx, ref_idx = _i32(idx), _i32(ref_idx)
