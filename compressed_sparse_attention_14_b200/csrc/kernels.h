@@ -306,6 +306,11 @@ cudaError_t mqa(const void* q, const void* KV, const int32_t* idx, int k, QueryS
                 int nq, int n_seq, int H, int c, int64_t Nmax, float scale, const float* sink, void* out,
                 float* lse, void* ws, ElemType t, cudaStream_t st, RowBlocks kvb = RowBlocks{0, 0});
 
+// mqa.cu: merge of nsplit partial results per query (part_o [nq, nsplit, H, c]
+// scaled by exp(-m), part_ml [nq, nsplit, H, 2] = (m, l); m = -inf: none)
+cudaError_t mqa_combine_bf16(const float* part_o, const float* part_ml, int nsplit, int nq, int H, int c,
+                             const float* sink, void* out, float* lse, cudaStream_t st);
+
 // norm_rope.cu: RMSNorm (gamma != nullptr) then rotary encoding of the last R
 // channels of every row of c channels; row r takes the position of group
 // r / group: pos[g], or pos0 + g * pos_step when pos is null. y may equal x.

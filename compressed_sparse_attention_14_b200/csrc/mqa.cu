@@ -215,6 +215,16 @@ __global__ void __launch_bounds__(kCombineHeads * 32) mqa_combine_kernel(const f
     }
 }
 
+cudaError_t mqa_combine_bf16(const float* part_o, const float* part_ml, int nsplit, int nq, int H, int c,
+                             const float* sink, void* out, float* lse, cudaStream_t st) {
+    cudaError_t e = cudaSuccess;
+    CSA_LAUNCH(st, "mqa_combine",
+               e = launch_pdl(mqa_combine_kernel<bf16>,
+                              dim3((H + kCombineHeads - 1) / kCombineHeads, nq, (c + kCombineDims - 1) / kCombineDims),
+                              dim3(kCombineHeads * 32), 0, st, 0, part_o, part_ml, nsplit, H, c, sink, (bf16*)out, lse));
+    return e;
+}
+
 static int mqa_nsplit(int nq, int H, int64_t max_entries) {
     int hg = (H + kMqaHeads - 1) / kMqaHeads;
     int64_t ctas = (int64_t)nq * hg;
@@ -261,11 +271,7 @@ cudaError_t mqa(const void* q, const void* KV, const int32_t* idx, int k, QueryS
         if (e != cudaSuccess || ns == 1 || mqa_tc_pair(ns)) return e;
         float* part_o = (float*)ws;
         float* part_ml = (float*)((char*)ws + align256((size_t)nq * ns * H * c * sizeof(float)));
-        CSA_LAUNCH(st, "mqa_combine",
-                   e = launch_pdl(mqa_combine_kernel<bf16>,
-                                  dim3((H + kCombineHeads - 1) / kCombineHeads, nq, (c + kCombineDims - 1) / kCombineDims),
-                                  dim3(kCombineHeads * 32), 0, st, 0, (const float*)part_o,
-                                  (const float*)part_ml, ns, H, c, sink, (bf16*)out, lse));
+        e = mqa_combine_bf16(part_o, part_ml, ns, nq, H, c, sink, out, lse, st);
         if (e != cudaSuccess) return e;
         return cudaGetLastError();
     }

@@ -1,147 +1,645 @@
-// Shared-KV attention over 4-bit entries (the format: fp4.cuh), and the
-// attention weight each entry received.
+// Shared-KV attention over 4-bit entries (the format: fp4.cuh) on the 5th
+// generation tensor cores:
 //
 //   z_s = scale * q . v_s,  out = sum_s e^{z_s} v_s / (sum_s e^{z_s} [+ e^{sink}])
-//   weight of s = sum over heads (and queries) of e^{z_s - lse}
 //
-// A warp per (query, head), its lanes over the channels: each entry is read
-// once per head, its logit is a warp sum, and the output is kept under a
-// running maximum.
+// One CTA serves (query, up to 64 heads, one split of the query's entries)
+// and walks the split in tiles of 128 entries. Producer warps read the packed
+// rows, expand them to bf16 (exact) and store the tile in shared memory, where
+// ONE copy of it (128 entries x c dims in 64-dim blocks, 128-byte swizzle)
+// feeds both products, key and value being the same row:
+//   S^T  = V_tile . q^T         M = 128 entries, N = 64 heads, K = c
+//   O^T += V_tile^T . P^T       M = 128 dims,    N = 64 heads, K = 128 entries
+// S^T (two buffers) and O^T live in tensor memory. The softmax keeps a
+// reference maximum per head that moves (O^T and the sums are then rescaled)
+// only when a logit passes it by 2^8; normalisation uses the same reference,
+// so the result does not depend on when it moves. P is rounded to bf16 for
+// the second product; the sums, maxima and O stay fp32.
+//
+// Warps 0-7: softmax and epilogue (warp w: TMEM lanes 32 (w % 4).., heads
+// 32 (w / 4)..). Warps 8-15: producers; a thread owns half of one row in
+// every 64-dim block (32 channels: 16 bytes of codes), keeps the next tile's
+// codes in registers while it waits for a block to be free, and copies rotary
+// channels with cp.async. Warp 16 issues the S products, warp 17 the O
+// products. A block is refilled as soon as the O product has read it, so the
+// expansion of tile j+1 overlaps the products of tile j.
+//
+// Entries outside the query's set are stored as zeros and get weight 0: no
+// row that the query does not see is read.
+//
+// Splits of a query: up to 8 form a cluster and merge on chip (each writes a
+// share of the output from all partial sums over distributed shared memory);
+// more go through the workspace and mqa_combine. Either way in split order.
 #include "fp4.cuh"
 #include "kernels.h"
+#include "tc.cuh"
+#include "tmap.h"
 
 namespace csa {
 
 namespace {
 
-constexpr int kDims = CSA_MAX_HEAD_DIM / 32;
+constexpr int kThreads = 576;
+constexpr int kE = 128;                 // entries per tile
+constexpr int kHg = 64;                 // heads per CTA
+constexpr int kBlocks = CSA_MAX_HEAD_DIM / 64;
+constexpr int kMaxCluster = 8;
+constexpr uint32_t kBlockBytes = kE * 128;
+constexpr uint32_t kWaitLimit = 1u << 24;
+constexpr float kMoveLog2 = 8.0f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// channel d of a row
-__device__ __forceinline__ float fp4_channel(const uint8_t* row, const Fp4Row& f, int d) {
-    if (d >= f.Q) return __bfloat162float(reinterpret_cast<const bf16*>(row + f.rope_off)[d - f.Q]);
-    const uint32_t w = reinterpret_cast<const uint32_t*>(row)[d / 8];
-    const uint32_t s = fp4_scale_bits(row[f.scale_off + d / 16], row[f.scale_off + f.Q / 16]) * 0x10001u;
-    uint32_t o[4];
-    fp4_word(w, s, o);
-    const uint32_t p = (d & 4) ? ((d & 2) ? o[3] : o[2]) : ((d & 2) ? o[1] : o[0]);
-    return __uint_as_float(d & 1 ? p & 0xFFFF0000u : p << 16);
+enum Merge { kDirect, kCluster, kWorkspace };
+
+struct Args {
+    QueryMap qm;
+    const uint8_t* kv4;
+    const int32_t* idx;
+    const float* sink;
+    bf16* out;
+    float* lse;
+    float* part_o;
+    float* part_ml;
+    int* status;
+    int64_t Nmax, split_len;
+    Fp4Row f;
+    int k, n_seq, mp, H, nsplit, merge, dblocks, mtiles;
+    uint32_t tmem_cols;
+    float scale_log2;
+};
+
+struct Shared {
+    float mref[kHg], alpha[kHg], lsum[kHg];
+    float red[4][kHg];
+    float coef[kMaxCluster][kHg];
+    uint64_t full[kBlocks], empty[kBlocks];   // a block of the tile stored / free
+    uint64_t s_full[2], s_empty[2], q_full, p_full, o_done, fin[2];
+    uint32_t tmem;
+    int abort;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 
-__device__ __forceinline__ float row_dot(const uint8_t* row, const Fp4Row& f, const float (&q)[kDims], int lane,
-                                         float (&v)[kDims]) {
-    float z = 0.f;
+// Bounded wait: false once it ran out here or another role gave up.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Shared& s, int* status) {
+    volatile int* abort = &s.abort;
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        if (tc::mbar_try_wait(bar, parity)) return true;
+        if ((i & 255u) == 255u && *abort) return false;
+    }
+    report_device_error(status, CSA_ERR_TIMEOUT);
+    *abort = 1;
+    return false;
+}
+
+// barrier (and vote) of the 128 softmax threads of one half of the heads
+__device__ __forceinline__ void half_sync(int half) {
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+}
+__device__ __forceinline__ bool half_any(int half, bool v) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "setp.ne.u32 q, %1, 0;\n\t"
+                 "bar.red.or.pred p, %2, 128, q;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r) : "r"((uint32_t)v), "r"(1 + half) : "memory");
+    return r != 0;
+}
+
+// v[i] of 32 lanes -> in lane l the combination of every lane's v[l] (31 shuffles)
+template <typename Op>
+__device__ __forceinline__ float lanes_transpose_reduce(float (&v)[32], int lane, Op op) {
 #pragma unroll
-    for (int i = 0; i < kDims; ++i) {
-        v[i] = 0.f;
-        if (i * 32 < f.c) {
-            v[i] = fp4_channel(row, f, i * 32 + lane);
-            z = fmaf(q[i], v[i], z);
+    for (int r = 0; r < 5; ++r) {
+        const int o = 16 >> r;
+        const bool upper = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (i < o) {
+                const float send = upper ? v[i] : v[i + o];
+                const float keep = upper ? v[i + o] : v[i];
+                v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+            }
         }
     }
-    return warp_sum(z);
+    return v[0];
 }
 
-__global__ void __launch_bounds__(128) mqa_fp4_kernel(const __grid_constant__ Fp4MqaArgs a) {
-    pdl_wait();
-    pdl_launch_next();
-    const int lane = threadIdx.x & 31, h = blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int t = blockIdx.y;
-    if (h >= a.H) return;
-    const Fp4Row f = fp4_row(a.c, a.R);
-    const QueryMap qm{a.qs.seq, a.qs.pos, a.qs.pos_base, a.qs.single_seq};
-    const int seq = qm.seq_of(t);
-    int64_t n = 0;
-    if (seq >= 0 && seq < a.n_seq) n = a.idx ? a.k : visible_entries(qm.pos_of(t), a.mp, a.Nmax);
-    const uint8_t* kv = a.kv4 + (int64_t)(n ? seq : 0) * a.Nmax * f.bytes;
-    const int64_t qrow = (int64_t)t * a.H + h;
-    float q[kDims], v[kDims], o[kDims];
+// Producer: rows of every tile, block by block from the last to the first.
+template <bool kSparse>
+__device__ __forceinline__ void produce(const Args& a, Shared& s, uint8_t* kv_s, int t, int64_t e_beg, int64_t e_end,
+                                        int ntiles, const uint8_t* seq_rows) {
+    const int pt = threadIdx.x - 256, row = pt >> 1, half = pt & 1, lane = threadIdx.x & 31;
+    const int nq32 = a.f.Q / 32, rope_b = nq32 / 2;       // first block with rotary channels
+    auto entry = [&](int j) -> int64_t {                  // entry index of this row in tile j, -1: none
+        const int64_t e = e_beg + (int64_t)j * kE + row;
+        if (e >= e_end) return -1;
+        if (!kSparse) return e;
+        const int64_t v = __ldg(a.idx + (int64_t)t * a.k + e);
+        return v < a.Nmax ? v : -1;
+    };
+    auto address = [&](int64_t e) { return e >= 0 ? seq_rows + e * a.f.bytes : nullptr; };
+    uint4 raw[kBlocks], sc[2], nsc[2];
+    uint32_t ebase, nebase;
+    auto load_codes = [&](const uint8_t* p, int b) {
+        return p && 2 * b + half < nq32 ? __ldg(reinterpret_cast<const uint4*>(p) + 2 * b + half)
+                                        : make_uint4(0, 0, 0, 0);
+    };
+    auto load_scales = [&](const uint8_t* p, uint4 (&o)[2], uint32_t& eb) {
+        o[0] = o[1] = make_uint4(0, 0, 0, 0);
+        eb = 128;                                         // a missing row: codes 0 times 2^-126
+        if (!p) return;
+        o[0] = __ldg(reinterpret_cast<const uint4*>(p + a.f.scale_off));
+        if (a.f.Q > 256) o[1] = __ldg(reinterpret_cast<const uint4*>(p + a.f.scale_off) + 1);
+        eb = ((uint32_t)__ldg(p + a.f.scale_off + a.f.Q / 16) - 31u) << 7;
+    };
+    const uint8_t* p = address(entry(0));
+    load_scales(p, sc, ebase);
 #pragma unroll
-    for (int i = 0; i < kDims; ++i) {
-        q[i] = i * 32 < a.c ? __bfloat162float(((const bf16*)a.q)[qrow * a.c + i * 32 + lane]) : 0.f;
-        o[i] = 0.f;
-    }
-    float m = a.sink ? a.sink[h] : -INFINITY, L = m == -INFINITY ? 0.f : 1.f;
-    for (int64_t e = 0; e < n; ++e) {
-        const int64_t s = a.idx ? a.idx[(int64_t)t * a.k + e] : e;
-        if (s < 0 || s >= a.Nmax) continue;
-        const float z = a.scale * row_dot(kv + s * f.bytes, f, q, lane, v);
-        const float mn = fmaxf(m, z);
-        const float al = mn == -INFINITY ? 1.f : expf(m - mn), p = mn == -INFINITY ? 0.f : expf(z - mn);
-        L = L * al + p;
+    for (int b = kBlocks - 1; b >= 0; --b)
+        if (b < a.dblocks) raw[b] = load_codes(p, b);
+    int64_t next = ntiles > 1 ? entry(1) : -1;
+    for (int j = 0; j < ntiles; ++j) {
+        const uint8_t* np = address(next);
+        next = j + 2 < ntiles ? entry(j + 2) : -1;
+        load_scales(np, nsc, nebase);
+        if (np)
+            for (int ch = nq32 + ((nq32 ^ half) & 1); ch < a.f.c / 32; ch += 2)
+                prefetch_l2(np + a.f.rope_off + (ch - nq32) * 64);
+        const uint32_t scw[8] = {sc[0].x, sc[0].y, sc[0].z, sc[0].w, sc[1].x, sc[1].y, sc[1].z, sc[1].w};
+        bool ok = true;
 #pragma unroll
-        for (int i = 0; i < kDims; ++i) o[i] = fmaf(p, v[i], o[i] * al);
-        m = mn;
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+        for (int b = kBlocks - 1; b >= 0; --b) {
+            if (b < a.dblocks && ok) {
+                if (j > 0) {
+                    if (lane == 0) ok = wait(&s.empty[b], (j - 1) & 1, s, a.status);
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                }
+                if (ok) {
+                    uint8_t* dst = kv_s + (size_t)b * kBlockBytes + row * 128;
+                    if (2 * b + half < nq32) {
+                        const uint32_t two = scw[b] >> (16 * half);
+                        const uint32_t S0 = ((ebase + ((two & 255u) << 4)) & 0xffffu) * 0x10001u;
+                        const uint32_t S1 = ((ebase + ((two >> 4) & 0xff0u)) & 0xffffu) * 0x10001u;
+                        const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
 #pragma unroll
-    for (int i = 0; i < kDims; ++i)
-        if (i * 32 < a.c) ((bf16*)a.out)[qrow * a.c + i * 32 + lane] = __float2bfloat16_rn(o[i] * inv);
-    if (a.lse && lane == 0) a.lse[qrow] = L == 0.f ? -INFINITY : m + logf(L);
-}
-
-// a warp per entry: selected entries (idx) of query t, or entry e of sequence t
-__global__ void __launch_bounds__(128) entry_weights_fp4_kernel(const __grid_constant__ Fp4WeightArgs a) {
-    pdl_wait();
-    pdl_launch_next();
-    const int lane = threadIdx.x & 31;
-    const int64_t e = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), n = a.idx ? a.k : a.Nmax;
-    const int b = blockIdx.y;
-    if (e >= n) return;
-    const Fp4Row f = fp4_row(a.c, a.R);
-    const int seq = a.seq_of_q ? a.seq_of_q[b] : b;
-    int64_t s = e;
-    bool ok = seq >= 0 && seq < a.n_seq;
-    if (a.idx) {
-        s = a.idx[(int64_t)b * a.k + e];
-        ok = ok && s >= 0 && s < a.Nmax;
-    }
-    float w = 0.f;
-    for (int t = 0; ok && t < a.T; ++t) {
-        if (!a.idx && s >= visible_entries(a.pos[(int64_t)b * a.T + t], a.mp, a.Nmax)) continue;
-        for (int h = 0; h < a.H; ++h) {
-            const int64_t qrow = ((int64_t)b * a.T + t) * a.H + h;
-            float q[kDims], v[kDims];
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t v[4];
+                            fp4_word(w[i], i < 2 ? S0 : S1, v);
+                            *reinterpret_cast<uint4*>(dst + (((half * 4 + i) ^ (row & 7)) << 4)) =
+                                make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                        raw[b] = load_codes(np, b);
+                    } else {
+                        const uint8_t* src = p ? p + a.f.rope_off + (2 * b + half - nq32) * 64 : nullptr;
 #pragma unroll
-            for (int i = 0; i < kDims; ++i)
-                q[i] = i * 32 < a.c ? __bfloat162float(((const bf16*)a.q)[qrow * a.c + i * 32 + lane]) : 0.f;
-            const float z = a.scale * row_dot(a.kv4 + ((int64_t)seq * a.Nmax + s) * f.bytes, f, q, lane, v);
-            const float l = a.lse[qrow];
-            if (l != -INFINITY) w += expf(z - l);
+                        for (int i = 0; i < 4; ++i) {
+                            uint8_t* d = dst + (((half * 4 + i) ^ (row & 7)) << 4);
+                            if (src) cp_async16(d, src + 16 * i);
+                            else *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    if (b < rope_b) {
+                        tc::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&s.full[b]);
+                    }
+                }
+            }
         }
+        cp_async_wait_all();
+        if (!ok) break;
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            for (int b = a.dblocks - 1; b >= rope_b; --b) tc::mbar_arrive(&s.full[b]);
+        p = np;
+        sc[0] = nsc[0];
+        sc[1] = nsc[1];
+        ebase = nebase;
     }
-    if (lane != 0) return;
-    if (a.idx) {
-        if (a.weights) a.weights[(int64_t)b * a.k + e] = w;
-        if (a.acc && ok) atomicAdd(a.acc + (int64_t)seq * a.Nmax + s, w);
+}
+
+template <bool kSparse>
+__global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_constant__ Args a,
+                                                              const __grid_constant__ CUtensorMap tmQ) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* kv_s = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);   // dblocks x 16 KB
+    uint8_t* q_s = kv_s + (size_t)a.dblocks * kBlockBytes;                         // dblocks x 8 KB
+    uint8_t* p_s = q_s + (size_t)a.dblocks * kHg * 128;                            // 128 entries x 64 heads
+    Shared& s = *reinterpret_cast<Shared*>(p_s + kE * 128);
+
+    pdl_wait();
+    pdl_launch_next();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int t = blockIdx.z, h0 = blockIdx.y * kHg, split = blockIdx.x;
+    const int seq = a.qm.seq_of(t);
+    int64_t n_ent = 0;
+    if (seq >= 0 && seq < a.n_seq) n_ent = kSparse ? (int64_t)a.k : visible_entries(a.qm.pos_of(t), a.mp, a.Nmax);
+    const int64_t e_beg = (int64_t)split * a.split_len;
+    const int64_t e_end = n_ent < e_beg + a.split_len ? n_ent : e_beg + a.split_len;
+    const int ntiles = e_end > e_beg ? (int)((e_end - e_beg + kE - 1) / kE) : 0;
+
+    if (tid == 0) {
+        for (int i = 0; i < kBlocks; ++i) {
+            tc::mbar_init(&s.full[i], 8);        // producer warps
+            tc::mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&s.s_full[i], 1);
+            tc::mbar_init(&s.s_empty[i], 8);     // softmax warps
+            tc::mbar_init(&s.fin[i], 1);
+        }
+        tc::mbar_init(&s.q_full, 1);
+        tc::mbar_init(&s.p_full, 8);
+        tc::mbar_init(&s.o_done, 1);
+        tc::fence_mbar_init();
+        s.abort = 0;
+    }
+    if (warp == 16) {
+        tc::tmem_alloc(&s.tmem, a.tmem_cols);
+        tc::tmem_relinquish();
+        tc::tc_fence_before();
+    }
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem_S = s.tmem, tmem_O = s.tmem + 2 * kHg;
+
+    if (warp >= 16) {
+        // ------------------------------------------------------------ products
+        if (lane == 0 && ntiles > 0) {
+            const uint32_t kv_addr = tc::smem_u32(kv_s), q_addr = tc::smem_u32(q_s), p_addr = tc::smem_u32(p_s);
+            bool ok = true;
+            if (warp == 16) {
+                tc::mbar_expect_tx(&s.q_full, (uint32_t)a.dblocks * kHg * 128);
+                for (int b = 0; b < a.dblocks; ++b)
+                    tc::tma_load_2d(q_s + (size_t)b * kHg * 128, &tmQ, &s.q_full, b * 64, t * a.H + h0);
+                ok = wait(&s.q_full, 0, s, a.status);
+                const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
+                const int rope_b = a.f.Q / 64;
+                for (int j = 0; ok && j < ntiles; ++j) {
+                    const int sb = j & 1;
+                    if (j >= 2 && !(ok = wait(&s.s_empty[sb], ((j >> 1) - 1) & 1, s, a.status))) break;
+                    // the order in which blocks arrive: quantised blocks from
+                    // the last to the first, then those with rotary channels
+                    for (int i = 0; i < a.dblocks; ++i) {
+                        const int b = i < rope_b ? rope_b - 1 - i : a.dblocks - 1 - (i - rope_b);
+                        if (!(ok = wait(&s.full[b], j & 1, s, a.status))) break;
+                        tc::tc_fence_after();
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc::umma_bf16(tmem_S + sb * kHg,
+                                          tc::sdesc_sw128(kv_addr + b * kBlockBytes + kk * 32, 16, 1024),
+                                          tc::sdesc_sw128(q_addr + b * (kHg * 128) + kk * 32, 16, 1024), idesc,
+                                          (i | kk) ? 1u : 0u);
+                    }
+                    if (!ok) break;
+                    tc::umma_commit(&s.s_full[sb]);
+                }
+            } else {
+                const uint32_t idesc = tc::idesc_bf16_f32(128, kHg, 1, 1);
+                for (int j = 0; j < ntiles; ++j) {
+                    if (!(ok = wait(&s.p_full, j & 1, s, a.status))) break;
+                    tc::tc_fence_after();
+                    for (int mt = a.mtiles - 1; mt >= 0; --mt) {
+                        for (int ke = 0; ke < kE / 16; ++ke)
+                            tc::umma_bf16(tmem_O + mt * kHg,
+                                          tc::sdesc_sw128(kv_addr + 2 * mt * kBlockBytes + ke * 2048, kBlockBytes, 1024),
+                                          tc::sdesc_sw128(p_addr + ke * 2048, kE * 128, 1024), idesc,
+                                          (j > 0 || ke > 0) ? 1u : 0u);
+                        tc::umma_commit(&s.empty[2 * mt + 1]);
+                        tc::umma_commit(&s.empty[2 * mt]);
+                    }
+                    tc::umma_commit(&s.o_done);
+                }
+            }
+            // every product this thread issued has ended before the CTA goes
+            // on to free the memory it uses (also when a wait ran out)
+            tc::umma_commit(&s.fin[warp - 16]);
+            tc::mbar_wait(&s.fin[warp - 16], 0, kWaitLimit);
+            if (warp == 16) tc::mbar_wait(&s.q_full, 0, kWaitLimit);
+        }
+    } else if (warp >= 8) {
+        produce<kSparse>(a, s, kv_s, t, e_beg, e_end, ntiles,
+                         a.kv4 + (int64_t)(ntiles ? seq : 0) * a.Nmax * a.f.bytes);
     } else {
-        const int64_t i = (int64_t)b * a.Nmax + e;
-        a.weights[i] = (a.acc ? a.acc[i] : 0.f) + w;
+        // ------------------------------------------------------------ softmax
+        const int quad = warp & 3, half = warp >> 2, hb = half * 32;
+        const int row = quad * 32 + lane;                 // entry of the tile / dim of an M tile
+        const int hth = tid & 127;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        if (hth < 32) { s.mref[hb + hth] = -INFINITY; s.lsum[hb + hth] = 0.f; }
+        float lpart[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) lpart[i] = 0.f;
+        half_sync(half);
+        bool ok = true;
+        for (int j = 0; j < ntiles; ++j) {
+            const int sb = j & 1;
+            const int64_t e = e_beg + (int64_t)j * kE + row;
+            bool valid = e < e_end;
+            if (kSparse && valid) {
+                const int v = __ldg(a.idx + (int64_t)t * a.k + e);
+                valid = v >= 0 && v < a.Nmax;
+            }
+            ok = ok && wait(&s.s_full[sb], (j >> 1) & 1, s, a.status);
+            tc::tc_fence_after();
+            float z[32];
+            {
+                float v[16];
+                tc::tmem_ld16(tmem_S + lanes + sb * kHg + hb, v);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) z[i] = v[i];
+                tc::tmem_ld16(tmem_S + lanes + sb * kHg + hb + 16, v);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) z[16 + i] = v[i];
+            }
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&s.s_empty[sb]);
+            bool move = false;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                z[i] = valid ? z[i] * a.scale_log2 : -INFINITY;
+                move |= z[i] > s.mref[hb + i] + kMoveLog2;
+            }
+            if (half_any(half, move || !ok)) {
+                // all leave together once a wait of one ran out
+                if (half_any(half, !ok)) { ok = false; break; }
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = z[i];
+                s.red[quad][hb + lane] = lanes_transpose_reduce(v, lane, [](float x, float y) { return fmaxf(x, y); });
+                half_sync(half);
+                if (hth < 32) {
+                    const int h = hb + hth;
+                    const float old = s.mref[h];
+                    const float m = fmaxf(fmaxf(fmaxf(s.red[0][h], s.red[1][h]), fmaxf(s.red[2][h], s.red[3][h])), old);
+                    s.alpha[h] = old == -INFINITY ? 0.f : ex2(old - m);
+                    s.mref[h] = m;
+                }
+                half_sync(half);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) lpart[i] *= s.alpha[hb + i];
+                if (j > 0) {
+                    ok = wait(&s.o_done, (j - 1) & 1, s, a.status);
+                    tc::tc_fence_after();
+                    for (int mt = 0; mt < a.mtiles; ++mt) {
+#pragma unroll
+                        for (int cc = 0; cc < 32; cc += 16) {
+                            float o[16];
+                            const uint32_t addr = tmem_O + lanes + mt * kHg + hb + cc;
+                            tc::tmem_ld16(addr, o);
+                            tc::tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] *= s.alpha[hb + cc + i];
+                            tc::tmem_st16(addr, o);
+                        }
+                    }
+                    tc::tmem_st_wait();
+                    tc::tc_fence_before();
+                }
+            }
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const float m0 = s.mref[hb + i], m1 = s.mref[hb + i + 1];
+                const float p0 = z[i] == -INFINITY ? 0.f : ex2(z[i] - m0);
+                const float p1 = z[i + 1] == -INFINITY ? 0.f : ex2(z[i + 1] - m1);
+                lpart[i] += p0;
+                lpart[i + 1] += p1;
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
+                pk[i >> 1] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            // the previous tile's O product has read P
+            if (j > 0) ok = wait(&s.o_done, (j - 1) & 1, s, a.status) && ok;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(p_s + row * 128 + (((half * 4 + i) ^ (row & 7)) << 4)) =
+                    make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&s.p_full);
+        }
+        // ------------------------------------------------------------ epilogue
+        if (ok && ntiles > 0) ok = wait(&s.o_done, (ntiles - 1) & 1, s, a.status);
+        tc::tc_fence_after();
+        // per-head sums in a fixed order: lanes, then the four warps
+        half_sync(half);                                  // red may still be read
+        s.red[quad][hb + lane] = lanes_transpose_reduce(lpart, lane, [](float x, float y) { return x + y; });
+        half_sync(half);
+        if (hth < 32) {
+            const int h = hb + hth;
+            s.lsum[h] = (s.red[0][h] + s.red[1][h]) + (s.red[2][h] + s.red[3][h]);
+        }
+        half_sync(half);
+        if (a.merge == kDirect) {
+            if (hth < 32) {
+                const int h = hb + hth;
+                const float m = s.mref[h], L = s.lsum[h];
+                const float sk = a.sink && h0 + h < a.H ? a.sink[h0 + h] * kLog2e : -INFINITY;
+                const float M = fmaxf(m, sk);
+                // (a sum of NaNs has no finite reference: it stays NaN)
+                const float w = L == 0.f ? 0.f : L != L ? L : ex2(m - M);
+                const float Lt = L * w + (sk == -INFINITY ? 0.f : ex2(sk - M));
+                s.alpha[h] = L == 0.f ? 0.f : w / Lt;
+                if (a.lse && h0 + h < a.H)
+                    a.lse[(int64_t)t * a.H + h0 + h] = Lt == 0.f ? -INFINITY : fmaf(M, kLn2, logf(Lt));
+            }
+            half_sync(half);
+            // normalised rows, staged as [head][dim] bf16 where the tile was
+            bf16* stage = reinterpret_cast<bf16*>(kv_s);
+            float al[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) al[i] = s.alpha[hb + i];
+#pragma unroll 1
+            for (int mt = 0; mt < a.mtiles; ++mt) {
+                bf16* col = stage + (size_t)hb * a.f.c + mt * 128 + row;
+#pragma unroll
+                for (int cc = 0; cc < 32; cc += 16) {
+                    float o[16];
+                    if (ntiles > 0) {
+                        tc::tmem_ld16(tmem_O + lanes + mt * kHg + hb + cc, o);
+                        tc::tmem_ld_wait();
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        col[(size_t)(cc + i) * a.f.c] = __float2bfloat16_rn(al[cc + i] != 0.f ? o[i] * al[cc + i] : 0.f);
+                }
+            }
+        } else if (ntiles > 0) {
+            // O^T staged as [head][dim] fp32 where the tile was
+            float* stage = reinterpret_cast<float*>(kv_s);
+#pragma unroll 1
+            for (int mt = 0; mt < a.mtiles; ++mt) {
+                float* col = stage + (size_t)hb * a.f.c + mt * 128 + row;
+#pragma unroll
+                for (int cc = 0; cc < 32; cc += 16) {
+                    float o[16];
+                    tc::tmem_ld16(tmem_O + lanes + mt * kHg + hb + cc, o);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) col[(size_t)(cc + i) * a.f.c] = o[i];
+                }
+            }
+        }
+        tc::tc_fence_before();
     }
+
+    const int nh = a.H - h0 < kHg ? a.H - h0 : kHg, c4 = a.f.c / 4;
+    bf16* out = a.out + ((int64_t)t * a.H + h0) * a.f.c;   // this CTA's heads: contiguous rows
+    if (a.merge == kCluster) {
+        tc::cluster_sync();                               // every split has staged its sums
+        if (tid < kHg) {
+            const float sk = a.sink && h0 + tid < a.H ? a.sink[h0 + tid] * kLog2e : -INFINITY;
+            float m[kMaxCluster], L[kMaxCluster], M = sk;
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) {
+                m[r] = -INFINITY;
+                L[r] = 0.f;
+                if (r < a.nsplit) {
+                    m[r] = tc::ld_cluster_f32(tc::mapa(tc::smem_u32(s.mref + tid), r));
+                    L[r] = tc::ld_cluster_f32(tc::mapa(tc::smem_u32(s.lsum + tid), r));
+                }
+                if (L[r] != 0.f) M = fmaxf(M, m[r]);
+            }
+            float Lt = sk == -INFINITY ? 0.f : ex2(sk - M);
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) {
+                m[r] = L[r] == 0.f ? 0.f : L[r] != L[r] ? L[r] : ex2(m[r] - M);
+                Lt = fmaf(L[r], m[r], Lt);
+            }
+            const float inv = Lt == 0.f ? 0.f : 1.f / Lt;
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) s.coef[r][tid] = m[r] * inv;
+            if (split == 0 && a.lse && h0 + tid < a.H)
+                a.lse[(int64_t)t * a.H + h0 + tid] = Lt == 0.f ? -INFINITY : fmaf(M, kLn2, logf(Lt));
+        }
+        __syncthreads();
+        // this split's share of the (head, 4 dims) items, all splits' sums in split order
+        const int items = nh * c4, lo = (int)((int64_t)items * split / a.nsplit);
+        const int hi = (int)((int64_t)items * (split + 1) / a.nsplit);
+        const uint32_t stage = tc::smem_u32(kv_s);
+        for (int i = lo + tid; i < hi; i += kThreads) {
+            const int h = i / c4;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) {
+                const float w = r < a.nsplit ? s.coef[r][h] : 0.f;
+                if (w != 0.f) {
+                    const float4 o = ld_cluster4(tc::mapa(stage + (uint32_t)i * 16, r));
+                    acc.x = fmaf(w, o.x, acc.x);
+                    acc.y = fmaf(w, o.y, acc.y);
+                    acc.z = fmaf(w, o.z, acc.z);
+                    acc.w = fmaf(w, o.w, acc.w);
+                }
+            }
+            store4(out + (int64_t)i * 4, acc.x, acc.y, acc.z, acc.w);
+        }
+        tc::cluster_sync();                               // no peer still reads this CTA's sums
+    } else {
+        __syncthreads();
+        if (a.merge == kDirect) {
+            const uint4* stage = reinterpret_cast<const uint4*>(kv_s);
+            for (int i = tid; i < nh * a.f.c / 8; i += kThreads) reinterpret_cast<uint4*>(out)[i] = stage[i];
+        } else {
+            const int64_t part = ((int64_t)t * a.nsplit + split) * a.H + h0;
+            if (tid < nh) {
+                const float m = s.mref[tid], L = s.lsum[tid];
+                a.part_ml[(part + tid) * 2] = L == 0.f ? -INFINITY : L != L ? 0.f : m * kLn2;
+                a.part_ml[(part + tid) * 2 + 1] = L;
+            }
+            if (ntiles > 0) {
+                const float4* stage = reinterpret_cast<const float4*>(kv_s);
+                float4* dst = reinterpret_cast<float4*>(a.part_o + part * a.f.c);
+                for (int i = tid; i < nh * c4; i += kThreads) dst[i] = stage[i];
+            }
+        }
+        __syncthreads();
+    }
+    if (warp == 16) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(s.tmem, a.tmem_cols);
+    }
+}
+
+// Splits per query: as many whole tiles per CTA as fill the SMs once.
+int nsplit_of(int nq, int H, int64_t max_entries) {
+    const int64_t ctas = (int64_t)nq * ((H + kHg - 1) / kHg), tiles = (max_entries + kE - 1) / kE;
+    int64_t ns = ctas > 0 ? 148 / ctas : 1;
+    ns = ns > 64 ? 64 : ns;
+    ns = ns > tiles ? tiles : ns;
+    if (ns <= 1) return 1;
+    const int64_t per = (tiles + ns - 1) / ns;
+    return (int)((tiles + per - 1) / per);
 }
 
 }  // namespace
 
 size_t mqa_fp4_workspace_bytes(int nq, int H, int c, int64_t max_entries) {
-    (void)nq; (void)H; (void)c; (void)max_entries;
-    return 0;
+    const int ns = nsplit_of(nq, H, max_entries);
+    if (ns <= kMaxCluster) return 0;
+    return align256((size_t)nq * ns * H * c * sizeof(float)) + align256((size_t)nq * ns * H * 2 * sizeof(float));
 }
 
-cudaError_t mqa_fp4(const Fp4MqaArgs& a, void* ws, cudaStream_t st) {
-    (void)ws;
-    if (a.nq == 0) return cudaSuccess;
-    cudaError_t e = cudaSuccess;
-    CSA_LAUNCH(st, "mqa_fp4", e = launch_pdl(mqa_fp4_kernel, dim3((a.H + 3) / 4, a.nq), dim3(128), 0, st, 0, a));
+cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {
+    if (x.nq == 0) return cudaSuccess;
+    const int64_t max_entries = x.idx ? x.k : x.Nmax;
+    const int ns = nsplit_of(x.nq, x.H, max_entries);
+    Args a{};
+    a.qm = QueryMap{x.qs.seq, x.qs.pos, x.qs.pos_base, x.qs.single_seq};
+    a.kv4 = x.kv4;
+    a.idx = x.idx;
+    a.sink = x.sink;
+    a.out = (bf16*)x.out;
+    a.lse = x.lse;
+    a.part_o = (float*)ws;
+    a.part_ml = (float*)((char*)ws + align256((size_t)x.nq * ns * x.H * x.c * sizeof(float)));
+    a.status = device_status();
+    a.Nmax = x.Nmax;
+    const int64_t tiles = (max_entries + kE - 1) / kE;
+    a.split_len = tiles ? (tiles + ns - 1) / ns * kE : kE;
+    a.f = fp4_row(x.c, x.R);
+    a.k = x.k;
+    a.n_seq = x.n_seq;
+    a.mp = x.mp;
+    a.H = x.H;
+    a.nsplit = ns;
+    a.merge = ns == 1 ? kDirect : ns <= kMaxCluster ? kCluster : kWorkspace;
+    a.dblocks = x.c / 64;
+    a.mtiles = x.c / 128;
+    a.tmem_cols = 2 * kHg + a.mtiles * kHg <= 256 ? 256 : 512;
+    a.scale_log2 = x.scale * kLog2e;
+    CUtensorMap tmQ;
+    if (!make_tmap_bf16_2d(&tmQ, x.q, (uint64_t)x.nq * x.H, x.c, x.c, kHg, 64)) return cudaErrorInvalidValue;
+    const size_t smem = 1024 + (size_t)a.dblocks * (kBlockBytes + kHg * 128) + kE * 128 + sizeof(Shared);
+    auto kern = x.idx ? mqa_fp4_kernel<true> : mqa_fp4_kernel<false>;
+    cudaError_t e = smem_ceiling(kern);
     if (e != cudaSuccess) return e;
-    return cudaGetLastError();
-}
-
-cudaError_t entry_weights_fp4(const Fp4WeightArgs& a, cudaStream_t st) {
-    const int64_t n = a.idx ? a.k : a.Nmax;
-    if (a.B == 0 || n == 0) return cudaSuccess;
-    cudaError_t e = cudaSuccess;
-    CSA_LAUNCH(st, "entry_weights_fp4",
-               e = launch_pdl(entry_weights_fp4_kernel, dim3((unsigned)((n + 3) / 4), a.B), dim3(128), 0, st, 0, a));
+    CSA_LAUNCH(st, "mqa_fp4",
+               e = launch_pdl(kern, dim3(ns, (x.H + kHg - 1) / kHg, x.nq), dim3(kThreads), smem, st,
+                              a.merge == kCluster ? (unsigned)ns : 0u, a, tmQ));
     if (e != cudaSuccess) return e;
+    if (a.merge == kWorkspace) {
+        e = mqa_combine_bf16(a.part_o, a.part_ml, ns, x.nq, x.H, x.c, x.sink, x.out, x.lse, st);
+        if (e != cudaSuccess) return e;
+    }
     return cudaGetLastError();
 }
 
