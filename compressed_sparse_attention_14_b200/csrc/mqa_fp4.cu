@@ -20,9 +20,15 @@
 // 32 (w / 4)..). Warps 8-15: producers; a thread owns half of one row in
 // every 64-dim block (32 channels: 16 bytes of codes), keeps the next tile's
 // codes in registers while it waits for a block to be free, and copies rotary
-// channels with cp.async. Warp 16 issues the S products, warp 17 the O
-// products. A block is refilled as soon as the O product has read it, so the
-// expansion of tile j+1 overlaps the products of tile j.
+// channels with cp.async. A block is refilled as soon as the O product has
+// read it, so the expansion of tile j+1 overlaps the products of tile j.
+//
+// The products are issued by softmax warps: the S product of a tile by warp
+// 4, the O product by warp 0. Neither has anything else to do meanwhile (the
+// softmax of tile j+1 needs its S product, which needs the blocks that the O
+// product of tile j frees), and without two issuing warps the 16 warps get
+// 128 registers each: with 18 warps the limit is 96, the producers' codes
+// spilled, and a tile took 10 us instead of TILE_US.
 //
 // Entries outside the query's set are stored as zeros and get weight 0: no
 // row that the query does not see is read.
@@ -39,7 +45,7 @@ namespace csa {
 
 namespace {
 
-constexpr int kThreads = 576;
+constexpr int kThreads = 512;
 constexpr int kE = 128;                 // entries per tile
 constexpr int kHg = 64;                 // heads per CTA
 constexpr int kBlocks = CSA_MAX_HEAD_DIM / 64;
@@ -73,7 +79,7 @@ struct Shared {
     float red[4][kHg];
     float coef[kMaxCluster][kHg];
     uint64_t full[kBlocks], empty[kBlocks];   // a block of the tile stored / free
-    uint64_t s_full[2], s_empty[2], q_full, p_full, o_done, fin[2];
+    uint64_t s_full, q_full, p_full, o_done, fin;
     uint32_t tmem;
     int abort;
 };
@@ -235,6 +241,50 @@ __device__ __forceinline__ void produce(const Args& a, Shared& s, uint8_t* kv_s,
     }
 }
 
+// S^T of tile j: one thread, blocks in the order in which they arrive
+// (quantised blocks from the last to the first, then those with rotary
+// channels).
+__device__ __forceinline__ bool issue_s(const Args& a, Shared& s, uint32_t kv_addr, uint32_t q_addr, uint32_t d_tmem,
+                                        int j) {
+    const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
+    const int rope_b = a.f.Q / 64;
+    for (int i = 0; i < a.dblocks; ++i) {
+        const int b = i < rope_b ? rope_b - 1 - i : a.dblocks - 1 - (i - rope_b);
+        if (!wait(&s.full[b], j & 1, s, a.status)) {
+            // the products already issued end before the CTA frees their memory
+            tc::umma_commit(&s.fin);
+            tc::mbar_wait(&s.fin, 0, kWaitLimit);
+            return false;
+        }
+        tc::tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+            tc::umma_bf16(d_tmem, tc::sdesc_sw128(kv_addr + b * kBlockBytes + kk * 32, 16, 1024),
+                          tc::sdesc_sw128(q_addr + b * (kHg * 128) + kk * 32, 16, 1024), idesc, (i | kk) ? 1u : 0u);
+    }
+    tc::umma_commit(&s.s_full);
+    return true;
+}
+
+// O^T += of tile j: one thread; each pair of blocks is handed back to the
+// producers once its product is done, the last first.
+__device__ __forceinline__ bool issue_o(const Args& a, Shared& s, uint32_t kv_addr, uint32_t p_addr, uint32_t d_tmem,
+                                        int j) {
+    const uint32_t idesc = tc::idesc_bf16_f32(128, kHg, 1, 1);
+    if (!wait(&s.p_full, j & 1, s, a.status)) return false;
+    tc::tc_fence_after();
+    for (int mt = a.mtiles - 1; mt >= 0; --mt) {
+#pragma unroll
+        for (int ke = 0; ke < kE / 16; ++ke)
+            tc::umma_bf16(d_tmem + mt * kHg, tc::sdesc_sw128(kv_addr + 2 * mt * kBlockBytes + ke * 2048, kBlockBytes, 1024),
+                          tc::sdesc_sw128(p_addr + ke * 2048, kE * 128, 1024), idesc, (j > 0 || ke > 0) ? 1u : 0u);
+        tc::umma_commit(&s.empty[2 * mt + 1]);
+        tc::umma_commit(&s.empty[2 * mt]);
+    }
+    tc::umma_commit(&s.o_done);
+    return true;
+}
+
 template <bool kSparse>
 __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_constant__ Args a,
                                                               const __grid_constant__ CUtensorMap tmQ) {
@@ -260,80 +310,24 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             tc::mbar_init(&s.full[i], 8);        // producer warps
             tc::mbar_init(&s.empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&s.s_full[i], 1);
-            tc::mbar_init(&s.s_empty[i], 8);     // softmax warps
-            tc::mbar_init(&s.fin[i], 1);
-        }
+        tc::mbar_init(&s.s_full, 1);
         tc::mbar_init(&s.q_full, 1);
-        tc::mbar_init(&s.p_full, 8);
+        tc::mbar_init(&s.fin, 1);
+        tc::mbar_init(&s.p_full, 8);             // softmax warps
         tc::mbar_init(&s.o_done, 1);
         tc::fence_mbar_init();
         s.abort = 0;
     }
-    if (warp == 16) {
+    if (warp == 0) {
         tc::tmem_alloc(&s.tmem, a.tmem_cols);
         tc::tmem_relinquish();
         tc::tc_fence_before();
     }
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tmem_S = s.tmem, tmem_O = s.tmem + 2 * kHg;
+    const uint32_t tmem_S = s.tmem, tmem_O = s.tmem + kHg;
 
-    if (warp >= 16) {
-        // ------------------------------------------------------------ products
-        if (lane == 0 && ntiles > 0) {
-            const uint32_t kv_addr = tc::smem_u32(kv_s), q_addr = tc::smem_u32(q_s), p_addr = tc::smem_u32(p_s);
-            bool ok = true;
-            if (warp == 16) {
-                tc::mbar_expect_tx(&s.q_full, (uint32_t)a.dblocks * kHg * 128);
-                for (int b = 0; b < a.dblocks; ++b)
-                    tc::tma_load_2d(q_s + (size_t)b * kHg * 128, &tmQ, &s.q_full, b * 64, t * a.H + h0);
-                ok = wait(&s.q_full, 0, s, a.status);
-                const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
-                const int rope_b = a.f.Q / 64;
-                for (int j = 0; ok && j < ntiles; ++j) {
-                    const int sb = j & 1;
-                    if (j >= 2 && !(ok = wait(&s.s_empty[sb], ((j >> 1) - 1) & 1, s, a.status))) break;
-                    // the order in which blocks arrive: quantised blocks from
-                    // the last to the first, then those with rotary channels
-                    for (int i = 0; i < a.dblocks; ++i) {
-                        const int b = i < rope_b ? rope_b - 1 - i : a.dblocks - 1 - (i - rope_b);
-                        if (!(ok = wait(&s.full[b], j & 1, s, a.status))) break;
-                        tc::tc_fence_after();
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc::umma_bf16(tmem_S + sb * kHg,
-                                          tc::sdesc_sw128(kv_addr + b * kBlockBytes + kk * 32, 16, 1024),
-                                          tc::sdesc_sw128(q_addr + b * (kHg * 128) + kk * 32, 16, 1024), idesc,
-                                          (i | kk) ? 1u : 0u);
-                    }
-                    if (!ok) break;
-                    tc::umma_commit(&s.s_full[sb]);
-                }
-            } else {
-                const uint32_t idesc = tc::idesc_bf16_f32(128, kHg, 1, 1);
-                for (int j = 0; j < ntiles; ++j) {
-                    if (!(ok = wait(&s.p_full, j & 1, s, a.status))) break;
-                    tc::tc_fence_after();
-                    for (int mt = a.mtiles - 1; mt >= 0; --mt) {
-                        for (int ke = 0; ke < kE / 16; ++ke)
-                            tc::umma_bf16(tmem_O + mt * kHg,
-                                          tc::sdesc_sw128(kv_addr + 2 * mt * kBlockBytes + ke * 2048, kBlockBytes, 1024),
-                                          tc::sdesc_sw128(p_addr + ke * 2048, kE * 128, 1024), idesc,
-                                          (j > 0 || ke > 0) ? 1u : 0u);
-                        tc::umma_commit(&s.empty[2 * mt + 1]);
-                        tc::umma_commit(&s.empty[2 * mt]);
-                    }
-                    tc::umma_commit(&s.o_done);
-                }
-            }
-            // every product this thread issued has ended before the CTA goes
-            // on to free the memory it uses (also when a wait ran out)
-            tc::umma_commit(&s.fin[warp - 16]);
-            tc::mbar_wait(&s.fin[warp - 16], 0, kWaitLimit);
-            if (warp == 16) tc::mbar_wait(&s.q_full, 0, kWaitLimit);
-        }
-    } else if (warp >= 8) {
+    if (warp >= 8) {
         produce<kSparse>(a, s, kv_s, t, e_beg, e_end, ntiles,
                          a.kv4 + (int64_t)(ntiles ? seq : 0) * a.Nmax * a.f.bytes);
     } else {
@@ -347,32 +341,41 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
 #pragma unroll
         for (int i = 0; i < 32; ++i) lpart[i] = 0.f;
         half_sync(half);
+        const uint32_t kv_addr = tc::smem_u32(kv_s), q_addr = tc::smem_u32(q_s), p_addr = tc::smem_u32(p_s);
         bool ok = true;
+        int done_s = 0, done_o = 0;       // products issued by this thread
+        if (tid == 128 && ntiles > 0) {
+            tc::mbar_expect_tx(&s.q_full, (uint32_t)a.dblocks * kHg * 128);
+            for (int b = 0; b < a.dblocks; ++b)
+                tc::tma_load_2d(q_s + (size_t)b * kHg * 128, &tmQ, &s.q_full, b * 64, t * a.H + h0);
+            ok = wait(&s.q_full, 0, s, a.status);
+        }
         for (int j = 0; j < ntiles; ++j) {
-            const int sb = j & 1;
+            if (tid == 128 && ok) {
+                ok = issue_s(a, s, kv_addr, q_addr, tmem_S, j);
+                done_s += ok;
+            }
+            __syncwarp();
             const int64_t e = e_beg + (int64_t)j * kE + row;
             bool valid = e < e_end;
             if (kSparse && valid) {
                 const int v = __ldg(a.idx + (int64_t)t * a.k + e);
                 valid = v >= 0 && v < a.Nmax;
             }
-            ok = ok && wait(&s.s_full[sb], (j >> 1) & 1, s, a.status);
+            ok = ok && wait(&s.s_full, j & 1, s, a.status);
             tc::tc_fence_after();
             float z[32];
             {
                 float v[16];
-                tc::tmem_ld16(tmem_S + lanes + sb * kHg + hb, v);
+                tc::tmem_ld16(tmem_S + lanes + hb, v);
                 tc::tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) z[i] = v[i];
-                tc::tmem_ld16(tmem_S + lanes + sb * kHg + hb + 16, v);
+                tc::tmem_ld16(tmem_S + lanes + hb + 16, v);
                 tc::tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) z[16 + i] = v[i];
             }
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&s.s_empty[sb]);
             bool move = false;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -433,12 +436,24 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             for (int i = 0; i < 4; ++i)
                 *reinterpret_cast<uint4*>(p_s + row * 128 + (((half * 4 + i) ^ (row & 7)) << 4)) =
                     make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+            tc::tc_fence_before();                        // S has been read, too
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&s.p_full);
+            if (tid == 0 && ok) {
+                ok = issue_o(a, s, kv_addr, p_addr, tmem_O, j);
+                done_o += ok;
+            }
+            __syncwarp();
         }
         // ------------------------------------------------------------ epilogue
         if (ok && ntiles > 0) ok = wait(&s.o_done, (ntiles - 1) & 1, s, a.status);
+        // when a wait ran out, the products and copies already issued still
+        // end before the CTA frees the memory they use
+        if (!ok && done_s) tc::mbar_wait(&s.s_full, (done_s - 1) & 1, kWaitLimit);
+        if (!ok && done_o) tc::mbar_wait(&s.o_done, (done_o - 1) & 1, kWaitLimit);
+        if (!ok && tid == 128) tc::mbar_wait(&s.q_full, 0, kWaitLimit);
+        __syncwarp();
         tc::tc_fence_after();
         // per-head sums in a fixed order: lanes, then the four warps
         half_sync(half);                                  // red may still be read
@@ -573,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         }
         __syncthreads();
     }
-    if (warp == 16) {
+    if (warp == 0) {
         tc::tc_fence_after();
         tc::tmem_dealloc(s.tmem, a.tmem_cols);
     }
@@ -624,7 +639,7 @@ cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {
     a.merge = ns == 1 ? kDirect : ns <= kMaxCluster ? kCluster : kWorkspace;
     a.dblocks = x.c / 64;
     a.mtiles = x.c / 128;
-    a.tmem_cols = 2 * kHg + a.mtiles * kHg <= 256 ? 256 : 512;
+    a.tmem_cols = kHg * (1 + a.mtiles) <= 128 ? 128 : kHg * (1 + a.mtiles) <= 256 ? 256 : 512;
     a.scale_log2 = x.scale * kLog2e;
     CUtensorMap tmQ;
     if (!make_tmap_bf16_2d(&tmQ, x.q, (uint64_t)x.nq * x.H, x.c, x.c, kHg, 64)) return cudaErrorInvalidValue;
