@@ -18,9 +18,8 @@
 //
 // Warps 0-7: softmax and epilogue (warp w: TMEM lanes 32 (w % 4).., heads
 // 32 (w / 4)..). Warps 8-15: producers; a thread owns half of one row in
-// every 64-dim block (32 channels: 16 bytes of codes), keeps the next tile's
-// codes in registers while it waits for a block to be free, and copies rotary
-// channels with cp.async. A block is refilled as soon as the O product has
+// every 64-dim block (32 channels: 16 bytes of codes) and has the next tile's
+// codes in registers by the time a block is free. A block is refilled as soon as the O product has
 // read it, so the expansion of tile j+1 overlaps the products of tile j.
 //
 // The products are issued by softmax warps: the S product of a tile by warp
@@ -127,6 +126,13 @@ __device__ __forceinline__ bool half_any(int half, bool v) {
     return r != 0;
 }
 
+// Blocks up to this one hold quantised channels or each thread's first
+// rotary chunk, which are loaded ahead; later ones are rotary throughout.
+__device__ __forceinline__ int last_early_block(const Args& a) {
+    const int b = a.f.Q / 64;
+    return b < a.dblocks - 1 ? b : a.dblocks - 1;
+}
+
 // v[i] of 32 lanes -> in lane l the combination of every lane's v[l] (31 shuffles)
 template <typename Op>
 __device__ __forceinline__ float lanes_transpose_reduce(float (&v)[32], int lane, Op op) {
@@ -147,11 +153,15 @@ __device__ __forceinline__ float lanes_transpose_reduce(float (&v)[32], int lane
 }
 
 // Producer: rows of every tile, block by block from the last to the first.
+// All of a tile's loads are issued together, after the tile before it has
+// been stored: a proxy fence waits for the thread's outstanding loads, so
+// loads issued between the blocks' fences would each be waited for at once.
 template <bool kSparse>
 __device__ __forceinline__ void produce(const Args& a, Shared& s, uint8_t* kv_s, int t, int64_t e_beg, int64_t e_end,
                                         int ntiles, const uint8_t* seq_rows) {
     const int pt = threadIdx.x - 256, row = pt >> 1, half = pt & 1, lane = threadIdx.x & 31;
-    const int nq32 = a.f.Q / 32, rope_b = nq32 / 2;       // first block with rotary channels
+    const int nq32 = a.f.Q / 32, first_rope = (nq32 - half + 1) / 2;   // this half's first rotary block
+    const int last = last_early_block(a);
     auto entry = [&](int j) -> int64_t {                  // entry index of this row in tile j, -1: none
         const int64_t e = e_beg + (int64_t)j * kE + row;
         if (e >= e_end) return -1;
@@ -159,97 +169,96 @@ __device__ __forceinline__ void produce(const Args& a, Shared& s, uint8_t* kv_s,
         const int64_t v = __ldg(a.idx + (int64_t)t * a.k + e);
         return v < a.Nmax ? v : -1;
     };
-    auto address = [&](int64_t e) { return e >= 0 ? seq_rows + e * a.f.bytes : nullptr; };
-    uint4 raw[kBlocks], sc[2], nsc[2];
-    uint32_t ebase, nebase;
-    auto load_codes = [&](const uint8_t* p, int b) {
-        return p && 2 * b + half < nq32 ? __ldg(reinterpret_cast<const uint4*>(p) + 2 * b + half)
-                                        : make_uint4(0, 0, 0, 0);
-    };
-    auto load_scales = [&](const uint8_t* p, uint4 (&o)[2], uint32_t& eb) {
-        o[0] = o[1] = make_uint4(0, 0, 0, 0);
-        eb = 128;                                         // a missing row: codes 0 times 2^-126
-        if (!p) return;
-        o[0] = __ldg(reinterpret_cast<const uint4*>(p + a.f.scale_off));
-        if (a.f.Q > 256) o[1] = __ldg(reinterpret_cast<const uint4*>(p + a.f.scale_off) + 1);
-        eb = ((uint32_t)__ldg(p + a.f.scale_off + a.f.Q / 16) - 31u) << 7;
-    };
-    const uint8_t* p = address(entry(0));
-    load_scales(p, sc, ebase);
-#pragma unroll
-    for (int b = kBlocks - 1; b >= 0; --b)
-        if (b < a.dblocks) raw[b] = load_codes(p, b);
-    int64_t next = ntiles > 1 ? entry(1) : -1;
+    int64_t next = entry(0);
     for (int j = 0; j < ntiles; ++j) {
-        const uint8_t* np = address(next);
-        next = j + 2 < ntiles ? entry(j + 2) : -1;
-        load_scales(np, nsc, nebase);
-        if (np)
-            for (int ch = nq32 + ((nq32 ^ half) & 1); ch < a.f.c / 32; ch += 2)
-                prefetch_l2(np + a.f.rope_off + (ch - nq32) * 64);
+        const uint8_t* p = next >= 0 ? seq_rows + next * a.f.bytes : nullptr;
+        // a missing row: codes 0 times 2^-126, rotary channels 0
+        uint4 raw[kBlocks], rope[4], sc[2];
+        uint32_t ebase = 128;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            raw[b] = make_uint4(0, 0, 0, 0);
+            if (p && b < first_rope) raw[b] = __ldg(reinterpret_cast<const uint4*>(p) + 2 * b + half);
+        }
+        sc[0] = sc[1] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rope[i] = make_uint4(0, 0, 0, 0);
+        if (p) {
+            const uint4* ps = reinterpret_cast<const uint4*>(p + a.f.scale_off);
+            sc[0] = __ldg(ps);
+            if (a.f.Q > 256) sc[1] = __ldg(ps + 1);
+            ebase = ((uint32_t)__ldg(p + a.f.scale_off + a.f.Q / 16) - 31u) << 7;
+            if (first_rope < a.dblocks) {
+                const uint4* pr = reinterpret_cast<const uint4*>(p + a.f.rope_off + (2 * first_rope + half - nq32) * 64);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) rope[i] = __ldg(pr + i);
+            }
+            for (int b = last + 1; b < a.dblocks; ++b) prefetch_l2(p + a.f.rope_off + (2 * b + half - nq32) * 64);
+        }
+        next = j + 1 < ntiles ? entry(j + 1) : -1;
         const uint32_t scw[8] = {sc[0].x, sc[0].y, sc[0].z, sc[0].w, sc[1].x, sc[1].y, sc[1].z, sc[1].w};
         bool ok = true;
+        auto free_block = [&](int b) {                    // tile j-1's O product has read it
+            if (j == 0 || !ok) return;
+            if (lane == 0) ok = wait(&s.empty[b], (j - 1) & 1, s, a.status);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        };
 #pragma unroll
         for (int b = kBlocks - 1; b >= 0; --b) {
-            if (b < a.dblocks && ok) {
-                if (j > 0) {
-                    if (lane == 0) ok = wait(&s.empty[b], (j - 1) & 1, s, a.status);
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (b > last) continue;
+            free_block(b);
+            if (!ok) continue;
+            uint8_t* dst = kv_s + (size_t)b * kBlockBytes + row * 128;
+            const uint32_t two = scw[b] >> (16 * half);
+            const uint32_t S0 = ((ebase + ((two & 255u) << 4)) & 0xffffu) * 0x10001u;
+            const uint32_t S1 = ((ebase + ((two >> 4) & 0xff0u)) & 0xffffu) * 0x10001u;
+            const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint4 v = rope[i];
+                if (b < first_rope) {
+                    uint32_t o[4];
+                    fp4_word(w[i], i < 2 ? S0 : S1, o);
+                    v = make_uint4(o[0], o[1], o[2], o[3]);
                 }
-                if (ok) {
-                    uint8_t* dst = kv_s + (size_t)b * kBlockBytes + row * 128;
-                    if (2 * b + half < nq32) {
-                        const uint32_t two = scw[b] >> (16 * half);
-                        const uint32_t S0 = ((ebase + ((two & 255u) << 4)) & 0xffffu) * 0x10001u;
-                        const uint32_t S1 = ((ebase + ((two >> 4) & 0xff0u)) & 0xffffu) * 0x10001u;
-                        const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+                *reinterpret_cast<uint4*>(dst + (((half * 4 + i) ^ (row & 7)) << 4)) = v;
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&s.full[b]);
+        }
+        if (last + 1 < a.dblocks) {
+            // further rotary blocks: copied as they are
+            for (int b = a.dblocks - 1; b > last; --b) {
+                free_block(b);
+                if (!ok) continue;
+                uint8_t* dst = kv_s + (size_t)b * kBlockBytes + row * 128;
+                const uint8_t* src = p ? p + a.f.rope_off + (2 * b + half - nq32) * 64 : nullptr;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t v[4];
-                            fp4_word(w[i], i < 2 ? S0 : S1, v);
-                            *reinterpret_cast<uint4*>(dst + (((half * 4 + i) ^ (row & 7)) << 4)) =
-                                make_uint4(v[0], v[1], v[2], v[3]);
-                        }
-                        raw[b] = load_codes(np, b);
-                    } else {
-                        const uint8_t* src = p ? p + a.f.rope_off + (2 * b + half - nq32) * 64 : nullptr;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint8_t* d = dst + (((half * 4 + i) ^ (row & 7)) << 4);
-                            if (src) cp_async16(d, src + 16 * i);
-                            else *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
-                        }
-                    }
-                    if (b < rope_b) {
-                        tc::fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&s.full[b]);
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    uint8_t* d = dst + (((half * 4 + i) ^ (row & 7)) << 4);
+                    if (src) cp_async16(d, src + 16 * i);
+                    else *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
                 }
             }
+            cp_async_wait_all();
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && ok)
+                for (int b = a.dblocks - 1; b > last; --b) tc::mbar_arrive(&s.full[b]);
         }
-        cp_async_wait_all();
         if (!ok) break;
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0)
-            for (int b = a.dblocks - 1; b >= rope_b; --b) tc::mbar_arrive(&s.full[b]);
-        p = np;
-        sc[0] = nsc[0];
-        sc[1] = nsc[1];
-        ebase = nebase;
     }
 }
 
 // S^T of tile j: one thread, blocks in the order in which they arrive
-// (quantised blocks from the last to the first, then those with rotary
-// channels).
+// (loaded ahead: from the last to the first; then the other rotary blocks).
 __device__ __forceinline__ bool issue_s(const Args& a, Shared& s, uint32_t kv_addr, uint32_t q_addr, uint32_t d_tmem,
                                         int j) {
     const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
-    const int rope_b = a.f.Q / 64;
+    const int last = last_early_block(a);
     for (int i = 0; i < a.dblocks; ++i) {
-        const int b = i < rope_b ? rope_b - 1 - i : a.dblocks - 1 - (i - rope_b);
+        const int b = i <= last ? last - i : a.dblocks - 1 - (i - last - 1);
         if (!wait(&s.full[b], j & 1, s, a.status)) {
             // the products already issued end before the CTA frees their memory
             tc::umma_commit(&s.fin);
