@@ -16,18 +16,18 @@
 // so the result does not depend on when it moves. P is rounded to bf16 for
 // the second product; the sums, maxima and O stay fp32.
 //
-// Warps 0-7: softmax and epilogue (warp w: TMEM lanes 32 (w % 4).., heads
-// 32 (w / 4)..). Warps 8-15: producers; a thread owns half of one row in
-// every 64-dim block (32 channels: 16 bytes of codes) and has the next tile's
-// codes in registers by the time a block is free. A block is refilled as soon as the O product has
-// read it, so the expansion of tile j+1 overlaps the products of tile j.
-//
-// The products are issued by softmax warps: the S product of a tile by warp
-// 4, the O product by warp 0. Neither has anything else to do meanwhile (the
-// softmax of tile j+1 needs its S product, which needs the blocks that the O
-// product of tile j frees), and without two issuing warps the 16 warps get
-// 128 registers each: with 18 warps the limit is 96, the producers' codes
-// spilled, and a tile took 10 us instead of TILE_US.
+// 16 worker warps do both the expansion and the softmax, which cannot overlap
+// for one tile buffer (the expansion of tile j+1 needs blocks that the O
+// product of tile j has read, the softmax of tile j+1 needs its S product).
+//   expansion: warps 0-7 the even, 8-15 the odd 64-dim blocks; a thread owns
+//     half a row of its blocks (32 channels: 16 bytes of codes) and has the
+//     next tile's codes in registers by the time a block is free;
+//   softmax and epilogue: warp w works on TMEM lanes 32 (w % 4).. and heads
+//     16 (w / 4)...
+// Warp 16 issues the S products, warp 17 the O products. Blocks go back and
+// forth in pairs (128 dims, one M tile of the O product), the last first, so
+// expansion and S product of tile j+1 run while the O product of tile j is
+// still busy with the pairs before.
 //
 // Entries outside the query's set are stored as zeros and get weight 0: no
 // row that the query does not see is read.
@@ -44,10 +44,11 @@ namespace csa {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kWorkers = 512, kThreads = kWorkers + 64;
 constexpr int kE = 128;                 // entries per tile
 constexpr int kHg = 64;                 // heads per CTA
-constexpr int kBlocks = CSA_MAX_HEAD_DIM / 64;
+constexpr int kPairs = CSA_MAX_HEAD_DIM / 128;   // pairs of 64-dim blocks
+constexpr int kGh = 16;                  // heads per worker warp
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kBlockBytes = kE * 128;
 constexpr uint32_t kWaitLimit = 1u << 24;
@@ -77,8 +78,8 @@ struct Shared {
     float mref[kHg], alpha[kHg], lsum[kHg];
     float red[4][kHg];
     float coef[kMaxCluster][kHg];
-    uint64_t full[kBlocks], empty[kBlocks];   // a block of the tile stored / free
-    uint64_t s_full, q_full, p_full, o_done, fin;
+    uint64_t full[kPairs], empty[kPairs];     // a pair of blocks stored / free
+    uint64_t s_full, q_full, p_full, o_done, fin[2];
     uint32_t tmem;
     int abort;
 };
@@ -112,193 +113,176 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Shared& s, 
     return false;
 }
 
-// barrier (and vote) of the 128 softmax threads of one half of the heads
-__device__ __forceinline__ void half_sync(int half) {
-    asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-}
-__device__ __forceinline__ bool half_any(int half, bool v) {
+// barrier (and vote) of the 4 warps that share 16 heads
+__device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
+__device__ __forceinline__ bool group_any(int g, bool v) {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p, q;\n\t"
                  "setp.ne.u32 q, %1, 0;\n\t"
                  "bar.red.or.pred p, %2, 128, q;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(r) : "r"((uint32_t)v), "r"(1 + half) : "memory");
+                 : "=r"(r) : "r"((uint32_t)v), "r"(1 + g) : "memory");
     return r != 0;
 }
 
-// Blocks up to this one hold quantised channels or each thread's first
-// rotary chunk, which are loaded ahead; later ones are rotary throughout.
-__device__ __forceinline__ int last_early_block(const Args& a) {
-    const int b = a.f.Q / 64;
-    return b < a.dblocks - 1 ? b : a.dblocks - 1;
-}
-
-// v[i] of 32 lanes -> in lane l the combination of every lane's v[l] (31 shuffles)
+// v[i] of 32 lanes -> in lane l every lane's v[l / 2] combined (16 shuffles)
 template <typename Op>
-__device__ __forceinline__ float lanes_transpose_reduce(float (&v)[32], int lane, Op op) {
+__device__ __forceinline__ float lanes_reduce16(float (&v)[kGh], int lane, Op op) {
 #pragma unroll
-    for (int r = 0; r < 5; ++r) {
-        const int o = 16 >> r;
+    for (int r = 0; r < 4; ++r) {
+        const int o = 16 >> r, n = 8 >> r;
         const bool upper = (lane & o) != 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            if (i < o) {
-                const float send = upper ? v[i] : v[i + o];
-                const float keep = upper ? v[i + o] : v[i];
+        for (int i = 0; i < 8; ++i) {
+            if (i < n) {
+                const float send = upper ? v[i] : v[i + n];
+                const float keep = upper ? v[i + n] : v[i];
                 v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
             }
         }
     }
-    return v[0];
+    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
-// Producer: rows of every tile, block by block from the last to the first.
-// All of a tile's loads are issued together, after the tile before it has
-// been stored: a proxy fence waits for the thread's outstanding loads, so
-// loads issued between the blocks' fences would each be waited for at once.
+// Pairs up to this one hold quantised channels or each thread's first rotary
+// chunk, which are loaded ahead; later ones are rotary throughout.
+__device__ __forceinline__ int last_early_pair(const Args& a) {
+    const int i = a.f.Q / 128;
+    return i < a.mtiles - 1 ? i : a.mtiles - 1;
+}
+
+// A thread's part of the expansion: half a row (32 channels) of every second block.
 template <bool kSparse>
-__device__ __forceinline__ void produce(const Args& a, Shared& s, uint8_t* kv_s, int t, int64_t e_beg, int64_t e_end,
-                                        int ntiles, const uint8_t* seq_rows) {
-    const int pt = threadIdx.x - 256, row = pt >> 1, half = pt & 1, lane = threadIdx.x & 31;
-    const int nq32 = a.f.Q / 32, first_rope = (nq32 - half + 1) / 2;   // this half's first rotary block
-    const int last = last_early_block(a);
-    auto entry = [&](int j) -> int64_t {                  // entry index of this row in tile j, -1: none
-        const int64_t e = e_beg + (int64_t)j * kE + row;
-        if (e >= e_end) return -1;
+struct Producer {
+    const Args& a;
+    Shared& s;
+    uint8_t* dst;             // this thread's row in its first block
+    const uint8_t* seq_rows;
+    const int32_t* list;
+    int e0, e_end, next;      // (entry indices fit: Nmax is below 2^31)
+    int ntiles, row, chunk, nq32, first_rope, last;
+    uint4 raw[kPairs], rope[4];
+    uint32_t scales[kPairs], ebase;
+    const uint8_t* p;
+
+    __device__ __forceinline__ Producer(const Args& a_, Shared& s_, uint8_t* kv_s, int t, int64_t e_beg, int64_t e_end_,
+                                        int ntiles_, const uint8_t* rows)
+        : a(a_), s(s_), seq_rows(rows), e_end((int)e_end_), ntiles(ntiles_) {
+        const int pt = threadIdx.x & 255, half = pt & 1, parity = threadIdx.x >> 8;
+        row = pt >> 1;
+        chunk = 2 * parity + half;                        // 32-channel chunk within a pair
+        dst = kv_s + parity * kBlockBytes + row * 128;
+        list = kSparse ? a.idx + (int64_t)t * a.k : nullptr;
+        e0 = (int)e_beg + row;
+        nq32 = a.f.Q / 32;
+        first_rope = nq32 > chunk ? (nq32 - chunk + 3) / 4 : 0;
+        last = last_early_pair(a);
+        next = entry(0);
+        if (ntiles > 0) load(0);
+    }
+    // entry index of this row in tile j, -1: none
+    __device__ __forceinline__ int entry(int j) const {
+        if (j >= ntiles || e_end - e0 <= j * kE) return -1;
+        const int e = e0 + j * kE;
         if (!kSparse) return e;
-        const int64_t v = __ldg(a.idx + (int64_t)t * a.k + e);
+        const int v = __ldg(list + e);
         return v < a.Nmax ? v : -1;
-    };
-    int64_t next = entry(0);
-    for (int j = 0; j < ntiles; ++j) {
-        const uint8_t* p = next >= 0 ? seq_rows + next * a.f.bytes : nullptr;
-        // a missing row: codes 0 times 2^-126, rotary channels 0
-        uint4 raw[kBlocks], rope[4], sc[2];
-        uint32_t ebase = 128;
+    }
+    __device__ __forceinline__ const uint8_t* rope_chunk(int i) const {
+        return p + a.f.rope_off + (4 * i + chunk - nq32) * 64;
+    }
+    // All of a tile's loads, issued together right after the tile before it
+    // is stored. A missing row: codes 0 times 2^-126, rotary channels 0.
+    __device__ __forceinline__ void load(int j) {
+        p = next >= 0 ? seq_rows + (int64_t)next * a.f.bytes : nullptr;
+        next = entry(j + 1);
+        ebase = 128;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-            raw[b] = make_uint4(0, 0, 0, 0);
-            if (p && b < first_rope) raw[b] = __ldg(reinterpret_cast<const uint4*>(p) + 2 * b + half);
+        for (int i = 0; i < kPairs; ++i) {
+            raw[i] = make_uint4(0, 0, 0, 0);
+            scales[i] = 0;
+            if (p && i < first_rope && i < a.mtiles) {
+                raw[i] = __ldg(reinterpret_cast<const uint4*>(p) + 4 * i + chunk);
+                scales[i] = __ldg(reinterpret_cast<const uint16_t*>(p + a.f.scale_off) + 4 * i + chunk);
+            }
         }
-        sc[0] = sc[1] = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) rope[i] = make_uint4(0, 0, 0, 0);
         if (p) {
-            const uint4* ps = reinterpret_cast<const uint4*>(p + a.f.scale_off);
-            sc[0] = __ldg(ps);
-            if (a.f.Q > 256) sc[1] = __ldg(ps + 1);
             ebase = ((uint32_t)__ldg(p + a.f.scale_off + a.f.Q / 16) - 31u) << 7;
-            if (first_rope < a.dblocks) {
-                const uint4* pr = reinterpret_cast<const uint4*>(p + a.f.rope_off + (2 * first_rope + half - nq32) * 64);
+            if (first_rope < a.mtiles) {
+                const uint4* pr = reinterpret_cast<const uint4*>(rope_chunk(first_rope));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) rope[i] = __ldg(pr + i);
             }
-            for (int b = last + 1; b < a.dblocks; ++b) prefetch_l2(p + a.f.rope_off + (2 * b + half - nq32) * 64);
+            for (int i = last + 1; i < a.mtiles; ++i)
+                if (i > first_rope) prefetch_l2(rope_chunk(i));
         }
-        next = j + 1 < ntiles ? entry(j + 1) : -1;
-        const uint32_t scw[8] = {sc[0].x, sc[0].y, sc[0].z, sc[0].w, sc[1].x, sc[1].y, sc[1].z, sc[1].w};
+    }
+    __device__ __forceinline__ uint8_t* piece(int i, int u) const {
+        return dst + (size_t)i * 2 * kBlockBytes + ((((chunk & 1) * 4 + u) ^ (row & 7)) << 4);
+    }
+    // stores tile j, then loads tile j + 1; false when a wait ran out
+    __device__ __forceinline__ bool store(int j) {
+        const int lane = threadIdx.x & 31;
         bool ok = true;
-        auto free_block = [&](int b) {                    // tile j-1's O product has read it
+        auto free_pair = [&](int i) {                     // tile j-1's O product has read it
             if (j == 0 || !ok) return;
-            if (lane == 0) ok = wait(&s.empty[b], (j - 1) & 1, s, a.status);
+            if (lane == 0) ok = wait(&s.empty[i], (j - 1) & 1, s, a.status);
             ok = __shfl_sync(0xffffffffu, ok, 0);
         };
 #pragma unroll
-        for (int b = kBlocks - 1; b >= 0; --b) {
-            if (b > last) continue;
-            free_block(b);
+        for (int i = kPairs - 1; i >= 0; --i) {
+            if (i > last) continue;
+            free_pair(i);
             if (!ok) continue;
-            uint8_t* dst = kv_s + (size_t)b * kBlockBytes + row * 128;
-            const uint32_t two = scw[b] >> (16 * half);
-            const uint32_t S0 = ((ebase + ((two & 255u) << 4)) & 0xffffu) * 0x10001u;
-            const uint32_t S1 = ((ebase + ((two >> 4) & 0xff0u)) & 0xffffu) * 0x10001u;
-            const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+            if (i < first_rope) {
+                const uint32_t S0 = ((ebase + ((scales[i] & 255u) << 4)) & 0xffffu) * 0x10001u;
+                const uint32_t S1 = ((ebase + ((scales[i] >> 8) << 4)) & 0xffffu) * 0x10001u;
+                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint4 v = rope[i];
-                if (b < first_rope) {
+                for (int u = 0; u < 4; ++u) {
                     uint32_t o[4];
-                    fp4_word(w[i], i < 2 ? S0 : S1, o);
-                    v = make_uint4(o[0], o[1], o[2], o[3]);
+                    fp4_word(w[u], u < 2 ? S0 : S1, o);
+                    *reinterpret_cast<uint4*>(piece(i, u)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
-                *reinterpret_cast<uint4*>(dst + (((half * 4 + i) ^ (row & 7)) << 4)) = v;
+            } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(piece(i, u)) = rope[u];
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&s.full[b]);
+            if (lane == 0) tc::mbar_arrive(&s.full[i]);
         }
-        if (last + 1 < a.dblocks) {
-            // further rotary blocks: copied as they are
-            for (int b = a.dblocks - 1; b > last; --b) {
-                free_block(b);
+        if (last + 1 < a.mtiles) {
+            // further rotary pairs: copied as they are
+            for (int i = a.mtiles - 1; i > last; --i) {
+                free_pair(i);
                 if (!ok) continue;
-                uint8_t* dst = kv_s + (size_t)b * kBlockBytes + row * 128;
-                const uint8_t* src = p ? p + a.f.rope_off + (2 * b + half - nq32) * 64 : nullptr;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint8_t* d = dst + (((half * 4 + i) ^ (row & 7)) << 4);
-                    if (src) cp_async16(d, src + 16 * i);
-                    else *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
+                for (int u = 0; u < 4; ++u) {
+                    if (i == first_rope) *reinterpret_cast<uint4*>(piece(i, u)) = rope[u];
+                    else if (p) cp_async16(piece(i, u), rope_chunk(i) + 16 * u);
+                    else *reinterpret_cast<uint4*>(piece(i, u)) = make_uint4(0, 0, 0, 0);
                 }
             }
             cp_async_wait_all();
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0 && ok)
-                for (int b = a.dblocks - 1; b > last; --b) tc::mbar_arrive(&s.full[b]);
+                for (int i = a.mtiles - 1; i > last; --i) tc::mbar_arrive(&s.full[i]);
         }
-        if (!ok) break;
+        if (j + 1 < ntiles) load(j + 1);
+        return ok;
     }
-}
-
-// S^T of tile j: one thread, blocks in the order in which they arrive
-// (loaded ahead: from the last to the first; then the other rotary blocks).
-__device__ __forceinline__ bool issue_s(const Args& a, Shared& s, uint32_t kv_addr, uint32_t q_addr, uint32_t d_tmem,
-                                        int j) {
-    const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
-    const int last = last_early_block(a);
-    for (int i = 0; i < a.dblocks; ++i) {
-        const int b = i <= last ? last - i : a.dblocks - 1 - (i - last - 1);
-        if (!wait(&s.full[b], j & 1, s, a.status)) {
-            // the products already issued end before the CTA frees their memory
-            tc::umma_commit(&s.fin);
-            tc::mbar_wait(&s.fin, 0, kWaitLimit);
-            return false;
-        }
-        tc::tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-            tc::umma_bf16(d_tmem, tc::sdesc_sw128(kv_addr + b * kBlockBytes + kk * 32, 16, 1024),
-                          tc::sdesc_sw128(q_addr + b * (kHg * 128) + kk * 32, 16, 1024), idesc, (i | kk) ? 1u : 0u);
-    }
-    tc::umma_commit(&s.s_full);
-    return true;
-}
-
-// O^T += of tile j: one thread; each pair of blocks is handed back to the
-// producers once its product is done, the last first.
-__device__ __forceinline__ bool issue_o(const Args& a, Shared& s, uint32_t kv_addr, uint32_t p_addr, uint32_t d_tmem,
-                                        int j) {
-    const uint32_t idesc = tc::idesc_bf16_f32(128, kHg, 1, 1);
-    if (!wait(&s.p_full, j & 1, s, a.status)) return false;
-    tc::tc_fence_after();
-    for (int mt = a.mtiles - 1; mt >= 0; --mt) {
-#pragma unroll
-        for (int ke = 0; ke < kE / 16; ++ke)
-            tc::umma_bf16(d_tmem + mt * kHg, tc::sdesc_sw128(kv_addr + 2 * mt * kBlockBytes + ke * 2048, kBlockBytes, 1024),
-                          tc::sdesc_sw128(p_addr + ke * 2048, kE * 128, 1024), idesc, (j > 0 || ke > 0) ? 1u : 0u);
-        tc::umma_commit(&s.empty[2 * mt + 1]);
-        tc::umma_commit(&s.empty[2 * mt]);
-    }
-    tc::umma_commit(&s.o_done);
-    return true;
-}
+};
 
 template <bool kSparse>
 __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_constant__ Args a,
                                                               const __grid_constant__ CUtensorMap tmQ) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* kv_s = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);   // dblocks x 16 KB
+    // (an offset, not a rounded pointer: the accesses stay shared-memory ones)
+    uint8_t* kv_s = smem_raw + ((0u - tc::smem_u32(smem_raw)) & 1023u);           // dblocks x 16 KB
     uint8_t* q_s = kv_s + (size_t)a.dblocks * kBlockBytes;                         // dblocks x 8 KB
     uint8_t* p_s = q_s + (size_t)a.dblocks * kHg * 128;                            // 128 entries x 64 heads
     Shared& s = *reinterpret_cast<Shared*>(p_s + kE * 128);
@@ -315,19 +299,20 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     const int ntiles = e_end > e_beg ? (int)((e_end - e_beg + kE - 1) / kE) : 0;
 
     if (tid == 0) {
-        for (int i = 0; i < kBlocks; ++i) {
-            tc::mbar_init(&s.full[i], 8);        // producer warps
+        for (int i = 0; i < kPairs; ++i) {
+            tc::mbar_init(&s.full[i], kWorkers / 32);
             tc::mbar_init(&s.empty[i], 1);
         }
         tc::mbar_init(&s.s_full, 1);
         tc::mbar_init(&s.q_full, 1);
-        tc::mbar_init(&s.fin, 1);
-        tc::mbar_init(&s.p_full, 8);             // softmax warps
+        tc::mbar_init(&s.p_full, kWorkers / 32);
         tc::mbar_init(&s.o_done, 1);
+        tc::mbar_init(&s.fin[0], 1);
+        tc::mbar_init(&s.fin[1], 1);
         tc::fence_mbar_init();
         s.abort = 0;
     }
-    if (warp == 0) {
+    if (warp == 16) {
         tc::tmem_alloc(&s.tmem, a.tmem_cols);
         tc::tmem_relinquish();
         tc::tc_fence_before();
@@ -336,35 +321,73 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     tc::tc_fence_after();
     const uint32_t tmem_S = s.tmem, tmem_O = s.tmem + kHg;
 
-    if (warp >= 8) {
-        produce<kSparse>(a, s, kv_s, t, e_beg, e_end, ntiles,
-                         a.kv4 + (int64_t)(ntiles ? seq : 0) * a.Nmax * a.f.bytes);
-    } else {
-        // ------------------------------------------------------------ softmax
-        const int quad = warp & 3, half = warp >> 2, hb = half * 32;
-        const int row = quad * 32 + lane;                 // entry of the tile / dim of an M tile
-        const int hth = tid & 127;
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        if (hth < 32) { s.mref[hb + hth] = -INFINITY; s.lsum[hb + hth] = 0.f; }
-        float lpart[32];
+    if (warp >= 16) {
+        // ------------------------------------------------------------ products
+        if (lane == 0 && ntiles > 0) {
+            const uint32_t kv_addr = tc::smem_u32(kv_s), q_addr = tc::smem_u32(q_s), p_addr = tc::smem_u32(p_s);
+            if (warp == 16) {
+                tc::mbar_expect_tx(&s.q_full, (uint32_t)a.dblocks * kHg * 128);
+                for (int b = 0; b < a.dblocks; ++b)
+                    tc::tma_load_2d(q_s + (size_t)b * kHg * 128, &tmQ, &s.q_full, b * 64, t * a.H + h0);
+                bool ok = wait(&s.q_full, 0, s, a.status);
+                const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
+                const int last = last_early_pair(a);
+                for (int j = 0; ok && j < ntiles; ++j) {
+                    for (int n = 0; n < a.mtiles; ++n) {
+                        const int i = n <= last ? last - n : a.mtiles - 1 - (n - last - 1);   // as they are stored
+                        if (!(ok = wait(&s.full[i], j & 1, s, a.status))) break;
+                        tc::tc_fence_after();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) lpart[i] = 0.f;
-        half_sync(half);
-        const uint32_t kv_addr = tc::smem_u32(kv_s), q_addr = tc::smem_u32(q_s), p_addr = tc::smem_u32(p_s);
-        bool ok = true;
-        int done_s = 0, done_o = 0;       // products issued by this thread
-        if (tid == 128 && ntiles > 0) {
-            tc::mbar_expect_tx(&s.q_full, (uint32_t)a.dblocks * kHg * 128);
-            for (int b = 0; b < a.dblocks; ++b)
-                tc::tma_load_2d(q_s + (size_t)b * kHg * 128, &tmQ, &s.q_full, b * 64, t * a.H + h0);
-            ok = wait(&s.q_full, 0, s, a.status);
-        }
-        for (int j = 0; j < ntiles; ++j) {
-            if (tid == 128 && ok) {
-                ok = issue_s(a, s, kv_addr, q_addr, tmem_S, j);
-                done_s += ok;
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const int b = 2 * i + (kk >> 2);
+                            tc::umma_bf16(tmem_S,
+                                          tc::sdesc_sw128(kv_addr + b * kBlockBytes + (kk & 3) * 32, 16, 1024),
+                                          tc::sdesc_sw128(q_addr + b * (kHg * 128) + (kk & 3) * 32, 16, 1024), idesc,
+                                          (n | kk) ? 1u : 0u);
+                        }
+                    }
+                    if (ok) tc::umma_commit(&s.s_full);
+                }
+                if (!ok) tc::mbar_wait(&s.q_full, 0, kWaitLimit);
+            } else {
+                const uint32_t idesc = tc::idesc_bf16_f32(128, kHg, 1, 1);
+                for (int j = 0; j < ntiles; ++j) {
+                    if (!wait(&s.p_full, j & 1, s, a.status)) break;
+                    tc::tc_fence_after();
+                    for (int mt = a.mtiles - 1; mt >= 0; --mt) {
+#pragma unroll
+                        for (int ke = 0; ke < kE / 16; ++ke)
+                            tc::umma_bf16(tmem_O + mt * kHg,
+                                          tc::sdesc_sw128(kv_addr + 2 * mt * kBlockBytes + ke * 2048, kBlockBytes, 1024),
+                                          tc::sdesc_sw128(p_addr + ke * 2048, kE * 128, 1024), idesc,
+                                          (j > 0 || ke > 0) ? 1u : 0u);
+                        tc::umma_commit(&s.empty[mt]);
+                    }
+                    tc::umma_commit(&s.o_done);
+                }
             }
-            __syncwarp();
+            // every product this thread issued has ended before the CTA goes
+            // on to free the memory it uses (also when a wait ran out)
+            tc::umma_commit(&s.fin[warp - 16]);
+            tc::mbar_wait(&s.fin[warp - 16], 0, kWaitLimit);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ workers
+        const int quad = warp & 3, g = warp >> 2, hb = g * kGh;
+        const int row = quad * 32 + lane;                 // entry of the tile / dim of an M tile
+        const int gth = tid & 127;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        Producer<kSparse> producer(a, s, kv_s, t, e_beg, e_end, ntiles,
+                                   a.kv4 + (int64_t)(ntiles ? seq : 0) * a.Nmax * a.f.bytes);
+        if (gth < kGh) { s.mref[hb + gth] = -INFINITY; s.lsum[hb + gth] = 0.f; }
+        float lpart[kGh];
+#pragma unroll
+        for (int i = 0; i < kGh; ++i) lpart[i] = 0.f;
+        group_sync(g);
+        bool ok = true;
+        for (int j = 0; j < ntiles; ++j) {
+            ok = producer.store(j) && ok;
             const int64_t e = e_beg + (int64_t)j * kE + row;
             bool valid = e < e_end;
             if (kSparse && valid) {
@@ -373,64 +396,53 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             }
             ok = ok && wait(&s.s_full, j & 1, s, a.status);
             tc::tc_fence_after();
-            float z[32];
-            {
-                float v[16];
-                tc::tmem_ld16(tmem_S + lanes + hb, v);
-                tc::tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) z[i] = v[i];
-                tc::tmem_ld16(tmem_S + lanes + hb + 16, v);
-                tc::tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) z[16 + i] = v[i];
-            }
+            float z[kGh];
+            tc::tmem_ld16(tmem_S + lanes + hb, z);
+            tc::tmem_ld_wait();
             bool move = false;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < kGh; ++i) {
                 z[i] = valid ? z[i] * a.scale_log2 : -INFINITY;
                 move |= z[i] > s.mref[hb + i] + kMoveLog2;
             }
-            if (half_any(half, move || !ok)) {
+            if (group_any(g, move || !ok)) {
                 // all leave together once a wait of one ran out
-                if (half_any(half, !ok)) { ok = false; break; }
-                float v[32];
+                if (group_any(g, !ok)) { ok = false; break; }
+                float v[kGh];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = z[i];
-                s.red[quad][hb + lane] = lanes_transpose_reduce(v, lane, [](float x, float y) { return fmaxf(x, y); });
-                half_sync(half);
-                if (hth < 32) {
-                    const int h = hb + hth;
+                for (int i = 0; i < kGh; ++i) v[i] = z[i];
+                const float top = lanes_reduce16(v, lane, [](float x, float y) { return fmaxf(x, y); });
+                if (!(lane & 1)) s.red[quad][hb + lane / 2] = top;
+                group_sync(g);
+                if (gth < kGh) {
+                    const int h = hb + gth;
                     const float old = s.mref[h];
                     const float m = fmaxf(fmaxf(fmaxf(s.red[0][h], s.red[1][h]), fmaxf(s.red[2][h], s.red[3][h])), old);
                     s.alpha[h] = old == -INFINITY ? 0.f : ex2(old - m);
                     s.mref[h] = m;
                 }
-                half_sync(half);
+                group_sync(g);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) lpart[i] *= s.alpha[hb + i];
+                for (int i = 0; i < kGh; ++i) lpart[i] *= s.alpha[hb + i];
                 if (j > 0) {
                     ok = wait(&s.o_done, (j - 1) & 1, s, a.status);
                     tc::tc_fence_after();
+#pragma unroll 1
                     for (int mt = 0; mt < a.mtiles; ++mt) {
+                        float o[kGh];
+                        const uint32_t addr = tmem_O + lanes + mt * kHg + hb;
+                        tc::tmem_ld16(addr, o);
+                        tc::tmem_ld_wait();
 #pragma unroll
-                        for (int cc = 0; cc < 32; cc += 16) {
-                            float o[16];
-                            const uint32_t addr = tmem_O + lanes + mt * kHg + hb + cc;
-                            tc::tmem_ld16(addr, o);
-                            tc::tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] *= s.alpha[hb + cc + i];
-                            tc::tmem_st16(addr, o);
-                        }
+                        for (int i = 0; i < kGh; ++i) o[i] *= s.alpha[hb + i];
+                        tc::tmem_st16(addr, o);
                     }
                     tc::tmem_st_wait();
-                    tc::tc_fence_before();
                 }
             }
-            uint32_t pk[16];
+            uint32_t pk[kGh / 2];
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
+            for (int i = 0; i < kGh; i += 2) {
                 const float m0 = s.mref[hb + i], m1 = s.mref[hb + i + 1];
                 const float p0 = z[i] == -INFINITY ? 0.f : ex2(z[i] - m0);
                 const float p1 = z[i + 1] == -INFINITY ? 0.f : ex2(z[i + 1] - m1);
@@ -442,40 +454,28 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             // the previous tile's O product has read P
             if (j > 0) ok = wait(&s.o_done, (j - 1) & 1, s, a.status) && ok;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4*>(p_s + row * 128 + (((half * 4 + i) ^ (row & 7)) << 4)) =
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<uint4*>(p_s + row * 128 + (((g * 2 + i) ^ (row & 7)) << 4)) =
                     make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
             tc::tc_fence_before();                        // S has been read, too
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&s.p_full);
-            if (tid == 0 && ok) {
-                ok = issue_o(a, s, kv_addr, p_addr, tmem_O, j);
-                done_o += ok;
-            }
-            __syncwarp();
         }
         // ------------------------------------------------------------ epilogue
         if (ok && ntiles > 0) ok = wait(&s.o_done, (ntiles - 1) & 1, s, a.status);
-        // when a wait ran out, the products and copies already issued still
-        // end before the CTA frees the memory they use
-        if (!ok && done_s) tc::mbar_wait(&s.s_full, (done_s - 1) & 1, kWaitLimit);
-        if (!ok && done_o) tc::mbar_wait(&s.o_done, (done_o - 1) & 1, kWaitLimit);
-        if (!ok && tid == 128) tc::mbar_wait(&s.q_full, 0, kWaitLimit);
-        __syncwarp();
         tc::tc_fence_after();
         // per-head sums in a fixed order: lanes, then the four warps
-        half_sync(half);                                  // red may still be read
-        s.red[quad][hb + lane] = lanes_transpose_reduce(lpart, lane, [](float x, float y) { return x + y; });
-        half_sync(half);
-        if (hth < 32) {
-            const int h = hb + hth;
-            s.lsum[h] = (s.red[0][h] + s.red[1][h]) + (s.red[2][h] + s.red[3][h]);
+        group_sync(g);                                    // red may still be read
+        {
+            const float sum = lanes_reduce16(lpart, lane, [](float x, float y) { return x + y; });
+            if (!(lane & 1)) s.red[quad][hb + lane / 2] = sum;
         }
-        half_sync(half);
-        if (a.merge == kDirect) {
-            if (hth < 32) {
-                const int h = hb + hth;
+        group_sync(g);
+        if (gth < kGh) {
+            const int h = hb + gth;
+            s.lsum[h] = (s.red[0][h] + s.red[1][h]) + (s.red[2][h] + s.red[3][h]);
+            if (a.merge == kDirect) {
                 const float m = s.mref[h], L = s.lsum[h];
                 const float sk = a.sink && h0 + h < a.H ? a.sink[h0 + h] * kLog2e : -INFINITY;
                 const float M = fmaxf(m, sk);
@@ -486,41 +486,35 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                 if (a.lse && h0 + h < a.H)
                     a.lse[(int64_t)t * a.H + h0 + h] = Lt == 0.f ? -INFINITY : fmaf(M, kLn2, logf(Lt));
             }
-            half_sync(half);
+        }
+        group_sync(g);
+        if (a.merge == kDirect) {
             // normalised rows, staged as [head][dim] bf16 where the tile was
-            bf16* stage = reinterpret_cast<bf16*>(kv_s);
-            float al[32];
+            bf16* stage = reinterpret_cast<bf16*>(kv_s) + (size_t)hb * a.f.c + row;
+            float al[kGh];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) al[i] = s.alpha[hb + i];
+            for (int i = 0; i < kGh; ++i) al[i] = s.alpha[hb + i];
 #pragma unroll 1
             for (int mt = 0; mt < a.mtiles; ++mt) {
-                bf16* col = stage + (size_t)hb * a.f.c + mt * 128 + row;
-#pragma unroll
-                for (int cc = 0; cc < 32; cc += 16) {
-                    float o[16];
-                    if (ntiles > 0) {
-                        tc::tmem_ld16(tmem_O + lanes + mt * kHg + hb + cc, o);
-                        tc::tmem_ld_wait();
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        col[(size_t)(cc + i) * a.f.c] = __float2bfloat16_rn(al[cc + i] != 0.f ? o[i] * al[cc + i] : 0.f);
+                float o[kGh];
+                if (ntiles > 0) {
+                    tc::tmem_ld16(tmem_O + lanes + mt * kHg + hb, o);
+                    tc::tmem_ld_wait();
                 }
+#pragma unroll
+                for (int i = 0; i < kGh; ++i)
+                    stage[(size_t)i * a.f.c + mt * 128] = __float2bfloat16_rn(al[i] != 0.f ? o[i] * al[i] : 0.f);
             }
         } else if (ntiles > 0) {
             // O^T staged as [head][dim] fp32 where the tile was
-            float* stage = reinterpret_cast<float*>(kv_s);
+            float* stage = reinterpret_cast<float*>(kv_s) + (size_t)hb * a.f.c + row;
 #pragma unroll 1
             for (int mt = 0; mt < a.mtiles; ++mt) {
-                float* col = stage + (size_t)hb * a.f.c + mt * 128 + row;
+                float o[kGh];
+                tc::tmem_ld16(tmem_O + lanes + mt * kHg + hb, o);
+                tc::tmem_ld_wait();
 #pragma unroll
-                for (int cc = 0; cc < 32; cc += 16) {
-                    float o[16];
-                    tc::tmem_ld16(tmem_O + lanes + mt * kHg + hb + cc, o);
-                    tc::tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) col[(size_t)(cc + i) * a.f.c] = o[i];
-                }
+                for (int i = 0; i < kGh; ++i) stage[(size_t)i * a.f.c + mt * 128] = o[i];
             }
         }
         tc::tc_fence_before();
@@ -562,16 +556,20 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         const uint32_t stage = tc::smem_u32(kv_s);
         for (int i = lo + tid; i < hi; i += kThreads) {
             const int h = i / c4;
+            // (every split's load is in flight before the first is used)
+            float4 o[kMaxCluster];
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r)
+                if (r < a.nsplit) o[r] = ld_cluster4(tc::mapa(stage + (uint32_t)i * 16, r));
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int r = 0; r < kMaxCluster; ++r) {
                 const float w = r < a.nsplit ? s.coef[r][h] : 0.f;
                 if (w != 0.f) {
-                    const float4 o = ld_cluster4(tc::mapa(stage + (uint32_t)i * 16, r));
-                    acc.x = fmaf(w, o.x, acc.x);
-                    acc.y = fmaf(w, o.y, acc.y);
-                    acc.z = fmaf(w, o.z, acc.z);
-                    acc.w = fmaf(w, o.w, acc.w);
+                    acc.x = fmaf(w, o[r].x, acc.x);
+                    acc.y = fmaf(w, o[r].y, acc.y);
+                    acc.z = fmaf(w, o[r].z, acc.z);
+                    acc.w = fmaf(w, o[r].w, acc.w);
                 }
             }
             store4(out + (int64_t)i * 4, acc.x, acc.y, acc.z, acc.w);
@@ -597,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         }
         __syncthreads();
     }
-    if (warp == 0) {
+    if (warp == 16) {
         tc::tc_fence_after();
         tc::tmem_dealloc(s.tmem, a.tmem_cols);
     }
