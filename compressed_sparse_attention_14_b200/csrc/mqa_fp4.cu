@@ -19,9 +19,8 @@
 // 16 worker warps do both the expansion and the softmax, which cannot overlap
 // for one tile buffer (the expansion of tile j+1 needs blocks that the O
 // product of tile j has read, the softmax of tile j+1 needs its S product).
-//   expansion: warps 0-7 the even, 8-15 the odd 64-dim blocks; a thread owns
-//     half a row of its blocks (32 channels: 16 bytes of codes) and has the
-//     next tile's codes in registers by the time a block is free;
+//   expansion: warp w has rows 8 w .. 8 w + 7; the next tile's codes are in
+//     registers by the time a block is free;
 //   softmax and epilogue: warp w works on TMEM lanes 32 (w % 4).. and heads
 //     16 (w / 4)...
 // Warp 16 issues the S products, warp 17 the O products. Blocks go back and
@@ -144,128 +143,129 @@ __device__ __forceinline__ float lanes_reduce16(float (&v)[kGh], int lane, Op op
     return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
-// Pairs up to this one hold quantised channels or each thread's first rotary
-// chunk, which are loaded ahead; later ones are rotary throughout.
+// The first 64 rotary channels are loaded ahead with the codes, the others
+// copied while a pair is stored; pairs up to this one hold none of the latter.
 __device__ __forceinline__ int last_early_pair(const Args& a) {
-    const int i = a.f.Q / 128;
-    return i < a.mtiles - 1 ? i : a.mtiles - 1;
+    return a.f.R <= 64 ? a.mtiles - 1 : (a.f.Q + 64) / 128 - 1;
 }
 
-// A thread's part of the expansion: half a row (32 channels) of every second block.
+// A thread's part of the expansion: of one row, the 32 channels of chunk
+// `chunk` in every pair of blocks and every fourth 16-byte piece of the rotary
+// channels. The 4 lanes of a row read 64 consecutive bytes per load: a load
+// instruction then touches 8 lines, and the lines touched, not the bytes, are
+// what a tile's loads cost (with 2 lanes per row and 32 bytes each, 16 lines,
+// they took 4400 cycles a tile).
 template <bool kSparse>
 struct Producer {
     const Args& a;
     Shared& s;
-    uint8_t* dst;             // this thread's row in its first block
-    const uint8_t* seq_rows;
-    const int32_t* list;
-    int e0, e_end, next;      // (entry indices fit: Nmax is below 2^31)
-    int ntiles, row, chunk, nq32, first_rope, last;
-    uint4 raw[kPairs], rope[4];
-    uint32_t scales[kPairs], ebase;
-    const uint8_t* p;
+    uint8_t* tile;
+    // (registers are short: row numbers instead of pointers; n_seq * Nmax is
+    // below 2^31)
+    int row0, t, e0, e_end, next, cur, ntiles, row, chunk;
+    uint4 raw[kPairs], rope[2];
+    uint32_t scales[kPairs], row_exp;
 
-    __device__ __forceinline__ Producer(const Args& a_, Shared& s_, uint8_t* kv_s, int t, int64_t e_beg, int64_t e_end_,
-                                        int ntiles_, const uint8_t* rows)
-        : a(a_), s(s_), seq_rows(rows), e_end((int)e_end_), ntiles(ntiles_) {
-        const int pt = threadIdx.x & 255, half = pt & 1, parity = threadIdx.x >> 8;
-        row = pt >> 1;
-        chunk = 2 * parity + half;                        // 32-channel chunk within a pair
-        dst = kv_s + parity * kBlockBytes + row * 128;
-        list = kSparse ? a.idx + (int64_t)t * a.k : nullptr;
+    __device__ __forceinline__ Producer(const Args& a_, Shared& s_, uint8_t* kv_s, int t_, int64_t e_beg, int64_t e_end_,
+                                        int ntiles_, int64_t first_row)
+        : a(a_), s(s_), tile(kv_s), row0((int)first_row), t(t_), e_end((int)e_end_), ntiles(ntiles_) {
+        row = threadIdx.x >> 2;
+        chunk = threadIdx.x & 3;
         e0 = (int)e_beg + row;
-        nq32 = a.f.Q / 32;
-        first_rope = nq32 > chunk ? (nq32 - chunk + 3) / 4 : 0;
-        last = last_early_pair(a);
         next = entry(0);
         if (ntiles > 0) load(0);
     }
-    // entry index of this row in tile j, -1: none
+    // entry index of this row in tile j (outside [0, Nmax): none)
     __device__ __forceinline__ int entry(int j) const {
         if (j >= ntiles || e_end - e0 <= j * kE) return -1;
         const int e = e0 + j * kE;
-        if (!kSparse) return e;
-        const int v = __ldg(list + e);
-        return v < a.Nmax ? v : -1;
-    }
-    __device__ __forceinline__ const uint8_t* rope_chunk(int i) const {
-        return p + a.f.rope_off + (4 * i + chunk - nq32) * 64;
+        return kSparse ? __ldg(a.idx + (int64_t)t * a.k + e) : e;
     }
     // All of a tile's loads, issued together right after the tile before it
-    // is stored. A missing row: codes 0 times 2^-126, rotary channels 0.
+    // is stored, and nothing computed from them until the tile is stored: a
+    // scale formed here would wait for its load. A missing row: codes 0 times
+    // 2^-126, rotary channels 0.
     __device__ __forceinline__ void load(int j) {
-        p = next >= 0 ? seq_rows + (int64_t)next * a.f.bytes : nullptr;
+        cur = next >= 0 && next < a.Nmax ? row0 + next : -1;
+        const uint8_t* p = cur >= 0 ? a.kv4 + (int64_t)cur * a.f.bytes : nullptr;
         next = entry(j + 1);
-        ebase = 128;
+        row_exp = 32;
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
             raw[i] = make_uint4(0, 0, 0, 0);
             scales[i] = 0;
-            if (p && i < first_rope && i < a.mtiles) {
+            if (p && 4 * i + chunk < a.f.Q / 32) {
                 raw[i] = __ldg(reinterpret_cast<const uint4*>(p) + 4 * i + chunk);
                 scales[i] = __ldg(reinterpret_cast<const uint16_t*>(p + a.f.scale_off) + 4 * i + chunk);
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) rope[i] = make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < 2; ++u) {
+            rope[u] = make_uint4(0, 0, 0, 0);
+            if (p && 4 * u + chunk < a.f.R / 8) rope[u] = __ldg(reinterpret_cast<const uint4*>(p + a.f.rope_off) + 4 * u + chunk);
+        }
         if (p) {
-            ebase = ((uint32_t)__ldg(p + a.f.scale_off + a.f.Q / 16) - 31u) << 7;
-            if (first_rope < a.mtiles) {
-                const uint4* pr = reinterpret_cast<const uint4*>(rope_chunk(first_rope));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) rope[i] = __ldg(pr + i);
-            }
-            for (int i = last + 1; i < a.mtiles; ++i)
-                if (i > first_rope) prefetch_l2(rope_chunk(i));
+            row_exp = __ldg(p + a.f.scale_off + a.f.Q / 16);
+            for (int n = 8 + chunk; n < a.f.R / 8; n += 4) prefetch_l2(p + a.f.rope_off + n * 16);
         }
     }
-    __device__ __forceinline__ uint8_t* piece(int i, int u) const {
-        return dst + (size_t)i * 2 * kBlockBytes + ((((chunk & 1) * 4 + u) ^ (row & 7)) << 4);
+    // where channels d .. d+7 of this row are stored
+    __device__ __forceinline__ uint8_t* at(int d) const {
+        return tile + (size_t)(d >> 6) * kBlockBytes + row * 128 + ((((d >> 3) & 7) ^ (row & 7)) << 4);
     }
     // stores tile j, then loads tile j + 1; false when a wait ran out
     __device__ __forceinline__ bool store(int j) {
-        const int lane = threadIdx.x & 31;
+        const int lane = threadIdx.x & 31, last = last_early_pair(a);
+        const uint32_t ebase = (row_exp - 31u) << 7;
         bool ok = true;
-        auto free_pair = [&](int i) {                     // tile j-1's O product has read it
-            if (j == 0 || !ok) return;
-            if (lane == 0) ok = wait(&s.empty[i], (j - 1) & 1, s, a.status);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-        };
 #pragma unroll
         for (int i = kPairs - 1; i >= 0; --i) {
-            if (i > last) continue;
-            free_pair(i);
-            if (!ok) continue;
-            if (i < first_rope) {
-                const uint32_t S0 = ((ebase + ((scales[i] & 255u) << 4)) & 0xffffu) * 0x10001u;
-                const uint32_t S1 = ((ebase + ((scales[i] >> 8) << 4)) & 0xffffu) * 0x10001u;
-                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            if (i >= a.mtiles || !ok) continue;
+            if (j > 0) {                                  // tile j-1's O product has read it
+                if (lane == 0) ok = wait(&s.empty[i], (j - 1) & 1, s, a.status);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) continue;
+            }
+            if (4 * i + chunk < a.f.Q / 32) {
+                // lanes of the second block store their pieces in another
+                // order (2 3 0 1), so that 8 lanes never meet in a bank
+                const bool second = chunk & 2;
+                const uint32_t sa = second ? scales[i] >> 8 : scales[i] & 255u;
+                const uint32_t sb = second ? scales[i] & 255u : scales[i] >> 8;
+                const uint32_t S0 = ((ebase + (sa << 4)) & 0xffffu) * 0x10001u;
+                const uint32_t S1 = ((ebase + (sb << 4)) & 0xffffu) * 0x10001u;
+                const uint32_t w[4] = {second ? raw[i].z : raw[i].x, second ? raw[i].w : raw[i].y,
+                                       second ? raw[i].x : raw[i].z, second ? raw[i].y : raw[i].w};
+                uint8_t* blk = tile + (size_t)(2 * i + (chunk >> 1)) * kBlockBytes + row * 128;
+                const int piece = ((chunk & 1) * 4 + (chunk & 2)) ^ (row & 7);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     uint32_t o[4];
                     fp4_word(w[u], u < 2 ? S0 : S1, o);
-                    *reinterpret_cast<uint4*>(piece(i, u)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(blk + ((piece ^ u) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
-            } else {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(piece(i, u)) = rope[u];
             }
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&s.full[i]);
+            if (128 * (i + 1) > a.f.Q) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int d = a.f.Q + (4 * u + chunk) * 8;
+                    if (4 * u + chunk < a.f.R / 8 && d >> 7 == i) *reinterpret_cast<uint4*>(at(d)) = rope[u];
+                }
+                if (i > last)
+                    for (int n = 8 + chunk; n < a.f.R / 8; n += 4) {
+                        const int d = a.f.Q + n * 8;
+                        if (d >> 7 != i) continue;
+                        if (cur >= 0) cp_async16(at(d), a.kv4 + (int64_t)cur * a.f.bytes + a.f.rope_off + n * 16);
+                        else *reinterpret_cast<uint4*>(at(d)) = make_uint4(0, 0, 0, 0);
+                    }
+            }
+            if (i <= last) {
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&s.full[i]);
+            }
         }
         if (last + 1 < a.mtiles) {
-            // further rotary pairs: copied as they are
-            for (int i = a.mtiles - 1; i > last; --i) {
-                free_pair(i);
-                if (!ok) continue;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if (i == first_rope) *reinterpret_cast<uint4*>(piece(i, u)) = rope[u];
-                    else if (p) cp_async16(piece(i, u), rope_chunk(i) + 16 * u);
-                    else *reinterpret_cast<uint4*>(piece(i, u)) = make_uint4(0, 0, 0, 0);
-                }
-            }
             cp_async_wait_all();
             tc::fence_proxy_async_smem();
             __syncwarp();
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         const int gth = tid & 127;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         Producer<kSparse> producer(a, s, kv_s, t, e_beg, e_end, ntiles,
-                                   a.kv4 + (int64_t)(ntiles ? seq : 0) * a.Nmax * a.f.bytes);
+                                   (ntiles ? seq : 0) * a.Nmax);
         if (gth < kGh) { s.mref[hb + gth] = -INFINITY; s.lsum[hb + gth] = 0.f; }
         float lpart[kGh];
 #pragma unroll
@@ -397,21 +397,21 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             ok = ok && wait(&s.s_full, j & 1, s, a.status);
             tc::tc_fence_after();
             float z[kGh];
-            tc::tmem_ld16(tmem_S + lanes + hb, z);
-            tc::tmem_ld_wait();
+            auto logits = [&]() {
+                tc::tmem_ld16(tmem_S + lanes + hb, z);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < kGh; ++i) z[i] = valid ? z[i] * a.scale_log2 : -INFINITY;
+            };
+            logits();
             bool move = false;
 #pragma unroll
-            for (int i = 0; i < kGh; ++i) {
-                z[i] = valid ? z[i] * a.scale_log2 : -INFINITY;
-                move |= z[i] > s.mref[hb + i] + kMoveLog2;
-            }
+            for (int i = 0; i < kGh; ++i) move |= z[i] > s.mref[hb + i] + kMoveLog2;
             if (group_any(g, move || !ok)) {
                 // all leave together once a wait of one ran out
                 if (group_any(g, !ok)) { ok = false; break; }
-                float v[kGh];
-#pragma unroll
-                for (int i = 0; i < kGh; ++i) v[i] = z[i];
-                const float top = lanes_reduce16(v, lane, [](float x, float y) { return fmaxf(x, y); });
+                // (the reduction consumes the logits; they are read again)
+                const float top = lanes_reduce16(z, lane, [](float x, float y) { return fmaxf(x, y); });
                 if (!(lane & 1)) s.red[quad][hb + lane / 2] = top;
                 group_sync(g);
                 if (gth < kGh) {
@@ -439,6 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                     }
                     tc::tmem_st_wait();
                 }
+                logits();
             }
             uint32_t pk[kGh / 2];
 #pragma unroll
