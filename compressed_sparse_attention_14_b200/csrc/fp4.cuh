@@ -47,18 +47,26 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 }
 
 // The 8 channels of word w times the scale (bf16 twice), as 4 bf16 pairs in
-// channel order. A code's 3 magnitude bits, put where bf16 has its lowest
-// exponent and highest mantissa bits, are the code's value times 2^-126
-// (subnormals included), so a product with 2^126 restores it; both products
-// are exact.
+// channel order, times 2^-126. A nibble times 2^12 + 2^6 has its sign at bit
+// 15 and its 3 magnitude bits at 8..6, where bf16 has its lowest exponent and
+// highest mantissa bits: the code's value times 2^-126, subnormals included.
+// The product with the scale is exact. (An and, a multiplication and an and
+// per pair: the integer pipe paces the expansion, and shifts and masks for
+// sign and magnitude apart took twice as many of its operations.)
+__device__ __forceinline__ void fp4_word_small(uint32_t w, uint32_t scale2, uint32_t (&out)[4]) {
+    const uint32_t v = w >> 8;
+    const uint32_t t[4] = {(w & 0x000F000Fu) * 0x1040u, (w & 0x00F000F0u) * 0x104u, (v & 0x000F000Fu) * 0x1040u,
+                           (v & 0x00F000F0u) * 0x104u};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) out[j] = mul_bf16x2(t[j] & 0x81C081C0u, scale2);
+}
+
+// The channels themselves.
 __device__ __forceinline__ void fp4_word(uint32_t w, uint32_t scale2, uint32_t (&out)[4]) {
     constexpr uint32_t k2p126 = 0x7E807E80u;   // 2^126 twice
+    fp4_word_small(w, 0x3F803F80u, out);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t sgn = (j < 3 ? w << (12 - 4 * j) : w) & 0x80008000u;
-        const uint32_t mag = (j < 2 ? w << (6 - 4 * j) : w >> (4 * j - 6)) & 0x01C001C0u;
-        out[j] = mul_bf16x2(mul_bf16x2(sgn | mag, k2p126), scale2);
-    }
+    for (int j = 0; j < 4; ++j) out[j] = mul_bf16x2(mul_bf16x2(out[j], k2p126), scale2);
 }
 
 }  // namespace csa
