@@ -2,89 +2,304 @@
 //
 //   weight of s = sum over heads (and queries) of e^{z_s - lse}
 //
-// A warp per entry, its lanes over the channels.
-#include "fp4.cuh"
+// The logits are the attention's S^T = V_tile . q^T product (128 entries x 64
+// heads, K = c; mqa_fp4.cu) without the second product: entries are the lanes
+// of the result, so a thread sums the weights of its entry over 16 heads in
+// registers and four threads' sums meet in shared memory. Bound by reading the
+// packed rows; what paces it is expanding them for the product.
+//
+// A CTA walks a run of tiles of one sequence (or of one query's entry list).
+// Each tile stays in shared memory for all query blocks (query, 64 heads) of
+// its sequence; their q blocks stream through one buffer, refilled in quarters
+// as the product has read them, unless there is only one, which stays. The
+// next tile is expanded while the last query block's product runs. Every sum
+// has a fixed order: heads, then queries, within a thread, then the four
+// threads.
+//
+// Warps 0-15: expansion and sums; 16: products; 17: query loads.
+#include "fp4_tile.cuh"
 #include "kernels.h"
+#include "tmap.h"
 
 namespace csa {
 
 namespace {
 
-constexpr int kDims = CSA_MAX_HEAD_DIM / 32;
+using namespace fp4_tile;
 
-// channel d of a row
-__device__ __forceinline__ float fp4_channel(const uint8_t* row, const Fp4Row& f, int d) {
-    if (d >= f.Q) return __bfloat162float(reinterpret_cast<const bf16*>(row + f.rope_off)[d - f.Q]);
-    const uint32_t w = reinterpret_cast<const uint32_t*>(row)[d / 8];
-    const uint32_t s = fp4_scale_bits(row[f.scale_off + d / 16], row[f.scale_off + f.Q / 16]) * 0x10001u;
-    uint32_t o[4];
-    fp4_word(w, s, o);
-    const uint32_t p = (d & 4) ? ((d & 2) ? o[3] : o[2]) : ((d & 2) ? o[1] : o[0]);
-    return __uint_as_float(d & 1 ? p & 0xFFFF0000u : p << 16);
-}
+struct Args : Fp4TileArgs {
+    const float* lse;
+    const int32_t* seq_of_q;
+    const int32_t* pos;
+    float* acc;
+    float* weights;
+    int T, n_seq, mp, H, hgroups, run;        // run: tiles per CTA
+    float scale_log2;
+};
 
-__device__ __forceinline__ float row_dot(const uint8_t* row, const Fp4Row& f, const float (&q)[kDims], int lane,
-                                         float (&v)[kDims]) {
-    float z = 0.f;
-#pragma unroll
-    for (int i = 0; i < kDims; ++i) {
-        v[i] = 0.f;
-        if (i * 32 < f.c) {
-            v[i] = fp4_channel(row, f, i * 32 + lane);
-            z = fmaf(q[i], v[i], z);
-        }
+struct Shared : Fp4TileShared {
+    float lse[kWorkers / 32][kGh];            // the query block's, per warp
+    float part[kWorkers / 128][kE];
+    uint64_t q_full[kPairs], q_empty[kPairs], s_full[2], s_empty[2], fin;
+    uint32_t tmem;
+    int n_max;
+};
+
+// Query blocks of a tile, in order: query t, head group g. Blocks whose query
+// sees no entry of the tile are left out (every role decides alike).
+template <bool kSparse>
+struct Blocks {
+    const Args& a;
+    int b;
+    __device__ __forceinline__ int visible(int t) const {
+        return kSparse ? a.k : (int)visible_entries(__ldg(a.pos + (int64_t)b * a.T + t), a.mp, a.Nmax);
     }
-    return warp_sum(z);
-}
+    __device__ __forceinline__ int last_query(int e_tile) const {
+        int t = a.T - 1;
+        while (t > 0 && visible(t) <= e_tile) --t;
+        return t;
+    }
+};
 
-// a warp per entry: selected entries (idx) of query t, or entry e of sequence t
-__global__ void __launch_bounds__(128) entry_weights_fp4_kernel(const __grid_constant__ Fp4WeightArgs a) {
+template <bool kSparse>
+__global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __grid_constant__ Args a,
+                                                                        const __grid_constant__ CUtensorMap tmQ) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* kv_s = smem_raw + ((0u - tc::smem_u32(smem_raw)) & 1023u);           // dblocks x 16 KB
+    uint8_t* q_s = kv_s + (size_t)a.dblocks * kBlockBytes;                         // dblocks x 8 KB
+    Shared& s = *reinterpret_cast<Shared*>(q_s + (size_t)a.dblocks * kHg * 128);
+
     pdl_wait();
     pdl_launch_next();
-    const int lane = threadIdx.x & 31;
-    const int64_t e = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), n = a.idx ? a.k : a.Nmax;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int b = blockIdx.y;
-    if (e >= n) return;
-    const Fp4Row f = fp4_row(a.c, a.R);
     const int seq = a.seq_of_q ? a.seq_of_q[b] : b;
-    int64_t s = e;
-    bool ok = seq >= 0 && seq < a.n_seq;
-    if (a.idx) {
-        s = a.idx[(int64_t)b * a.k + e];
-        ok = ok && s >= 0 && s < a.Nmax;
-    }
-    float w = 0.f;
-    for (int t = 0; ok && t < a.T; ++t) {
-        if (!a.idx && s >= visible_entries(a.pos[(int64_t)b * a.T + t], a.mp, a.Nmax)) continue;
-        for (int h = 0; h < a.H; ++h) {
-            const int64_t qrow = ((int64_t)b * a.T + t) * a.H + h;
-            float q[kDims], v[kDims];
-#pragma unroll
-            for (int i = 0; i < kDims; ++i)
-                q[i] = i * 32 < a.c ? __bfloat162float(((const bf16*)a.q)[qrow * a.c + i * 32 + lane]) : 0.f;
-            const float z = a.scale * row_dot(a.kv4 + ((int64_t)seq * a.Nmax + s) * f.bytes, f, q, lane, v);
-            const float l = a.lse[qrow];
-            if (l != -INFINITY) w += expf(z - l);
+    const Blocks<kSparse> blocks{a, b};
+    const int e_beg = blockIdx.x * a.run * kE, n_all = kSparse ? a.k : (int)a.Nmax;
+    const int e_stop = (int64_t)a.run * kE > n_all - e_beg ? n_all : e_beg + a.run * kE;   // this CTA's entries
+    if (tid == 0) {
+        for (int i = 0; i < kPairs; ++i) {
+            tc::mbar_init(&s.full[i], kWorkers / 32);
+            tc::mbar_init(&s.empty[i], 1);
+            tc::mbar_init(&s.q_full[i], 1);
+            tc::mbar_init(&s.q_empty[i], 1);
         }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&s.s_full[i], 1);
+            tc::mbar_init(&s.s_empty[i], kWorkers / 32);
+        }
+        tc::mbar_init(&s.fin, 1);
+        tc::fence_mbar_init();
+        s.abort = 0;
+        s.n_max = 0;
     }
-    if (lane != 0) return;
-    if (a.idx) {
-        if (a.weights) a.weights[(int64_t)b * a.k + e] = w;
-        if (a.acc && ok) atomicAdd(a.acc + (int64_t)seq * a.Nmax + s, w);
+    if (warp == 16) {
+        tc::tmem_alloc(&s.tmem, 128);
+        tc::tmem_relinquish();
+        tc::tc_fence_before();
+    }
+    __syncthreads();
+    // the last entry that any query sees
+    if (seq >= 0 && seq < a.n_seq) {
+        int n = 0;
+        for (int t = tid; t < a.T; t += kThreads) n = max(n, blocks.visible(t));
+        n = __reduce_max_sync(0xffffffffu, n);
+        if (lane == 0 && n > 0) atomicMax(&s.n_max, n);
+    }
+    __syncthreads();
+    tc::tc_fence_after();
+    const int e_end = s.n_max < e_stop ? s.n_max : e_stop;
+    const int ntiles = e_end > e_beg ? (e_end - e_beg + kE - 1) / kE : 0;
+    const uint32_t tmem_S = s.tmem;
+    const bool stay = a.T * a.hgroups == 1;
+
+    if (warp == 17) {
+        // ------------------------------------------------------------ query loads
+        if (lane == 0) {
+            uint32_t n = 0;
+            bool ok = true;
+            for (int j = 0; ok && j < (stay ? (ntiles > 0 ? 1 : 0) : ntiles); ++j) {
+                const int e_tile = e_beg + j * kE;
+                for (int t = 0; ok && t <= blocks.last_query(e_tile); ++t) {
+                    if (blocks.visible(t) <= e_tile) continue;
+                    for (int g = 0; ok && g < a.hgroups; ++g, ++n)
+                        for (int i = a.mtiles - 1; i >= 0; --i) {
+                            if (n > 0 && !(ok = wait(&s.q_empty[i], (n - 1) & 1, s, a.status))) break;
+                            tc::mbar_expect_tx(&s.q_full[i], 2 * kHg * 128);
+                            for (int h = 0; h < 2; ++h)
+                                tc::tma_load_2d(q_s + (size_t)(2 * i + h) * kHg * 128, &tmQ, &s.q_full[i],
+                                                (2 * i + h) * 64, (b * a.T + t) * a.H + g * kHg);
+                        }
+                }
+            }
+            // the copies of the last block of each pair have landed
+            if (n > 0)
+                for (int i = 0; i < a.mtiles; ++i) tc::mbar_wait(&s.q_full[i], (n - 1) & 1, ok ? kWaitLimit : 1u << 16);
+        }
+        __syncwarp();
+    } else if (warp == 16) {
+        // ------------------------------------------------------------ products
+        if (lane == 0 && ntiles > 0) {
+            const uint32_t kv_addr = tc::smem_u32(kv_s), q_addr = tc::smem_u32(q_s);
+            const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
+            const int early = last_early_pair(a);
+            uint32_t n = 0;
+            bool ok = true;
+            for (int j = 0; ok && j < ntiles; ++j) {
+                const int e_tile = e_beg + j * kE, last = blocks.last_query(e_tile);
+                bool first = true;
+                for (int t = 0; ok && t <= last; ++t) {
+                    if (blocks.visible(t) <= e_tile) continue;
+                    for (int g = 0; ok && g < a.hgroups; ++g, ++n) {
+                        const uint32_t sb = n & 1;
+                        if (n >= 2 && !(ok = wait(&s.s_empty[sb], ((n >> 1) - 1) & 1, s, a.status))) break;
+                        for (int o = 0; o < a.mtiles; ++o) {
+                            const int i = o <= early ? early - o : a.mtiles - 1 - (o - early - 1);
+                            if (!(ok = wait(&s.q_full[i], stay ? 0 : n & 1, s, a.status))) break;
+                            if (first && !(ok = wait(&s.full[i], j & 1, s, a.status))) break;
+                            tc::tc_fence_after();
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk) {
+                                const int blk = 2 * i + (kk >> 2);
+                                tc::umma_bf16(tmem_S + sb * kHg,
+                                              tc::sdesc_sw128(kv_addr + blk * kBlockBytes + (kk & 3) * 32, 16, 1024),
+                                              tc::sdesc_sw128(q_addr + blk * (kHg * 128) + (kk & 3) * 32, 16, 1024),
+                                              idesc, (o | kk) ? 1u : 0u);
+                            }
+                            if (!stay) tc::umma_commit(&s.q_empty[i]);
+                            if (t == last && g == a.hgroups - 1) tc::umma_commit(&s.empty[i]);
+                        }
+                        if (ok) tc::umma_commit(&s.s_full[sb]);
+                        first = false;
+                    }
+                }
+            }
+            tc::umma_commit(&s.fin);
+            tc::mbar_wait(&s.fin, 0, kWaitLimit);
+        }
+        __syncwarp();
     } else {
-        const int64_t i = (int64_t)b * a.Nmax + e;
-        a.weights[i] = (a.acc ? a.acc[i] : 0.f) + w;
+        // ------------------------------------------------------------ workers
+        const int quad = warp & 3, grp = warp >> 2, hb = grp * kGh;
+        const int row = quad * 32 + lane;                 // entry of the tile
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        Producer<kSparse> producer(a, s, kv_s, b, e_beg, e_end, ntiles, (int64_t)(ntiles ? seq : 0) * a.Nmax);
+        uint32_t n = 0;
+        bool ok = true;
+        if (ntiles > 0) ok = producer.store(0);
+        for (int j = 0; j < ntiles; ++j) {
+            const int e_tile = e_beg + j * kE, last = blocks.last_query(e_tile), e = e_tile + row;
+            int entry = e < e_end ? e : -1;
+            if (kSparse && entry >= 0) {
+                const int v = __ldg(a.idx + (int64_t)b * a.k + e);
+                entry = v < a.Nmax ? v : -1;
+            }
+            float w = 0.f;
+            for (int t = 0; t <= last; ++t) {
+                const int seen = blocks.visible(t);
+                if (seen <= e_tile) continue;
+                for (int g = 0; g < a.hgroups; ++g, ++n) {
+                    // the next tile's expansion goes with this tile's last product
+                    if (t == last && g == a.hgroups - 1 && j + 1 < ntiles) ok = producer.store(j + 1) && ok;
+                    // lse of this warp's heads (+inf: adds nothing)
+                    if (lane < kGh) {
+                        const int h = g * kHg + hb + lane;
+                        const float l = h < a.H ? a.lse[((int64_t)b * a.T + t) * a.H + h] : INFINITY;
+                        s.lse[warp][lane] = l == -INFINITY ? INFINITY : l * kLog2e;
+                    }
+                    __syncwarp();
+                    const uint32_t sb = n & 1;
+                    ok = ok && wait(&s.s_full[sb], (n >> 1) & 1, s, a.status);
+                    tc::tc_fence_after();
+                    float z[kGh];
+                    tc::tmem_ld16(tmem_S + lanes + sb * kHg + hb, z);
+                    tc::tmem_ld_wait();
+                    tc::tc_fence_before();
+                    float p = 0.f;
+#pragma unroll
+                    for (int i = 0; i < kGh; ++i) {
+                        const float l = s.lse[warp][i];
+                        p += l == INFINITY ? 0.f : ex2(fmaf(z[i], a.scale_log2, -l));
+                    }
+                    if (kSparse || e < seen) w += p;
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&s.s_empty[sb]);
+                }
+            }
+            s.part[grp][row] = w;
+            asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory");
+            if (grp == 0) {
+                w = (s.part[0][row] + s.part[1][row]) + (s.part[2][row] + s.part[3][row]);
+                if (entry < 0) w = 0.f;
+                if (kSparse) {
+                    if (a.weights && e < e_end) a.weights[(int64_t)b * a.k + e] = w;
+                    // (entries listed twice add twice the same value, in any order)
+                    if (a.acc && entry >= 0) atomicAdd(a.acc + (int64_t)seq * a.Nmax + entry, w);
+                } else if (e < e_end) {
+                    const int64_t i = (int64_t)b * a.Nmax + e;
+                    a.weights[i] = (a.acc ? a.acc[i] : 0.f) + w;
+                }
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory");
+        }
+        // entries that no query sees
+        for (int e = (e_end > e_beg ? e_end : e_beg) + tid; e < e_stop; e += kWorkers) {
+            if (kSparse) {
+                if (a.weights) a.weights[(int64_t)b * a.k + e] = 0.f;
+            } else {
+                const int64_t i = (int64_t)b * a.Nmax + e;
+                a.weights[i] = a.acc ? a.acc[i] : 0.f;
+            }
+        }
+        tc::tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 16) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(s.tmem, 128);
     }
 }
 
 }  // namespace
 
-cudaError_t entry_weights_fp4(const Fp4WeightArgs& a, cudaStream_t st) {
-    const int64_t n = a.idx ? a.k : a.Nmax;
-    if (a.B == 0 || n == 0) return cudaSuccess;
-    cudaError_t e = cudaSuccess;
+cudaError_t entry_weights_fp4(const Fp4WeightArgs& x, cudaStream_t st) {
+    const int64_t n = x.idx ? x.k : x.Nmax;
+    if (x.B == 0 || n == 0) return cudaSuccess;
+    Args a{};
+    a.kv4 = x.kv4;
+    a.idx = x.idx;
+    a.status = device_status();
+    a.Nmax = x.Nmax;
+    a.f = fp4_row(x.c, x.R);
+    a.k = x.k;
+    a.dblocks = x.c / 64;
+    a.mtiles = x.c / 128;
+    a.lse = x.lse;
+    a.seq_of_q = x.seq_of_q;
+    a.pos = x.pos;
+    a.acc = x.acc;
+    a.weights = x.weights;
+    a.T = x.T;
+    a.n_seq = x.n_seq;
+    a.mp = x.mp;
+    a.H = x.H;
+    a.hgroups = (x.H + kHg - 1) / kHg;
+    a.scale_log2 = x.scale * kLog2e;
+    // tiles per CTA: one wave of CTAs, as even as whole tiles allow
+    const int64_t tiles = (n + kE - 1) / kE;
+    int64_t runs = 148 / x.B > 1 ? 148 / x.B : 1;
+    if (runs > tiles) runs = tiles;
+    a.run = (int)((tiles + runs - 1) / runs);
+    runs = (tiles + a.run - 1) / a.run;
+    CUtensorMap tmQ;
+    const uint64_t rows = (uint64_t)x.B * (x.T > 0 ? x.T : 1) * x.H;
+    if (!make_tmap_bf16_2d(&tmQ, x.T > 0 ? x.q : x.kv4, rows, x.c, x.c, kHg, 64)) return cudaErrorInvalidValue;
+    const size_t smem = 1024 + (size_t)a.dblocks * (kBlockBytes + kHg * 128) + sizeof(Shared);
+    auto kern = x.idx ? entry_weights_fp4_kernel<true> : entry_weights_fp4_kernel<false>;
+    cudaError_t e = smem_ceiling(kern);
+    if (e != cudaSuccess) return e;
     CSA_LAUNCH(st, "entry_weights_fp4",
-               e = launch_pdl(entry_weights_fp4_kernel, dim3((unsigned)((n + 3) / 4), a.B), dim3(128), 0, st, 0, a));
+               e = launch_pdl(kern, dim3((unsigned)runs, x.B), dim3(kThreads), smem, st, 0, a, tmQ));
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
