@@ -444,11 +444,20 @@ int nsplit_of(int nq, int H, int64_t max_entries) {
     return (int)((tiles + per - 1) / per);
 }
 
+// How the splits merge. Clusters of n CTAs need n free SMs in one GPC, so
+// fewer of them fit at a time than 148 / n (8: 15, with a CTA per SM);
+// clusters that would take a second wave go through the workspace.
+Merge merge_of(int nq, int H, int ns) {
+    constexpr int fit[kMaxCluster + 1] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
+    if (ns == 1) return kDirect;
+    return ns <= kMaxCluster && (int64_t)nq * ((H + kHg - 1) / kHg) <= fit[ns] ? kCluster : kWorkspace;
+}
+
 }  // namespace
 
 size_t mqa_fp4_workspace_bytes(int nq, int H, int c, int64_t max_entries) {
     const int ns = nsplit_of(nq, H, max_entries);
-    if (ns <= kMaxCluster) return 0;
+    if (merge_of(nq, H, ns) != kWorkspace) return 0;
     return align256((size_t)nq * ns * H * c * sizeof(float)) + align256((size_t)nq * ns * H * 2 * sizeof(float));
 }
 
@@ -475,7 +484,7 @@ cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {
     a.mp = x.mp;
     a.H = x.H;
     a.nsplit = ns;
-    a.merge = ns == 1 ? kDirect : ns <= kMaxCluster ? kCluster : kWorkspace;
+    a.merge = merge_of(x.nq, x.H, ns);
     a.dblocks = x.c / 64;
     a.mtiles = x.c / 128;
     a.tmem_cols = kHg * (1 + a.mtiles) <= 128 ? 128 : kHg * (1 + a.mtiles) <= 256 ? 256 : 512;
