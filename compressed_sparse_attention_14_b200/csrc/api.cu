@@ -856,7 +856,7 @@ int hca_entry_weights_fp4kv(const void* q, const float* lse, const uint8_t* kv4,
 static int check_evict(int B, int64_t Nmax, const char* who) {
     if (B < 0 || Nmax < 0) return fail(CSA_ERR_INVALID_ARG, "%s: bad B/Nmax", who);
     CSA_TRY(check_rows(B, who));
-    if (Nmax > INT32_MAX) return fail(CSA_ERR_UNSUPPORTED, "Nmax beyond int32 entry indices");
+    if (Nmax > (1 << 30)) return fail(CSA_ERR_UNSUPPORTED, "%s: Nmax beyond 2^30 entries", who);
     return CSA_OK;
 }
 
@@ -897,8 +897,8 @@ int csa_evict_plan(const float* acc, const int32_t* n_ent, const int32_t* entry_
 int csa_evict_rows(void* cache, int64_t row_bytes, int B, int64_t Nmax, const int32_t* src, const int32_t* dst,
                    const int32_t* n_moves, int64_t max_moves, void* stream) {
     CSA_TRY(check_evict(B, Nmax, "csa_evict_rows"));
-    if (row_bytes < 16 || row_bytes % 16)
-        return fail(CSA_ERR_INVALID_ARG, "csa_evict_rows: row_bytes=%lld must be a positive multiple of 16",
+    if (row_bytes < 16 || row_bytes % 16 || row_bytes > (1 << 30))
+        return fail(CSA_ERR_INVALID_ARG, "csa_evict_rows: row_bytes=%lld must be a positive multiple of 16 (up to 2^30)",
                     (long long)row_bytes);
     if (max_moves < 0 || max_moves > Nmax) return fail(CSA_ERR_INVALID_ARG, "csa_evict_rows: bad max_moves");
     if (B == 0 || max_moves == 0) return CSA_OK;

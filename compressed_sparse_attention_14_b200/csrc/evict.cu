@@ -7,145 +7,278 @@
 // slots of [0, keep), in order. Sources and destinations never overlap, and
 // only rows that have to move do.
 //
-// evict_plan: a CTA per sequence. The keep-th key is found by radix select
-// (a 9-bit digit with the protected bit on top, then three of 8), ties are
-// taken in index order, and holes and movers are listed with block scans.
-// evict_rows: a warp per moved row. evict_slot: a CTA per sequence, one
-// reduction.
+// evict_plan: a cluster of up to 8 CTAs per sequence, each with a contiguous
+// part of the entries, their keys in shared memory. The keep-th key is found
+// by radix select, 8 bits a pass (local histograms, summed over the cluster
+// through distributed shared memory). Ties stay in index order: every warp
+// owns a contiguous segment and counts it, the counts are scanned over warps
+// and CTAs, and a second walk writes holes and movers at their places without
+// another barrier. Bound by latency: a few passes over some thousand keys per
+// CTA and 13 cluster barriers.
+// evict_rows: a thread per 16 bytes, four of them in flight; bound by memory.
+// evict_slot: a CTA per sequence, one reduction.
 #include "common.cuh"
 #include "kernels.h"
+#include "tc.cuh"
 
 namespace csa {
 
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxCached = 48 * 1024;      // keys of a CTA's part kept in shared memory
 
-// 33 bits: protected, then the orderable weight (NaN as -inf)
-__device__ __forceinline__ uint64_t evict_key(float w, bool prot) {
-    const uint32_t o = orderable(w != w ? -INFINITY : w);
-    return ((uint64_t)(prot ? 1u : 0u) << 32) | o;
+// NaN counts as -inf
+__device__ __forceinline__ uint32_t weight_key(float w) { return orderable(w != w ? -INFINITY : w); }
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
 
-// exclusive rank of a flag over the block, in thread order; total of the flags
-__device__ __forceinline__ int block_rank(bool flag, int* warp_cnt, int& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t b = __ballot_sync(0xffffffffu, flag);
-    __syncthreads();
-    if (lane == 0) warp_cnt[warp] = __popc(b);
-    __syncthreads();
-    int before = 0, sum = 0;
-    for (int i = 0; i < kThreads / 32; ++i) {
-        const int c = warp_cnt[i];
-        if (i < warp) before += c;
-        sum += c;
-    }
-    total = sum;
-    return before + __popc(b & ((1u << lane) - 1u));
-}
+struct PlanShared {
+    int hist[2][256];
+    int scan[kWarps];
+    int ties[kWarps], holes[kWarps], movers[kWarps];   // per warp, then exclusive sums
+    int total[3];                                      // this CTA's: protected / ties, holes, movers
+    int digit, need;
+};
 
-__global__ void __launch_bounds__(kThreads) evict_plan_kernel(const __grid_constant__ EvictPlanArgs a) {
-    __shared__ int hist[512];
-    __shared__ int warp_cnt[kThreads / 32];
-    __shared__ uint64_t s_prefix;
-    __shared__ int s_need;
+__global__ void __launch_bounds__(kThreads) evict_plan_kernel(const __grid_constant__ EvictPlanArgs a, int csize,
+                                                              int cached) {
+    extern __shared__ uint32_t keys[];
+    __shared__ PlanShared s;
     pdl_wait();
     pdl_launch_next();
-    const int b = blockIdx.x, tid = threadIdx.x;
+    const int b = blockIdx.y, rank = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t base = (int64_t)b * a.Nmax;
     const float* acc = a.acc + base;
     const int32_t* pos = a.entry_pos ? a.entry_pos + base : nullptr;
-    int64_t n = a.n_ent[b];
-    n = n < 0 ? 0 : n > a.Nmax ? a.Nmax : n;
-    __syncthreads();                      // n_out may be n_ent
-    const int64_t n_out = n < a.keep ? n : a.keep;
-    const int64_t M = a.M;
+    const int Nmax = (int)a.Nmax, keep = (int)a.keep, M = (int)a.M;
+    int n = a.n_ent[b];
+    n = n < 0 ? 0 : n > Nmax ? Nmax : n;
+    const int n_out = n < keep ? n : keep;
     int32_t* src = a.src + (int64_t)b * M;
     int32_t* dst = a.dst + (int64_t)b * M;
     const bool guard = pos && a.protect_from;
     const int from = guard ? a.protect_from[b] : 0;
-    auto key = [&](int64_t i) { return evict_key(acc[i], guard && pos[i] >= from); };
+
+    auto sync_all = [&]() {
+        if (csize > 1) tc::cluster_sync();
+        else __syncthreads();
+    };
+    // sum of a counter over the CTAs before this one, and over all
+    auto cluster_sum = [&](const int* counter, int& before, int& all) {
+        before = all = 0;
+        for (int r = 0; r < csize; ++r) {
+            const int v = csize > 1 ? (int)ld_cluster_u32(tc::mapa(tc::smem_u32(counter), r)) : *counter;
+            if (r < rank) before += v;
+            all += v;
+        }
+    };
     int moves = 0;
-    if (n > a.keep) {
-        // the keep-th largest key, digit by digit
-        if (tid == 0) { s_prefix = 0; s_need = (int)a.keep; }
+    if (n > keep) {
+        // this CTA's part, and this warp's segment of it (whole groups of 32)
+        const int groups = (n + 31) / 32, per_cta = (groups + csize - 1) / csize;
+        const int g0 = min(groups, rank * per_cta), g1 = min(groups, g0 + per_cta);
+        const int per_warp = (g1 - g0 + kWarps - 1) / kWarps;
+        const int w0 = min(g1, g0 + warp * per_warp), w1 = min(g1, w0 + per_warp);
+        bool prot_only = false;           // more protected entries than stay: only they compete
+        auto raw_key = [&](int i) {
+            const uint32_t k = weight_key(acc[i]);
+            if (!guard) return k;
+            const bool p = pos[i] >= from;
+            // protected entries above every weight, or the others below
+            return prot_only ? (p ? k : 0u) : (p ? 0xFFFFFFFFu : k);
+        };
+        auto key = [&](int i) { return cached ? keys[i - 32 * g0] : raw_key(i); };
+        if (tid < 3) s.total[tid] = 0;
+        for (int i = tid; i < 256; i += kThreads) s.hist[0][i] = 0;
+        __syncthreads();
+        if (guard) {
+            int c = 0;
+            for (int g = w0; g < w1; ++g) {
+                const int i = 32 * g + lane;
+                c += __popc(__ballot_sync(0xffffffffu, i < n && pos[i] >= from));
+            }
+            if (lane == 0 && c) atomicAdd(&s.total[0], c);
+            sync_all();
+            int before, all;
+            cluster_sum(&s.total[0], before, all);
+            prot_only = all > keep;
+        }
+        if (cached) {
+#pragma unroll 4
+            for (int g = w0; g < w1; ++g)
+                if (32 * g + lane < n) keys[32 * (g - g0) + lane] = raw_key(32 * g + lane);
+            __syncwarp();
+        }
+        uint32_t prefix = 0;
+        int need = keep;
         for (int d = 0; d < 4; ++d) {
-            const int shift = 24 - 8 * d, bins = d == 0 ? 512 : 256;
-            for (int i = tid; i < 512; i += kThreads) hist[i] = 0;
-            __syncthreads();
-            const uint64_t prefix = s_prefix;
-            for (int64_t i = tid; i < n; i += kThreads) {
-                const uint64_t k = key(i);
-                if (d == 0 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
+            const int shift = 24 - 8 * d;
+            int* hist = s.hist[d & 1];
+            for (int g = w0; g < w1; ++g) {
+                const int i = 32 * g + lane;
+                const uint32_t k = i < n ? key(i) : 0;
+                const bool in = i < n && (d == 0 || (k >> (shift + 8)) == prefix);
+                const uint32_t m = __ballot_sync(0xffffffffu, in);
+                if (!m) continue;
+                // equal digits (zero weights, say) would queue up at one counter
+                const uint32_t digit = (k >> shift) & 255u;
+                const uint32_t lead = __shfl_sync(0xffffffffu, digit, __ffs(m) - 1);
+                const uint32_t same = __ballot_sync(0xffffffffu, in && digit == lead);
+                if (in && digit != lead) atomicAdd(&hist[digit], 1);
+                if (lane == __ffs(m) - 1) atomicAdd(&hist[lead], __popc(same));
             }
-            __syncthreads();
-            if (tid == 0) {
-                int need = s_need, v = bins - 1;
-                while (v > 0 && hist[v] < need) need -= hist[v--];
-                s_prefix = (prefix << 8) | (uint64_t)v;
-                s_need = need;
+            sync_all();
+            // entries with this digit, of all CTAs; from the largest digit down
+            int c = 0;
+            if (tid < 256)
+                for (int r = 0; r < csize; ++r)
+                    c += csize > 1 ? (int)ld_cluster_u32(tc::mapa(tc::smem_u32(hist + 255 - tid), r)) : hist[255 - tid];
+            int sum = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
             }
+            if (lane == 31) s.scan[warp] = sum;
             __syncthreads();
+            int above = sum - c;          // entries with a larger digit
+            for (int w = 0; w < warp && w < 8; ++w) above += s.scan[w];
+            if (tid < 256 && above < need && above + c >= need) {
+                s.digit = 255 - tid;
+                s.need = need - above;
+            }
+            // the other histogram is free: its readers passed the last barrier
+            for (int i = tid; i < 256; i += kThreads) s.hist[(d + 1) & 1][i] = 0;
+            sync_all();
+            prefix = (prefix << 8) | (uint32_t)s.digit;
+            need = s.need;
         }
-        const uint64_t kth = s_prefix;
-        const int ties = s_need;          // entries equal to it that stay
-        int seen = 0, holes = 0, movers = 0;
-        for (int64_t c0 = 0; c0 < n; c0 += kThreads) {
-            const int64_t i = c0 + tid;
-            const uint64_t k = i < n ? key(i) : 0;
-            const bool tie = i < n && k == kth;
-            int tot;
-            const int tr = block_rank(tie, warp_cnt, tot);
-            const bool kept = i < n && (k > kth || (tie && seen + tr < ties));
-            seen += tot;
-            const int hr = block_rank(i < a.keep && !kept, warp_cnt, tot);
-            if (i < a.keep && !kept) dst[holes + hr] = (int32_t)i;
-            holes += tot;
-            const int mr = block_rank(i >= a.keep && kept, warp_cnt, tot);
-            if (i >= a.keep && kept) src[movers + mr] = (int32_t)i;
-            movers += tot;
+        // `need` of the entries equal to the keep-th key stay, the first ones
+        const uint32_t kth = prefix;
+        int gt_lo = 0, gt_hi = 0, tie_lo = 0, tie_hi = 0;
+        for (int g = w0; g < w1; ++g) {
+            const int i = 32 * g + lane;
+            const uint32_t k = i < n ? key(i) : 0;
+            const bool lo = i < keep;
+            const uint32_t gt = __ballot_sync(0xffffffffu, i < n && k > kth), eq = __ballot_sync(0xffffffffu, i < n && k == kth);
+            const uint32_t lom = __ballot_sync(0xffffffffu, lo);
+            gt_lo += __popc(gt & lom);
+            gt_hi += __popc(gt & ~lom);
+            tie_lo += __popc(eq & lom);
+            tie_hi += __popc(eq & ~lom);
         }
-        moves = holes;
+        if (lane == 0) s.ties[warp] = tie_lo + tie_hi;
+        __syncthreads();
+        if (tid == 0) {
+            int sum = 0;
+            for (int w = 0; w < kWarps; ++w) sum += s.ties[w];
+            s.total[0] = sum;
+        }
+        sync_all();
+        int tie_base, tie_all;
+        cluster_sum(&s.total[0], tie_base, tie_all);
+        for (int w = 0; w < warp; ++w) tie_base += s.ties[w];
+        const int n_lo = max(0, min(32 * w1, min(n, keep)) - 32 * w0);
+        const int keep_lo = min(max(need - tie_base, 0), tie_lo);
+        const int keep_hi = min(max(need - tie_base - tie_lo, 0), tie_hi);
+        if (lane == 0) {
+            s.holes[warp] = n_lo - gt_lo - keep_lo;
+            s.movers[warp] = gt_hi + keep_hi;
+        }
+        __syncthreads();
+        if (tid == 0) {
+            int h = 0, m = 0;
+            for (int w = 0; w < kWarps; ++w) { h += s.holes[w]; m += s.movers[w]; }
+            s.total[1] = h;
+            s.total[2] = m;
+        }
+        sync_all();
+        int hole, mover, all;
+        cluster_sum(&s.total[2], mover, all);
+        cluster_sum(&s.total[1], hole, moves);
+        for (int w = 0; w < warp; ++w) { hole += s.holes[w]; mover += s.movers[w]; }
+        int tie = tie_base;
+        const uint32_t below = (1u << lane) - 1u;
+        for (int g = w0; g < w1; ++g) {
+            const int i = 32 * g + lane;
+            const uint32_t k = i < n ? key(i) : 0;
+            const uint32_t eq = __ballot_sync(0xffffffffu, i < n && k == kth);
+            const bool kept = i < n && (k > kth || (k == kth && tie + __popc(eq & below) < need));
+            tie += __popc(eq);
+            const uint32_t hm = __ballot_sync(0xffffffffu, i < keep && !kept);
+            const uint32_t mm = __ballot_sync(0xffffffffu, i >= keep && kept);
+            if (i < keep && !kept) dst[hole + __popc(hm & below)] = i;
+            if (i >= keep && kept) src[mover + __popc(mm & below)] = i;
+            hole += __popc(hm);
+            mover += __popc(mm);
+        }
     }
-    for (int64_t i = moves + tid; i < M; i += kThreads) src[i] = dst[i] = -1;
-    if (tid == 0) {
-        a.n_moves[b] = moves;
-        a.n_out[b] = (int32_t)n_out;
-    }
+    const int t0 = rank * kThreads + tid, step = csize * kThreads;
+    for (int i = moves + t0; i < M; i += step) src[i] = dst[i] = -1;
     // the weights (and positions) follow their entries
     float* ao = a.acc_out + base;
     int32_t* po = a.pos_out ? a.pos_out + base : nullptr;
     if (ao != acc)
-        for (int64_t i = tid; i < n_out; i += kThreads) ao[i] = acc[i];
+        for (int i = t0; i < n_out; i += step) ao[i] = acc[i];
     if (po && po != pos)
-        for (int64_t i = tid; i < n_out; i += kThreads) po[i] = pos[i];
-    __syncthreads();
-    for (int i = tid; i < moves; i += kThreads) {
-        ao[dst[i]] = acc[src[i]];
-        if (po) po[dst[i]] = pos[src[i]];
+        for (int i = t0; i < n_out; i += step) po[i] = pos[i];
+    sync_all();                           // also: every CTA has read n_ent, which n_out may be
+    if (rank == 0 && tid == 0) {
+        a.n_moves[b] = moves;
+        a.n_out[b] = n_out;
     }
-    __syncthreads();
-    for (int64_t i = n_out + tid; i < a.Nmax; i += kThreads) {
+    for (int i = t0; i < moves; i += step) {
+        const int f = __ldcg(src + i), d = __ldcg(dst + i);
+        ao[d] = acc[f];
+        if (po) po[d] = pos[f];
+    }
+    sync_all();
+    for (int i = n_out + t0; i < Nmax; i += step) {
         ao[i] = 0.f;
         if (po) po[i] = -1;
     }
 }
 
-// a warp per move, 16 bytes per lane
-__global__ void __launch_bounds__(256) evict_rows_kernel(uint8_t* __restrict__ cache, int64_t row_bytes, int64_t Nmax,
+// rows of `pieces` 16-byte pieces; a block takes 1024 consecutive pieces of a sequence's moves
+__global__ void __launch_bounds__(256) evict_rows_kernel(uint4* __restrict__ cache, int pieces, int64_t Nmax,
                                                          const int32_t* __restrict__ src,
                                                          const int32_t* __restrict__ dst,
                                                          const int32_t* __restrict__ n_moves, int64_t M) {
     pdl_wait();
     pdl_launch_next();
-    const int b = blockIdx.y, lane = threadIdx.x & 31;
-    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (i >= M || i >= n_moves[b]) return;
-    const int s = src[(int64_t)b * M + i], d = dst[(int64_t)b * M + i];
-    if (s < 0 || d < 0 || s >= Nmax || d >= Nmax) return;
-    const uint4* p = reinterpret_cast<const uint4*>(cache + ((int64_t)b * Nmax + s) * row_bytes);
-    uint4* o = reinterpret_cast<uint4*>(cache + ((int64_t)b * Nmax + d) * row_bytes);
-    for (int64_t j = lane; j < row_bytes / 16; j += 32) o[j] = p[j];
+    const int b = blockIdx.y;
+    const int64_t moves = n_moves[b] < M ? n_moves[b] : M;
+    const int64_t i0 = (int64_t)blockIdx.x * 1024 / pieces;
+    const uint32_t p0 = (uint32_t)((int64_t)blockIdx.x * 1024 - i0 * pieces) + threadIdx.x;
+    if (i0 >= moves) return;
+    uint4 v[4];
+    uint4* to[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const uint32_t k = (p0 + 256 * u) / (uint32_t)pieces;
+        const int64_t i = i0 + k;
+        to[u] = nullptr;
+        if (i >= moves) continue;
+        const uint32_t p = p0 + 256 * u - k * (uint32_t)pieces;
+        const int f = __ldg(src + (int64_t)b * M + i), d = __ldg(dst + (int64_t)b * M + i);
+        if (f < 0 || d < 0 || f >= Nmax || d >= Nmax) continue;
+        v[u] = __ldcs(cache + ((int64_t)b * Nmax + f) * pieces + p);
+        to[u] = cache + ((int64_t)b * Nmax + d) * pieces + p;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        if (to[u]) *to[u] = v[u];
+}
+
+// 33 bits: protected, then the key
+__device__ __forceinline__ uint64_t evict_key(float w, bool prot) {
+    return ((uint64_t)(prot ? 1u : 0u) << 32) | weight_key(w);
 }
 
 __global__ void __launch_bounds__(256) evict_slot_kernel(const __grid_constant__ EvictSlotArgs a) {
@@ -202,8 +335,17 @@ size_t evict_plan_workspace_bytes(int B, int64_t Nmax, int64_t keep) {
 cudaError_t evict_plan(const EvictPlanArgs& a, void* ws, cudaStream_t st) {
     (void)ws;
     if (a.B == 0) return cudaSuccess;
-    cudaError_t e = cudaSuccess;
-    CSA_LAUNCH(st, "evict_plan", e = launch_pdl(evict_plan_kernel, dim3(a.B), dim3(kThreads), 0, st, 0, a));
+    // 2048 entries and more per CTA: a part smaller than that costs less than
+    // another CTA at the barriers
+    int csize = 1;
+    while (csize < kMaxCluster && a.Nmax > 2048 * (int64_t)csize) csize <<= 1;
+    const int64_t part = ((a.Nmax + 31) / 32 + csize - 1) / csize * 32;
+    const size_t smem = part <= kMaxCached ? part * sizeof(uint32_t) : 0;
+    cudaError_t e = smem_ceiling(evict_plan_kernel);
+    if (e != cudaSuccess) return e;
+    CSA_LAUNCH(st, "evict_plan",
+               e = launch_pdl(evict_plan_kernel, dim3(csize, a.B), dim3(kThreads), smem, st,
+                              csize > 1 ? (unsigned)csize : 0u, a, csize, smem ? 1 : 0));
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
@@ -211,10 +353,11 @@ cudaError_t evict_plan(const EvictPlanArgs& a, void* ws, cudaStream_t st) {
 cudaError_t evict_rows(void* cache, int64_t row_bytes, int B, int64_t Nmax, const int32_t* src, const int32_t* dst,
                        const int32_t* n_moves, int64_t M, cudaStream_t st) {
     if (B == 0 || M == 0) return cudaSuccess;
+    const int64_t pieces = row_bytes / 16;
     cudaError_t e = cudaSuccess;
     CSA_LAUNCH(st, "evict_rows",
-               e = launch_pdl(evict_rows_kernel, dim3((unsigned)((M + 7) / 8), B), dim3(256), 0, st, 0, (uint8_t*)cache,
-                              row_bytes, Nmax, src, dst, n_moves, M));
+               e = launch_pdl(evict_rows_kernel, dim3((unsigned)((M * pieces + 1023) / 1024), B), dim3(256), 0, st, 0,
+                              (uint4*)cache, (int)pieces, Nmax, src, dst, n_moves, M));
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
