@@ -24,9 +24,9 @@
 //   softmax and epilogue: warp w works on TMEM lanes 32 (w % 4).. and heads
 //     16 (w / 4)...
 // Warp 16 issues the S products, warp 17 the O products. Blocks go back and
-// forth in pairs (128 dims, one M tile of the O product), the last first, so
-// expansion and S product of tile j+1 run while the O product of tile j is
-// still busy with the pairs before.
+// forth in groups of 256 dims (two M tiles of the O product), the last first,
+// so expansion and S product of tile j+1 begin while the O product of tile j
+// is still busy with the group before.
 //
 // Entries outside the query's set are stored as zeros and get weight 0: no
 // row that the query does not see is read.
@@ -63,7 +63,8 @@ struct Args : Fp4TileArgs {
 };
 
 struct Shared : Fp4TileShared {
-    float mref[kHg], alpha[kHg], lsum[kHg];
+    float mref[kHg], mexp[kHg];               // reference maximum; the same, 0 for none
+    float alpha[kHg], lsum[kHg];
     float red[4][kHg];
     float coef[kMaxCluster][kHg];
     uint64_t s_full, q_full, p_full, o_done, fin[2];
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     const int ntiles = e_end > e_beg ? (int)((e_end - e_beg + kE - 1) / kE) : 0;
 
     if (tid == 0) {
-        for (int i = 0; i < kPairs; ++i) {
+        for (int i = 0; i < kGroups; ++i) {
             tc::mbar_init(&s.full[i], kWorkers / 32);
             tc::mbar_init(&s.empty[i], 1);
         }
@@ -162,20 +163,18 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                     tc::tma_load_2d(q_s + (size_t)b * kHg * 128, &tmQ, &s.q_full, b * 64, t * a.H + h0);
                 bool ok = wait(&s.q_full, 0, s, a.status);
                 const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
-                const int last = last_early_pair(a);
                 for (int j = 0; ok && j < ntiles; ++j) {
-                    for (int n = 0; n < a.mtiles; ++n) {
-                        const int i = n <= last ? last - n : a.mtiles - 1 - (n - last - 1);   // as they are stored
-                        if (!(ok = wait(&s.full[i], j & 1, s, a.status))) break;
+                    for (int n = 0; n < a.groups; ++n) {
+                        const int gr = stored_group(a, n);
+                        if (!(ok = wait(&s.full[gr], j & 1, s, a.status))) break;
                         tc::tc_fence_after();
+                        const int b_end = 4 * gr + 4 < a.dblocks ? 4 * gr + 4 : a.dblocks;
+                        for (int b = 4 * gr; b < b_end; ++b)
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) {
-                            const int b = 2 * i + (kk >> 2);
-                            tc::umma_bf16(tmem_S,
-                                          tc::sdesc_sw128(kv_addr + b * kBlockBytes + (kk & 3) * 32, 16, 1024),
-                                          tc::sdesc_sw128(q_addr + b * (kHg * 128) + (kk & 3) * 32, 16, 1024), idesc,
-                                          (n | kk) ? 1u : 0u);
-                        }
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc::umma_bf16(tmem_S, tc::sdesc_sw128(kv_addr + b * kBlockBytes + kk * 32, 16, 1024),
+                                              tc::sdesc_sw128(q_addr + b * (kHg * 128) + kk * 32, 16, 1024), idesc,
+                                              (n || b > 4 * gr || kk) ? 1u : 0u);
                     }
                     if (ok) tc::umma_commit(&s.s_full);
                 }
@@ -192,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                                           tc::sdesc_sw128(kv_addr + 2 * mt * kBlockBytes + ke * 2048, kBlockBytes, 1024),
                                           tc::sdesc_sw128(p_addr + ke * 2048, kE * 128, 1024), idesc,
                                           (j > 0 || ke > 0) ? 1u : 0u);
-                        tc::umma_commit(&s.empty[mt]);
+                        if (!(mt & 1)) tc::umma_commit(&s.empty[mt >> 1]);
                     }
                     tc::umma_commit(&s.o_done);
                 }
@@ -211,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         Producer<kSparse> producer(a, s, kv_s, t, (int)e_beg, (int)e_end, ntiles,
                                    (ntiles ? seq : 0) * a.Nmax);
-        if (gth < kGh) { s.mref[hb + gth] = -INFINITY; s.lsum[hb + gth] = 0.f; }
+        if (gth < kGh) { s.mref[hb + gth] = -INFINITY; s.mexp[hb + gth] = s.lsum[hb + gth] = 0.f; }
         float lpart[kGh];
 #pragma unroll
         for (int i = 0; i < kGh; ++i) lpart[i] = 0.f;
@@ -251,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                     const float m = fmaxf(fmaxf(fmaxf(s.red[0][h], s.red[1][h]), fmaxf(s.red[2][h], s.red[3][h])), old);
                     s.alpha[h] = old == -INFINITY ? 0.f : ex2(old - m);
                     s.mref[h] = m;
+                    s.mexp[h] = m == -INFINITY ? 0.f : m;
                 }
                 group_sync(g);
 #pragma unroll
@@ -275,9 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             uint32_t pk[kGh / 2];
 #pragma unroll
             for (int i = 0; i < kGh; i += 2) {
-                const float m0 = s.mref[hb + i], m1 = s.mref[hb + i + 1];
-                const float p0 = z[i] == -INFINITY ? 0.f : ex2(z[i] - m0);
-                const float p1 = z[i + 1] == -INFINITY ? 0.f : ex2(z[i + 1] - m1);
+                const float p0 = ex2(z[i] - s.mexp[hb + i]), p1 = ex2(z[i + 1] - s.mexp[hb + i + 1]);
                 lpart[i] += p0;
                 lpart[i + 1] += p1;
                 const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
@@ -487,6 +485,7 @@ cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {
     a.merge = merge_of(x.nq, x.H, ns);
     a.dblocks = x.c / 64;
     a.mtiles = x.c / 128;
+    a.groups = (x.c + 255) / 256;
     a.tmem_cols = kHg * (1 + a.mtiles) <= 128 ? 128 : kHg * (1 + a.mtiles) <= 256 ? 256 : 512;
     a.scale_log2 = x.scale * kLog2e;
     CUtensorMap tmQ;

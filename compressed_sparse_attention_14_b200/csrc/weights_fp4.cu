@@ -10,7 +10,7 @@
 //
 // A CTA walks a run of tiles of one sequence (or of one query's entry list).
 // Each tile stays in shared memory for all query blocks (query, 64 heads) of
-// its sequence; their q blocks stream through one buffer, refilled in quarters
+// its sequence; their q blocks stream through one buffer, refilled in halves
 // as the product has read them, unless there is only one, which stays. The
 // next tile is expanded while the last query block's product runs. Every sum
 // has a fixed order: heads, then queries, within a thread, then the four
@@ -40,7 +40,7 @@ struct Args : Fp4TileArgs {
 struct Shared : Fp4TileShared {
     float lse[kWorkers / 32][kGh];            // the query block's, per warp
     float part[kWorkers / 128][kE];
-    uint64_t q_full[kPairs], q_empty[kPairs], s_full[2], s_empty[2], fin;
+    uint64_t q_full[kGroups], q_empty[kGroups], s_full[2], s_empty[2], fin;
     uint32_t tmem;
     int n_max;
 };
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
     const int e_beg = blockIdx.x * a.run * kE, n_all = kSparse ? a.k : (int)a.Nmax;
     const int e_stop = (int64_t)a.run * kE > n_all - e_beg ? n_all : e_beg + a.run * kE;   // this CTA's entries
     if (tid == 0) {
-        for (int i = 0; i < kPairs; ++i) {
+        for (int i = 0; i < kGroups; ++i) {
             tc::mbar_init(&s.full[i], kWorkers / 32);
             tc::mbar_init(&s.empty[i], 1);
             tc::mbar_init(&s.q_full[i], 1);
@@ -123,18 +123,20 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
                 for (int t = 0; ok && t <= blocks.last_query(e_tile); ++t) {
                     if (blocks.visible(t) <= e_tile) continue;
                     for (int g = 0; ok && g < a.hgroups; ++g, ++n)
-                        for (int i = a.mtiles - 1; i >= 0; --i) {
+                        for (int o = 0; o < a.groups; ++o) {
+                            const int i = stored_group(a, o);
                             if (n > 0 && !(ok = wait(&s.q_empty[i], (n - 1) & 1, s, a.status))) break;
-                            tc::mbar_expect_tx(&s.q_full[i], 2 * kHg * 128);
-                            for (int h = 0; h < 2; ++h)
-                                tc::tma_load_2d(q_s + (size_t)(2 * i + h) * kHg * 128, &tmQ, &s.q_full[i],
-                                                (2 * i + h) * 64, (b * a.T + t) * a.H + g * kHg);
+                            const int b_end = 4 * i + 4 < a.dblocks ? 4 * i + 4 : a.dblocks;
+                            tc::mbar_expect_tx(&s.q_full[i], (uint32_t)(b_end - 4 * i) * kHg * 128);
+                            for (int blk = 4 * i; blk < b_end; ++blk)
+                                tc::tma_load_2d(q_s + (size_t)blk * kHg * 128, &tmQ, &s.q_full[i], blk * 64,
+                                                (b * a.T + t) * a.H + g * kHg);
                         }
                 }
             }
-            // the copies of the last block of each pair have landed
+            // the last copies of each group have landed
             if (n > 0)
-                for (int i = 0; i < a.mtiles; ++i) tc::mbar_wait(&s.q_full[i], (n - 1) & 1, ok ? kWaitLimit : 1u << 16);
+                for (int i = 0; i < a.groups; ++i) tc::mbar_wait(&s.q_full[i], (n - 1) & 1, ok ? kWaitLimit : 1u << 16);
         }
         __syncwarp();
     } else if (warp == 16) {
@@ -142,7 +144,6 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
         if (lane == 0 && ntiles > 0) {
             const uint32_t kv_addr = tc::smem_u32(kv_s), q_addr = tc::smem_u32(q_s);
             const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
-            const int early = last_early_pair(a);
             uint32_t n = 0;
             bool ok = true;
             for (int j = 0; ok && j < ntiles; ++j) {
@@ -153,19 +154,19 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
                     for (int g = 0; ok && g < a.hgroups; ++g, ++n) {
                         const uint32_t sb = n & 1;
                         if (n >= 2 && !(ok = wait(&s.s_empty[sb], ((n >> 1) - 1) & 1, s, a.status))) break;
-                        for (int o = 0; o < a.mtiles; ++o) {
-                            const int i = o <= early ? early - o : a.mtiles - 1 - (o - early - 1);
+                        for (int o = 0; o < a.groups; ++o) {
+                            const int i = stored_group(a, o);
                             if (!(ok = wait(&s.q_full[i], stay ? 0 : n & 1, s, a.status))) break;
                             if (first && !(ok = wait(&s.full[i], j & 1, s, a.status))) break;
                             tc::tc_fence_after();
+                            const int b_end = 4 * i + 4 < a.dblocks ? 4 * i + 4 : a.dblocks;
+                            for (int blk = 4 * i; blk < b_end; ++blk)
 #pragma unroll
-                            for (int kk = 0; kk < 8; ++kk) {
-                                const int blk = 2 * i + (kk >> 2);
-                                tc::umma_bf16(tmem_S + sb * kHg,
-                                              tc::sdesc_sw128(kv_addr + blk * kBlockBytes + (kk & 3) * 32, 16, 1024),
-                                              tc::sdesc_sw128(q_addr + blk * (kHg * 128) + (kk & 3) * 32, 16, 1024),
-                                              idesc, (o | kk) ? 1u : 0u);
-                            }
+                                for (int kk = 0; kk < 4; ++kk)
+                                    tc::umma_bf16(tmem_S + sb * kHg,
+                                                  tc::sdesc_sw128(kv_addr + blk * kBlockBytes + kk * 32, 16, 1024),
+                                                  tc::sdesc_sw128(q_addr + blk * (kHg * 128) + kk * 32, 16, 1024),
+                                                  idesc, (o || blk > 4 * i || kk) ? 1u : 0u);
                             if (!stay) tc::umma_commit(&s.q_empty[i]);
                             if (t == last && g == a.hgroups - 1) tc::umma_commit(&s.empty[i]);
                         }
@@ -274,6 +275,7 @@ cudaError_t entry_weights_fp4(const Fp4WeightArgs& x, cudaStream_t st) {
     a.k = x.k;
     a.dblocks = x.c / 64;
     a.mtiles = x.c / 128;
+    a.groups = (x.c + 255) / 256;
     a.lse = x.lse;
     a.seq_of_q = x.seq_of_q;
     a.pos = x.pos;
