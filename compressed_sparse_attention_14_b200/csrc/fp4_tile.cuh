@@ -1,8 +1,8 @@
 // Tiles of 4-bit entries (the format: fp4.cuh) in shared memory as tensor-core
 // operands: 128 entries x c channels, bf16, in 64-channel blocks of 16 KB with
-// the 128-byte swizzle. 16 worker warps read the packed rows, expand them
+// the 128-byte swizzle. 8 producer warps read the packed rows, expand them
 // (exactly) and store them; blocks are handed to the products and back in
-// groups of 256 channels.
+// pairs (128 channels).
 #pragma once
 
 #include "csa.h"
@@ -12,11 +12,10 @@
 namespace csa {
 namespace fp4_tile {
 
-constexpr int kWorkers = 512, kThreads = kWorkers + 64;
+constexpr int kProducers = 256;         // producer threads
 constexpr int kE = 128;                 // entries per tile
 constexpr int kHg = 64;                 // heads per CTA
-constexpr int kGroups = CSA_MAX_HEAD_DIM / 256;  // groups of four 64-channel blocks
-constexpr int kGh = 16;                 // heads per worker warp
+constexpr int kPairs = CSA_MAX_HEAD_DIM / 128;   // pairs of 64-channel blocks
 constexpr uint32_t kBlockBytes = kE * 128;
 constexpr uint32_t kWaitLimit = 1u << 24;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -27,11 +26,11 @@ struct Fp4TileArgs {
     int* status;
     int64_t Nmax;
     Fp4Row f;
-    int k, dblocks, mtiles, groups;   // c / 64, c / 128, c / 256 rounded up
+    int k, dblocks, mtiles;   // c / 64, c / 128
 };
 
 struct Fp4TileShared {
-    uint64_t full[kGroups], empty[kGroups];   // a group of blocks stored / free
+    uint64_t full[kPairs], empty[kPairs];     // a pair of blocks stored / free
     int abort;
 };
 
@@ -61,45 +60,43 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Fp4TileShar
 }
 
 // The first 64 rotary channels are loaded ahead with the codes, the others
-// copied while a group is stored; groups up to this one hold none of the latter.
-__device__ __forceinline__ int last_early_group(const Fp4TileArgs& a) {
-    return a.f.R <= 64 ? a.groups - 1 : (a.f.Q + 64) / 256 - 1;
+// copied while a pair is stored; pairs up to this one hold none of the latter.
+__device__ __forceinline__ int last_early_pair(const Fp4TileArgs& a) {
+    return a.f.R <= 64 ? a.mtiles - 1 : (a.f.Q + 64) / 128 - 1;
 }
-// The n-th group in the order in which groups are stored.
-__device__ __forceinline__ int stored_group(const Fp4TileArgs& a, int n) {
-    const int last = last_early_group(a);
-    return n <= last ? last - n : a.groups - 1 - (n - last - 1);
+// The n-th pair in the order in which pairs are stored.
+__device__ __forceinline__ int stored_pair(const Fp4TileArgs& a, int n) {
+    const int last = last_early_pair(a);
+    return n <= last ? last - n : a.mtiles - 1 - (n - last - 1);
 }
 
-// A thread's part of the expansion: of two rows, the 32 channels of chunk
-// `piece` in every group, and the piece-th 16 bytes of the rotary channels.
-// What a tile's loads cost is the 128-byte lines touched, not the bytes, and
-// the 8 lanes of a row read one line per instruction (4 lines an instruction:
-// two lanes to a row and 16 lines took 4400 cycles a tile, four lanes 2000).
-// The 8 lanes that store together are 4 rows of one block, whose pieces lie in
+// A producer thread's part: of two rows, the 32 channels of chunk `chunk` in
+// every pair of blocks and every fourth 16-byte piece of the rotary channels.
+// The 4 lanes of a row read 64 consecutive bytes, a load instruction touches
+// 8 lines (two lanes to a row and 16 lines took twice as long to issue). The 8
+// lanes that store together are 4 rows of one block, whose pieces lie in
 // different banks.
 template <bool kSparse>
 struct Producer {
     const Fp4TileArgs& a;
     Fp4TileShared& s;
-    // (registers are short: row numbers instead of pointers; n_seq * Nmax is
-    // below 2^31)
-    uint32_t tile;            // this thread's first row in block 0; the second is 4 rows on
-    int row0, t, e0, e_end, ntiles;
+    uint32_t tile;            // this thread's first row in block 0; the second is 8 rows on
+    int warp, lane, row0, t, e0, e_end, ntiles;   // (rows as numbers: n_seq * Nmax is below 2^31)
     int next[2], cur[2];
-    uint4 raw[2][kGroups], rope[2];
-    uint32_t scales[2];       // 4 bytes of the row's scale area, the piece-th 4
+    uint4 raw[2][kPairs], rope[2][2];
+    uint2 scales[2];          // 8 bytes of the row's scale area, the chunk-th 8
 
-    __device__ __forceinline__ static int lane() { return threadIdx.x & 31; }
-    __device__ __forceinline__ static int piece() { return (lane() >> 3) * 2 + (lane() & 1); }
-    __device__ __forceinline__ static int row() { return (threadIdx.x >> 5) * 8 + ((lane() >> 1) & 3); }
-    // the lane that has piece p of this lane's rows
-    __device__ __forceinline__ static int lane_of(int p) { return (lane() & 6) | ((p >> 1) << 3) | (p & 1); }
+    __device__ __forceinline__ int chunk() const { return (lane >> 4) * 2 + (lane & 1); }
+    __device__ __forceinline__ int row() const { return warp * 16 + ((lane >> 1) & 7); }
+    // the lane that has chunk i of this lane's rows
+    __device__ __forceinline__ int lane_of(int i) const { return (lane & 0x0E) | ((i >> 1) << 4) | (i & 1); }
 
-    __device__ __forceinline__ Producer(const Fp4TileArgs& a_, Fp4TileShared& s_, uint8_t* kv_s, int t_, int e_beg,
-                                        int e_end_, int ntiles_, int64_t first_row)
-        : a(a_), s(s_), tile(tc::smem_u32(kv_s) + row() * 128), row0((int)first_row), t(t_), e_end(e_end_),
+    // warp: 0 .. 7; first_row: row of the sequence's entry 0 in the cache
+    __device__ __forceinline__ Producer(const Fp4TileArgs& a_, Fp4TileShared& s_, uint8_t* kv_s, int warp_, int t_,
+                                        int e_beg, int e_end_, int ntiles_, int64_t first_row)
+        : a(a_), s(s_), warp(warp_), lane(threadIdx.x & 31), row0((int)first_row), t(t_), e_end(e_end_),
           ntiles(ntiles_) {
+        tile = tc::smem_u32(kv_s) + row() * 128;
         e0 = e_beg + row();
         next[0] = entry(0, 0);
         next[1] = entry(0, 1);
@@ -107,8 +104,8 @@ struct Producer {
     }
     // entry index of row r in tile j (outside [0, Nmax): none)
     __device__ __forceinline__ int entry(int j, int r) const {
-        if (j >= ntiles || e_end - e0 <= j * kE + 4 * r) return -1;
-        const int e = e0 + j * kE + 4 * r;
+        if (j >= ntiles || e_end - e0 <= j * kE + 8 * r) return -1;
+        const int e = e0 + j * kE + 8 * r;
         return kSparse ? __ldg(a.idx + (int64_t)t * a.k + e) : e;
     }
     // All of a tile's loads, issued together right after the tile before it
@@ -123,31 +120,35 @@ struct Producer {
             const bool ok = cur[r] >= 0;
             const uint8_t* p = a.kv4 + (int64_t)cur[r] * a.f.bytes;
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                raw[r][g] = make_uint4(0, 0, 0, 0);
-                if (ok && 8 * g + piece() < a.f.Q / 32) raw[r][g] = __ldg(reinterpret_cast<const uint4*>(p) + 8 * g + piece());
+            for (int i = 0; i < kPairs; ++i) {
+                raw[r][i] = make_uint4(0, 0, 0, 0);
+                if (ok && 4 * i + chunk() < a.f.Q / 32) raw[r][i] = __ldg(reinterpret_cast<const uint4*>(p) + 4 * i + chunk());
             }
-            scales[r] = 0x20202020u;                      // every byte 32, the exponent among them
-            if (ok && piece() * 4 < a.f.rope_off - a.f.scale_off)
-                scales[r] = __ldg(reinterpret_cast<const uint32_t*>(p + a.f.scale_off) + piece());
-            rope[r] = make_uint4(0, 0, 0, 0);
-            if (ok && piece() < a.f.R / 8) rope[r] = __ldg(reinterpret_cast<const uint4*>(p + a.f.rope_off) + piece());
+            scales[r] = make_uint2(0x20202020u, 0x20202020u);   // every byte 32, the exponent among them
+            if (ok && chunk() * 8 < a.f.rope_off - a.f.scale_off)
+                scales[r] = __ldg(reinterpret_cast<const uint2*>(p + a.f.scale_off) + chunk());
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                rope[r][u] = make_uint4(0, 0, 0, 0);
+                if (ok && 4 * u + chunk() < a.f.R / 8)
+                    rope[r][u] = __ldg(reinterpret_cast<const uint4*>(p + a.f.rope_off) + 4 * u + chunk());
+            }
             if (ok)
-                for (int n = 8 + piece(); n < a.f.R / 8; n += 8) prefetch_l2(p + a.f.rope_off + n * 16);
+                for (int n = 8 + chunk(); n < a.f.R / 8; n += 4) prefetch_l2(p + a.f.rope_off + n * 16);
         }
     }
     // where channels d .. d+7 of row r are stored
     __device__ __forceinline__ uint32_t at(int d, int r) const {
-        return tile + (d >> 6) * kBlockBytes + r * 512 + ((((d >> 3) & 7) ^ ((row() + 4 * r) & 7)) << 4);
+        return tile + (d >> 6) * kBlockBytes + r * 1024 + ((((d >> 3) & 7) ^ (row() & 7)) << 4);
     }
     // stores tile j, then loads tile j + 1; false when a wait ran out
     __device__ __forceinline__ bool store(int j) {
-        const int last = last_early_group(a), nq = a.f.Q / 16;
+        const int last = last_early_pair(a), nq = a.f.Q / 16;
         uint32_t base[2], post[2];
         bool large = false;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            uint32_t E = __shfl_sync(0xffffffffu, scales[r], lane_of((nq >> 2) & 7));
+            uint32_t E = __shfl_sync(0xffffffffu, nq & 4 ? scales[r].y : scales[r].x, lane_of((nq >> 3) & 3));
             E = (E >> (8 * (nq & 3))) & 255u;
             // (without rotary channels it lies past the 32 bytes that are kept)
             if (nq == 32) E = cur[r] >= 0 ? __ldg(a.kv4 + (int64_t)cur[r] * a.f.bytes + a.f.scale_off + 32) : 32;
@@ -160,22 +161,24 @@ struct Producer {
         large = __any_sync(0xffffffffu, large);
         bool ok = true;
 #pragma unroll
-        for (int g = kGroups - 1; g >= 0; --g) {
-            if (g >= a.groups || !ok) continue;
+        for (int i = kPairs - 1; i >= 0; --i) {
+            if (i >= a.mtiles || !ok) continue;
             if (j > 0) {                                  // tile j-1's products have read it
-                if (lane() == 0) ok = wait(&s.empty[g], (j - 1) & 1, s, a.status);
+                if (lane == 0) ok = wait(&s.empty[i], (j - 1) & 1, s, a.status);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) continue;
             }
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                // the two scales of this lane's chunk
-                const uint32_t two = __shfl_sync(0xffffffffu, scales[r], lane_of(4 * g + (piece() >> 1))) >> (16 * (piece() & 1));
-                if (8 * g + piece() < a.f.Q / 32) {
+                // the two scales of this lane's chunk in pair i
+                const uint32_t sx = __shfl_sync(0xffffffffu, scales[r].x, lane_of(i));
+                const uint32_t sy = __shfl_sync(0xffffffffu, scales[r].y, lane_of(i));
+                if (4 * i + chunk() < a.f.Q / 32) {
+                    const uint32_t two = (chunk() & 2 ? sy : sx) >> (16 * (chunk() & 1));
                     const uint32_t S0 = __byte_perm(base[r] + ((two & 255u) << 4), 0, 0x1010);
                     const uint32_t S1 = __byte_perm(base[r] + ((two >> 4) & 0xff0u), 0, 0x1010);
-                    const uint32_t w[4] = {raw[r][g].x, raw[r][g].y, raw[r][g].z, raw[r][g].w};
-                    const uint32_t dst = at(256 * g + 32 * piece(), r);
+                    const uint32_t w[4] = {raw[r][i].x, raw[r][i].y, raw[r][i].z, raw[r][i].w};
+                    const uint32_t dst = at(128 * i + 32 * chunk(), r);
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         uint32_t o[4];
@@ -187,30 +190,33 @@ struct Producer {
                         st_shared16(dst ^ (u << 4), make_uint4(o[0], o[1], o[2], o[3]));
                     }
                 }
-                if (256 * (g + 1) > a.f.Q) {
-                    const int d = a.f.Q + piece() * 8;
-                    if (piece() < a.f.R / 8 && d >> 8 == g) st_shared16(at(d, r), rope[r]);
-                    if (g > last)
-                        for (int n = 8 + piece(); n < a.f.R / 8; n += 8) {
-                            const int dn = a.f.Q + n * 8;
-                            if (dn >> 8 != g) continue;
-                            if (cur[r] >= 0) cp_async16(at(dn, r), a.kv4 + (int64_t)cur[r] * a.f.bytes + a.f.rope_off + n * 16);
-                            else st_shared16(at(dn, r), make_uint4(0, 0, 0, 0));
+                if (128 * (i + 1) > a.f.Q) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int d = a.f.Q + (4 * u + chunk()) * 8;
+                        if (4 * u + chunk() < a.f.R / 8 && d >> 7 == i) st_shared16(at(d, r), rope[r][u]);
+                    }
+                    if (i > last)
+                        for (int n = 8 + chunk(); n < a.f.R / 8; n += 4) {
+                            const int d = a.f.Q + n * 8;
+                            if (d >> 7 != i) continue;
+                            if (cur[r] >= 0) cp_async16(at(d, r), a.kv4 + (int64_t)cur[r] * a.f.bytes + a.f.rope_off + n * 16);
+                            else st_shared16(at(d, r), make_uint4(0, 0, 0, 0));
                         }
                 }
             }
-            if (g <= last) {
+            if (i <= last) {
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane() == 0) tc::mbar_arrive(&s.full[g]);
+                if (lane == 0) tc::mbar_arrive(&s.full[i]);
             }
         }
-        if (last + 1 < a.groups) {
+        if (last + 1 < a.mtiles) {
             cp_async_wait_all();
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (lane() == 0 && ok)
-                for (int g = a.groups - 1; g > last; --g) tc::mbar_arrive(&s.full[g]);
+            if (lane == 0 && ok)
+                for (int i = a.mtiles - 1; i > last; --i) tc::mbar_arrive(&s.full[i]);
         }
         if (j + 1 < ntiles) load(j + 1);
         return ok;

@@ -16,17 +16,14 @@
 // so the result does not depend on when it moves. P is rounded to bf16 for
 // the second product; the sums, maxima and O stay fp32.
 //
-// 16 worker warps do both the expansion and the softmax, which cannot overlap
-// for one tile buffer (the expansion of tile j+1 needs blocks that the O
-// product of tile j has read, the softmax of tile j+1 needs its S product).
-//   expansion: warp w has rows 8 w .. 8 w + 7; the next tile's codes are in
-//     registers by the time a block is free;
-//   softmax and epilogue: warp w works on TMEM lanes 32 (w % 4).. and heads
-//     16 (w / 4)...
-// Warp 16 issues the S products, warp 17 the O products. Blocks go back and
-// forth in groups of 256 dims (two M tiles of the O product), the last first,
-// so expansion and S product of tile j+1 begin while the O product of tile j
-// is still busy with the group before.
+// Warps 0-3: softmax, a thread per entry (TMEM lane) and 64 heads. Warps 4-11:
+// producers, with the next tile's codes in registers by the time a block is
+// free. Warp 12 issues the S products, warp 13 the O products. Blocks go back
+// and forth in pairs (128 dims, one M tile of the O product), the last first,
+// so expansion and S product of tile j+1 run while the O product of tile j is
+// still busy with the pairs before. 14 warps leave each thread 128 registers:
+// loaded codes that spill are waited for at once (with 18 warps and 96
+// registers a tile took 10500 cycles).
 //
 // Entries outside the query's set are stored as zeros and get weight 0: no
 // row that the query does not see is read.
@@ -44,6 +41,7 @@ namespace {
 
 using namespace fp4_tile;
 
+constexpr int kThreads = 448;           // 4 softmax warps, 8 producers, 2 issuers
 constexpr int kMaxCluster = 8;
 constexpr float kMoveLog2 = 8.0f, kLn2 = 0.6931471805599453f;
 
@@ -63,7 +61,8 @@ struct Args : Fp4TileArgs {
 };
 
 struct Shared : Fp4TileShared {
-    float mref[kHg], mexp[kHg];               // reference maximum; the same, 0 for none
+    // the heads' reference maxima; the same plus 8; the same, 0 for none
+    float mref[kHg], limit[kHg], mexp[kHg];
     float alpha[kHg], lsum[kHg];
     float red[4][kHg];
     float coef[kMaxCluster][kHg];
@@ -78,21 +77,21 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
     return v;
 }
 
-// barrier (and vote) of the 4 warps that share 16 heads
-__device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
-__device__ __forceinline__ bool group_any(int g, bool v) {
+// barrier (and vote) of the softmax warps
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool v) {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p, q;\n\t"
                  "setp.ne.u32 q, %1, 0;\n\t"
-                 "bar.red.or.pred p, %2, 128, q;\n\t"
+                 "bar.red.or.pred p, 1, 128, q;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(r) : "r"((uint32_t)v), "r"(1 + g) : "memory");
+                 : "=r"(r) : "r"((uint32_t)v) : "memory");
     return r != 0;
 }
 
 // v[i] of 32 lanes -> in lane l every lane's v[l / 2] combined (16 shuffles)
 template <typename Op>
-__device__ __forceinline__ float lanes_reduce16(float (&v)[kGh], int lane, Op op) {
+__device__ __forceinline__ float lanes_reduce16(float* v, int lane, Op op) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int o = 16 >> r, n = 8 >> r;
@@ -131,20 +130,20 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     const int ntiles = e_end > e_beg ? (int)((e_end - e_beg + kE - 1) / kE) : 0;
 
     if (tid == 0) {
-        for (int i = 0; i < kGroups; ++i) {
-            tc::mbar_init(&s.full[i], kWorkers / 32);
+        for (int i = 0; i < kPairs; ++i) {
+            tc::mbar_init(&s.full[i], kProducers / 32);
             tc::mbar_init(&s.empty[i], 1);
         }
         tc::mbar_init(&s.s_full, 1);
         tc::mbar_init(&s.q_full, 1);
-        tc::mbar_init(&s.p_full, kWorkers / 32);
+        tc::mbar_init(&s.p_full, 4);
         tc::mbar_init(&s.o_done, 1);
         tc::mbar_init(&s.fin[0], 1);
         tc::mbar_init(&s.fin[1], 1);
         tc::fence_mbar_init();
         s.abort = 0;
     }
-    if (warp == 16) {
+    if (warp == 12) {
         tc::tmem_alloc(&s.tmem, a.tmem_cols);
         tc::tmem_relinquish();
         tc::tc_fence_before();
@@ -153,28 +152,28 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     tc::tc_fence_after();
     const uint32_t tmem_S = s.tmem, tmem_O = s.tmem + kHg;
 
-    if (warp >= 16) {
+    if (warp >= 12) {
         // ------------------------------------------------------------ products
         if (lane == 0 && ntiles > 0) {
             const uint32_t kv_addr = tc::smem_u32(kv_s), q_addr = tc::smem_u32(q_s), p_addr = tc::smem_u32(p_s);
-            if (warp == 16) {
+            if (warp == 12) {
                 tc::mbar_expect_tx(&s.q_full, (uint32_t)a.dblocks * kHg * 128);
                 for (int b = 0; b < a.dblocks; ++b)
                     tc::tma_load_2d(q_s + (size_t)b * kHg * 128, &tmQ, &s.q_full, b * 64, t * a.H + h0);
                 bool ok = wait(&s.q_full, 0, s, a.status);
                 const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
                 for (int j = 0; ok && j < ntiles; ++j) {
-                    for (int n = 0; n < a.groups; ++n) {
-                        const int gr = stored_group(a, n);
-                        if (!(ok = wait(&s.full[gr], j & 1, s, a.status))) break;
+                    for (int n = 0; n < a.mtiles; ++n) {
+                        const int i = stored_pair(a, n);
+                        if (!(ok = wait(&s.full[i], j & 1, s, a.status))) break;
                         tc::tc_fence_after();
-                        const int b_end = 4 * gr + 4 < a.dblocks ? 4 * gr + 4 : a.dblocks;
-                        for (int b = 4 * gr; b < b_end; ++b)
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                tc::umma_bf16(tmem_S, tc::sdesc_sw128(kv_addr + b * kBlockBytes + kk * 32, 16, 1024),
-                                              tc::sdesc_sw128(q_addr + b * (kHg * 128) + kk * 32, 16, 1024), idesc,
-                                              (n || b > 4 * gr || kk) ? 1u : 0u);
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const int b = 2 * i + (kk >> 2);
+                            tc::umma_bf16(tmem_S, tc::sdesc_sw128(kv_addr + b * kBlockBytes + (kk & 3) * 32, 16, 1024),
+                                          tc::sdesc_sw128(q_addr + b * (kHg * 128) + (kk & 3) * 32, 16, 1024), idesc,
+                                          (n | kk) ? 1u : 0u);
+                        }
                     }
                     if (ok) tc::umma_commit(&s.s_full);
                 }
@@ -191,33 +190,35 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                                           tc::sdesc_sw128(kv_addr + 2 * mt * kBlockBytes + ke * 2048, kBlockBytes, 1024),
                                           tc::sdesc_sw128(p_addr + ke * 2048, kE * 128, 1024), idesc,
                                           (j > 0 || ke > 0) ? 1u : 0u);
-                        if (!(mt & 1)) tc::umma_commit(&s.empty[mt >> 1]);
+                        tc::umma_commit(&s.empty[mt]);
                     }
                     tc::umma_commit(&s.o_done);
                 }
             }
             // every product this thread issued has ended before the CTA goes
             // on to free the memory it uses (also when a wait ran out)
-            tc::umma_commit(&s.fin[warp - 16]);
-            tc::mbar_wait(&s.fin[warp - 16], 0, kWaitLimit);
+            tc::umma_commit(&s.fin[warp - 12]);
+            tc::mbar_wait(&s.fin[warp - 12], 0, kWaitLimit);
         }
         __syncwarp();
+    } else if (warp >= 4) {
+        Producer<kSparse> producer(a, s, kv_s, warp - 4, t, (int)e_beg, (int)e_end, ntiles, (ntiles ? seq : 0) * a.Nmax);
+        for (int j = 0; j < ntiles; ++j)
+            if (!producer.store(j)) break;
     } else {
-        // ------------------------------------------------------------ workers
-        const int quad = warp & 3, g = warp >> 2, hb = g * kGh;
-        const int row = quad * 32 + lane;                 // entry of the tile / dim of an M tile
-        const int gth = tid & 127;
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        Producer<kSparse> producer(a, s, kv_s, t, (int)e_beg, (int)e_end, ntiles,
-                                   (ntiles ? seq : 0) * a.Nmax);
-        if (gth < kGh) { s.mref[hb + gth] = -INFINITY; s.mexp[hb + gth] = s.lsum[hb + gth] = 0.f; }
-        float lpart[kGh];
+        // ------------------------------------------------------------ softmax
+        const int row = tid;                              // entry of the tile, TMEM lane
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        if (tid < kHg) {
+            s.mref[tid] = s.limit[tid] = -INFINITY;
+            s.mexp[tid] = 0.f;
+        }
+        float lpart[kHg];
 #pragma unroll
-        for (int i = 0; i < kGh; ++i) lpart[i] = 0.f;
-        group_sync(g);
+        for (int i = 0; i < kHg; ++i) lpart[i] = 0.f;
+        softmax_sync();
         bool ok = true;
         for (int j = 0; j < ntiles; ++j) {
-            ok = producer.store(j) && ok;
             const int64_t e = e_beg + (int64_t)j * kE + row;
             bool valid = e < e_end;
             if (kSparse && valid) {
@@ -226,84 +227,93 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             }
             ok = ok && wait(&s.s_full, j & 1, s, a.status);
             tc::tc_fence_after();
-            float z[kGh];
-            auto logits = [&]() {
-                tc::tmem_ld16(tmem_S + lanes + hb, z);
-                tc::tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < kGh; ++i) z[i] = valid ? z[i] * a.scale_log2 : -INFINITY;
-            };
-            logits();
             bool move = false;
 #pragma unroll
-            for (int i = 0; i < kGh; ++i) move |= z[i] > s.mref[hb + i] + kMoveLog2;
-            if (group_any(g, move || !ok)) {
-                // all leave together once a wait of one ran out
-                if (group_any(g, !ok)) { ok = false; break; }
-                // (the reduction consumes the logits; they are read again)
-                const float top = lanes_reduce16(z, lane, [](float x, float y) { return fmaxf(x, y); });
-                if (!(lane & 1)) s.red[quad][hb + lane / 2] = top;
-                group_sync(g);
-                if (gth < kGh) {
-                    const int h = hb + gth;
-                    const float old = s.mref[h];
-                    const float m = fmaxf(fmaxf(fmaxf(s.red[0][h], s.red[1][h]), fmaxf(s.red[2][h], s.red[3][h])), old);
-                    s.alpha[h] = old == -INFINITY ? 0.f : ex2(old - m);
-                    s.mref[h] = m;
-                    s.mexp[h] = m == -INFINITY ? 0.f : m;
-                }
-                group_sync(g);
+            for (int cc = 0; cc < kHg; cc += 16) {
+                float z[16];
+                tc::tmem_ld16(tmem_S + lanes + cc, z);
+                tc::tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < kGh; ++i) lpart[i] *= s.alpha[hb + i];
+                for (int i = 0; i < 16; ++i) move |= z[i] * a.scale_log2 > s.limit[cc + i];
+            }
+            if (softmax_any((move && valid) || !ok)) {
+                // all leave together once a wait of one ran out
+                if (softmax_any(!ok)) { ok = false; break; }
+#pragma unroll
+                for (int cc = 0; cc < kHg; cc += 16) {
+                    float z[16];
+                    tc::tmem_ld16(tmem_S + lanes + cc, z);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) z[i] = valid ? z[i] * a.scale_log2 : -INFINITY;
+                    const float top = lanes_reduce16(z, lane, [](float x, float y) { return fmaxf(x, y); });
+                    if (!(lane & 1)) s.red[warp][cc + lane / 2] = top;
+                }
+                softmax_sync();
+                if (tid < kHg) {
+                    const float old = s.mref[tid];
+                    const float m = fmaxf(fmaxf(fmaxf(s.red[0][tid], s.red[1][tid]), fmaxf(s.red[2][tid], s.red[3][tid])), old);
+                    s.alpha[tid] = old == -INFINITY ? 0.f : ex2(old - m);
+                    s.mref[tid] = m;
+                    s.limit[tid] = m + kMoveLog2;
+                    s.mexp[tid] = m == -INFINITY ? 0.f : m;
+                }
+                softmax_sync();
+#pragma unroll
+                for (int i = 0; i < kHg; ++i) lpart[i] *= s.alpha[i];
                 if (j > 0) {
                     ok = wait(&s.o_done, (j - 1) & 1, s, a.status);
                     tc::tc_fence_after();
 #pragma unroll 1
-                    for (int mt = 0; mt < a.mtiles; ++mt) {
-                        float o[kGh];
-                        const uint32_t addr = tmem_O + lanes + mt * kHg + hb;
-                        tc::tmem_ld16(addr, o);
+                    for (int cc = 0; cc < a.mtiles * kHg; cc += 16) {
+                        float o[16];
+                        tc::tmem_ld16(tmem_O + lanes + cc, o);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < kGh; ++i) o[i] *= s.alpha[hb + i];
-                        tc::tmem_st16(addr, o);
+                        for (int i = 0; i < 16; ++i) o[i] *= s.alpha[(cc & (kHg - 1)) + i];
+                        tc::tmem_st16(tmem_O + lanes + cc, o);
                     }
                     tc::tmem_st_wait();
                 }
-                logits();
-            }
-            uint32_t pk[kGh / 2];
-#pragma unroll
-            for (int i = 0; i < kGh; i += 2) {
-                const float p0 = ex2(z[i] - s.mexp[hb + i]), p1 = ex2(z[i + 1] - s.mexp[hb + i + 1]);
-                lpart[i] += p0;
-                lpart[i + 1] += p1;
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
-                pk[i >> 1] = *reinterpret_cast<const uint32_t*>(&b2);
             }
             // the previous tile's O product has read P
             if (j > 0) ok = wait(&s.o_done, (j - 1) & 1, s, a.status) && ok;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                *reinterpret_cast<uint4*>(p_s + row * 128 + (((g * 2 + i) ^ (row & 7)) << 4)) =
-                    make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+            for (int cc = 0; cc < kHg; cc += 16) {
+                float z[16];
+                tc::tmem_ld16(tmem_S + lanes + cc, z);
+                tc::tmem_ld_wait();
+                uint32_t pk[8];
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float p0 = ex2(valid ? fmaf(z[i], a.scale_log2, -s.mexp[cc + i]) : -INFINITY);
+                    const float p1 = ex2(valid ? fmaf(z[i + 1], a.scale_log2, -s.mexp[cc + i + 1]) : -INFINITY);
+                    lpart[cc + i] += p0;
+                    lpart[cc + i + 1] += p1;
+                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
+                    pk[i >> 1] = *reinterpret_cast<const uint32_t*>(&b2);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    *reinterpret_cast<uint4*>(p_s + row * 128 + (((cc / 8 + i) ^ (row & 7)) << 4)) =
+                        make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+            }
             tc::tc_fence_before();                        // S has been read, too
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&s.p_full);
         }
-        // ------------------------------------------------------------ epilogue
-        if (ok && ntiles > 0) ok = wait(&s.o_done, (ntiles - 1) & 1, s, a.status);
-        tc::tc_fence_after();
+        if (ok && ntiles > 0) wait(&s.o_done, (ntiles - 1) & 1, s, a.status);
         // per-head sums in a fixed order: lanes, then the four warps
-        group_sync(g);                                    // red may still be read
-        {
-            const float sum = lanes_reduce16(lpart, lane, [](float x, float y) { return x + y; });
-            if (!(lane & 1)) s.red[quad][hb + lane / 2] = sum;
+        softmax_sync();                                   // red may still be read
+#pragma unroll
+        for (int cc = 0; cc < kHg; cc += 16) {
+            const float sum = lanes_reduce16(lpart + cc, lane, [](float x, float y) { return x + y; });
+            if (!(lane & 1)) s.red[warp][cc + lane / 2] = sum;
         }
-        group_sync(g);
-        if (gth < kGh) {
-            const int h = hb + gth;
+        softmax_sync();
+        if (tid < kHg) {
+            const int h = tid;
             s.lsum[h] = (s.red[0][h] + s.red[1][h]) + (s.red[2][h] + s.red[3][h]);
             if (a.merge == kDirect) {
                 const float m = s.mref[h], L = s.lsum[h];
@@ -317,34 +327,35 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                     a.lse[(int64_t)t * a.H + h0 + h] = Lt == 0.f ? -INFINITY : fmaf(M, kLn2, logf(Lt));
             }
         }
-        group_sync(g);
-        if (a.merge == kDirect) {
-            // normalised rows, staged as [head][dim] bf16 where the tile was
-            bf16* stage = reinterpret_cast<bf16*>(kv_s) + (size_t)hb * a.f.c + row;
-            float al[kGh];
-#pragma unroll
-            for (int i = 0; i < kGh; ++i) al[i] = s.alpha[hb + i];
+        tc::tc_fence_before();
+    }
+    // ---------------------------------------------------------------- epilogue
+    __syncthreads();
+    if (warp < 8) {
+        // O^T to shared memory where the tile was, as rows of a head: warp w
+        // has dims 32 (w % 4).. of every M tile and 32 heads
+        tc::tc_fence_after();
+        const int hb = (warp >> 2) * 32, row = (warp & 3) * 32 + lane;
+        const uint32_t addr = tmem_O + ((uint32_t)((warp & 3) * 32) << 16) + hb;
 #pragma unroll 1
-            for (int mt = 0; mt < a.mtiles; ++mt) {
-                float o[kGh];
-                if (ntiles > 0) {
-                    tc::tmem_ld16(tmem_O + lanes + mt * kHg + hb, o);
-                    tc::tmem_ld_wait();
-                }
-#pragma unroll
-                for (int i = 0; i < kGh; ++i)
-                    stage[(size_t)i * a.f.c + mt * 128] = __float2bfloat16_rn(al[i] != 0.f ? o[i] * al[i] : 0.f);
-            }
-        } else if (ntiles > 0) {
-            // O^T staged as [head][dim] fp32 where the tile was
-            float* stage = reinterpret_cast<float*>(kv_s) + (size_t)hb * a.f.c + row;
-#pragma unroll 1
-            for (int mt = 0; mt < a.mtiles; ++mt) {
-                float o[kGh];
-                tc::tmem_ld16(tmem_O + lanes + mt * kHg + hb, o);
+        for (int n = 0; n < 2 * a.mtiles; ++n) {
+            const int mt = n >> 1, cc = (n & 1) * 16, d = mt * 128 + row;
+            float o[16];
+            if (ntiles > 0) {
+                tc::tmem_ld16(addr + mt * kHg + cc, o);
                 tc::tmem_ld_wait();
+            }
+            if (a.merge == kDirect) {                     // normalised, bf16
+                bf16* stage = reinterpret_cast<bf16*>(kv_s) + (size_t)(hb + cc) * a.f.c + d;
 #pragma unroll
-                for (int i = 0; i < kGh; ++i) stage[(size_t)i * a.f.c + mt * 128] = o[i];
+                for (int i = 0; i < 16; ++i) {
+                    const float al = s.alpha[hb + cc + i];
+                    stage[(size_t)i * a.f.c] = __float2bfloat16_rn(al != 0.f ? o[i] * al : 0.f);
+                }
+            } else if (ntiles > 0) {
+                float* stage = reinterpret_cast<float*>(kv_s) + (size_t)(hb + cc) * a.f.c + d;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) stage[(size_t)i * a.f.c] = o[i];
             }
         }
         tc::tc_fence_before();
@@ -425,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         }
         __syncthreads();
     }
-    if (warp == 16) {
+    if (warp == 12) {
         tc::tc_fence_after();
         tc::tmem_dealloc(s.tmem, a.tmem_cols);
     }
@@ -485,7 +496,6 @@ cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {
     a.merge = merge_of(x.nq, x.H, ns);
     a.dblocks = x.c / 64;
     a.mtiles = x.c / 128;
-    a.groups = (x.c + 255) / 256;
     a.tmem_cols = kHg * (1 + a.mtiles) <= 128 ? 128 : kHg * (1 + a.mtiles) <= 256 ? 256 : 512;
     a.scale_log2 = x.scale * kLog2e;
     CUtensorMap tmQ;

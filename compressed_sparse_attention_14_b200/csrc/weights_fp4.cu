@@ -4,19 +4,17 @@
 //
 // The logits are the attention's S^T = V_tile . q^T product (128 entries x 64
 // heads, K = c; mqa_fp4.cu) without the second product: entries are the lanes
-// of the result, so a thread sums the weights of its entry over 16 heads in
-// registers and four threads' sums meet in shared memory. Bound by reading the
-// packed rows; what paces it is expanding them for the product.
+// of the result, and a thread sums the weights of its entry over 64 heads.
+// Bound by reading the packed rows; what paces it is expanding them.
 //
 // A CTA walks a run of tiles of one sequence (or of one query's entry list).
 // Each tile stays in shared memory for all query blocks (query, 64 heads) of
-// its sequence; their q blocks stream through one buffer, refilled in halves
+// its sequence; their q blocks stream through one buffer, refilled in quarters
 // as the product has read them, unless there is only one, which stays. The
-// next tile is expanded while the last query block's product runs. Every sum
-// has a fixed order: heads, then queries, within a thread, then the four
-// threads.
+// next tile is expanded as the last query block's product releases the blocks.
+// Every sum has a fixed order: heads, then queries.
 //
-// Warps 0-15: expansion and sums; 16: products; 17: query loads.
+// Warps 0-3: sums; 4-11: producers; 12: products; 13: query loads.
 #include "fp4_tile.cuh"
 #include "kernels.h"
 #include "tmap.h"
@@ -26,6 +24,8 @@ namespace csa {
 namespace {
 
 using namespace fp4_tile;
+
+constexpr int kThreads = 448;           // 4 summing warps, 8 producers, products, query loads
 
 struct Args : Fp4TileArgs {
     const float* lse;
@@ -38,9 +38,8 @@ struct Args : Fp4TileArgs {
 };
 
 struct Shared : Fp4TileShared {
-    float lse[kWorkers / 32][kGh];            // the query block's, per warp
-    float part[kWorkers / 128][kE];
-    uint64_t q_full[kGroups], q_empty[kGroups], s_full[2], s_empty[2], fin;
+    float lse[4][kHg];                        // the query block's, per warp
+    uint64_t q_full[kPairs], q_empty[kPairs], s_full[2], s_empty[2], fin;
     uint32_t tmem;
     int n_max;
 };
@@ -78,22 +77,22 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
     const int e_beg = blockIdx.x * a.run * kE, n_all = kSparse ? a.k : (int)a.Nmax;
     const int e_stop = (int64_t)a.run * kE > n_all - e_beg ? n_all : e_beg + a.run * kE;   // this CTA's entries
     if (tid == 0) {
-        for (int i = 0; i < kGroups; ++i) {
-            tc::mbar_init(&s.full[i], kWorkers / 32);
+        for (int i = 0; i < kPairs; ++i) {
+            tc::mbar_init(&s.full[i], kProducers / 32);
             tc::mbar_init(&s.empty[i], 1);
             tc::mbar_init(&s.q_full[i], 1);
             tc::mbar_init(&s.q_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&s.s_full[i], 1);
-            tc::mbar_init(&s.s_empty[i], kWorkers / 32);
+            tc::mbar_init(&s.s_empty[i], 4);
         }
         tc::mbar_init(&s.fin, 1);
         tc::fence_mbar_init();
         s.abort = 0;
         s.n_max = 0;
     }
-    if (warp == 16) {
+    if (warp == 12) {
         tc::tmem_alloc(&s.tmem, 128);
         tc::tmem_relinquish();
         tc::tc_fence_before();
@@ -113,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
     const uint32_t tmem_S = s.tmem;
     const bool stay = a.T * a.hgroups == 1;
 
-    if (warp == 17) {
+    if (warp == 13) {
         // ------------------------------------------------------------ query loads
         if (lane == 0) {
             uint32_t n = 0;
@@ -123,23 +122,22 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
                 for (int t = 0; ok && t <= blocks.last_query(e_tile); ++t) {
                     if (blocks.visible(t) <= e_tile) continue;
                     for (int g = 0; ok && g < a.hgroups; ++g, ++n)
-                        for (int o = 0; o < a.groups; ++o) {
-                            const int i = stored_group(a, o);
+                        for (int o = 0; o < a.mtiles; ++o) {
+                            const int i = stored_pair(a, o);
                             if (n > 0 && !(ok = wait(&s.q_empty[i], (n - 1) & 1, s, a.status))) break;
-                            const int b_end = 4 * i + 4 < a.dblocks ? 4 * i + 4 : a.dblocks;
-                            tc::mbar_expect_tx(&s.q_full[i], (uint32_t)(b_end - 4 * i) * kHg * 128);
-                            for (int blk = 4 * i; blk < b_end; ++blk)
-                                tc::tma_load_2d(q_s + (size_t)blk * kHg * 128, &tmQ, &s.q_full[i], blk * 64,
-                                                (b * a.T + t) * a.H + g * kHg);
+                            tc::mbar_expect_tx(&s.q_full[i], 2 * kHg * 128);
+                            for (int h = 0; h < 2; ++h)
+                                tc::tma_load_2d(q_s + (size_t)(2 * i + h) * kHg * 128, &tmQ, &s.q_full[i],
+                                                (2 * i + h) * 64, (b * a.T + t) * a.H + g * kHg);
                         }
                 }
             }
-            // the last copies of each group have landed
+            // the last copies of each pair have landed
             if (n > 0)
-                for (int i = 0; i < a.groups; ++i) tc::mbar_wait(&s.q_full[i], (n - 1) & 1, ok ? kWaitLimit : 1u << 16);
+                for (int i = 0; i < a.mtiles; ++i) tc::mbar_wait(&s.q_full[i], (n - 1) & 1, ok ? kWaitLimit : 1u << 16);
         }
         __syncwarp();
-    } else if (warp == 16) {
+    } else if (warp == 12) {
         // ------------------------------------------------------------ products
         if (lane == 0 && ntiles > 0) {
             const uint32_t kv_addr = tc::smem_u32(kv_s), q_addr = tc::smem_u32(q_s);
@@ -154,19 +152,19 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
                     for (int g = 0; ok && g < a.hgroups; ++g, ++n) {
                         const uint32_t sb = n & 1;
                         if (n >= 2 && !(ok = wait(&s.s_empty[sb], ((n >> 1) - 1) & 1, s, a.status))) break;
-                        for (int o = 0; o < a.groups; ++o) {
-                            const int i = stored_group(a, o);
+                        for (int o = 0; o < a.mtiles; ++o) {
+                            const int i = stored_pair(a, o);
                             if (!(ok = wait(&s.q_full[i], stay ? 0 : n & 1, s, a.status))) break;
                             if (first && !(ok = wait(&s.full[i], j & 1, s, a.status))) break;
                             tc::tc_fence_after();
-                            const int b_end = 4 * i + 4 < a.dblocks ? 4 * i + 4 : a.dblocks;
-                            for (int blk = 4 * i; blk < b_end; ++blk)
 #pragma unroll
-                                for (int kk = 0; kk < 4; ++kk)
-                                    tc::umma_bf16(tmem_S + sb * kHg,
-                                                  tc::sdesc_sw128(kv_addr + blk * kBlockBytes + kk * 32, 16, 1024),
-                                                  tc::sdesc_sw128(q_addr + blk * (kHg * 128) + kk * 32, 16, 1024),
-                                                  idesc, (o || blk > 4 * i || kk) ? 1u : 0u);
+                            for (int kk = 0; kk < 8; ++kk) {
+                                const int blk = 2 * i + (kk >> 2);
+                                tc::umma_bf16(tmem_S + sb * kHg,
+                                              tc::sdesc_sw128(kv_addr + blk * kBlockBytes + (kk & 3) * 32, 16, 1024),
+                                              tc::sdesc_sw128(q_addr + blk * (kHg * 128) + (kk & 3) * 32, 16, 1024),
+                                              idesc, (o | kk) ? 1u : 0u);
+                            }
                             if (!stay) tc::umma_commit(&s.q_empty[i]);
                             if (t == last && g == a.hgroups - 1) tc::umma_commit(&s.empty[i]);
                         }
@@ -179,72 +177,65 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
             tc::mbar_wait(&s.fin, 0, kWaitLimit);
         }
         __syncwarp();
+    } else if (warp >= 4) {
+        Producer<kSparse> producer(a, s, kv_s, warp - 4, b, e_beg, e_end, ntiles, (int64_t)(ntiles ? seq : 0) * a.Nmax);
+        for (int j = 0; j < ntiles; ++j)
+            if (!producer.store(j)) break;
     } else {
-        // ------------------------------------------------------------ workers
-        const int quad = warp & 3, grp = warp >> 2, hb = grp * kGh;
-        const int row = quad * 32 + lane;                 // entry of the tile
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        Producer<kSparse> producer(a, s, kv_s, b, e_beg, e_end, ntiles, (int64_t)(ntiles ? seq : 0) * a.Nmax);
+        // ------------------------------------------------------------ sums
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         uint32_t n = 0;
         bool ok = true;
-        if (ntiles > 0) ok = producer.store(0);
         for (int j = 0; j < ntiles; ++j) {
-            const int e_tile = e_beg + j * kE, last = blocks.last_query(e_tile), e = e_tile + row;
-            int entry = e < e_end ? e : -1;
-            if (kSparse && entry >= 0) {
-                const int v = __ldg(a.idx + (int64_t)b * a.k + e);
-                entry = v < a.Nmax ? v : -1;
-            }
+            const int e_tile = e_beg + j * kE, last = blocks.last_query(e_tile), e = e_tile + tid;
             float w = 0.f;
             for (int t = 0; t <= last; ++t) {
                 const int seen = blocks.visible(t);
                 if (seen <= e_tile) continue;
                 for (int g = 0; g < a.hgroups; ++g, ++n) {
-                    // the next tile's expansion goes with this tile's last product
-                    if (t == last && g == a.hgroups - 1 && j + 1 < ntiles) ok = producer.store(j + 1) && ok;
-                    // lse of this warp's heads (+inf: adds nothing)
-                    if (lane < kGh) {
-                        const int h = g * kHg + hb + lane;
+                    // lse of the heads (+inf: adds nothing)
+#pragma unroll
+                    for (int i = lane; i < kHg; i += 32) {
+                        const int h = g * kHg + i;
                         const float l = h < a.H ? a.lse[((int64_t)b * a.T + t) * a.H + h] : INFINITY;
-                        s.lse[warp][lane] = l == -INFINITY ? INFINITY : l * kLog2e;
+                        s.lse[warp][i] = l == -INFINITY ? INFINITY : l * kLog2e;
                     }
                     __syncwarp();
                     const uint32_t sb = n & 1;
                     ok = ok && wait(&s.s_full[sb], (n >> 1) & 1, s, a.status);
                     tc::tc_fence_after();
-                    float z[kGh];
-                    tc::tmem_ld16(tmem_S + lanes + sb * kHg + hb, z);
-                    tc::tmem_ld_wait();
-                    tc::tc_fence_before();
                     float p = 0.f;
 #pragma unroll
-                    for (int i = 0; i < kGh; ++i) {
-                        const float l = s.lse[warp][i];
-                        p += l == INFINITY ? 0.f : ex2(fmaf(z[i], a.scale_log2, -l));
+                    for (int cc = 0; cc < kHg; cc += 16) {
+                        float z[16];
+                        tc::tmem_ld16(tmem_S + lanes + sb * kHg + cc, z);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float l = s.lse[warp][cc + i];
+                            p += l == INFINITY ? 0.f : ex2(fmaf(z[i], a.scale_log2, -l));
+                        }
                     }
+                    tc::tc_fence_before();
                     if (kSparse || e < seen) w += p;
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&s.s_empty[sb]);
                 }
             }
-            s.part[grp][row] = w;
-            asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory");
-            if (grp == 0) {
-                w = (s.part[0][row] + s.part[1][row]) + (s.part[2][row] + s.part[3][row]);
-                if (entry < 0) w = 0.f;
-                if (kSparse) {
-                    if (a.weights && e < e_end) a.weights[(int64_t)b * a.k + e] = w;
-                    // (entries listed twice add twice the same value, in any order)
-                    if (a.acc && entry >= 0) atomicAdd(a.acc + (int64_t)seq * a.Nmax + entry, w);
-                } else if (e < e_end) {
-                    const int64_t i = (int64_t)b * a.Nmax + e;
-                    a.weights[i] = (a.acc ? a.acc[i] : 0.f) + w;
-                }
+            if (e >= e_end) continue;
+            if (kSparse) {
+                const int entry = __ldg(a.idx + (int64_t)b * a.k + e);
+                if (entry < 0 || entry >= a.Nmax) w = 0.f;
+                if (a.weights) a.weights[(int64_t)b * a.k + e] = w;
+                // (entries listed twice add twice the same value, in any order)
+                if (a.acc && entry >= 0 && entry < a.Nmax) atomicAdd(a.acc + (int64_t)seq * a.Nmax + entry, w);
+            } else {
+                const int64_t i = (int64_t)b * a.Nmax + e;
+                a.weights[i] = (a.acc ? a.acc[i] : 0.f) + w;
             }
-            asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory");
         }
         // entries that no query sees
-        for (int e = (e_end > e_beg ? e_end : e_beg) + tid; e < e_stop; e += kWorkers) {
+        for (int e = (e_end > e_beg ? e_end : e_beg) + tid; e < e_stop; e += 128) {
             if (kSparse) {
                 if (a.weights) a.weights[(int64_t)b * a.k + e] = 0.f;
             } else {
@@ -255,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
         tc::tc_fence_before();
     }
     __syncthreads();
-    if (warp == 16) {
+    if (warp == 12) {
         tc::tc_fence_after();
         tc::tmem_dealloc(s.tmem, 128);
     }
@@ -275,7 +266,6 @@ cudaError_t entry_weights_fp4(const Fp4WeightArgs& x, cudaStream_t st) {
     a.k = x.k;
     a.dblocks = x.c / 64;
     a.mtiles = x.c / 128;
-    a.groups = (x.c + 255) / 256;
     a.lse = x.lse;
     a.seq_of_q = x.seq_of_q;
     a.pos = x.pos;
