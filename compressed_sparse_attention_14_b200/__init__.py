@@ -13,6 +13,8 @@ dtype: bf16 tensors run the CSA_BF16 mode, fp32 tensors the CSA_FP32 mode
 from __future__ import annotations
 
 import ctypes
+import functools
+import math
 import os
 from typing import Optional
 
@@ -831,38 +833,65 @@ def csa_decode_fp8kv(qI, w, idx_cache, q, kv_codes, kv_scales, kv_rope, ctx_len,
 
 
 # ---------------------------------------------------------------- 4-bit KV
-def _arg(t: Optional[torch.Tensor], dev, dtype: torch.dtype, want: tuple, name: str):
-    """The pointer of a contiguous tensor of this dtype and shape on device dev (None: NULL)."""
+# (a small call costs the GPU 3 to 15 us: the checks below are written to take
+# the host about as long as the launch itself)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_BF, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _arg(t: Optional[torch.Tensor], index: int, dtype: torch.dtype, want: tuple, name: str):
+    """The pointer of a contiguous tensor of this dtype and shape on device `index` (None: NULL)."""
     if t is None:
         return None
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype is dtype and t.shape == want and t.is_cuda and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    if not t.is_cuda or t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != want:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(want)}")
-    return _ptr(t)
+    raise ValueError(f"{name}: libcsa takes contiguous tensors only")
 
 
-def _run_on(dev, fn, *args) -> None:
-    """Calls fn(*args, stream) on dev's current stream, with dev the current device."""
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
-        return
-    with torch.cuda.device(dev):
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+def _run_on(index: int, fn, *args) -> None:
+    """Calls fn(*args, stream) on the device's current stream, with it the current device."""
+    if index == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
+    if rc != CSA_OK:
+        _check(rc)
 
 
-def _cuda_device(t: torch.Tensor):
+def _cuda_index(t: torch.Tensor) -> int:
     if not t.is_cuda:
         raise ValueError("libcsa takes CUDA tensors only")
-    return t.device
+    return t.get_device()
+
+
+@functools.lru_cache(maxsize=256)
+def _size_of(name: str, *args) -> int:
+    return int(getattr(_lib, name)(*args))
+
+
+def _scratch(nbytes: int, index: int, ws: Optional[torch.Tensor]):
+    """(pointer, bytes, tensor kept alive by the caller) of a workspace."""
+    if nbytes == 0:
+        return None, 0, None
+    if ws is not None and (not ws.is_cuda or ws.get_device() != index):
+        raise ValueError(f"ws is on {ws.device}, expected cuda:{index}")
+    ws = _ws(nbytes, torch.device("cuda", index), ws)
+    return _ptr(ws), _nbytes(ws), ws
 
 
 def csa_fp4_row_bytes(c: int, rope_dims: int = 64) -> int:
     """Bytes of a 4-bit entry of c channels (include/csa.h has the layout)."""
-    n = int(_lib.csa_fp4_row_bytes(c, rope_dims))
+    n = _size_of("csa_fp4_row_bytes", c, rope_dims)
     if n == 0:
+        _lib.csa_fp4_row_bytes(c, rope_dims)               # (sets the message)
         raise CsaError(CSA_ERR_UNSUPPORTED, _lib.csa_last_error().decode())
     return n
 
@@ -870,44 +899,46 @@ def csa_fp4_row_bytes(c: int, rope_dims: int = 64) -> int:
 def _fp4_cache(kv4: torch.Tensor, c: int, rope_dims: int):
     """(n_seq, Nmax, row bytes) of a 4-bit cache [n_seq, Nmax, row_bytes] or, of one sequence, [Nmax, row_bytes]."""
     rb = csa_fp4_row_bytes(c, rope_dims)
-    if kv4.dim() not in (2, 3) or kv4.shape[-1] != rb:
-        raise ValueError(f"kv4 has shape {tuple(kv4.shape)}, expected (n_seq, Nmax, {rb}) for c={c} "
-                         f"rope_dims={rope_dims}")
-    return (1, kv4.shape[0], rb) if kv4.dim() == 2 else (kv4.shape[0], kv4.shape[1], rb)
+    shape = kv4.shape
+    if len(shape) == 3 and shape[2] == rb:
+        return shape[0], shape[1], rb
+    if len(shape) == 2 and shape[1] == rb:
+        return 1, shape[0], rb
+    raise ValueError(f"kv4 has shape {tuple(shape)}, expected (n_seq, Nmax, {rb}) for c={c} rope_dims={rope_dims}")
 
 
 def csa_quantize_kv_fp4(kv, rope_dims: int = 64, out=None):
     """KV entries [..., c] bf16 -> 4-bit rows [..., row_bytes] uint8: e2m1
     codes, a scale per 16 channels, the last rope_dims channels kept bf16."""
-    dev = _cuda_device(kv)
+    dev = _cuda_index(kv)
     c = kv.shape[-1]
     want = tuple(kv.shape[:-1]) + (csa_fp4_row_bytes(c, rope_dims),)
     out = torch.empty(want, dtype=torch.uint8, device=dev) if out is None else out
-    _run_on(dev, _lib.csa_quantize_kv_fp4, _arg(kv, dev, torch.bfloat16, kv.shape, "kv"), kv.numel() // c, c,
-            rope_dims, _arg(out, dev, torch.uint8, want, "out"))
+    _run_on(dev, _lib.csa_quantize_kv_fp4, _arg(kv, dev, _BF, kv.shape, "kv"), kv.numel() // c, c,
+            rope_dims, _arg(out, dev, _U8, want, "out"))
     return out
 
 
 def csa_append_kv_fp4(kv, slot, cache, rope_dims: int = 64):
     """One new entry per sequence: kv [B, c] bf16 -> row slot[b] (int32; outside
     [0, Nmax): none) of cache [B, Nmax, row_bytes], in place."""
-    dev = _cuda_device(kv)
+    dev = _cuda_index(kv)
     B, c = kv.shape
     _, Nmax, rb = _fp4_cache(cache, c, rope_dims)
-    _run_on(dev, _lib.csa_append_kv_fp4, _arg(kv, dev, torch.bfloat16, (B, c), "kv"),
-            _arg(slot, dev, torch.int32, (B,), "slot"), B, c, rope_dims,
-            _arg(cache, dev, torch.uint8, (B, Nmax, rb), "cache"), Nmax)
+    _run_on(dev, _lib.csa_append_kv_fp4, _arg(kv, dev, _BF, (B, c), "kv"),
+            _arg(slot, dev, _I32, (B,), "slot"), B, c, rope_dims,
+            _arg(cache, dev, _U8, (B, Nmax, rb), "cache"), Nmax)
     return cache
 
 
 def csa_dequantize_kv_fp4(kv4, c: int, rope_dims: int = 64, out=None):
     """The values of 4-bit rows [..., row_bytes] as bf16 [..., c] (exact)."""
-    dev = _cuda_device(kv4)
+    dev = _cuda_index(kv4)
     rb = csa_fp4_row_bytes(c, rope_dims)
     lead = tuple(kv4.shape[:-1])
     out = torch.empty(lead + (c,), dtype=torch.bfloat16, device=dev) if out is None else out
-    _run_on(dev, _lib.csa_dequantize_kv_fp4, _arg(kv4, dev, torch.uint8, lead + (rb,), "kv4"), kv4.numel() // rb, c,
-            rope_dims, _arg(out, dev, torch.bfloat16, lead + (c,), "out"))
+    _run_on(dev, _lib.csa_dequantize_kv_fp4, _arg(kv4, dev, _U8, lead + (rb,), "kv4"), kv4.numel() // rb, c,
+            rope_dims, _arg(out, dev, _BF, lead + (c,), "out"))
     return out
 
 
@@ -923,17 +954,17 @@ def csa_sparse_mqa_fp4kv(q, kv4, idx, scale: float = 0.0, sink=None, seq_of_q=No
     """csa_sparse_mqa over 4-bit entries: q [nq, H, c] bf16, kv4 [n_seq, Nmax,
     row_bytes] (csa_quantize_kv_fp4), idx [nq, k] int32 (outside [0, Nmax):
     empty). Returns (out, lse)."""
-    dev = _cuda_device(q)
+    dev = _cuda_index(q)
     nq, H, c = q.shape
     n_seq, Nmax, _ = _fp4_cache(kv4, c, rope_dims)
     k = idx.shape[-1]
     out, lse = _attn_out(q, out, lse)
-    ws = _ws(_lib.csa_sparse_mqa_fp4kv_workspace_size(nq, H, c, k), dev, ws)
-    _run_on(dev, _lib.csa_sparse_mqa_fp4kv, _arg(q, dev, torch.bfloat16, q.shape, "q"),
-            _arg(kv4, dev, torch.uint8, kv4.shape, "kv4"), _arg(idx, dev, torch.int32, (nq, k), "idx"),
-            _arg(seq_of_q, dev, torch.int32, (nq,), "seq_of_q"), nq, n_seq, H, c, rope_dims, Nmax, k, scale,
-            _arg(sink, dev, torch.float32, (H,), "sink"), _arg(out, dev, torch.bfloat16, q.shape, "out"),
-            _arg(lse, dev, torch.float32, (nq, H), "lse"), _ptr(ws), _nbytes(ws))
+    wp, wn, ws = _scratch(_size_of("csa_sparse_mqa_fp4kv_workspace_size", nq, H, c, k), dev, ws)
+    _run_on(dev, _lib.csa_sparse_mqa_fp4kv, _arg(q, dev, _BF, q.shape, "q"),
+            _arg(kv4, dev, _U8, kv4.shape, "kv4"), _arg(idx, dev, _I32, (nq, k), "idx"),
+            _arg(seq_of_q, dev, _I32, (nq,), "seq_of_q"), nq, n_seq, H, c, rope_dims, Nmax, k, scale,
+            _arg(sink, dev, _F32, (H,), "sink"), _arg(out, dev, _BF, q.shape, "out"),
+            _arg(lse, dev, _F32, (nq, H), "lse"), wp, wn)
     return out, lse
 
 
@@ -942,16 +973,16 @@ def hca_dense_mqa_fp4kv(q, kv4, pos, mp: int, scale: float = 0.0, sink=None, seq
     """hca_dense_mqa over 4-bit entries: query t sees entries s < pos[t] // mp
     of its sequence. A cache that no longer holds its entries in order (after
     an eviction) is read with mp = 1 and pos = its number of entries."""
-    dev = _cuda_device(q)
+    dev = _cuda_index(q)
     nq, H, c = q.shape
     n_seq, Nmax, _ = _fp4_cache(kv4, c, rope_dims)
     out, lse = _attn_out(q, out, lse)
-    ws = _ws(_lib.hca_dense_mqa_fp4kv_workspace_size(nq, H, c, Nmax), dev, ws)
-    _run_on(dev, _lib.hca_dense_mqa_fp4kv, _arg(q, dev, torch.bfloat16, q.shape, "q"),
-            _arg(kv4, dev, torch.uint8, kv4.shape, "kv4"), _arg(pos, dev, torch.int32, (nq,), "pos"),
-            _arg(seq_of_q, dev, torch.int32, (nq,), "seq_of_q"), nq, n_seq, H, c, rope_dims, Nmax, mp, scale,
-            _arg(sink, dev, torch.float32, (H,), "sink"), _arg(out, dev, torch.bfloat16, q.shape, "out"),
-            _arg(lse, dev, torch.float32, (nq, H), "lse"), _ptr(ws), _nbytes(ws))
+    wp, wn, ws = _scratch(_size_of("hca_dense_mqa_fp4kv_workspace_size", nq, H, c, Nmax), dev, ws)
+    _run_on(dev, _lib.hca_dense_mqa_fp4kv, _arg(q, dev, _BF, q.shape, "q"),
+            _arg(kv4, dev, _U8, kv4.shape, "kv4"), _arg(pos, dev, _I32, (nq,), "pos"),
+            _arg(seq_of_q, dev, _I32, (nq,), "seq_of_q"), nq, n_seq, H, c, rope_dims, Nmax, mp, scale,
+            _arg(sink, dev, _F32, (H,), "sink"), _arg(out, dev, _BF, q.shape, "out"),
+            _arg(lse, dev, _F32, (nq, H), "lse"), wp, wn)
     return out, lse
 
 
@@ -959,21 +990,21 @@ def csa_decode_fp4kv(qI, w, idx_cache, q, kv4, ctx_len, m: int, k: int, scale: f
                      rope_dims: int = 64, out=None, lse=None, topk_idx=None, ws=None, return_topk: bool = False):
     """csa_decode with the KV entries in 4-bit storage (csa_quantize_kv_fp4);
     the index keys stay bf16 and the selection is csa_decode's."""
-    dev = _cuda_device(q)
+    dev = _cuda_index(q)
     B, H, c = q.shape
     _, HI, cI = qI.shape
     n_seq, Nmax, rb = _fp4_cache(kv4, c, rope_dims)
     out, lse = _attn_out(q, out, lse)
     if return_topk and topk_idx is None:
         topk_idx = torch.empty((B, k), dtype=torch.int32, device=dev)
-    ws = _ws(_lib.csa_decode_fp4kv_workspace_size(B, Nmax, H, c, HI, cI, k), dev, ws)
-    _run_on(dev, _lib.csa_decode_fp4kv, _arg(qI, dev, torch.bfloat16, (B, HI, cI), "qI"),
-            _arg(w, dev, torch.float32, (B, HI), "w"), _arg(idx_cache, dev, torch.bfloat16, (B, Nmax, cI), "idx_cache"),
-            _arg(q, dev, torch.bfloat16, q.shape, "q"), _arg(kv4, dev, torch.uint8, (B, Nmax, rb), "kv4"),
-            _arg(ctx_len, dev, torch.int32, (B,), "ctx_len"), B, Nmax, m, H, c, rope_dims, HI, cI, k, scale,
-            _arg(sink, dev, torch.float32, (H,), "sink"), _arg(out, dev, torch.bfloat16, q.shape, "out"),
-            _arg(lse, dev, torch.float32, (B, H), "lse"), _arg(topk_idx, dev, torch.int32, (B, k), "topk_idx"),
-            _ptr(ws), _nbytes(ws))
+    wp, wn, ws = _scratch(_size_of("csa_decode_fp4kv_workspace_size", B, Nmax, H, c, HI, cI, k), dev, ws)
+    _run_on(dev, _lib.csa_decode_fp4kv, _arg(qI, dev, _BF, (B, HI, cI), "qI"),
+            _arg(w, dev, _F32, (B, HI), "w"), _arg(idx_cache, dev, _BF, (B, Nmax, cI), "idx_cache"),
+            _arg(q, dev, _BF, q.shape, "q"), _arg(kv4, dev, _U8, (B, Nmax, rb), "kv4"),
+            _arg(ctx_len, dev, _I32, (B,), "ctx_len"), B, Nmax, m, H, c, rope_dims, HI, cI, k, scale,
+            _arg(sink, dev, _F32, (H,), "sink"), _arg(out, dev, _BF, q.shape, "out"),
+            _arg(lse, dev, _F32, (B, H), "lse"), _arg(topk_idx, dev, _I32, (B, k), "topk_idx"),
+            wp, wn)
     return (out, lse, topk_idx) if return_topk else (out, lse)
 
 
@@ -993,16 +1024,16 @@ def csa_entry_weights_fp4kv(q, lse, kv4, idx, acc=None, scale: float = 0.0, seq_
     [nq, k] fp32 (0 for an empty slot), from the queries and the lse that the
     attention returned. acc [n_seq, Nmax] fp32 (one query per sequence only)
     has them added in place."""
-    dev = _cuda_device(q)
+    dev = _cuda_index(q)
     nq, H, c = q.shape
     n_seq, Nmax, _ = _fp4_cache(kv4, c, rope_dims)
     k = idx.shape[-1]
     weights = torch.empty((nq, k), dtype=torch.float32, device=dev) if weights is None else weights
-    _run_on(dev, _lib.csa_entry_weights_fp4kv, _arg(q, dev, torch.bfloat16, q.shape, "q"),
-            _arg(lse, dev, torch.float32, (nq, H), "lse"), _arg(kv4, dev, torch.uint8, kv4.shape, "kv4"),
-            _arg(idx, dev, torch.int32, (nq, k), "idx"), _arg(seq_of_q, dev, torch.int32, (nq,), "seq_of_q"), nq,
-            n_seq, H, c, rope_dims, Nmax, k, scale, _arg(weights, dev, torch.float32, (nq, k), "weights"),
-            _arg(acc, dev, torch.float32, (n_seq, Nmax), "acc"))
+    _run_on(dev, _lib.csa_entry_weights_fp4kv, _arg(q, dev, _BF, q.shape, "q"),
+            _arg(lse, dev, _F32, (nq, H), "lse"), _arg(kv4, dev, _U8, kv4.shape, "kv4"),
+            _arg(idx, dev, _I32, (nq, k), "idx"), _arg(seq_of_q, dev, _I32, (nq,), "seq_of_q"), nq,
+            n_seq, H, c, rope_dims, Nmax, k, scale, _arg(weights, dev, _F32, (nq, k), "weights"),
+            _arg(acc, dev, _F32, (n_seq, Nmax), "acc"))
     return weights
 
 
@@ -1011,16 +1042,16 @@ def hca_entry_weights_fp4kv(q, lse, kv4, pos, mp: int, acc=None, scale: float = 
     the T queries of its sequence: out [B, Nmax] = acc (or 0) + sum. q [B, T,
     H, c], lse [B, T, H], pos [B, T], or without T ([B, H, c], [B, H], [B]);
     kv4 [B, Nmax, row_bytes]. out may be acc (in place)."""
-    dev = _cuda_device(q)
+    dev = _cuda_index(q)
     T = q.shape[1] if q.dim() == 4 else 1
     B, H, c = q.shape[0], q.shape[-2], q.shape[-1]
     _, Nmax, rb = _fp4_cache(kv4, c, rope_dims)
     out = torch.empty((B, Nmax), dtype=torch.float32, device=dev) if out is None else out
     lead = (B, T) if q.dim() == 4 else (B,)
-    _run_on(dev, _lib.hca_entry_weights_fp4kv, _arg(q, dev, torch.bfloat16, lead + (H, c), "q"),
-            _arg(lse, dev, torch.float32, lead + (H,), "lse"), _arg(kv4, dev, torch.uint8, (B, Nmax, rb), "kv4"),
-            _arg(pos, dev, torch.int32, lead, "pos"), B, T, H, c, rope_dims, Nmax, mp, scale,
-            _arg(acc, dev, torch.float32, (B, Nmax), "acc"), _arg(out, dev, torch.float32, (B, Nmax), "out"))
+    _run_on(dev, _lib.hca_entry_weights_fp4kv, _arg(q, dev, _BF, lead + (H, c), "q"),
+            _arg(lse, dev, _F32, lead + (H,), "lse"), _arg(kv4, dev, _U8, (B, Nmax, rb), "kv4"),
+            _arg(pos, dev, _I32, lead, "pos"), B, T, H, c, rope_dims, Nmax, mp, scale,
+            _arg(acc, dev, _F32, (B, Nmax), "acc"), _arg(out, dev, _F32, (B, Nmax), "out"))
     return out
 
 
@@ -1033,7 +1064,7 @@ def csa_evict_plan(acc, n_ent, keep: int, entry_pos=None, protect_from=None, src
     n_moves[b] (-1 after), n_out entries are left, and acc_out / pos_out hold
     their weights and positions (0 / -1 past them; they may be acc / entry_pos
     themselves)."""
-    dev = _cuda_device(acc)
+    dev = _cuda_index(acc)
     B, Nmax = acc.shape
     M = max(0, min(keep, Nmax - keep))
 
@@ -1044,27 +1075,26 @@ def csa_evict_plan(acc, n_ent, keep: int, entry_pos=None, protect_from=None, src
     acc_out = new(acc_out, (B, Nmax), torch.float32)
     if entry_pos is not None:
         pos_out = new(pos_out, (B, Nmax), torch.int32)
-    ws = _ws(_lib.csa_evict_plan_workspace_size(B, Nmax, keep), dev, ws)
-    i32 = torch.int32
-    _run_on(dev, _lib.csa_evict_plan, _arg(acc, dev, torch.float32, (B, Nmax), "acc"),
-            _arg(n_ent, dev, i32, (B,), "n_ent"), _arg(entry_pos, dev, i32, (B, Nmax), "entry_pos"),
-            _arg(protect_from, dev, i32, (B,), "protect_from"), B, Nmax, keep, _arg(src, dev, i32, (B, M), "src"),
-            _arg(dst, dev, i32, (B, M), "dst"), _arg(n_moves, dev, i32, (B,), "n_moves"),
-            _arg(n_out, dev, i32, (B,), "n_out"), _arg(acc_out, dev, torch.float32, (B, Nmax), "acc_out"),
-            _arg(pos_out, dev, i32, (B, Nmax), "pos_out"), _ptr(ws), _nbytes(ws))
+    wp, wn, ws = _scratch(_size_of("csa_evict_plan_workspace_size", B, Nmax, keep), dev, ws)
+    _run_on(dev, _lib.csa_evict_plan, _arg(acc, dev, _F32, (B, Nmax), "acc"),
+            _arg(n_ent, dev, _I32, (B,), "n_ent"), _arg(entry_pos, dev, _I32, (B, Nmax), "entry_pos"),
+            _arg(protect_from, dev, _I32, (B,), "protect_from"), B, Nmax, keep, _arg(src, dev, _I32, (B, M), "src"),
+            _arg(dst, dev, _I32, (B, M), "dst"), _arg(n_moves, dev, _I32, (B,), "n_moves"),
+            _arg(n_out, dev, _I32, (B,), "n_out"), _arg(acc_out, dev, _F32, (B, Nmax), "acc_out"),
+            _arg(pos_out, dev, _I32, (B, Nmax), "pos_out"), wp, wn)
     return src, dst, n_moves, n_out, acc_out, pos_out
 
 
 def csa_evict_rows(cache, src, dst, n_moves):
     """Carries out a plan's moves on a cache [B, Nmax, ...] of any dtype (rows
     of a multiple of 16 bytes), in place: KV entries, index keys."""
-    dev = _cuda_device(cache)
+    dev = _cuda_index(cache)
     B, Nmax = cache.shape[:2]
-    row_bytes = cache[0, 0].numel() * cache.element_size() if B and Nmax else 16
+    row_bytes = math.prod(cache.shape[2:]) * cache.element_size()
     M = src.shape[-1]
     _run_on(dev, _lib.csa_evict_rows, _arg(cache, dev, cache.dtype, cache.shape, "cache"), row_bytes, B, Nmax,
-            _arg(src, dev, torch.int32, (B, M), "src"), _arg(dst, dev, torch.int32, (B, M), "dst"),
-            _arg(n_moves, dev, torch.int32, (B,), "n_moves"), M)
+            _arg(src, dev, _I32, (B, M), "src"), _arg(dst, dev, _I32, (B, M), "dst"),
+            _arg(n_moves, dev, _I32, (B,), "n_moves"), M)
     return cache
 
 
@@ -1083,11 +1113,10 @@ def csa_evict_slot(acc, n_ent, pos, m: int, cap: int, entry_pos=None, recent: in
     full cache, evicts the entry of least weight (not one of the `recent`
     newest while others are left). slot[b] is -1 where no block closes. acc,
     n_ent and entry_pos are updated in place (weight 0, the new entry's index)."""
-    dev = _cuda_device(acc)
+    dev = _cuda_index(acc)
     B, Nmax = acc.shape
     slot = torch.empty((B,), dtype=torch.int32, device=dev) if slot is None else slot
-    i32 = torch.int32
-    _run_on(dev, _lib.csa_evict_slot, _arg(acc, dev, torch.float32, (B, Nmax), "acc"),
-            _arg(n_ent, dev, i32, (B,), "n_ent"), _arg(entry_pos, dev, i32, (B, Nmax), "entry_pos"),
-            _arg(pos, dev, i32, (B,), "pos"), B, Nmax, m, cap, recent, _arg(slot, dev, i32, (B,), "slot"))
+    _run_on(dev, _lib.csa_evict_slot, _arg(acc, dev, _F32, (B, Nmax), "acc"),
+            _arg(n_ent, dev, _I32, (B,), "n_ent"), _arg(entry_pos, dev, _I32, (B, Nmax), "entry_pos"),
+            _arg(pos, dev, _I32, (B,), "pos"), B, Nmax, m, cap, recent, _arg(slot, dev, _I32, (B,), "slot"))
     return slot

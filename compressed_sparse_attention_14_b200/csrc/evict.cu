@@ -9,12 +9,12 @@
 //
 // evict_plan: a cluster of up to 8 CTAs per sequence, each with a contiguous
 // part of the entries, their keys in shared memory. The keep-th key is found
-// by radix select, 8 bits a pass (local histograms, summed over the cluster
-// through distributed shared memory). Ties stay in index order: every warp
+// by radix select, the protected bit and 8 bits, then 8 a pass (local
+// histograms, summed over the cluster through distributed shared memory). Ties stay in index order: every warp
 // owns a contiguous segment and counts it, the counts are scanned over warps
 // and CTAs, and a second walk writes holes and movers at their places without
 // another barrier. Bound by latency: a few passes over some thousand keys per
-// CTA and 13 cluster barriers.
+// CTA and 7 cluster barriers.
 // evict_rows: a thread per 16 bytes, four of them in flight; bound by memory.
 // evict_slot: a CTA per sequence, one reduction.
 #include "common.cuh"
@@ -39,10 +39,10 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 }
 
 struct PlanShared {
-    int hist[2][256];
+    int hist[512 + 3 * 256];               // one histogram per pass: none is reused
     int scan[kWarps];
-    int ties[kWarps], holes[kWarps], movers[kWarps];   // per warp, then exclusive sums
-    int total[3];                                      // this CTA's: protected / ties, holes, movers
+    int count[kWarps][4];                  // per warp: above the keep-th key before / after slot keep, ties likewise
+    int total[5];                          // this CTA's sums, and its entries before slot keep
     int digit, need;
 };
 
@@ -64,81 +64,84 @@ __global__ void __launch_bounds__(kThreads) evict_plan_kernel(const __grid_const
     int32_t* dst = a.dst + (int64_t)b * M;
     const bool guard = pos && a.protect_from;
     const int from = guard ? a.protect_from[b] : 0;
+    const uint32_t below = (1u << lane) - 1u;
 
     auto sync_all = [&]() {
         if (csize > 1) tc::cluster_sync();
         else __syncthreads();
     };
-    // sum of a counter over the CTAs before this one, and over all
-    auto cluster_sum = [&](const int* counter, int& before, int& all) {
-        before = all = 0;
-        for (int r = 0; r < csize; ++r) {
-            const int v = csize > 1 ? (int)ld_cluster_u32(tc::mapa(tc::smem_u32(counter), r)) : *counter;
-            if (r < rank) before += v;
-            all += v;
-        }
+    auto peek = [&](const int* p, int r) {
+        return csize > 1 ? (int)ld_cluster_u32(tc::mapa(tc::smem_u32(p), r)) : *p;
     };
     int moves = 0;
-    if (n > keep) {
+    if (n > keep && keep > 0) {           // (with keep = 0 there is no keep-th key, and nothing to move)
         // this CTA's part, and this warp's segment of it (whole groups of 32)
         const int groups = (n + 31) / 32, per_cta = (groups + csize - 1) / csize;
         const int g0 = min(groups, rank * per_cta), g1 = min(groups, g0 + per_cta);
         const int per_warp = (g1 - g0 + kWarps - 1) / kWarps;
         const int w0 = min(g1, g0 + warp * per_warp), w1 = min(g1, w0 + per_warp);
-        bool prot_only = false;           // more protected entries than stay: only they compete
-        auto raw_key = [&](int i) {
-            const uint32_t k = weight_key(acc[i]);
-            if (!guard) return k;
-            const bool p = pos[i] >= from;
-            // protected entries above every weight, or the others below
-            return prot_only ? (p ? k : 0u) : (p ? 0xFFFFFFFFu : k);
+        uint32_t* prot = keys + per_cta * 32;             // a bit per entry: protected
+        // an entry's key, and the protected bits of its group
+        auto read = [&](int g, uint32_t& k, uint32_t& pm) {
+            const int i = 32 * g + lane;
+            k = i < n ? weight_key(acc[i]) : 0;
+            pm = guard ? __ballot_sync(0xffffffffu, i < n && pos[i] >= from) : 0;
         };
-        auto key = [&](int i) { return cached ? keys[i - 32 * g0] : raw_key(i); };
-        if (tid < 3) s.total[tid] = 0;
-        for (int i = tid; i < 256; i += kThreads) s.hist[0][i] = 0;
+        auto get = [&](int g, uint32_t& k, uint32_t& pm) {
+            if (!cached) return read(g, k, pm);
+            k = keys[32 * (g - g0) + lane];
+            pm = guard ? prot[g - g0] : 0;
+        };
+        // one more of this digit for every lane with `in`; equal digits (zero
+        // weights, say) would queue up at one counter
+        auto tally = [&](int* hist, bool in, uint32_t digit) {
+            const uint32_t m = __ballot_sync(0xffffffffu, in);
+            if (!m) return;
+            const uint32_t lead = __shfl_sync(0xffffffffu, digit, __ffs(m) - 1);
+            const uint32_t same = __ballot_sync(0xffffffffu, in && digit == lead);
+            if (in && digit != lead) atomicAdd(&hist[digit], 1);
+            if (lane == __ffs(m) - 1) atomicAdd(&hist[lead], __popc(same));
+        };
+        for (int i = tid; i < 512 + 3 * 256; i += kThreads) s.hist[i] = 0;
+        if (tid < 5) s.total[tid] = 0;
         __syncthreads();
-        if (guard) {
-            int c = 0;
-            for (int g = w0; g < w1; ++g) {
-                const int i = 32 * g + lane;
-                c += __popc(__ballot_sync(0xffffffffu, i < n && pos[i] >= from));
-            }
-            if (lane == 0 && c) atomicAdd(&s.total[0], c);
-            sync_all();
-            int before, all;
-            cluster_sum(&s.total[0], before, all);
-            prot_only = all > keep;
-        }
-        if (cached) {
-#pragma unroll 4
-            for (int g = w0; g < w1; ++g)
-                if (32 * g + lane < n) keys[32 * (g - g0) + lane] = raw_key(32 * g + lane);
-            __syncwarp();
-        }
-        uint32_t prefix = 0;
+        // the keep-th key, from the top: protected bit and 8 bits, then 8 a pass
+        uint32_t cls = 0, prefix = 0;
         int need = keep;
+#pragma unroll 1
         for (int d = 0; d < 4; ++d) {
-            const int shift = 24 - 8 * d;
-            int* hist = s.hist[d & 1];
-            for (int g = w0; g < w1; ++g) {
-                const int i = 32 * g + lane;
-                const uint32_t k = i < n ? key(i) : 0;
-                const bool in = i < n && (d == 0 || (k >> (shift + 8)) == prefix);
-                const uint32_t m = __ballot_sync(0xffffffffu, in);
-                if (!m) continue;
-                // equal digits (zero weights, say) would queue up at one counter
-                const uint32_t digit = (k >> shift) & 255u;
-                const uint32_t lead = __shfl_sync(0xffffffffu, digit, __ffs(m) - 1);
-                const uint32_t same = __ballot_sync(0xffffffffu, in && digit == lead);
-                if (in && digit != lead) atomicAdd(&hist[digit], 1);
-                if (lane == __ffs(m) - 1) atomicAdd(&hist[lead], __popc(same));
+            int* hist = d == 0 ? s.hist : s.hist + 256 + 256 * d;
+            const int bins = d == 0 ? 512 : 256;
+            if (d == 0) {
+                for (int g = w0; g < w1; g += 4) {
+                    uint32_t k[4], pm[4];                 // (four loads in flight)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (g + u < w1) read(g + u, k[u], pm[u]);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        if (g + u >= w1) continue;
+                        if (cached) {
+                            keys[32 * (g + u - g0) + lane] = k[u];
+                            if (lane == 0 && guard) prot[g + u - g0] = pm[u];
+                        }
+                        tally(hist, 32 * (g + u) + lane < n, ((pm[u] >> lane) & 1u) << 8 | k[u] >> 24);
+                    }
+                }
+                __syncwarp();
+            } else {
+                for (int g = w0; g < w1; ++g) {
+                    uint32_t k, pm;
+                    get(g, k, pm);
+                    const bool in = 32 * g + lane < n && ((pm >> lane) & 1u) == cls && k >> (32 - 8 * d) == prefix;
+                    tally(hist, in, (k >> (24 - 8 * d)) & 255u);
+                }
             }
             sync_all();
             // entries with this digit, of all CTAs; from the largest digit down
             int c = 0;
-            if (tid < 256)
-                for (int r = 0; r < csize; ++r)
-                    c += csize > 1 ? (int)ld_cluster_u32(tc::mapa(tc::smem_u32(hist + 255 - tid), r)) : hist[255 - tid];
+            if (tid < bins)
+                for (int r = 0; r < csize; ++r) c += peek(hist + bins - 1 - tid, r);
             int sum = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -147,74 +150,77 @@ __global__ void __launch_bounds__(kThreads) evict_plan_kernel(const __grid_const
             }
             if (lane == 31) s.scan[warp] = sum;
             __syncthreads();
-            int above = sum - c;          // entries with a larger digit
-            for (int w = 0; w < warp && w < 8; ++w) above += s.scan[w];
-            if (tid < 256 && above < need && above + c >= need) {
-                s.digit = 255 - tid;
+            int above = sum - c;                          // entries with a larger digit
+            for (int w = 0; w < warp; ++w) above += s.scan[w];
+            if (above < need && above + c >= need) {
+                s.digit = bins - 1 - tid;
                 s.need = need - above;
             }
-            // the other histogram is free: its readers passed the last barrier
-            for (int i = tid; i < 256; i += kThreads) s.hist[(d + 1) & 1][i] = 0;
-            sync_all();
-            prefix = (prefix << 8) | (uint32_t)s.digit;
+            __syncthreads();
+            if (d == 0) cls = (uint32_t)s.digit >> 8;
+            prefix = (prefix << 8) | ((uint32_t)s.digit & 255u);
             need = s.need;
         }
         // `need` of the entries equal to the keep-th key stay, the first ones
         const uint32_t kth = prefix;
-        int gt_lo = 0, gt_hi = 0, tie_lo = 0, tie_hi = 0;
+        auto compare = [&](int g, uint32_t& gt, uint32_t& eq) {
+            uint32_t k, pm;
+            get(g, k, pm);
+            const uint32_t p = (pm >> lane) & 1u;
+            const bool live = 32 * g + lane < n;
+            gt = __ballot_sync(0xffffffffu, live && (p > cls || (p == cls && k > kth)));
+            eq = __ballot_sync(0xffffffffu, live && p == cls && k == kth);
+        };
+        int cnt[4] = {0, 0, 0, 0};
+        for (int g = w0; g < w1; ++g) {
+            uint32_t gt, eq;
+            compare(g, gt, eq);
+            const uint32_t lo = 32 * g >= keep ? 0u : keep - 32 * g >= 32 ? 0xffffffffu : (1u << (keep - 32 * g)) - 1u;
+            cnt[0] += __popc(gt & lo);
+            cnt[1] += __popc(gt & ~lo);
+            cnt[2] += __popc(eq & lo);
+            cnt[3] += __popc(eq & ~lo);
+        }
+        if (lane < 4) {
+            const int v = lane == 0 ? cnt[0] : lane == 1 ? cnt[1] : lane == 2 ? cnt[2] : cnt[3];
+            s.count[warp][lane] = v;
+            atomicAdd(&s.total[lane], v);
+        }
+        if (tid == 0) s.total[4] = max(0, min(32 * g1, min(n, keep)) - 32 * g0);
+        sync_all();
+        // what lies before this warp: ties, then (they decide which ties stay) holes and movers
+        int tie = 0, hole = 0, mover = 0;
+        auto pass_over = [&](int in_lo, const int (&v)[4]) {
+            const int keep_lo = min(max(need - tie, 0), v[2]), keep_hi = min(max(need - tie - v[2], 0), v[3]);
+            hole += in_lo - v[0] - keep_lo;
+            mover += v[1] + keep_hi;
+            tie += v[2] + v[3];
+        };
+        int own_tie = 0, own_hole = 0, own_mover = 0;
+        for (int r = 0; r < csize; ++r) {
+            if (r == rank) { own_tie = tie; own_hole = hole; own_mover = mover; }
+            const int v[4] = {peek(&s.total[0], r), peek(&s.total[1], r), peek(&s.total[2], r), peek(&s.total[3], r)};
+            pass_over(peek(&s.total[4], r), v);
+        }
+        moves = hole;
+        tie = own_tie;
+        hole = own_hole;
+        mover = own_mover;
+        for (int w = 0; w < warp; ++w) {
+            const int b0 = min(g1, g0 + w * per_warp), b1 = min(g1, b0 + per_warp);
+            const int v[4] = {s.count[w][0], s.count[w][1], s.count[w][2], s.count[w][3]};
+            pass_over(max(0, min(32 * b1, min(n, keep)) - 32 * b0), v);
+        }
         for (int g = w0; g < w1; ++g) {
             const int i = 32 * g + lane;
-            const uint32_t k = i < n ? key(i) : 0;
-            const bool lo = i < keep;
-            const uint32_t gt = __ballot_sync(0xffffffffu, i < n && k > kth), eq = __ballot_sync(0xffffffffu, i < n && k == kth);
-            const uint32_t lom = __ballot_sync(0xffffffffu, lo);
-            gt_lo += __popc(gt & lom);
-            gt_hi += __popc(gt & ~lom);
-            tie_lo += __popc(eq & lom);
-            tie_hi += __popc(eq & ~lom);
-        }
-        if (lane == 0) s.ties[warp] = tie_lo + tie_hi;
-        __syncthreads();
-        if (tid == 0) {
-            int sum = 0;
-            for (int w = 0; w < kWarps; ++w) sum += s.ties[w];
-            s.total[0] = sum;
-        }
-        sync_all();
-        int tie_base, tie_all;
-        cluster_sum(&s.total[0], tie_base, tie_all);
-        for (int w = 0; w < warp; ++w) tie_base += s.ties[w];
-        const int n_lo = max(0, min(32 * w1, min(n, keep)) - 32 * w0);
-        const int keep_lo = min(max(need - tie_base, 0), tie_lo);
-        const int keep_hi = min(max(need - tie_base - tie_lo, 0), tie_hi);
-        if (lane == 0) {
-            s.holes[warp] = n_lo - gt_lo - keep_lo;
-            s.movers[warp] = gt_hi + keep_hi;
-        }
-        __syncthreads();
-        if (tid == 0) {
-            int h = 0, m = 0;
-            for (int w = 0; w < kWarps; ++w) { h += s.holes[w]; m += s.movers[w]; }
-            s.total[1] = h;
-            s.total[2] = m;
-        }
-        sync_all();
-        int hole, mover, all;
-        cluster_sum(&s.total[2], mover, all);
-        cluster_sum(&s.total[1], hole, moves);
-        for (int w = 0; w < warp; ++w) { hole += s.holes[w]; mover += s.movers[w]; }
-        int tie = tie_base;
-        const uint32_t below = (1u << lane) - 1u;
-        for (int g = w0; g < w1; ++g) {
-            const int i = 32 * g + lane;
-            const uint32_t k = i < n ? key(i) : 0;
-            const uint32_t eq = __ballot_sync(0xffffffffu, i < n && k == kth);
-            const bool kept = i < n && (k > kth || (k == kth && tie + __popc(eq & below) < need));
+            uint32_t gt, eq;
+            compare(g, gt, eq);
+            const bool kept = (gt >> lane & 1u) || ((eq >> lane & 1u) && tie + __popc(eq & below) < need);
             tie += __popc(eq);
-            const uint32_t hm = __ballot_sync(0xffffffffu, i < keep && !kept);
-            const uint32_t mm = __ballot_sync(0xffffffffu, i >= keep && kept);
-            if (i < keep && !kept) dst[hole + __popc(hm & below)] = i;
-            if (i >= keep && kept) src[mover + __popc(mm & below)] = i;
+            const bool h = i < keep && !kept, m = i >= keep && kept;
+            const uint32_t hm = __ballot_sync(0xffffffffu, h), mm = __ballot_sync(0xffffffffu, m);
+            if (h) dst[hole + __popc(hm & below)] = i;
+            if (m) src[mover + __popc(mm & below)] = i;
             hole += __popc(hm);
             mover += __popc(mm);
         }
@@ -340,7 +346,7 @@ cudaError_t evict_plan(const EvictPlanArgs& a, void* ws, cudaStream_t st) {
     int csize = 1;
     while (csize < kMaxCluster && a.Nmax > 2048 * (int64_t)csize) csize <<= 1;
     const int64_t part = ((a.Nmax + 31) / 32 + csize - 1) / csize * 32;
-    const size_t smem = part <= kMaxCached ? part * sizeof(uint32_t) : 0;
+    const size_t smem = part <= kMaxCached ? (part + part / 32) * sizeof(uint32_t) : 0;
     cudaError_t e = smem_ceiling(evict_plan_kernel);
     if (e != cudaSuccess) return e;
     CSA_LAUNCH(st, "evict_plan",

@@ -163,11 +163,9 @@ struct Producer {
 #pragma unroll
         for (int i = kPairs - 1; i >= 0; --i) {
             if (i >= a.mtiles || !ok) continue;
-            if (j > 0) {                                  // tile j-1's products have read it
-                if (lane == 0) ok = wait(&s.empty[i], (j - 1) & 1, s, a.status);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) continue;
-            }
+            // tile j-1's products have read it
+            if (j > 0) ok = __all_sync(0xffffffffu, wait(&s.empty[i], (j - 1) & 1, s, a.status));
+            if (!ok) continue;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 // the two scales of this lane's chunk in pair i

@@ -12,18 +12,24 @@
 //   O^T += V_tile^T . P^T       M = 128 dims,    N = 64 heads, K = 128 entries
 // S^T (two buffers) and O^T live in tensor memory. The softmax keeps a
 // reference maximum per head that moves (O^T and the sums are then rescaled)
-// only when a logit passes it by 2^8; normalisation uses the same reference,
-// so the result does not depend on when it moves. P is rounded to bf16 for
-// the second product; the sums, maxima and O stay fp32.
+// only when a logit passes it by 2^24; normalisation uses the same reference,
+// so the result does not depend on when it moves, and the weights' rounding is
+// relative (with 2^8 it moved in every second tile, 2500 cycles each). P is
+// rounded to bf16 for the second product; sums, maxima and O stay fp32.
 //
-// Warps 0-3: softmax, a thread per entry (TMEM lane) and 64 heads. Warps 4-11:
-// producers, with the next tile's codes in registers by the time a block is
-// free. Warp 12 issues the S products, warp 13 the O products. Blocks go back
-// and forth in pairs (128 dims, one M tile of the O product), the last first,
-// so expansion and S product of tile j+1 run while the O product of tile j is
-// still busy with the pairs before. 14 warps leave each thread 128 registers:
-// loaded codes that spill are waited for at once (with 18 warps and 96
-// registers a tile took 10500 cycles).
+// Warps 0-7: softmax, warp w on TMEM lanes 32 (w % 4).. (a thread per entry)
+// and 32 heads. Warps 8-15: producers, with the next tile's codes in registers
+// by the time a block is free. Blocks go back and forth in pairs (128 dims, one
+// M tile of the O product), the last first. One thread of warp 0 issues the S
+// products, one of warp 4 the O products: those warps would only wait
+// meanwhile, and 16 warps leave each thread 128 registers (loaded codes that
+// spill are waited for at once: with 18 warps and 96 registers a tile took
+// 10500 cycles).
+//
+// What a tile costs is shared-memory bandwidth: the two products read 384 KB
+// (O at 113 bytes a cycle, near the 128 there are, so the expansion's stores
+// hardly advance while it runs), the stores write 128 KB; 4900 cycles with
+// nothing else in the way.
 //
 // Entries outside the query's set are stored as zeros and get weight 0: no
 // row that the query does not see is read.
@@ -41,9 +47,10 @@ namespace {
 
 using namespace fp4_tile;
 
-constexpr int kThreads = 448;           // 4 softmax warps, 8 producers, 2 issuers
+constexpr int kThreads = 512;           // 8 softmax warps, 8 producers
+constexpr int kHalf = kHg / 2;          // heads per softmax warp
 constexpr int kMaxCluster = 8;
-constexpr float kMoveLog2 = 8.0f, kLn2 = 0.6931471805599453f;
+constexpr float kMoveLog2 = 24.0f, kLn2 = 0.6931471805599453f;
 
 enum Merge { kDirect, kCluster, kWorkspace };
 
@@ -61,12 +68,12 @@ struct Args : Fp4TileArgs {
 };
 
 struct Shared : Fp4TileShared {
-    // the heads' reference maxima; the same plus 8; the same, 0 for none
+    // the heads' reference maxima; the same plus the limit; the same, 0 for none
     float mref[kHg], limit[kHg], mexp[kHg];
     float alpha[kHg], lsum[kHg];
     float red[4][kHg];
     float coef[kMaxCluster][kHg];
-    uint64_t s_full, q_full, p_full, o_done, fin[2];
+    uint64_t s_full, q_full, p_full, o_done, fin;
     uint32_t tmem;
 };
 
@@ -77,16 +84,58 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
     return v;
 }
 
-// barrier (and vote) of the softmax warps
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool softmax_any(bool v) {
+// barrier (and vote) of the 4 softmax warps that share 32 heads
+__device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
+__device__ __forceinline__ bool half_any(int half, bool v) {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p, q;\n\t"
                  "setp.ne.u32 q, %1, 0;\n\t"
-                 "bar.red.or.pred p, 1, 128, q;\n\t"
+                 "bar.red.or.pred p, %2, 128, q;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(r) : "r"((uint32_t)v) : "memory");
+                 : "=r"(r) : "r"((uint32_t)v), "r"(1 + half) : "memory");
     return r != 0;
+}
+
+// S^T of tile j (one thread): pairs as they are stored.
+__device__ __forceinline__ bool issue_s(const Args& a, Shared& s, uint32_t kv_addr, uint32_t q_addr, uint32_t d_tmem,
+                                        int j) {
+    const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
+    for (int n = 0; n < a.mtiles; ++n) {
+        const int i = stored_pair(a, n);
+        if (!wait(&s.full[i], j & 1, s, a.status)) {
+            // the products already issued end before the CTA frees their memory
+            tc::umma_commit(&s.fin);
+            tc::mbar_wait(&s.fin, 0, kWaitLimit);
+            return false;
+        }
+        tc::tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+            const int b = 2 * i + (kk >> 2);
+            tc::umma_bf16(d_tmem, tc::sdesc_sw128(kv_addr + b * kBlockBytes + (kk & 3) * 32, 16, 1024),
+                          tc::sdesc_sw128(q_addr + b * (kHg * 128) + (kk & 3) * 32, 16, 1024), idesc, (n | kk) ? 1u : 0u);
+        }
+    }
+    tc::umma_commit(&s.s_full);
+    return true;
+}
+
+// O^T += of tile j (one thread); each pair of blocks goes back to the
+// producers once its product is done, the last first.
+__device__ __forceinline__ bool issue_o(const Args& a, Shared& s, uint32_t kv_addr, uint32_t p_addr, uint32_t d_tmem,
+                                        int j) {
+    const uint32_t idesc = tc::idesc_bf16_f32(128, kHg, 1, 1);
+    if (!wait(&s.p_full, j & 1, s, a.status)) return false;
+    tc::tc_fence_after();
+    for (int mt = a.mtiles - 1; mt >= 0; --mt) {
+#pragma unroll
+        for (int ke = 0; ke < kE / 16; ++ke)
+            tc::umma_bf16(d_tmem + mt * kHg, tc::sdesc_sw128(kv_addr + 2 * mt * kBlockBytes + ke * 2048, kBlockBytes, 1024),
+                          tc::sdesc_sw128(p_addr + ke * 2048, kE * 128, 1024), idesc, (j > 0 || ke > 0) ? 1u : 0u);
+        tc::umma_commit(&s.empty[mt]);
+    }
+    tc::umma_commit(&s.o_done);
+    return true;
 }
 
 // v[i] of 32 lanes -> in lane l every lane's v[l / 2] combined (16 shuffles)
@@ -136,14 +185,13 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         }
         tc::mbar_init(&s.s_full, 1);
         tc::mbar_init(&s.q_full, 1);
-        tc::mbar_init(&s.p_full, 4);
+        tc::mbar_init(&s.p_full, 8);
         tc::mbar_init(&s.o_done, 1);
-        tc::mbar_init(&s.fin[0], 1);
-        tc::mbar_init(&s.fin[1], 1);
+        tc::mbar_init(&s.fin, 1);
         tc::fence_mbar_init();
         s.abort = 0;
     }
-    if (warp == 12) {
+    if (warp == 0) {
         tc::tmem_alloc(&s.tmem, a.tmem_cols);
         tc::tmem_relinquish();
         tc::tc_fence_before();
@@ -152,73 +200,39 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     tc::tc_fence_after();
     const uint32_t tmem_S = s.tmem, tmem_O = s.tmem + kHg;
 
-    if (warp >= 12) {
-        // ------------------------------------------------------------ products
-        if (lane == 0 && ntiles > 0) {
-            const uint32_t kv_addr = tc::smem_u32(kv_s), q_addr = tc::smem_u32(q_s), p_addr = tc::smem_u32(p_s);
-            if (warp == 12) {
-                tc::mbar_expect_tx(&s.q_full, (uint32_t)a.dblocks * kHg * 128);
-                for (int b = 0; b < a.dblocks; ++b)
-                    tc::tma_load_2d(q_s + (size_t)b * kHg * 128, &tmQ, &s.q_full, b * 64, t * a.H + h0);
-                bool ok = wait(&s.q_full, 0, s, a.status);
-                const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
-                for (int j = 0; ok && j < ntiles; ++j) {
-                    for (int n = 0; n < a.mtiles; ++n) {
-                        const int i = stored_pair(a, n);
-                        if (!(ok = wait(&s.full[i], j & 1, s, a.status))) break;
-                        tc::tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) {
-                            const int b = 2 * i + (kk >> 2);
-                            tc::umma_bf16(tmem_S, tc::sdesc_sw128(kv_addr + b * kBlockBytes + (kk & 3) * 32, 16, 1024),
-                                          tc::sdesc_sw128(q_addr + b * (kHg * 128) + (kk & 3) * 32, 16, 1024), idesc,
-                                          (n | kk) ? 1u : 0u);
-                        }
-                    }
-                    if (ok) tc::umma_commit(&s.s_full);
-                }
-                if (!ok) tc::mbar_wait(&s.q_full, 0, kWaitLimit);
-            } else {
-                const uint32_t idesc = tc::idesc_bf16_f32(128, kHg, 1, 1);
-                for (int j = 0; j < ntiles; ++j) {
-                    if (!wait(&s.p_full, j & 1, s, a.status)) break;
-                    tc::tc_fence_after();
-                    for (int mt = a.mtiles - 1; mt >= 0; --mt) {
-#pragma unroll
-                        for (int ke = 0; ke < kE / 16; ++ke)
-                            tc::umma_bf16(tmem_O + mt * kHg,
-                                          tc::sdesc_sw128(kv_addr + 2 * mt * kBlockBytes + ke * 2048, kBlockBytes, 1024),
-                                          tc::sdesc_sw128(p_addr + ke * 2048, kE * 128, 1024), idesc,
-                                          (j > 0 || ke > 0) ? 1u : 0u);
-                        tc::umma_commit(&s.empty[mt]);
-                    }
-                    tc::umma_commit(&s.o_done);
-                }
-            }
-            // every product this thread issued has ended before the CTA goes
-            // on to free the memory it uses (also when a wait ran out)
-            tc::umma_commit(&s.fin[warp - 12]);
-            tc::mbar_wait(&s.fin[warp - 12], 0, kWaitLimit);
-        }
-        __syncwarp();
-    } else if (warp >= 4) {
-        Producer<kSparse> producer(a, s, kv_s, warp - 4, t, (int)e_beg, (int)e_end, ntiles, (ntiles ? seq : 0) * a.Nmax);
+    if (warp >= 8) {
+        Producer<kSparse> producer(a, s, kv_s, warp - 8, t, (int)e_beg, (int)e_end, ntiles, (ntiles ? seq : 0) * a.Nmax);
         for (int j = 0; j < ntiles; ++j)
             if (!producer.store(j)) break;
     } else {
         // ------------------------------------------------------------ softmax
-        const int row = tid;                              // entry of the tile, TMEM lane
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-        if (tid < kHg) {
-            s.mref[tid] = s.limit[tid] = -INFINITY;
-            s.mexp[tid] = 0.f;
+        const int quad = warp & 3, half = warp >> 2, hb = half * kHalf;
+        const int row = quad * 32 + lane;                 // entry of the tile, TMEM lane
+        const int hth = tid & 127;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const uint32_t kv_addr = tc::smem_u32(kv_s), q_addr = tc::smem_u32(q_s), p_addr = tc::smem_u32(p_s);
+        if (hth < kHalf) {
+            s.mref[hb + hth] = s.limit[hb + hth] = -INFINITY;
+            s.mexp[hb + hth] = 0.f;
         }
-        float lpart[kHg];
+        float lpart[kHalf];
 #pragma unroll
-        for (int i = 0; i < kHg; ++i) lpart[i] = 0.f;
-        softmax_sync();
+        for (int i = 0; i < kHalf; ++i) lpart[i] = 0.f;
+        half_sync(half);
         bool ok = true;
+        int done_s = 0, done_o = 0;                       // products issued by this thread
+        if (tid == 0 && ntiles > 0) {
+            tc::mbar_expect_tx(&s.q_full, (uint32_t)a.dblocks * kHg * 128);
+            for (int b = 0; b < a.dblocks; ++b)
+                tc::tma_load_2d(q_s + (size_t)b * kHg * 128, &tmQ, &s.q_full, b * 64, t * a.H + h0);
+            ok = wait(&s.q_full, 0, s, a.status);
+        }
         for (int j = 0; j < ntiles; ++j) {
+            if (tid == 0 && ok) {
+                ok = issue_s(a, s, kv_addr, q_addr, tmem_S, j);
+                done_s += ok;
+            }
+            __syncwarp();
             const int64_t e = e_beg + (int64_t)j * kE + row;
             bool valid = e < e_end;
             if (kSparse && valid) {
@@ -227,93 +241,100 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             }
             ok = ok && wait(&s.s_full, j & 1, s, a.status);
             tc::tc_fence_after();
-            bool move = false;
-#pragma unroll
-            for (int cc = 0; cc < kHg; cc += 16) {
-                float z[16];
-                tc::tmem_ld16(tmem_S + lanes + cc, z);
+            float z[kHalf];
+            auto logits = [&]() {
+                tc::tmem_ld16(tmem_S + lanes + hb, *reinterpret_cast<float(*)[16]>(z));
+                tc::tmem_ld16(tmem_S + lanes + hb + 16, *reinterpret_cast<float(*)[16]>(z + 16));
                 tc::tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) move |= z[i] * a.scale_log2 > s.limit[cc + i];
-            }
-            if (softmax_any((move && valid) || !ok)) {
+                for (int i = 0; i < kHalf; ++i) z[i] = valid ? z[i] * a.scale_log2 : -INFINITY;
+            };
+            logits();
+            bool move = false;
+#pragma unroll
+            for (int i = 0; i < kHalf; ++i) move |= z[i] > s.limit[hb + i];
+            if (half_any(half, move || !ok)) {
                 // all leave together once a wait of one ran out
-                if (softmax_any(!ok)) { ok = false; break; }
+                if (half_any(half, !ok)) { ok = false; break; }
+                // (the reduction consumes the logits; they are read again)
 #pragma unroll
-                for (int cc = 0; cc < kHg; cc += 16) {
-                    float z[16];
-                    tc::tmem_ld16(tmem_S + lanes + cc, z);
-                    tc::tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) z[i] = valid ? z[i] * a.scale_log2 : -INFINITY;
-                    const float top = lanes_reduce16(z, lane, [](float x, float y) { return fmaxf(x, y); });
-                    if (!(lane & 1)) s.red[warp][cc + lane / 2] = top;
+                for (int cc = 0; cc < kHalf; cc += 16) {
+                    const float top = lanes_reduce16(z + cc, lane, [](float x, float y) { return fmaxf(x, y); });
+                    if (!(lane & 1)) s.red[quad][hb + cc + lane / 2] = top;
                 }
-                softmax_sync();
-                if (tid < kHg) {
-                    const float old = s.mref[tid];
-                    const float m = fmaxf(fmaxf(fmaxf(s.red[0][tid], s.red[1][tid]), fmaxf(s.red[2][tid], s.red[3][tid])), old);
-                    s.alpha[tid] = old == -INFINITY ? 0.f : ex2(old - m);
-                    s.mref[tid] = m;
-                    s.limit[tid] = m + kMoveLog2;
-                    s.mexp[tid] = m == -INFINITY ? 0.f : m;
+                half_sync(half);
+                if (hth < kHalf) {
+                    const int h = hb + hth;
+                    const float old = s.mref[h];
+                    const float m = fmaxf(fmaxf(fmaxf(s.red[0][h], s.red[1][h]), fmaxf(s.red[2][h], s.red[3][h])), old);
+                    s.alpha[h] = old == -INFINITY ? 0.f : ex2(old - m);
+                    s.mref[h] = m;
+                    s.limit[h] = m + kMoveLog2;
+                    s.mexp[h] = m == -INFINITY ? 0.f : m;
                 }
-                softmax_sync();
+                half_sync(half);
 #pragma unroll
-                for (int i = 0; i < kHg; ++i) lpart[i] *= s.alpha[i];
+                for (int i = 0; i < kHalf; ++i) lpart[i] *= s.alpha[hb + i];
                 if (j > 0) {
                     ok = wait(&s.o_done, (j - 1) & 1, s, a.status);
                     tc::tc_fence_after();
 #pragma unroll 1
-                    for (int cc = 0; cc < a.mtiles * kHg; cc += 16) {
+                    for (int n = 0; n < 2 * a.mtiles; ++n) {
+                        const int cc = hb + 16 * (n & 1);
                         float o[16];
-                        tc::tmem_ld16(tmem_O + lanes + cc, o);
+                        tc::tmem_ld16(tmem_O + lanes + (n >> 1) * kHg + cc, o);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] *= s.alpha[(cc & (kHg - 1)) + i];
-                        tc::tmem_st16(tmem_O + lanes + cc, o);
+                        for (int i = 0; i < 16; ++i) o[i] *= s.alpha[cc + i];
+                        tc::tmem_st16(tmem_O + lanes + (n >> 1) * kHg + cc, o);
                     }
                     tc::tmem_st_wait();
                 }
+                logits();
+            }
+            uint32_t pk[kHalf / 2];
+#pragma unroll
+            for (int i = 0; i < kHalf; i += 2) {
+                const float p0 = ex2(z[i] - s.mexp[hb + i]), p1 = ex2(z[i + 1] - s.mexp[hb + i + 1]);
+                lpart[i] += p0;
+                lpart[i + 1] += p1;
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
+                pk[i >> 1] = *reinterpret_cast<const uint32_t*>(&b2);
             }
             // the previous tile's O product has read P
             if (j > 0) ok = wait(&s.o_done, (j - 1) & 1, s, a.status) && ok;
 #pragma unroll
-            for (int cc = 0; cc < kHg; cc += 16) {
-                float z[16];
-                tc::tmem_ld16(tmem_S + lanes + cc, z);
-                tc::tmem_ld_wait();
-                uint32_t pk[8];
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const float p0 = ex2(valid ? fmaf(z[i], a.scale_log2, -s.mexp[cc + i]) : -INFINITY);
-                    const float p1 = ex2(valid ? fmaf(z[i + 1], a.scale_log2, -s.mexp[cc + i + 1]) : -INFINITY);
-                    lpart[cc + i] += p0;
-                    lpart[cc + i + 1] += p1;
-                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
-                    pk[i >> 1] = *reinterpret_cast<const uint32_t*>(&b2);
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    *reinterpret_cast<uint4*>(p_s + row * 128 + (((cc / 8 + i) ^ (row & 7)) << 4)) =
-                        make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-            }
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(p_s + row * 128 + (((half * 4 + i) ^ (row & 7)) << 4)) =
+                    make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
             tc::tc_fence_before();                        // S has been read, too
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&s.p_full);
+            if (tid == 128 && ok) {
+                ok = issue_o(a, s, kv_addr, p_addr, tmem_O, j);
+                done_o += ok;
+            }
+            __syncwarp();
         }
-        if (ok && ntiles > 0) wait(&s.o_done, (ntiles - 1) & 1, s, a.status);
+        if (ok && ntiles > 0) ok = wait(&s.o_done, (ntiles - 1) & 1, s, a.status);
+        if (!ok) {
+            // a wait ran out: the products and copies already issued still end
+            if (done_s) tc::mbar_wait(&s.s_full, (done_s - 1) & 1, kWaitLimit);
+            if (done_o) tc::mbar_wait(&s.o_done, (done_o - 1) & 1, kWaitLimit);
+            if (tid == 0) tc::mbar_wait(&s.q_full, 0, kWaitLimit);
+        }
+        __syncwarp();
         // per-head sums in a fixed order: lanes, then the four warps
-        softmax_sync();                                   // red may still be read
+        half_sync(half);                                  // red may still be read
 #pragma unroll
-        for (int cc = 0; cc < kHg; cc += 16) {
+        for (int cc = 0; cc < kHalf; cc += 16) {
             const float sum = lanes_reduce16(lpart + cc, lane, [](float x, float y) { return x + y; });
-            if (!(lane & 1)) s.red[warp][cc + lane / 2] = sum;
+            if (!(lane & 1)) s.red[quad][hb + cc + lane / 2] = sum;
         }
-        softmax_sync();
-        if (tid < kHg) {
-            const int h = tid;
+        half_sync(half);
+        if (hth < kHalf) {
+            const int h = hb + hth;
             s.lsum[h] = (s.red[0][h] + s.red[1][h]) + (s.red[2][h] + s.red[3][h]);
             if (a.merge == kDirect) {
                 const float m = s.mref[h], L = s.lsum[h];
@@ -436,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         }
         __syncthreads();
     }
-    if (warp == 12) {
+    if (warp == 0) {
         tc::tc_fence_after();
         tc::tmem_dealloc(s.tmem, a.tmem_cols);
     }
