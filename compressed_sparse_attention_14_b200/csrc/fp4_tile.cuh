@@ -16,8 +16,9 @@ constexpr int kProducers = 256;         // producer threads
 constexpr int kE = 128;                 // entries per tile
 constexpr int kHg = 64;                 // heads per CTA
 constexpr int kPairs = CSA_MAX_HEAD_DIM / 128;   // pairs of 64-channel blocks
+constexpr int kSlots = 3;                // pairs in tensor memory
 constexpr uint32_t kBlockBytes = kE * 128;
-constexpr uint32_t kWaitLimit = 1u << 24;
+constexpr uint32_t kWaitLimit = 1u << 20;   // (2 us each)
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Fp4TileArgs {
@@ -31,6 +32,7 @@ struct Fp4TileArgs {
 
 struct Fp4TileShared {
     uint64_t full[kPairs], empty[kPairs];     // a pair of blocks stored / free
+    uint64_t slot_free;                       // a tile's first tensor-memory copy has been read
     int abort;
 };
 
@@ -51,53 +53,56 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Fp4TileShared& s, int* status) {
     volatile int* abort = &s.abort;
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
-        if (tc::mbar_try_wait(bar, parity)) return true;
-        if ((i & 255u) == 255u && *abort) return false;
+        if (tc::mbar_try_wait_for(bar, parity, 2000)) return true;
+        if ((i & 15u) == 15u && *abort) return false;
     }
     report_device_error(status, CSA_ERR_TIMEOUT);
     *abort = 1;
     return false;
 }
 
-// The first 64 rotary channels are loaded ahead with the codes, the others
-// copied while a pair is stored; pairs up to this one hold none of the latter.
-__device__ __forceinline__ int last_early_pair(const Fp4TileArgs& a) {
-    return a.f.R <= 64 ? a.mtiles - 1 : (a.f.Q + 64) / 128 - 1;
-}
-// The n-th pair in the order in which pairs are stored.
-__device__ __forceinline__ int stored_pair(const Fp4TileArgs& a, int n) {
-    const int last = last_early_pair(a);
-    return n <= last ? last - n : a.mtiles - 1 - (n - last - 1);
+__device__ __forceinline__ uint4 ld_shared16(uint32_t src) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+    return v;
 }
 
 // A producer thread's part: of two rows, the 32 channels of chunk `chunk` in
 // every pair of blocks and every fourth 16-byte piece of the rotary channels.
 // The 4 lanes of a row read 64 consecutive bytes, a load instruction touches
-// 8 lines (two lanes to a row and 16 lines took twice as long to issue). The 8
-// lanes that store together are 4 rows of one block, whose pieces lie in
-// different banks.
-template <bool kSparse>
+// 8 lines (two lanes to a row and 16 lines took twice as long to issue).
+//
+// kTmem: each pair also goes to tensor memory, as the A operand of a product
+// over entries: row = lane, kSlots pairs of 64 columns in turn. The registers
+// a thread has are 4 pieces of 32 channels, and the store puts its words 2u,
+// 2u + 1 into columns 8u + 2 chunk and the next, so K runs over the channels
+// of a pair in another order: channel_order() of it.
+template <bool kSparse, bool kTmem>
 struct Producer {
     const Fp4TileArgs& a;
     Fp4TileShared& s;
-    uint32_t tile;            // this thread's first row in block 0; the second is 8 rows on
-    int warp, lane, row0, t, e0, e_end, ntiles;   // (rows as numbers: n_seq * Nmax is below 2^31)
+    uint32_t tile, tmem;      // this thread's first row in block 0 (the second is 8 rows on); its lanes of slot 0
+    int lane, row, row0, t, e0, e_end, ntiles;    // (rows as numbers: n_seq * Nmax is below 2^31)
     int next[2], cur[2];
     uint4 raw[2][kPairs], rope[2][2];
     uint2 scales[2];          // 8 bytes of the row's scale area, the chunk-th 8
 
-    __device__ __forceinline__ int chunk() const { return (lane >> 4) * 2 + (lane & 1); }
-    __device__ __forceinline__ int row() const { return warp * 16 + ((lane >> 1) & 7); }
-    // the lane that has chunk i of this lane's rows
-    __device__ __forceinline__ int lane_of(int i) const { return (lane & 0x0E) | ((i >> 1) << 4) | (i & 1); }
+    __device__ __forceinline__ int chunk() const { return lane & 3; }
+    // 8 lanes that store together are two rows and both blocks of a pair: in
+    // the second block the pieces go in the order 2 3 0 1, so that none of the
+    // 8 meet in a bank
+    __device__ __forceinline__ int turn() const { return lane & 2; }
 
-    // warp: 0 .. 7; first_row: row of the sequence's entry 0 in the cache
-    __device__ __forceinline__ Producer(const Fp4TileArgs& a_, Fp4TileShared& s_, uint8_t* kv_s, int warp_, int t_,
-                                        int e_beg, int e_end_, int ntiles_, int64_t first_row)
-        : a(a_), s(s_), warp(warp_), lane(threadIdx.x & 31), row0((int)first_row), t(t_), e_end(e_end_),
-          ntiles(ntiles_) {
-        tile = tc::smem_u32(kv_s) + row() * 128;
-        e0 = e_beg + row();
+    // warp: 0 .. 7 of the producers (warp % 4 is its tensor-memory quarter);
+    // first_row: row of the sequence's entry 0 in the cache
+    __device__ __forceinline__ Producer(const Fp4TileArgs& a_, Fp4TileShared& s_, uint8_t* kv_s, uint32_t slots, int warp,
+                                        int t_, int e_beg, int e_end_, int ntiles_, int64_t first_row)
+        : a(a_), s(s_), lane(threadIdx.x & 31), row0((int)first_row), t(t_), e_end(e_end_), ntiles(ntiles_) {
+        const int rows = 32 * (warp & 3) + 16 * (warp >> 2);
+        row = rows + (lane >> 2);
+        tile = tc::smem_u32(kv_s) + row * 128;
+        tmem = slots + ((uint32_t)rows << 16);
+        e0 = e_beg + row;
         next[0] = entry(0, 0);
         next[1] = entry(0, 1);
         if (ntiles > 0) load(0);
@@ -139,16 +144,16 @@ struct Producer {
     }
     // where channels d .. d+7 of row r are stored
     __device__ __forceinline__ uint32_t at(int d, int r) const {
-        return tile + (d >> 6) * kBlockBytes + r * 1024 + ((((d >> 3) & 7) ^ (row() & 7)) << 4);
+        return tile + (d >> 6) * kBlockBytes + r * 1024 + ((((d >> 3) & 7) ^ (row & 7)) << 4);
     }
     // stores tile j, then loads tile j + 1; false when a wait ran out
     __device__ __forceinline__ bool store(int j) {
-        const int last = last_early_pair(a), nq = a.f.Q / 16;
+        const int nq = a.f.Q / 16;
         uint32_t base[2], post[2];
         bool large = false;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            uint32_t E = __shfl_sync(0xffffffffu, nq & 4 ? scales[r].y : scales[r].x, lane_of((nq >> 3) & 3));
+            uint32_t E = __shfl_sync(0xffffffffu, nq & 4 ? scales[r].y : scales[r].x, (lane & 28) | ((nq >> 3) & 3));
             E = (E >> (8 * (nq & 3))) & 255u;
             // (without rotary channels it lies past the 32 bytes that are kept)
             if (nq == 32) E = cur[r] >= 0 ? __ldg(a.kv4 + (int64_t)cur[r] * a.f.bytes + a.f.scale_off + 32) : 32;
@@ -163,63 +168,102 @@ struct Producer {
 #pragma unroll
         for (int i = kPairs - 1; i >= 0; --i) {
             if (i >= a.mtiles || !ok) continue;
-            // tile j-1's products have read it
-            if (j > 0) ok = __all_sync(0xffffffffu, wait(&s.empty[i], (j - 1) & 1, s, a.status));
+            // tile j-1's O product has read the blocks. (Its S products then
+            // have read all slots; a tile's last pair of 4 takes the slot of
+            // its first.)
+            const int order = a.mtiles - 1 - i, slot = order % kSlots;
+            if (j > 0) ok = wait(&s.empty[i], (j - 1) & 1, s, a.status);
+            if (kTmem && order >= kSlots) ok = wait(&s.slot_free, j & 1, s, a.status) && ok;
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) continue;
+            const bool codes = 4 * i + chunk() < a.f.Q / 32;
+            if (128 * (i + 1) > a.f.Q) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                // the two scales of this lane's chunk in pair i
-                const uint32_t sx = __shfl_sync(0xffffffffu, scales[r].x, lane_of(i));
-                const uint32_t sy = __shfl_sync(0xffffffffu, scales[r].y, lane_of(i));
-                if (4 * i + chunk() < a.f.Q / 32) {
-                    const uint32_t two = (chunk() & 2 ? sy : sx) >> (16 * (chunk() & 1));
-                    const uint32_t S0 = __byte_perm(base[r] + ((two & 255u) << 4), 0, 0x1010);
-                    const uint32_t S1 = __byte_perm(base[r] + ((two >> 4) & 0xff0u), 0, 0x1010);
-                    const uint32_t w[4] = {raw[r][i].x, raw[r][i].y, raw[r][i].z, raw[r][i].w};
-                    const uint32_t dst = at(128 * i + 32 * chunk(), r);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        uint32_t o[4];
-                        fp4_word_small(w[u], u < 2 ? S0 : S1, o);
-                        if (large) {
-#pragma unroll
-                            for (int v = 0; v < 4; ++v) o[v] = mul_bf16x2(o[v], post[r]);
-                        }
-                        st_shared16(dst ^ (u << 4), make_uint4(o[0], o[1], o[2], o[3]));
-                    }
-                }
-                if (128 * (i + 1) > a.f.Q) {
+                for (int r = 0; r < 2; ++r) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const int d = a.f.Q + (4 * u + chunk()) * 8;
                         if (4 * u + chunk() < a.f.R / 8 && d >> 7 == i) st_shared16(at(d, r), rope[r][u]);
                     }
-                    if (i > last)
-                        for (int n = 8 + chunk(); n < a.f.R / 8; n += 4) {
-                            const int d = a.f.Q + n * 8;
-                            if (d >> 7 != i) continue;
-                            if (cur[r] >= 0) cp_async16(at(d, r), a.kv4 + (int64_t)cur[r] * a.f.bytes + a.f.rope_off + n * 16);
-                            else st_shared16(at(d, r), make_uint4(0, 0, 0, 0));
+                    for (int n = 8 + chunk(); n < a.f.R / 8; n += 4) {
+                        const int d = a.f.Q + n * 8;
+                        if (d >> 7 != i) continue;
+                        if (cur[r] >= 0) cp_async16(at(d, r), a.kv4 + (int64_t)cur[r] * a.f.bytes + a.f.rope_off + n * 16);
+                        else st_shared16(at(d, r), make_uint4(0, 0, 0, 0));
+                    }
+                }
+                if (a.f.R > 64) cp_async_wait_all();
+                __syncwarp();
+            }
+            // the two scales of this lane's chunk in pair i
+            uint32_t two[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint32_t sx = __shfl_sync(0xffffffffu, scales[r].x, (lane & 28) | i);
+                const uint32_t sy = __shfl_sync(0xffffffffu, scales[r].y, (lane & 28) | i);
+                two[r] = (chunk() & 2 ? sy : sx) >> (16 * (chunk() & 1));
+                if (turn()) two[r] = __byte_perm(two[r], 0, 0x4401);
+            }
+            const uint32_t dst = at(128 * i + 32 * chunk(), 0) ^ (turn() << 4);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {                 // 16 channels of a scale
+                uint32_t v[16];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    if (codes) {
+                        const uint32_t S = __byte_perm(base[r] + (((two[r] >> (8 * n)) & 255u) << 4), 0, 0x1010);
+                        const uint4 x = raw[r][i];
+                        const bool high = (n == 1) != (turn() != 0);
+                        const uint32_t w[2] = {high ? x.z : x.x, high ? x.w : x.y};
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            uint32_t o[4];
+                            fp4_word_small(w[u], S, o);
+                            if (large) {
+#pragma unroll
+                                for (int m = 0; m < 4; ++m) o[m] = mul_bf16x2(o[m], post[r]);
+                            }
+                            st_shared16((dst + r * 1024) ^ ((2 * n + u) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+                            v[8 * u + 2 * r] = o[0];
+                            v[8 * u + 2 * r + 1] = o[1];
+                            v[8 * u + 2 * r + 4] = o[2];
+                            v[8 * u + 2 * r + 5] = o[3];
                         }
+                    } else if (kTmem) {
+                        // a rotary chunk, as the lanes of the row have stored it
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const uint4 o = ld_shared16((dst + r * 1024) ^ ((2 * n + u) << 4));
+                            v[8 * u + 2 * r] = o.x;
+                            v[8 * u + 2 * r + 1] = o.y;
+                            v[8 * u + 2 * r + 4] = o.z;
+                            v[8 * u + 2 * r + 5] = o.w;
+                        }
+                    }
+                }
+                if (kTmem) {
+                    __syncwarp();
+                    tc::tmem_st_16x32(tmem + slot * 64 + n * 32, v);
                 }
             }
-            if (i <= last) {
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&s.full[i]);
+            if (kTmem) {
+                tc::tmem_st_wait();
+                tc::tc_fence_before();
             }
-        }
-        if (last + 1 < a.mtiles) {
-            cp_async_wait_all();
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && ok)
-                for (int i = a.mtiles - 1; i > last; --i) tc::mbar_arrive(&s.full[i]);
+            if (lane == 0) tc::mbar_arrive(&s.full[i]);
         }
         if (j + 1 < ntiles) load(j + 1);
         return ok;
     }
 };
+
+// Where channel d (even) of a pair lies in the K order of a kTmem product.
+__device__ __forceinline__ int channel_order(int d) {
+    const int chunk = d >> 5, word = ((d & 31) >> 1) ^ (chunk & 2 ? 8 : 0);
+    return (word >> 1) * 16 + chunk * 4 + (word & 1) * 2;
+}
 
 }  // namespace fp4_tile
 }  // namespace csa

@@ -5,31 +5,32 @@
 //
 // One CTA serves (query, up to 64 heads, one split of the query's entries)
 // and walks the split in tiles of 128 entries. Producer warps read the packed
-// rows, expand them to bf16 (exact) and store the tile in shared memory, where
-// ONE copy of it (128 entries x c dims in 64-dim blocks, 128-byte swizzle)
-// feeds both products, key and value being the same row:
-//   S^T  = V_tile . q^T         M = 128 entries, N = 64 heads, K = c
-//   O^T += V_tile^T . P^T       M = 128 dims,    N = 64 heads, K = 128 entries
-// S^T (two buffers) and O^T live in tensor memory. The softmax keeps a
-// reference maximum per head that moves (O^T and the sums are then rescaled)
-// only when a logit passes it by 2^24; normalisation uses the same reference,
-// so the result does not depend on when it moves, and the weights' rounding is
+// rows, expand them to bf16 (exact) and store the tile twice, key and value
+// being the same row: in shared memory (64-dim blocks, 128-byte swizzle) and,
+// pair of blocks by pair, in tensor memory, entries as lanes:
+//   S^T  = V_tile . q^T         M = 128 entries, N = 64 heads, K = c  (tensor memory)
+//   O^T += V_tile^T . P^T       M = 128 dims,    N = 64 heads, K = 128 entries (shared)
+// S^T and O^T live in tensor memory, too. The softmax keeps a reference
+// maximum per head that moves (O^T and the sums are then rescaled) only when a
+// logit passes it by 2^24; normalisation uses the same reference, so the
+// result does not depend on when it moves, and the weights' rounding is
 // relative (with 2^8 it moved in every second tile, 2500 cycles each). P is
 // rounded to bf16 for the second product; sums, maxima and O stay fp32.
 //
 // Warps 0-7: softmax, warp w on TMEM lanes 32 (w % 4).. (a thread per entry)
 // and 32 heads. Warps 8-15: producers, with the next tile's codes in registers
 // by the time a block is free. Blocks go back and forth in pairs (128 dims, one
-// M tile of the O product), the last first. One thread of warp 0 issues the S
-// products, one of warp 4 the O products: those warps would only wait
+// M tile of the O product), the last first. Warp 0 issues the S
+// products, warp 4 the O products: those warps would only wait
 // meanwhile, and 16 warps leave each thread 128 registers (loaded codes that
 // spill are waited for at once: with 18 warps and 96 registers a tile took
 // 10500 cycles).
 //
-// What a tile costs is shared-memory bandwidth: the two products read 384 KB
-// (O at 113 bytes a cycle, near the 128 there are, so the expansion's stores
-// hardly advance while it runs), the stores write 128 KB; 4900 cycles with
-// nothing else in the way.
+// What a tile costs is shared-memory bandwidth: the expansion's stores write
+// 128 KB, the O product reads 192 KB (113 bytes a cycle, near the 128 there
+// are, so the stores hardly advance while it runs), the S product the 64 KB of
+// q; reading its V operand from shared memory, too, took 130 cycles per
+// instruction instead of IFM.
 //
 // Entries outside the query's set are stored as zeros and get weight 0: no
 // row that the query does not see is read.
@@ -39,7 +40,6 @@
 // more go through the workspace and mqa_combine. Either way in split order.
 #include "fp4_tile.cuh"
 #include "kernels.h"
-#include "tmap.h"
 
 namespace csa {
 
@@ -49,6 +49,7 @@ using namespace fp4_tile;
 
 constexpr int kThreads = 512;           // 8 softmax warps, 8 producers
 constexpr int kHalf = kHg / 2;          // heads per softmax warp
+constexpr uint32_t kTmemCols = 512;     // S^T 64, slots 192, O^T up to 256
 constexpr int kMaxCluster = 8;
 constexpr float kMoveLog2 = 24.0f, kLn2 = 0.6931471805599453f;
 
@@ -56,6 +57,7 @@ enum Merge { kDirect, kCluster, kWorkspace };
 
 struct Args : Fp4TileArgs {
     QueryMap qm;
+    const bf16* q;
     const float* sink;
     bf16* out;
     float* lse;
@@ -63,7 +65,6 @@ struct Args : Fp4TileArgs {
     float* part_ml;
     int64_t split_len;
     int n_seq, mp, H, nsplit, merge;
-    uint32_t tmem_cols;
     float scale_log2;
 };
 
@@ -96,46 +97,72 @@ __device__ __forceinline__ bool half_any(int half, bool v) {
     return r != 0;
 }
 
-// S^T of tile j (one thread): pairs as they are stored.
-__device__ __forceinline__ bool issue_s(const Args& a, Shared& s, uint32_t kv_addr, uint32_t q_addr, uint32_t d_tmem,
+// S^T of tile j (a whole warp): pairs as they are stored, each from its slot.
+__device__ __forceinline__ bool issue_s(const Args& a, Shared& s, uint32_t slots, uint32_t q_addr, uint32_t d_tmem,
                                         int j) {
     const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
-    for (int n = 0; n < a.mtiles; ++n) {
-        const int i = stored_pair(a, n);
-        if (!wait(&s.full[i], j & 1, s, a.status)) {
+    for (int i = a.mtiles - 1, slot = 0; i >= 0; --i, slot = slot == kSlots - 1 ? 0 : slot + 1) {
+        const bool ok = __all_sync(0xffffffffu, wait(&s.full[i], j & 1, s, a.status));
+        if (!ok) {
             // the products already issued end before the CTA frees their memory
-            tc::umma_commit(&s.fin);
+            tc::umma_commit_warp(&s.fin);
             tc::mbar_wait(&s.fin, 0, kWaitLimit);
             return false;
         }
         tc::tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-            const int b = 2 * i + (kk >> 2);
-            tc::umma_bf16(d_tmem, tc::sdesc_sw128(kv_addr + b * kBlockBytes + (kk & 3) * 32, 16, 1024),
-                          tc::sdesc_sw128(q_addr + b * (kHg * 128) + (kk & 3) * 32, 16, 1024), idesc, (n | kk) ? 1u : 0u);
-        }
+        for (int kk = 0; kk < 8; ++kk)
+            tc::umma_bf16_ta_warp(d_tmem, slots + slot * 64 + kk * 8,
+                                  tc::sdesc_sw128(q_addr + (2 * i + (kk >> 2)) * (kHg * 128) + (kk & 3) * 32, 16, 1024),
+                                  idesc, (i < a.mtiles - 1 || kk) ? 1u : 0u);
+        if (i == kSlots) tc::umma_commit_warp(&s.slot_free);
     }
-    tc::umma_commit(&s.s_full);
+    tc::umma_commit_warp(&s.s_full);
     return true;
 }
 
-// O^T += of tile j (one thread); each pair of blocks goes back to the
+// O^T += of tile j (a whole warp); each pair of blocks goes back to the
 // producers once its product is done, the last first.
 __device__ __forceinline__ bool issue_o(const Args& a, Shared& s, uint32_t kv_addr, uint32_t p_addr, uint32_t d_tmem,
                                         int j) {
     const uint32_t idesc = tc::idesc_bf16_f32(128, kHg, 1, 1);
-    if (!wait(&s.p_full, j & 1, s, a.status)) return false;
+    if (!__all_sync(0xffffffffu, wait(&s.p_full, j & 1, s, a.status))) return false;
     tc::tc_fence_after();
     for (int mt = a.mtiles - 1; mt >= 0; --mt) {
 #pragma unroll
         for (int ke = 0; ke < kE / 16; ++ke)
-            tc::umma_bf16(d_tmem + mt * kHg, tc::sdesc_sw128(kv_addr + 2 * mt * kBlockBytes + ke * 2048, kBlockBytes, 1024),
-                          tc::sdesc_sw128(p_addr + ke * 2048, kE * 128, 1024), idesc, (j > 0 || ke > 0) ? 1u : 0u);
-        tc::umma_commit(&s.empty[mt]);
+            tc::umma_bf16_warp(d_tmem + mt * kHg,
+                               tc::sdesc_sw128(kv_addr + 2 * mt * kBlockBytes + ke * 2048, kBlockBytes, 1024),
+                               tc::sdesc_sw128(p_addr + ke * 2048, kE * 128, 1024), idesc, (j > 0 || ke > 0) ? 1u : 0u);
+        tc::umma_commit_warp(&s.empty[mt]);
     }
-    tc::umma_commit(&s.o_done);
+    tc::umma_commit_warp(&s.o_done);
     return true;
+}
+
+// The query block [64 heads][c] as B operand of S^T: K-major, the channels of
+// each pair in the order in which the expansion leaves them in tensor memory.
+// Rows past the last head are zero.
+__device__ __forceinline__ void load_q(const Args& a, const bf16* q, int heads, uint8_t* q_s, int tid) {
+    const int cpr = a.f.c / 8, pieces = kHg * cpr;        // 16-byte pieces
+    for (int p0 = tid; p0 < pieces; p0 += 4 * 256) {
+        uint4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int p = p0 + 256 * u, h = p / cpr;
+            v[u] = make_uint4(0, 0, 0, 0);
+            if (p < pieces && h < heads) v[u] = __ldg(reinterpret_cast<const uint4*>(q) + p);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int p = p0 + 256 * u, h = p / cpr, d = (p - h * cpr) * 8;
+            if (p >= pieces) continue;
+            uint8_t* blk = q_s + (size_t)(d >> 7) * 2 * kHg * 128;
+            const int k0 = channel_order(d & 127), k1 = channel_order((d & 127) + 4);
+            *reinterpret_cast<uint2*>(blk + (k0 >> 6) * kHg * 128 + tc::sw128_offset(h, k0 & 63)) = make_uint2(v[u].x, v[u].y);
+            *reinterpret_cast<uint2*>(blk + (k1 >> 6) * kHg * 128 + tc::sw128_offset(h, k1 & 63)) = make_uint2(v[u].z, v[u].w);
+        }
+    }
 }
 
 // v[i] of 32 lanes -> in lane l every lane's v[l / 2] combined (16 shuffles)
@@ -157,9 +184,42 @@ __device__ __forceinline__ float lanes_reduce16(float* v, int lane, Op op) {
     return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
+// out[i] (4 dims each) for i in [lo, hi): the cluster's staged sums, weighted.
+template <int kN>
+__device__ __forceinline__ void merge_items(const Args& a, const Shared& s, const uint8_t* stage, bf16* out, int lo,
+                                            int hi, int c4) {
+    constexpr int kB = 8 / kN;
+    const uint32_t addr = tc::smem_u32(stage);
+    for (int i0 = lo + threadIdx.x; i0 < hi; i0 += kB * kThreads) {
+        float4 o[kB][kN];
+#pragma unroll
+        for (int u = 0; u < kB; ++u)
+#pragma unroll
+            for (int r = 0; r < kN; ++r)
+                if (i0 + u * kThreads < hi && r < a.nsplit)
+                    o[u][r] = ld_cluster4(tc::mapa(addr + (uint32_t)(i0 + u * kThreads) * 16, r));
+#pragma unroll
+        for (int u = 0; u < kB; ++u) {
+            const int i = i0 + u * kThreads, h = i / c4;
+            if (i >= hi) break;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int r = 0; r < kN; ++r) {
+                const float w = r < a.nsplit ? s.coef[r][h] : 0.f;
+                if (w != 0.f) {                           // (a split without entries has staged nothing)
+                    acc.x = fmaf(w, o[u][r].x, acc.x);
+                    acc.y = fmaf(w, o[u][r].y, acc.y);
+                    acc.z = fmaf(w, o[u][r].z, acc.z);
+                    acc.w = fmaf(w, o[u][r].w, acc.w);
+                }
+            }
+            store4(out + (int64_t)i * 4, acc.x, acc.y, acc.z, acc.w);
+        }
+    }
+}
+
 template <bool kSparse>
-__global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_constant__ Args a,
-                                                              const __grid_constant__ CUtensorMap tmQ) {
+__global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_constant__ Args a) {
     extern __shared__ uint8_t smem_raw[];
     // (an offset, not a rounded pointer: the accesses stay shared-memory ones)
     uint8_t* kv_s = smem_raw + ((0u - tc::smem_u32(smem_raw)) & 1023u);           // dblocks x 16 KB
@@ -169,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
 
     pdl_wait();
     pdl_launch_next();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // (uniform)
     const int t = blockIdx.z, h0 = blockIdx.y * kHg, split = blockIdx.x;
     const int seq = a.qm.seq_of(t);
     int64_t n_ent = 0;
@@ -183,8 +243,9 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             tc::mbar_init(&s.full[i], kProducers / 32);
             tc::mbar_init(&s.empty[i], 1);
         }
+        tc::mbar_init(&s.slot_free, 1);
         tc::mbar_init(&s.s_full, 1);
-        tc::mbar_init(&s.q_full, 1);
+        tc::mbar_init(&s.q_full, 8);             // softmax warps
         tc::mbar_init(&s.p_full, 8);
         tc::mbar_init(&s.o_done, 1);
         tc::mbar_init(&s.fin, 1);
@@ -192,16 +253,17 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         s.abort = 0;
     }
     if (warp == 0) {
-        tc::tmem_alloc(&s.tmem, a.tmem_cols);
+        tc::tmem_alloc(&s.tmem, kTmemCols);
         tc::tmem_relinquish();
         tc::tc_fence_before();
     }
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tmem_S = s.tmem, tmem_O = s.tmem + kHg;
+    const uint32_t tmem_S = __shfl_sync(0xffffffffu, s.tmem, 0), slots = tmem_S + kHg, tmem_O = slots + kSlots * 64;
 
     if (warp >= 8) {
-        Producer<kSparse> producer(a, s, kv_s, warp - 8, t, (int)e_beg, (int)e_end, ntiles, (ntiles ? seq : 0) * a.Nmax);
+        Producer<kSparse, true> producer(a, s, kv_s, slots, warp - 8, t, (int)e_beg, (int)e_end, ntiles,
+                                         (ntiles ? seq : 0) * a.Nmax);
         for (int j = 0; j < ntiles; ++j)
             if (!producer.store(j)) break;
     } else {
@@ -210,7 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         const int row = quad * 32 + lane;                 // entry of the tile, TMEM lane
         const int hth = tid & 127;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const uint32_t kv_addr = tc::smem_u32(kv_s), q_addr = tc::smem_u32(q_s), p_addr = tc::smem_u32(p_s);
+        const uint32_t kv_addr = __shfl_sync(0xffffffffu, tc::smem_u32(kv_s), 0);
+        const uint32_t q_addr = kv_addr + a.dblocks * kBlockBytes, p_addr = q_addr + a.dblocks * kHg * 128;
         if (hth < kHalf) {
             s.mref[hb + hth] = s.limit[hb + hth] = -INFINITY;
             s.mexp[hb + hth] = 0.f;
@@ -220,16 +283,17 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         for (int i = 0; i < kHalf; ++i) lpart[i] = 0.f;
         half_sync(half);
         bool ok = true;
-        int done_s = 0, done_o = 0;                       // products issued by this thread
-        if (tid == 0 && ntiles > 0) {
-            tc::mbar_expect_tx(&s.q_full, (uint32_t)a.dblocks * kHg * 128);
-            for (int b = 0; b < a.dblocks; ++b)
-                tc::tma_load_2d(q_s + (size_t)b * kHg * 128, &tmQ, &s.q_full, b * 64, t * a.H + h0);
-            ok = wait(&s.q_full, 0, s, a.status);
+        int done_s = 0, done_o = 0;                       // products issued by this warp
+        if (ntiles > 0) {
+            load_q(a, a.q + ((int64_t)t * a.H + h0) * a.f.c, a.H - h0, q_s, tid);
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&s.q_full);
+            if (warp == 0) ok = __all_sync(0xffffffffu, wait(&s.q_full, 0, s, a.status));
         }
         for (int j = 0; j < ntiles; ++j) {
-            if (tid == 0 && ok) {
-                ok = issue_s(a, s, kv_addr, q_addr, tmem_S, j);
+            if (warp == 0 && __all_sync(0xffffffffu, ok)) {
+                ok = issue_s(a, s, slots, q_addr, tmem_S, j);
                 done_s += ok;
             }
             __syncwarp();
@@ -311,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&s.p_full);
-            if (tid == 128 && ok) {
+            if (warp == 4 && __all_sync(0xffffffffu, ok)) {
                 ok = issue_o(a, s, kv_addr, p_addr, tmem_O, j);
                 done_o += ok;
             }
@@ -319,10 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         }
         if (ok && ntiles > 0) ok = wait(&s.o_done, (ntiles - 1) & 1, s, a.status);
         if (!ok) {
-            // a wait ran out: the products and copies already issued still end
+            // a wait ran out: the products already issued still end
             if (done_s) tc::mbar_wait(&s.s_full, (done_s - 1) & 1, kWaitLimit);
             if (done_o) tc::mbar_wait(&s.o_done, (done_o - 1) & 1, kWaitLimit);
-            if (tid == 0) tc::mbar_wait(&s.q_full, 0, kWaitLimit);
         }
         __syncwarp();
         // per-head sums in a fixed order: lanes, then the four warps
@@ -412,30 +475,13 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                 a.lse[(int64_t)t * a.H + h0 + tid] = Lt == 0.f ? -INFINITY : fmaf(M, kLn2, logf(Lt));
         }
         __syncthreads();
-        // this split's share of the (head, 4 dims) items, all splits' sums in split order
+        // this split's share of the (head, 4 dims) items, all splits' sums in
+        // split order; 8 loads in flight before the first is used
         const int items = nh * c4, lo = (int)((int64_t)items * split / a.nsplit);
         const int hi = (int)((int64_t)items * (split + 1) / a.nsplit);
-        const uint32_t stage = tc::smem_u32(kv_s);
-        for (int i = lo + tid; i < hi; i += kThreads) {
-            const int h = i / c4;
-            // (every split's load is in flight before the first is used)
-            float4 o[kMaxCluster];
-#pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r)
-                if (r < a.nsplit) o[r] = ld_cluster4(tc::mapa(stage + (uint32_t)i * 16, r));
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r) {
-                const float w = r < a.nsplit ? s.coef[r][h] : 0.f;
-                if (w != 0.f) {
-                    acc.x = fmaf(w, o[r].x, acc.x);
-                    acc.y = fmaf(w, o[r].y, acc.y);
-                    acc.z = fmaf(w, o[r].z, acc.z);
-                    acc.w = fmaf(w, o[r].w, acc.w);
-                }
-            }
-            store4(out + (int64_t)i * 4, acc.x, acc.y, acc.z, acc.w);
-        }
+        if (a.nsplit <= 2) merge_items<2>(a, s, kv_s, out, lo, hi, c4);
+        else if (a.nsplit <= 4) merge_items<4>(a, s, kv_s, out, lo, hi, c4);
+        else merge_items<8>(a, s, kv_s, out, lo, hi, c4);
         tc::cluster_sync();                               // no peer still reads this CTA's sums
     } else {
         __syncthreads();
@@ -459,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     }
     if (warp == 0) {
         tc::tc_fence_after();
-        tc::tmem_dealloc(s.tmem, a.tmem_cols);
+        tc::tmem_dealloc(s.tmem, kTmemCols);
     }
 }
 
@@ -498,6 +544,7 @@ cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {
     Args a{};
     a.qm = QueryMap{x.qs.seq, x.qs.pos, x.qs.pos_base, x.qs.single_seq};
     a.kv4 = x.kv4;
+    a.q = (const bf16*)x.q;
     a.idx = x.idx;
     a.sink = x.sink;
     a.out = (bf16*)x.out;
@@ -517,17 +564,14 @@ cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {
     a.merge = merge_of(x.nq, x.H, ns);
     a.dblocks = x.c / 64;
     a.mtiles = x.c / 128;
-    a.tmem_cols = kHg * (1 + a.mtiles) <= 128 ? 128 : kHg * (1 + a.mtiles) <= 256 ? 256 : 512;
     a.scale_log2 = x.scale * kLog2e;
-    CUtensorMap tmQ;
-    if (!make_tmap_bf16_2d(&tmQ, x.q, (uint64_t)x.nq * x.H, x.c, x.c, kHg, 64)) return cudaErrorInvalidValue;
     const size_t smem = 1024 + (size_t)a.dblocks * (kBlockBytes + kHg * 128) + kE * 128 + sizeof(Shared);
     auto kern = x.idx ? mqa_fp4_kernel<true> : mqa_fp4_kernel<false>;
     cudaError_t e = smem_ceiling(kern);
     if (e != cudaSuccess) return e;
     CSA_LAUNCH(st, "mqa_fp4",
                e = launch_pdl(kern, dim3(ns, (x.H + kHg - 1) / kHg, x.nq), dim3(kThreads), smem, st,
-                              a.merge == kCluster ? (unsigned)ns : 0u, a, tmQ));
+                              a.merge == kCluster ? (unsigned)ns : 0u, a));
     if (e != cudaSuccess) return e;
     if (a.merge == kWorkspace) {
         e = mqa_combine_bf16(a.part_o, a.part_ml, ns, x.nq, x.H, x.c, x.sink, x.out, x.lse, st);

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
 
     pdl_wait();
     pdl_launch_next();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // (uniform)
     const int b = blockIdx.y;
     const int seq = a.seq_of_q ? a.seq_of_q[b] : b;
     const Blocks<kSparse> blocks{a, b};
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
     tc::tc_fence_after();
     const int e_end = s.n_max < e_stop ? s.n_max : e_stop;
     const int ntiles = e_end > e_beg ? (e_end - e_beg + kE - 1) / kE : 0;
-    const uint32_t tmem_S = s.tmem;
+    const uint32_t tmem_S = __shfl_sync(0xffffffffu, s.tmem, 0);
     const bool stay = a.T * a.hgroups == 1;
 
     if (warp == 13) {
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
                     if (blocks.visible(t) <= e_tile) continue;
                     for (int g = 0; ok && g < a.hgroups; ++g, ++n)
                         for (int o = 0; o < a.mtiles; ++o) {
-                            const int i = stored_pair(a, o);
+                            const int i = a.mtiles - 1 - o;               // as they are stored
                             if (n > 0 && !(ok = wait(&s.q_empty[i], (n - 1) & 1, s, a.status))) break;
                             tc::mbar_expect_tx(&s.q_full[i], 2 * kHg * 128);
                             for (int h = 0; h < 2; ++h)
@@ -139,8 +139,9 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
         __syncwarp();
     } else if (warp == 12) {
         // ------------------------------------------------------------ products
-        if (lane == 0 && ntiles > 0) {
-            const uint32_t kv_addr = tc::smem_u32(kv_s), q_addr = tc::smem_u32(q_s);
+        if (ntiles > 0) {
+            const uint32_t kv_addr = __shfl_sync(0xffffffffu, tc::smem_u32(kv_s), 0);
+            const uint32_t q_addr = kv_addr + a.dblocks * kBlockBytes;
             const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
             uint32_t n = 0;
             bool ok = true;
@@ -151,34 +152,34 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
                     if (blocks.visible(t) <= e_tile) continue;
                     for (int g = 0; ok && g < a.hgroups; ++g, ++n) {
                         const uint32_t sb = n & 1;
-                        if (n >= 2 && !(ok = wait(&s.s_empty[sb], ((n >> 1) - 1) & 1, s, a.status))) break;
+                        if (n >= 2 && !(ok = __all_sync(0xffffffffu, wait(&s.s_empty[sb], ((n >> 1) - 1) & 1, s, a.status)))) break;
                         for (int o = 0; o < a.mtiles; ++o) {
-                            const int i = stored_pair(a, o);
-                            if (!(ok = wait(&s.q_full[i], stay ? 0 : n & 1, s, a.status))) break;
-                            if (first && !(ok = wait(&s.full[i], j & 1, s, a.status))) break;
+                            const int i = a.mtiles - 1 - o;               // as they are stored
+                            if (!(ok = __all_sync(0xffffffffu, wait(&s.q_full[i], stay ? 0 : n & 1, s, a.status)))) break;
+                            if (first && !(ok = __all_sync(0xffffffffu, wait(&s.full[i], j & 1, s, a.status)))) break;
                             tc::tc_fence_after();
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk) {
                                 const int blk = 2 * i + (kk >> 2);
-                                tc::umma_bf16(tmem_S + sb * kHg,
+                                tc::umma_bf16_warp(tmem_S + sb * kHg,
                                               tc::sdesc_sw128(kv_addr + blk * kBlockBytes + (kk & 3) * 32, 16, 1024),
                                               tc::sdesc_sw128(q_addr + blk * (kHg * 128) + (kk & 3) * 32, 16, 1024),
                                               idesc, (o | kk) ? 1u : 0u);
                             }
-                            if (!stay) tc::umma_commit(&s.q_empty[i]);
-                            if (t == last && g == a.hgroups - 1) tc::umma_commit(&s.empty[i]);
+                            if (!stay) tc::umma_commit_warp(&s.q_empty[i]);
+                            if (t == last && g == a.hgroups - 1) tc::umma_commit_warp(&s.empty[i]);
                         }
-                        if (ok) tc::umma_commit(&s.s_full[sb]);
+                        if (ok) tc::umma_commit_warp(&s.s_full[sb]);
                         first = false;
                     }
                 }
             }
-            tc::umma_commit(&s.fin);
+            tc::umma_commit_warp(&s.fin);
             tc::mbar_wait(&s.fin, 0, kWaitLimit);
         }
         __syncwarp();
     } else if (warp >= 4) {
-        Producer<kSparse> producer(a, s, kv_s, warp - 4, b, e_beg, e_end, ntiles, (int64_t)(ntiles ? seq : 0) * a.Nmax);
+        Producer<kSparse, false> producer(a, s, kv_s, 0, warp - 4, b, e_beg, e_end, ntiles, (int64_t)(ntiles ? seq : 0) * a.Nmax);
         for (int j = 0; j < ntiles; ++j)
             if (!producer.store(j)) break;
     } else {
