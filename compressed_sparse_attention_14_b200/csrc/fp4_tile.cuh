@@ -68,7 +68,8 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t src) {
 }
 
 // A producer thread's part: of two rows, the 32 channels of chunk `chunk` in
-// every pair of blocks and every fourth 16-byte piece of the rotary channels.
+// its pairs of blocks (8 warps share a pair; with kSets = 2, 16 warps take
+// every second one) and every fourth 16-byte piece of their rotary channels.
 // The 4 lanes of a row read 64 consecutive bytes, a load instruction touches
 // 8 lines (two lanes to a row and 16 lines took twice as long to issue).
 //
@@ -77,14 +78,15 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t src) {
 // a thread has are 4 pieces of 32 channels, and the store puts its words 2u,
 // 2u + 1 into columns 8u + 2 chunk and the next, so K runs over the channels
 // of a pair in another order: channel_order() of it.
-template <bool kSparse, bool kTmem>
+template <bool kSparse, bool kTmem, int kSets>
 struct Producer {
+    static constexpr int kMine = kPairs / kSets;          // pairs of this thread's warp
     const Fp4TileArgs& a;
     Fp4TileShared& s;
     uint32_t tile, tmem;      // this thread's first row in block 0 (the second is 8 rows on); its lanes of slot 0
-    int lane, row, row0, t, e0, e_end, ntiles;    // (rows as numbers: n_seq * Nmax is below 2^31)
+    int lane, set, row, row0, t, e0, e_end, ntiles;   // (rows as numbers: n_seq * Nmax is below 2^31)
     int next[2], cur[2];
-    uint4 raw[2][kPairs], rope[2][2];
+    uint4 raw[2][kMine], rope[2][2];
     uint2 scales[2];          // 8 bytes of the row's scale area, the chunk-th 8
 
     __device__ __forceinline__ int chunk() const { return lane & 3; }
@@ -93,12 +95,17 @@ struct Producer {
     // 8 meet in a bank
     __device__ __forceinline__ int turn() const { return lane & 2; }
 
-    // warp: 0 .. 7 of the producers (warp % 4 is its tensor-memory quarter);
+    // pair k of this thread's, and its place in the order of storing
+    __device__ __forceinline__ int order(int k) const { return set + kSets * k; }
+    __device__ __forceinline__ int pair(int k) const { return a.mtiles - 1 - order(k); }
+    __device__ __forceinline__ bool mine(int i) const { return kSets == 1 || ((a.mtiles - 1 - i) & 1) == set; }
+
+    // warp: 0 .. 8 kSets - 1 of the producers (warp % 4 is its tensor-memory quarter);
     // first_row: row of the sequence's entry 0 in the cache
     __device__ __forceinline__ Producer(const Fp4TileArgs& a_, Fp4TileShared& s_, uint8_t* kv_s, uint32_t slots, int warp,
                                         int t_, int e_beg, int e_end_, int ntiles_, int64_t first_row)
-        : a(a_), s(s_), lane(threadIdx.x & 31), row0((int)first_row), t(t_), e_end(e_end_), ntiles(ntiles_) {
-        const int rows = 32 * (warp & 3) + 16 * (warp >> 2);
+        : a(a_), s(s_), lane(threadIdx.x & 31), set(warp >> 3), row0((int)first_row), t(t_), e_end(e_end_), ntiles(ntiles_) {
+        const int rows = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);
         row = rows + (lane >> 2);
         tile = tc::smem_u32(kv_s) + row * 128;
         tmem = slots + ((uint32_t)rows << 16);
@@ -125,9 +132,10 @@ struct Producer {
             const bool ok = cur[r] >= 0;
             const uint8_t* p = a.kv4 + (int64_t)cur[r] * a.f.bytes;
 #pragma unroll
-            for (int i = 0; i < kPairs; ++i) {
-                raw[r][i] = make_uint4(0, 0, 0, 0);
-                if (ok && 4 * i + chunk() < a.f.Q / 32) raw[r][i] = __ldg(reinterpret_cast<const uint4*>(p) + 4 * i + chunk());
+            for (int k = 0; k < kMine; ++k) {
+                raw[r][k] = make_uint4(0, 0, 0, 0);
+                const int n = 4 * pair(k) + chunk();
+                if (ok && n >= 0 && n < a.f.Q / 32) raw[r][k] = __ldg(reinterpret_cast<const uint4*>(p) + n);
             }
             scales[r] = make_uint2(0x20202020u, 0x20202020u);   // every byte 32, the exponent among them
             if (ok && chunk() * 8 < a.f.rope_off - a.f.scale_off)
@@ -135,7 +143,8 @@ struct Producer {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 rope[r][u] = make_uint4(0, 0, 0, 0);
-                if (ok && 4 * u + chunk() < a.f.R / 8)
+                const int n = 4 * u + chunk();
+                if (ok && n < a.f.R / 8 && mine((a.f.Q + 8 * n) >> 7))
                     rope[r][u] = __ldg(reinterpret_cast<const uint4*>(p + a.f.rope_off) + 4 * u + chunk());
             }
             if (ok)
@@ -166,14 +175,14 @@ struct Producer {
         large = __any_sync(0xffffffffu, large);
         bool ok = true;
 #pragma unroll
-        for (int i = kPairs - 1; i >= 0; --i) {
-            if (i >= a.mtiles || !ok) continue;
+        for (int k = 0; k < kMine; ++k) {
+            const int i = pair(k), slot = order(k) % kSlots;
+            if (i < 0 || !ok) continue;
             // tile j-1's O product has read the blocks. (Its S products then
             // have read all slots; a tile's last pair of 4 takes the slot of
             // its first.)
-            const int order = a.mtiles - 1 - i, slot = order % kSlots;
             if (j > 0) ok = wait(&s.empty[i], (j - 1) & 1, s, a.status);
-            if (kTmem && order >= kSlots) ok = wait(&s.slot_free, j & 1, s, a.status) && ok;
+            if (kTmem && order(k) >= kSlots) ok = wait(&s.slot_free, j & 1, s, a.status) && ok;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) continue;
             const bool codes = 4 * i + chunk() < a.f.Q / 32;
@@ -212,7 +221,7 @@ struct Producer {
                 for (int r = 0; r < 2; ++r) {
                     if (codes) {
                         const uint32_t S = __byte_perm(base[r] + (((two[r] >> (8 * n)) & 255u) << 4), 0, 0x1010);
-                        const uint4 x = raw[r][i];
+                        const uint4 x = raw[r][k];
                         const bool high = (n == 1) != (turn() != 0);
                         const uint32_t w[2] = {high ? x.z : x.x, high ? x.w : x.y};
 #pragma unroll

@@ -17,14 +17,17 @@
 // relative (with 2^8 it moved in every second tile, 2500 cycles each). P is
 // rounded to bf16 for the second product; sums, maxima and O stay fp32.
 //
-// Warps 0-7: softmax, warp w on TMEM lanes 32 (w % 4).. (a thread per entry)
-// and 32 heads. Warps 8-15: producers, with the next tile's codes in registers
-// by the time a block is free. Blocks go back and forth in pairs (128 dims, one
-// M tile of the O product), the last first. Warp 0 issues the S
-// products, warp 4 the O products: those warps would only wait
-// meanwhile, and 16 warps leave each thread 128 registers (loaded codes that
-// spill are waited for at once: with 18 warps and 96 registers a tile took
-// 10500 cycles).
+// Warps 0-15 both expand and do the softmax, which cannot overlap for one tile
+// buffer (the expansion of tile j+1 needs blocks that the O product of tile j
+// has read, the softmax of tile j+1 its S product):
+//   expansion: blocks go back and forth in pairs (128 dims, one M tile of the
+//     O product), the last first; warps 0-7 take every second pair, 8-15 the
+//     others, each 16 entries, with the codes in registers by then;
+//   softmax: warp w has TMEM lanes 32 (w % 4).. (a thread per entry), 16 heads.
+// Warp 16 issues the products: O of tile j, then S of tile j+1 pair by pair as
+// it is stored. It is alone in a warpgroup that gives its registers away: 112
+// are left for each worker (loaded codes that spill are waited for at once:
+// with 96 a tile took 10500 cycles).
 //
 // What a tile costs is shared-memory bandwidth: the expansion's stores write
 // 128 KB, the O product reads 192 KB (113 bytes a cycle, near the 128 there
@@ -47,8 +50,8 @@ namespace {
 
 using namespace fp4_tile;
 
-constexpr int kThreads = 512;           // 8 softmax warps, 8 producers
-constexpr int kHalf = kHg / 2;          // heads per softmax warp
+constexpr int kWorkers = 512, kThreads = kWorkers + 128;
+constexpr int kGh = 16;                 // heads per worker warp
 constexpr uint32_t kTmemCols = 512;     // S^T 64, slots 192, O^T up to 256
 constexpr int kMaxCluster = 8;
 constexpr float kMoveLog2 = 24.0f, kLn2 = 0.6931471805599453f;
@@ -85,15 +88,15 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
     return v;
 }
 
-// barrier (and vote) of the 4 softmax warps that share 32 heads
-__device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
-__device__ __forceinline__ bool half_any(int half, bool v) {
+// barrier (and vote) of the 4 warps that share 16 heads
+__device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
+__device__ __forceinline__ bool group_any(int g, bool v) {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p, q;\n\t"
                  "setp.ne.u32 q, %1, 0;\n\t"
                  "bar.red.or.pred p, %2, 128, q;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(r) : "r"((uint32_t)v), "r"(1 + half) : "memory");
+                 : "=r"(r) : "r"((uint32_t)v), "r"(1 + g) : "memory");
     return r != 0;
 }
 
@@ -145,17 +148,17 @@ __device__ __forceinline__ bool issue_o(const Args& a, Shared& s, uint32_t kv_ad
 // Rows past the last head are zero.
 __device__ __forceinline__ void load_q(const Args& a, const bf16* q, int heads, uint8_t* q_s, int tid) {
     const int cpr = a.f.c / 8, pieces = kHg * cpr;        // 16-byte pieces
-    for (int p0 = tid; p0 < pieces; p0 += 4 * 256) {
+    for (int p0 = tid; p0 < pieces; p0 += 4 * kWorkers) {
         uint4 v[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int p = p0 + 256 * u, h = p / cpr;
+            const int p = p0 + kWorkers * u, h = p / cpr;
             v[u] = make_uint4(0, 0, 0, 0);
             if (p < pieces && h < heads) v[u] = __ldg(reinterpret_cast<const uint4*>(q) + p);
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int p = p0 + 256 * u, h = p / cpr, d = (p - h * cpr) * 8;
+            const int p = p0 + kWorkers * u, h = p / cpr, d = (p - h * cpr) * 8;
             if (p >= pieces) continue;
             uint8_t* blk = q_s + (size_t)(d >> 7) * 2 * kHg * 128;
             const int k0 = channel_order(d & 127), k1 = channel_order((d & 127) + 4);
@@ -190,17 +193,17 @@ __device__ __forceinline__ void merge_items(const Args& a, const Shared& s, cons
                                             int hi, int c4) {
     constexpr int kB = 8 / kN;
     const uint32_t addr = tc::smem_u32(stage);
-    for (int i0 = lo + threadIdx.x; i0 < hi; i0 += kB * kThreads) {
+    for (int i0 = lo + threadIdx.x; i0 < hi; i0 += kB * kWorkers) {
         float4 o[kB][kN];
 #pragma unroll
         for (int u = 0; u < kB; ++u)
 #pragma unroll
             for (int r = 0; r < kN; ++r)
-                if (i0 + u * kThreads < hi && r < a.nsplit)
-                    o[u][r] = ld_cluster4(tc::mapa(addr + (uint32_t)(i0 + u * kThreads) * 16, r));
+                if (i0 + u * kWorkers < hi && r < a.nsplit)
+                    o[u][r] = ld_cluster4(tc::mapa(addr + (uint32_t)(i0 + u * kWorkers) * 16, r));
 #pragma unroll
         for (int u = 0; u < kB; ++u) {
-            const int i = i0 + u * kThreads, h = i / c4;
+            const int i = i0 + u * kWorkers, h = i / c4;
             if (i >= hi) break;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -240,19 +243,19 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
 
     if (tid == 0) {
         for (int i = 0; i < kPairs; ++i) {
-            tc::mbar_init(&s.full[i], kProducers / 32);
+            tc::mbar_init(&s.full[i], 8);            // the warps that share a pair
             tc::mbar_init(&s.empty[i], 1);
         }
         tc::mbar_init(&s.slot_free, 1);
         tc::mbar_init(&s.s_full, 1);
-        tc::mbar_init(&s.q_full, 8);             // softmax warps
-        tc::mbar_init(&s.p_full, 8);
+        tc::mbar_init(&s.q_full, kWorkers / 32);
+        tc::mbar_init(&s.p_full, kWorkers / 32);
         tc::mbar_init(&s.o_done, 1);
         tc::mbar_init(&s.fin, 1);
         tc::fence_mbar_init();
         s.abort = 0;
     }
-    if (warp == 0) {
+    if (warp == 16) {
         tc::tmem_alloc(&s.tmem, kTmemCols);
         tc::tmem_relinquish();
         tc::tc_fence_before();
@@ -261,42 +264,65 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     tc::tc_fence_after();
     const uint32_t tmem_S = __shfl_sync(0xffffffffu, s.tmem, 0), slots = tmem_S + kHg, tmem_O = slots + kSlots * 64;
 
-    if (warp >= 8) {
-        Producer<kSparse, true> producer(a, s, kv_s, slots, warp - 8, t, (int)e_beg, (int)e_end, ntiles,
-                                         (ntiles ? seq : 0) * a.Nmax);
-        for (int j = 0; j < ntiles; ++j)
-            if (!producer.store(j)) break;
-    } else {
-        // ------------------------------------------------------------ softmax
-        const int quad = warp & 3, half = warp >> 2, hb = half * kHalf;
-        const int row = quad * 32 + lane;                 // entry of the tile, TMEM lane
-        const int hth = tid & 127;
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const uint32_t kv_addr = __shfl_sync(0xffffffffu, tc::smem_u32(kv_s), 0);
-        const uint32_t q_addr = kv_addr + a.dblocks * kBlockBytes, p_addr = q_addr + a.dblocks * kHg * 128;
-        if (hth < kHalf) {
-            s.mref[hb + hth] = s.limit[hb + hth] = -INFINITY;
-            s.mexp[hb + hth] = 0.f;
+    if (warp >= 16) {
+        // ------------------------------------------------------------ products
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+        if (warp == 16 && ntiles > 0) {
+            const uint32_t kv_addr = __shfl_sync(0xffffffffu, tc::smem_u32(kv_s), 0);
+            const uint32_t q_addr = kv_addr + a.dblocks * kBlockBytes, p_addr = q_addr + a.dblocks * kHg * 128;
+            bool ok = __all_sync(0xffffffffu, wait(&s.q_full, 0, s, a.status));
+            ok = ok && issue_s(a, s, slots, q_addr, tmem_S, 0);
+            for (int j = 0; ok && j < ntiles; ++j)
+                ok = issue_o(a, s, kv_addr, p_addr, tmem_O, j) &&
+                     (j + 1 == ntiles || issue_s(a, s, slots, q_addr, tmem_S, j + 1));
+            // every product issued has ended before the CTA goes on to free the
+            // memory it uses (also when a wait ran out)
+            tc::umma_commit_warp(&s.fin);
+            tc::mbar_wait(&s.fin, 0, kWaitLimit);
         }
-        float lpart[kHalf];
-#pragma unroll
-        for (int i = 0; i < kHalf; ++i) lpart[i] = 0.f;
-        half_sync(half);
-        bool ok = true;
-        int done_s = 0, done_o = 0;                       // products issued by this warp
+        // the workers' barriers below (code that both ran would have to do
+        // with the fewer registers)
+        __syncthreads();
+        if (a.merge == kCluster) {
+            tc::cluster_sync();
+            __syncthreads();
+            tc::cluster_sync();
+        } else {
+            __syncthreads();
+            __syncthreads();
+        }
+        if (warp == 16) {
+            tc::tc_fence_after();
+            tc::tmem_dealloc(tmem_S, kTmemCols);
+        }
+        return;
+    }
+    // ---------------------------------------------------------------- workers
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+    {
+        const int quad = warp & 3, g = warp >> 2, hb = g * kGh;
+        const int row = quad * 32 + lane;                 // entry of the tile, TMEM lane
+        const int gth = tid & 127;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        if (gth < kGh) {
+            s.mref[hb + gth] = s.limit[hb + gth] = -INFINITY;
+            s.mexp[hb + gth] = 0.f;
+        }
+        Producer<kSparse, true, 2> producer(a, s, kv_s, slots, warp, t, (int)e_beg, (int)e_end, ntiles,
+                                            (ntiles ? seq : 0) * a.Nmax);
         if (ntiles > 0) {
             load_q(a, a.q + ((int64_t)t * a.H + h0) * a.f.c, a.H - h0, q_s, tid);
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&s.q_full);
-            if (warp == 0) ok = __all_sync(0xffffffffu, wait(&s.q_full, 0, s, a.status));
         }
+        float lpart[kGh];
+#pragma unroll
+        for (int i = 0; i < kGh; ++i) lpart[i] = 0.f;
+        group_sync(g);
+        bool ok = true;
         for (int j = 0; j < ntiles; ++j) {
-            if (warp == 0 && __all_sync(0xffffffffu, ok)) {
-                ok = issue_s(a, s, slots, q_addr, tmem_S, j);
-                done_s += ok;
-            }
-            __syncwarp();
+            ok = producer.store(j) && ok;
             const int64_t e = e_beg + (int64_t)j * kE + row;
             bool valid = e < e_end;
             if (kSparse && valid) {
@@ -305,30 +331,26 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             }
             ok = ok && wait(&s.s_full, j & 1, s, a.status);
             tc::tc_fence_after();
-            float z[kHalf];
+            float z[kGh];
             auto logits = [&]() {
-                tc::tmem_ld16(tmem_S + lanes + hb, *reinterpret_cast<float(*)[16]>(z));
-                tc::tmem_ld16(tmem_S + lanes + hb + 16, *reinterpret_cast<float(*)[16]>(z + 16));
+                tc::tmem_ld16(tmem_S + lanes + hb, z);
                 tc::tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < kHalf; ++i) z[i] = valid ? z[i] * a.scale_log2 : -INFINITY;
+                for (int i = 0; i < kGh; ++i) z[i] = valid ? z[i] * a.scale_log2 : -INFINITY;
             };
             logits();
             bool move = false;
 #pragma unroll
-            for (int i = 0; i < kHalf; ++i) move |= z[i] > s.limit[hb + i];
-            if (half_any(half, move || !ok)) {
+            for (int i = 0; i < kGh; ++i) move |= z[i] > s.limit[hb + i];
+            if (group_any(g, move || !ok)) {
                 // all leave together once a wait of one ran out
-                if (half_any(half, !ok)) { ok = false; break; }
+                if (group_any(g, !ok)) { ok = false; break; }
                 // (the reduction consumes the logits; they are read again)
-#pragma unroll
-                for (int cc = 0; cc < kHalf; cc += 16) {
-                    const float top = lanes_reduce16(z + cc, lane, [](float x, float y) { return fmaxf(x, y); });
-                    if (!(lane & 1)) s.red[quad][hb + cc + lane / 2] = top;
-                }
-                half_sync(half);
-                if (hth < kHalf) {
-                    const int h = hb + hth;
+                const float top = lanes_reduce16(z, lane, [](float x, float y) { return fmaxf(x, y); });
+                if (!(lane & 1)) s.red[quad][hb + lane / 2] = top;
+                group_sync(g);
+                if (gth < kGh) {
+                    const int h = hb + gth;
                     const float old = s.mref[h];
                     const float m = fmaxf(fmaxf(fmaxf(s.red[0][h], s.red[1][h]), fmaxf(s.red[2][h], s.red[3][h])), old);
                     s.alpha[h] = old == -INFINITY ? 0.f : ex2(old - m);
@@ -336,68 +358,56 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                     s.limit[h] = m + kMoveLog2;
                     s.mexp[h] = m == -INFINITY ? 0.f : m;
                 }
-                half_sync(half);
+                group_sync(g);
 #pragma unroll
-                for (int i = 0; i < kHalf; ++i) lpart[i] *= s.alpha[hb + i];
+                for (int i = 0; i < kGh; ++i) lpart[i] *= s.alpha[hb + i];
                 if (j > 0) {
                     ok = wait(&s.o_done, (j - 1) & 1, s, a.status);
                     tc::tc_fence_after();
 #pragma unroll 1
-                    for (int n = 0; n < 2 * a.mtiles; ++n) {
-                        const int cc = hb + 16 * (n & 1);
-                        float o[16];
-                        tc::tmem_ld16(tmem_O + lanes + (n >> 1) * kHg + cc, o);
+                    for (int mt = 0; mt < a.mtiles; ++mt) {
+                        float o[kGh];
+                        tc::tmem_ld16(tmem_O + lanes + mt * kHg + hb, o);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] *= s.alpha[cc + i];
-                        tc::tmem_st16(tmem_O + lanes + (n >> 1) * kHg + cc, o);
+                        for (int i = 0; i < kGh; ++i) o[i] *= s.alpha[hb + i];
+                        tc::tmem_st16(tmem_O + lanes + mt * kHg + hb, o);
                     }
                     tc::tmem_st_wait();
                 }
                 logits();
             }
-            uint32_t pk[kHalf / 2];
+            uint32_t pk[kGh / 2];
 #pragma unroll
-            for (int i = 0; i < kHalf; i += 2) {
+            for (int i = 0; i < kGh; i += 2) {
                 const float p0 = ex2(z[i] - s.mexp[hb + i]), p1 = ex2(z[i + 1] - s.mexp[hb + i + 1]);
                 lpart[i] += p0;
                 lpart[i + 1] += p1;
                 const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
                 pk[i >> 1] = *reinterpret_cast<const uint32_t*>(&b2);
             }
-            // the previous tile's O product has read P
-            if (j > 0) ok = wait(&s.o_done, (j - 1) & 1, s, a.status) && ok;
+            // (the previous tile's O product has read P: every pair was free
+            // for this tile, its last included)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4*>(p_s + row * 128 + (((half * 4 + i) ^ (row & 7)) << 4)) =
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<uint4*>(p_s + row * 128 + (((g * 2 + i) ^ (row & 7)) << 4)) =
                     make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
             tc::tc_fence_before();                        // S has been read, too
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&s.p_full);
-            if (warp == 4 && __all_sync(0xffffffffu, ok)) {
-                ok = issue_o(a, s, kv_addr, p_addr, tmem_O, j);
-                done_o += ok;
-            }
-            __syncwarp();
         }
-        if (ok && ntiles > 0) ok = wait(&s.o_done, (ntiles - 1) & 1, s, a.status);
-        if (!ok) {
-            // a wait ran out: the products already issued still end
-            if (done_s) tc::mbar_wait(&s.s_full, (done_s - 1) & 1, kWaitLimit);
-            if (done_o) tc::mbar_wait(&s.o_done, (done_o - 1) & 1, kWaitLimit);
-        }
+        if (ok && ntiles > 0) wait(&s.o_done, (ntiles - 1) & 1, s, a.status);
         __syncwarp();
         // per-head sums in a fixed order: lanes, then the four warps
-        half_sync(half);                                  // red may still be read
-#pragma unroll
-        for (int cc = 0; cc < kHalf; cc += 16) {
-            const float sum = lanes_reduce16(lpart + cc, lane, [](float x, float y) { return x + y; });
-            if (!(lane & 1)) s.red[quad][hb + cc + lane / 2] = sum;
+        group_sync(g);                                    // red may still be read
+        {
+            const float sum = lanes_reduce16(lpart, lane, [](float x, float y) { return x + y; });
+            if (!(lane & 1)) s.red[quad][hb + lane / 2] = sum;
         }
-        half_sync(half);
-        if (hth < kHalf) {
-            const int h = hb + hth;
+        group_sync(g);
+        if (gth < kGh) {
+            const int h = hb + gth;
             s.lsum[h] = (s.red[0][h] + s.red[1][h]) + (s.red[2][h] + s.red[3][h]);
             if (a.merge == kDirect) {
                 const float m = s.mref[h], L = s.lsum[h];
@@ -415,31 +425,31 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     }
     // ---------------------------------------------------------------- epilogue
     __syncthreads();
-    if (warp < 8) {
+    {
         // O^T to shared memory where the tile was, as rows of a head: warp w
-        // has dims 32 (w % 4).. of every M tile and 32 heads
+        // has dims 32 (w % 4).. of every M tile and 16 heads
         tc::tc_fence_after();
-        const int hb = (warp >> 2) * 32, row = (warp & 3) * 32 + lane;
+        const int hb = (warp >> 2) * kGh, row = (warp & 3) * 32 + lane;
         const uint32_t addr = tmem_O + ((uint32_t)((warp & 3) * 32) << 16) + hb;
 #pragma unroll 1
-        for (int n = 0; n < 2 * a.mtiles; ++n) {
-            const int mt = n >> 1, cc = (n & 1) * 16, d = mt * 128 + row;
-            float o[16];
+        for (int mt = 0; mt < a.mtiles; ++mt) {
+            const int d = mt * 128 + row;
+            float o[kGh];
             if (ntiles > 0) {
-                tc::tmem_ld16(addr + mt * kHg + cc, o);
+                tc::tmem_ld16(addr + mt * kHg, o);
                 tc::tmem_ld_wait();
             }
             if (a.merge == kDirect) {                     // normalised, bf16
-                bf16* stage = reinterpret_cast<bf16*>(kv_s) + (size_t)(hb + cc) * a.f.c + d;
+                bf16* stage = reinterpret_cast<bf16*>(kv_s) + (size_t)hb * a.f.c + d;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float al = s.alpha[hb + cc + i];
+                for (int i = 0; i < kGh; ++i) {
+                    const float al = s.alpha[hb + i];
                     stage[(size_t)i * a.f.c] = __float2bfloat16_rn(al != 0.f ? o[i] * al : 0.f);
                 }
             } else if (ntiles > 0) {
-                float* stage = reinterpret_cast<float*>(kv_s) + (size_t)(hb + cc) * a.f.c + d;
+                float* stage = reinterpret_cast<float*>(kv_s) + (size_t)hb * a.f.c + d;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) stage[(size_t)i * a.f.c] = o[i];
+                for (int i = 0; i < kGh; ++i) stage[(size_t)i * a.f.c] = o[i];
             }
         }
         tc::tc_fence_before();
@@ -487,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         __syncthreads();
         if (a.merge == kDirect) {
             const uint4* stage = reinterpret_cast<const uint4*>(kv_s);
-            for (int i = tid; i < nh * a.f.c / 8; i += kThreads) reinterpret_cast<uint4*>(out)[i] = stage[i];
+            for (int i = tid; i < nh * a.f.c / 8; i += kWorkers) reinterpret_cast<uint4*>(out)[i] = stage[i];
         } else {
             const int64_t part = ((int64_t)t * a.nsplit + split) * a.H + h0;
             if (tid < nh) {
@@ -498,14 +508,10 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             if (ntiles > 0) {
                 const float4* stage = reinterpret_cast<const float4*>(kv_s);
                 float4* dst = reinterpret_cast<float4*>(a.part_o + part * a.f.c);
-                for (int i = tid; i < nh * c4; i += kThreads) dst[i] = stage[i];
+                for (int i = tid; i < nh * c4; i += kWorkers) dst[i] = stage[i];
             }
         }
         __syncthreads();
-    }
-    if (warp == 0) {
-        tc::tc_fence_after();
-        tc::tmem_dealloc(s.tmem, kTmemCols);
     }
 }
 
