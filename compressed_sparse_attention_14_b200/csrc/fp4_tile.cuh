@@ -100,6 +100,7 @@ struct Producer {
     __device__ __forceinline__ int pair(int k) const { return a.mtiles - 1 - order(k); }
     __device__ __forceinline__ bool mine(int i) const { return kSets == 1 || ((a.mtiles - 1 - i) & 1) == set; }
 
+    // (load(0) comes before the first store.)
     // warp: 0 .. 8 kSets - 1 of the producers (warp % 4 is its tensor-memory quarter);
     // first_row: row of the sequence's entry 0 in the cache
     __device__ __forceinline__ Producer(const Fp4TileArgs& a_, Fp4TileShared& s_, uint8_t* kv_s, uint32_t slots, int warp,
@@ -112,7 +113,6 @@ struct Producer {
         e0 = e_beg + row;
         next[0] = entry(0, 0);
         next[1] = entry(0, 1);
-        if (ntiles > 0) load(0);
     }
     // entry index of row r in tile j (outside [0, Nmax): none)
     __device__ __forceinline__ int entry(int j, int r) const {
@@ -145,9 +145,9 @@ struct Producer {
                 rope[r][u] = make_uint4(0, 0, 0, 0);
                 const int n = 4 * u + chunk();
                 if (ok && n < a.f.R / 8 && mine((a.f.Q + 8 * n) >> 7))
-                    rope[r][u] = __ldg(reinterpret_cast<const uint4*>(p + a.f.rope_off) + 4 * u + chunk());
+                    rope[r][u] = __ldg(reinterpret_cast<const uint4*>(p + a.f.rope_off) + n);
             }
-            if (ok)
+            if (ok && a.f.R > 64)
                 for (int n = 8 + chunk(); n < a.f.R / 8; n += 4) prefetch_l2(p + a.f.rope_off + n * 16);
         }
     }
@@ -155,7 +155,7 @@ struct Producer {
     __device__ __forceinline__ uint32_t at(int d, int r) const {
         return tile + (d >> 6) * kBlockBytes + r * 1024 + ((((d >> 3) & 7) ^ (row & 7)) << 4);
     }
-    // stores tile j, then loads tile j + 1; false when a wait ran out
+    // stores tile j and loads tile j + 1; false when a wait ran out
     __device__ __forceinline__ bool store(int j) {
         const int nq = a.f.Q / 16;
         uint32_t base[2], post[2];
@@ -194,6 +194,7 @@ struct Producer {
                         const int d = a.f.Q + (4 * u + chunk()) * 8;
                         if (4 * u + chunk() < a.f.R / 8 && d >> 7 == i) st_shared16(at(d, r), rope[r][u]);
                     }
+                    if (a.f.R <= 64) continue;
                     for (int n = 8 + chunk(); n < a.f.R / 8; n += 4) {
                         const int d = a.f.Q + n * 8;
                         if (d >> 7 != i) continue;
@@ -263,6 +264,7 @@ struct Producer {
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&s.full[i]);
         }
+        // (loads between the pairs slow their arithmetic by more)
         if (j + 1 < ntiles) load(j + 1);
         return ok;
     }

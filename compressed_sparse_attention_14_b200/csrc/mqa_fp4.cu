@@ -77,7 +77,8 @@ struct Shared : Fp4TileShared {
     float alpha[kHg], lsum[kHg];
     float red[4][kHg];
     float coef[kMaxCluster][kHg];
-    uint64_t s_full, q_full, p_full, o_done, fin;
+    uint64_t s_full, q_raw, q_full, p_full, o_done, fin;
+    uint64_t peer;                            // the other split's sums have arrived (clusters of two)
     uint32_t tmem;
 };
 
@@ -143,29 +144,21 @@ __device__ __forceinline__ bool issue_o(const Args& a, Shared& s, uint32_t kv_ad
     return true;
 }
 
-// The query block [64 heads][c] as B operand of S^T: K-major, the channels of
-// each pair in the order in which the expansion leaves them in tensor memory.
-// Rows past the last head are zero.
-__device__ __forceinline__ void load_q(const Args& a, const bf16* q, int heads, uint8_t* q_s, int tid) {
-    const int cpr = a.f.c / 8, pieces = kHg * cpr;        // 16-byte pieces
-    for (int p0 = tid; p0 < pieces; p0 += 4 * kWorkers) {
-        uint4 v[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int p = p0 + kWorkers * u, h = p / cpr;
-            v[u] = make_uint4(0, 0, 0, 0);
-            if (p < pieces && h < heads) v[u] = __ldg(reinterpret_cast<const uint4*>(q) + p);
+// The query block [heads][c], as it lies in memory, to the B operand of S^T:
+// K-major, the channels of each pair in the order in which the expansion
+// leaves them in tensor memory, rows past the last head zero. (It arrives by
+// one bulk copy; loaded through registers, its 64 KB kept the workers 4000
+// cycles at issuing them.)
+__device__ __forceinline__ void arrange_q(const uint8_t* raw, int heads, uint8_t* q_s, int c, int warp, int lane) {
+    for (int h = warp * 4; h < warp * 4 + 4; ++h)
+        for (int p = lane; p < c / 8; p += 32) {
+            const uint4 v = h < heads ? *reinterpret_cast<const uint4*>(raw + (size_t)h * c * 2 + p * 16)
+                                      : make_uint4(0, 0, 0, 0);
+            const int d = (p & 15) * 8, k0 = channel_order(d), k1 = channel_order(d + 4);
+            uint8_t* pair = q_s + (size_t)(p >> 4) * 2 * kHg * 128;
+            *reinterpret_cast<uint2*>(pair + (k0 >> 6) * kHg * 128 + tc::sw128_offset(h, k0 & 63)) = make_uint2(v.x, v.y);
+            *reinterpret_cast<uint2*>(pair + (k1 >> 6) * kHg * 128 + tc::sw128_offset(h, k1 & 63)) = make_uint2(v.z, v.w);
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int p = p0 + kWorkers * u, h = p / cpr, d = (p - h * cpr) * 8;
-            if (p >= pieces) continue;
-            uint8_t* blk = q_s + (size_t)(d >> 7) * 2 * kHg * 128;
-            const int k0 = channel_order(d & 127), k1 = channel_order((d & 127) + 4);
-            *reinterpret_cast<uint2*>(blk + (k0 >> 6) * kHg * 128 + tc::sw128_offset(h, k0 & 63)) = make_uint2(v[u].x, v[u].y);
-            *reinterpret_cast<uint2*>(blk + (k1 >> 6) * kHg * 128 + tc::sw128_offset(h, k1 & 63)) = make_uint2(v[u].z, v[u].w);
-        }
-    }
 }
 
 // v[i] of 32 lanes -> in lane l every lane's v[l / 2] combined (16 shuffles)
@@ -193,14 +186,18 @@ __device__ __forceinline__ void merge_items(const Args& a, const Shared& s, cons
                                             int hi, int c4) {
     constexpr int kB = 8 / kN;
     const uint32_t addr = tc::smem_u32(stage);
+    const int own = blockIdx.x;
     for (int i0 = lo + threadIdx.x; i0 < hi; i0 += kB * kWorkers) {
         float4 o[kB][kN];
 #pragma unroll
         for (int u = 0; u < kB; ++u)
 #pragma unroll
             for (int r = 0; r < kN; ++r)
-                if (i0 + u * kWorkers < hi && r < a.nsplit)
-                    o[u][r] = ld_cluster4(tc::mapa(addr + (uint32_t)(i0 + u * kWorkers) * 16, r));
+                if (i0 + u * kWorkers < hi && r < a.nsplit) {
+                    const int i = i0 + u * kWorkers;
+                    o[u][r] = r == own ? reinterpret_cast<const float4*>(stage)[i]
+                                       : ld_cluster4(tc::mapa(addr + (uint32_t)i * 16, r));
+                }
 #pragma unroll
         for (int u = 0; u < kB; ++u) {
             const int i = i0 + u * kWorkers, h = i / c4;
@@ -248,7 +245,9 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         }
         tc::mbar_init(&s.slot_free, 1);
         tc::mbar_init(&s.s_full, 1);
-        tc::mbar_init(&s.q_full, kWorkers / 32);
+        tc::mbar_init(&s.q_raw, 1);
+        tc::mbar_init(&s.q_full, 1);
+        tc::mbar_init(&s.peer, 1);
         tc::mbar_init(&s.p_full, kWorkers / 32);
         tc::mbar_init(&s.o_done, 1);
         tc::mbar_init(&s.fin, 1);
@@ -270,7 +269,15 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         if (warp == 16 && ntiles > 0) {
             const uint32_t kv_addr = __shfl_sync(0xffffffffu, tc::smem_u32(kv_s), 0);
             const uint32_t q_addr = kv_addr + a.dblocks * kBlockBytes, p_addr = q_addr + a.dblocks * kHg * 128;
-            bool ok = __all_sync(0xffffffffu, wait(&s.q_full, 0, s, a.status));
+            if (lane == 0) {
+                // (where the tile's last blocks will be)
+                const uint32_t bytes = (uint32_t)(a.H - h0 < kHg ? a.H - h0 : kHg) * a.f.c * 2;
+                tc::mbar_expect_tx(&s.q_raw, bytes);
+                tc::bulk_load(kv_s, a.q + ((int64_t)t * a.H + h0) * a.f.c, bytes, &s.q_raw);
+            }
+            __syncwarp();
+            bool ok = __all_sync(0xffffffffu, wait(&s.q_raw, 0, s, a.status));
+            ok = __all_sync(0xffffffffu, wait(&s.q_full, 0, s, a.status)) && ok;
             ok = ok && issue_s(a, s, slots, q_addr, tmem_S, 0);
             for (int j = 0; ok && j < ntiles; ++j)
                 ok = issue_o(a, s, kv_addr, p_addr, tmem_O, j) &&
@@ -311,10 +318,12 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         Producer<kSparse, true, 2> producer(a, s, kv_s, slots, warp, t, (int)e_beg, (int)e_end, ntiles,
                                             (ntiles ? seq : 0) * a.Nmax);
         if (ntiles > 0) {
-            load_q(a, a.q + ((int64_t)t * a.H + h0) * a.f.c, a.H - h0, q_s, tid);
+            producer.load(0);
+            if (__all_sync(0xffffffffu, wait(&s.q_raw, 0, s, a.status)))
+                arrange_q(kv_s, a.H - h0, q_s, a.f.c, warp, lane);
             tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&s.q_full);
+            asm volatile("bar.sync 5, %0;" ::"n"(kWorkers) : "memory");   // the tile may overwrite it
+            if (tid == 0) tc::mbar_arrive(&s.q_full);
         }
         float lpart[kGh];
 #pragma unroll
@@ -458,7 +467,19 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     const int nh = a.H - h0 < kHg ? a.H - h0 : kHg, c4 = a.f.c / 4;
     bf16* out = a.out + ((int64_t)t * a.H + h0) * a.f.c;   // this CTA's heads: contiguous rows
     if (a.merge == kCluster) {
+        // two splits send each other the half of their sums that the other
+        // writes out, one bulk copy to where its queries were; more read their
+        // peers' in place. (A bulk copy moves the 64 KB in SENT us, loads from
+        // the peer in 3.)
+        const int items = nh * c4, lo = (int)((int64_t)items * split / a.nsplit);
+        const int hi = (int)((int64_t)items * (split + 1) / a.nsplit);
+        const bool two = a.nsplit == 2 && items % 2 == 0;
+        if (two && tid == 0) tc::mbar_expect_tx(&s.peer, (uint32_t)(items / 2) * 16);
+        tc::fence_proxy_async_smem();
         tc::cluster_sync();                               // every split has staged its sums
+        if (two && tid == 0)
+            tc::bulk_copy_to_peer(tc::mapa(tc::smem_u32(q_s), split ^ 1), kv_s + (split ? 0 : (size_t)(items / 2) * 16),
+                                  (uint32_t)(items / 2) * 16, tc::mapa(tc::smem_u32(&s.peer), split ^ 1));
         if (tid < kHg) {
             const float sk = a.sink && h0 + tid < a.H ? a.sink[h0 + tid] * kLog2e : -INFINITY;
             float m[kMaxCluster], L[kMaxCluster], M = sk;
@@ -486,12 +507,26 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         }
         __syncthreads();
         // this split's share of the (head, 4 dims) items, all splits' sums in
-        // split order; 8 loads in flight before the first is used
-        const int items = nh * c4, lo = (int)((int64_t)items * split / a.nsplit);
-        const int hi = (int)((int64_t)items * (split + 1) / a.nsplit);
-        if (a.nsplit <= 2) merge_items<2>(a, s, kv_s, out, lo, hi, c4);
-        else if (a.nsplit <= 4) merge_items<4>(a, s, kv_s, out, lo, hi, c4);
-        else merge_items<8>(a, s, kv_s, out, lo, hi, c4);
+        // split order
+        if (two) {
+            wait(&s.peer, 0, s, a.status);
+            const float4* mine = reinterpret_cast<const float4*>(kv_s) + lo;
+            const float4* theirs = reinterpret_cast<const float4*>(q_s);
+            for (int i = tid; i < hi - lo; i += kWorkers) {
+                const int h = (lo + i) / c4;
+                const float4 x = mine[i], y = theirs[i];
+                const float w0 = s.coef[split][h], w1 = s.coef[split ^ 1][h];
+                // (a split without entries has staged nothing)
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (w0 != 0.f) acc = make_float4(w0 * x.x, w0 * x.y, w0 * x.z, w0 * x.w);
+                if (w1 != 0.f) acc = make_float4(fmaf(w1, y.x, acc.x), fmaf(w1, y.y, acc.y), fmaf(w1, y.z, acc.z), fmaf(w1, y.w, acc.w));
+                store4(out + (int64_t)(lo + i) * 4, acc.x, acc.y, acc.z, acc.w);
+            }
+        } else if (a.nsplit <= 4) {
+            merge_items<4>(a, s, kv_s, out, lo, hi, c4);
+        } else {
+            merge_items<8>(a, s, kv_s, out, lo, hi, c4);
+        }
         tc::cluster_sync();                               // no peer still reads this CTA's sums
     } else {
         __syncthreads();

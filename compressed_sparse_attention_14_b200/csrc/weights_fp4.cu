@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
         __syncwarp();
     } else if (warp >= 4) {
         Producer<kSparse, false, 1> producer(a, s, kv_s, 0, warp - 4, b, e_beg, e_end, ntiles, (int64_t)(ntiles ? seq : 0) * a.Nmax);
+        if (ntiles > 0) producer.load(0);
         for (int j = 0; j < ntiles; ++j)
             if (!producer.store(j)) break;
     } else {
