@@ -913,7 +913,7 @@ def csa_quantize_kv_fp4(kv, rope_dims: int = 64, out=None):
     dev = _cuda_index(kv)
     c = kv.shape[-1]
     want = tuple(kv.shape[:-1]) + (csa_fp4_row_bytes(c, rope_dims),)
-    out = torch.empty(want, dtype=torch.uint8, device=dev) if out is None else out
+    out = kv.new_empty(want, dtype=_U8) if out is None else out
     _run_on(dev, _lib.csa_quantize_kv_fp4, _arg(kv, dev, _BF, kv.shape, "kv"), kv.numel() // c, c,
             rope_dims, _arg(out, dev, _U8, want, "out"))
     return out
@@ -936,7 +936,7 @@ def csa_dequantize_kv_fp4(kv4, c: int, rope_dims: int = 64, out=None):
     dev = _cuda_index(kv4)
     rb = csa_fp4_row_bytes(c, rope_dims)
     lead = tuple(kv4.shape[:-1])
-    out = torch.empty(lead + (c,), dtype=torch.bfloat16, device=dev) if out is None else out
+    out = kv4.new_empty(lead + (c,), dtype=_BF) if out is None else out
     _run_on(dev, _lib.csa_dequantize_kv_fp4, _arg(kv4, dev, _U8, lead + (rb,), "kv4"), kv4.numel() // rb, c,
             rope_dims, _arg(out, dev, _BF, lead + (c,), "out"))
     return out
@@ -945,7 +945,7 @@ def csa_dequantize_kv_fp4(kv4, c: int, rope_dims: int = 64, out=None):
 def _attn_out(q, out, lse):
     out = torch.empty_like(q) if out is None else out
     if lse is None:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        lse = q.new_empty(q.shape[:-1], dtype=_F32)
     return out, lse
 
 
@@ -1028,7 +1028,7 @@ def csa_entry_weights_fp4kv(q, lse, kv4, idx, acc=None, scale: float = 0.0, seq_
     nq, H, c = q.shape
     n_seq, Nmax, _ = _fp4_cache(kv4, c, rope_dims)
     k = idx.shape[-1]
-    weights = torch.empty((nq, k), dtype=torch.float32, device=dev) if weights is None else weights
+    weights = q.new_empty((nq, k), dtype=_F32) if weights is None else weights
     _run_on(dev, _lib.csa_entry_weights_fp4kv, _arg(q, dev, _BF, q.shape, "q"),
             _arg(lse, dev, _F32, (nq, H), "lse"), _arg(kv4, dev, _U8, kv4.shape, "kv4"),
             _arg(idx, dev, _I32, (nq, k), "idx"), _arg(seq_of_q, dev, _I32, (nq,), "seq_of_q"), nq,
@@ -1068,13 +1068,13 @@ def csa_evict_plan(acc, n_ent, keep: int, entry_pos=None, protect_from=None, src
     B, Nmax = acc.shape
     M = max(0, min(keep, Nmax - keep))
 
-    def new(t, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=dev) if t is None else t
-    src, dst = new(src, (B, M), torch.int32), new(dst, (B, M), torch.int32)
-    n_moves, n_out = new(n_moves, (B,), torch.int32), new(n_out, (B,), torch.int32)
-    acc_out = new(acc_out, (B, Nmax), torch.float32)
-    if entry_pos is not None:
-        pos_out = new(pos_out, (B, Nmax), torch.int32)
+    src = acc.new_empty((B, M), dtype=_I32) if src is None else src
+    dst = torch.empty_like(src) if dst is None else dst
+    n_moves = torch.empty_like(n_ent) if n_moves is None else n_moves
+    n_out = torch.empty_like(n_ent) if n_out is None else n_out
+    acc_out = torch.empty_like(acc) if acc_out is None else acc_out
+    if entry_pos is not None and pos_out is None:
+        pos_out = torch.empty_like(entry_pos)
     wp, wn, ws = _scratch(_size_of("csa_evict_plan_workspace_size", B, Nmax, keep), dev, ws)
     _run_on(dev, _lib.csa_evict_plan, _arg(acc, dev, _F32, (B, Nmax), "acc"),
             _arg(n_ent, dev, _I32, (B,), "n_ent"), _arg(entry_pos, dev, _I32, (B, Nmax), "entry_pos"),

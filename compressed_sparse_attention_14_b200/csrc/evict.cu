@@ -17,6 +17,8 @@
 // CTA and 7 cluster barriers.
 // evict_rows: a thread per 16 bytes, four of them in flight; bound by memory.
 // evict_slot: a CTA per sequence, one reduction.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
@@ -43,6 +45,7 @@ struct PlanShared {
     int scan[kWarps];
     int count[kWarps][4];                  // per warp: above the keep-th key before / after slot keep, ties likewise
     int total[5];                          // this CTA's sums, and its entries before slot keep
+    int all[kMaxCluster][5];               // every CTA's total
     int digit, need;
 };
 
@@ -140,8 +143,13 @@ __global__ void __launch_bounds__(kThreads) evict_plan_kernel(const __grid_const
             sync_all();
             // entries with this digit, of all CTAs; from the largest digit down
             int c = 0;
-            if (tid < bins)
-                for (int r = 0; r < csize; ++r) c += peek(hist + bins - 1 - tid, r);
+            if (tid < bins) {
+                int v[kMaxCluster];                       // (all CTAs' loads in flight)
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r) v[r] = r < csize ? peek(hist + bins - 1 - tid, r) : 0;
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r) c += v[r];
+            }
             int sum = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -188,6 +196,8 @@ __global__ void __launch_bounds__(kThreads) evict_plan_kernel(const __grid_const
         }
         if (tid == 0) s.total[4] = max(0, min(32 * g1, min(n, keep)) - 32 * g0);
         sync_all();
+        if (tid < 5 * csize) s.all[tid / 5][tid % 5] = peek(&s.total[tid % 5], tid / 5);
+        __syncthreads();
         // what lies before this warp: ties, then (they decide which ties stay) holes and movers
         int tie = 0, hole = 0, mover = 0;
         auto pass_over = [&](int in_lo, const int (&v)[4]) {
@@ -199,8 +209,8 @@ __global__ void __launch_bounds__(kThreads) evict_plan_kernel(const __grid_const
         int own_tie = 0, own_hole = 0, own_mover = 0;
         for (int r = 0; r < csize; ++r) {
             if (r == rank) { own_tie = tie; own_hole = hole; own_mover = mover; }
-            const int v[4] = {peek(&s.total[0], r), peek(&s.total[1], r), peek(&s.total[2], r), peek(&s.total[3], r)};
-            pass_over(peek(&s.total[4], r), v);
+            const int v[4] = {s.all[r][0], s.all[r][1], s.all[r][2], s.all[r][3]};
+            pass_over(s.all[r][4], v);
         }
         moves = hole;
         tie = own_tie;
@@ -230,10 +240,19 @@ __global__ void __launch_bounds__(kThreads) evict_plan_kernel(const __grid_const
     // the weights (and positions) follow their entries
     float* ao = a.acc_out + base;
     int32_t* po = a.pos_out ? a.pos_out + base : nullptr;
-    if (ao != acc)
-        for (int i = t0; i < n_out; i += step) ao[i] = acc[i];
-    if (po && po != pos)
-        for (int i = t0; i < n_out; i += step) po[i] = pos[i];
+    auto copy = [&](auto* to, const auto* from) {         // (four loads in flight)
+        for (int i = t0; i < n_out; i += 4 * step) {
+            std::remove_pointer_t<decltype(to)> v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i + u * step < n_out) v[u] = from[i + u * step];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i + u * step < n_out) to[i + u * step] = v[u];
+        }
+    };
+    if (ao != acc) copy(ao, acc);
+    if (po && po != pos) copy(po, pos);
     sync_all();                           // also: every CTA has read n_ent, which n_out may be
     if (rank == 0 && tid == 0) {
         a.n_moves[b] = moves;
