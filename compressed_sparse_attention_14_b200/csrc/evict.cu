@@ -27,7 +27,7 @@ namespace csa {
 
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxCached = 48 * 1024;      // keys of a CTA's part kept in shared memory
 
