@@ -4,36 +4,29 @@
 //   z_s = scale * q . v_s,  out = sum_s e^{z_s} v_s / (sum_s e^{z_s} [+ e^{sink}])
 //
 // One CTA serves (query, up to 64 heads, one split of the query's entries)
-// and walks the split in tiles of 128 entries. Producer warps read the packed
-// rows, expand them to bf16 (exact) and store the tile twice, key and value
-// being the same row: in shared memory (64-dim blocks, 128-byte swizzle) and,
-// pair of blocks by pair, in tensor memory, entries as lanes:
-//   S^T  = V_tile . q^T         M = 128 entries, N = 64 heads, K = c  (tensor memory)
-//   O^T += V_tile^T . P^T       M = 128 dims,    N = 64 heads, K = 128 entries (shared)
-// S^T and O^T live in tensor memory, too. The softmax keeps a reference
-// maximum per head that moves (O^T and the sums are then rescaled) only when a
-// logit passes it by 2^24; normalisation uses the same reference, so the
-// result does not depend on when it moves, and the weights' rounding is
-// relative (with 2^8 it moved in every second tile, 2500 cycles each). P is
+// and walks the split in tiles of 64 entries. Producer warps read the packed
+// rows, expand them to bf16 (exact) and store the tile in shared memory, where
+// ONE copy of it (64-dim blocks, 128-byte swizzle) feeds both products, key
+// and value being the same row:
+//   S^T  = V_tile . q^T         M = 64 entries, N = 64 heads, K = c
+//   O^T += V_tile^T . P^T       M = 128 dims,   N = 64 heads, K = 64 entries
+// S^T and O^T live in tensor memory. The softmax keeps a reference maximum per
+// head that moves (O^T and the sums are then rescaled) only when a logit
+// passes it by 2^24; normalisation uses the same reference, so the result does
+// not depend on when it moves, and the weights' rounding is relative. P is
 // rounded to bf16 for the second product; sums, maxima and O stay fp32.
 //
-// Warps 0-15 both expand and do the softmax, which cannot overlap for one tile
-// buffer (the expansion of tile j+1 needs blocks that the O product of tile j
-// has read, the softmax of tile j+1 its S product):
-//   expansion: blocks go back and forth in pairs (128 dims, one M tile of the
-//     O product), the last first; warps 0-7 take every second pair, 8-15 the
-//     others, each 16 entries, with the codes in registers by then;
-//   softmax: warp w has TMEM lanes 32 (w % 4).. (a thread per entry), 16 heads.
-// Warp 16 issues the products: O of tile j, then S of tile j+1 pair by pair as
-// it is stored. It is alone in a warpgroup that gives its registers away: 112
-// are left for each worker (loaded codes that spill are waited for at once:
-// with 96 a tile took 10500 cycles).
-//
-// What a tile costs is shared-memory bandwidth: the expansion's stores write
-// 128 KB, the O product reads 192 KB (113 bytes a cycle, near the 128 there
-// are, so the stores hardly advance while it runs), the S product the 64 KB of
-// q; reading its V operand from shared memory, too, took 130 cycles per
-// instruction instead of IFM.
+// Two tiles (and two S^T, two P) are in work at a time, so that producers,
+// softmax and products overlap:
+//   warps 0-7   softmax; warp w has entries 16 (w % 4).. and 32 heads, a
+//               thread 2 entries x 8 heads (the 16-lane tensor-memory loads)
+//   warps 8-23  producers (fp4_tile.cuh)
+//   warp 24     S products, pair of blocks by pair as they are stored
+//   warp 25     O products; each hands a pair back to the producers
+// One buffer of 128 entries left the four steps of a tile one after another,
+// 8700 cycles for 128 entries, half of them handing over; two of 64 take TWO64.
+// The least is the shared memory's 128 bytes a cycle: 128 entries are written
+// (128 KB) and read by the products (448 KB with q and P), 4600 cycles.
 //
 // Entries outside the query's set are stored as zeros and get weight 0: no
 // row that the query does not see is read.
@@ -43,6 +36,7 @@
 // more go through the workspace and mqa_combine. Either way in split order.
 #include "fp4_tile.cuh"
 #include "kernels.h"
+#include "tmap.h"
 
 namespace csa {
 
@@ -50,9 +44,10 @@ namespace {
 
 using namespace fp4_tile;
 
-constexpr int kWorkers = 512, kThreads = kWorkers + 128;
-constexpr int kGh = 16;                 // heads per worker warp
-constexpr uint32_t kTmemCols = 512;     // S^T 64, slots 192, O^T up to 256
+constexpr int kSoftmaxWarps = 8, kThreads = (kSoftmaxWarps + kProducerWarps + 2) * 32;
+constexpr int kSWarp = kSoftmaxWarps + kProducerWarps;   // and the next: products
+constexpr int kHalf = kHg / 2;          // heads per softmax warp
+constexpr uint32_t kTmemCols = 512;     // S^T 2 x 64, O^T up to 256
 constexpr int kMaxCluster = 8;
 constexpr float kMoveLog2 = 24.0f, kLn2 = 0.6931471805599453f;
 
@@ -60,7 +55,6 @@ enum Merge { kDirect, kCluster, kWorkspace };
 
 struct Args : Fp4TileArgs {
     QueryMap qm;
-    const bf16* q;
     const float* sink;
     bf16* out;
     float* lse;
@@ -77,7 +71,7 @@ struct Shared : Fp4TileShared {
     float alpha[kHg], lsum[kHg];
     float red[4][kHg];
     float coef[kMaxCluster][kHg];
-    uint64_t s_full, q_raw, q_full, p_full, o_done, fin;
+    uint64_t s_full[2], p_full[2], q_full, o_done, fin[2];
     uint64_t peer;                            // the other split's sums have arrived (clusters of two)
     uint32_t tmem;
 };
@@ -89,95 +83,24 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
     return v;
 }
 
-// barrier (and vote) of the 4 warps that share 16 heads
-__device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
-__device__ __forceinline__ bool group_any(int g, bool v) {
+// barrier (and vote) of the 4 softmax warps that share 32 heads
+__device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
+__device__ __forceinline__ bool half_any(int half, bool v) {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p, q;\n\t"
                  "setp.ne.u32 q, %1, 0;\n\t"
                  "bar.red.or.pred p, %2, 128, q;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(r) : "r"((uint32_t)v), "r"(1 + g) : "memory");
+                 : "=r"(r) : "r"((uint32_t)v), "r"(1 + half) : "memory");
     return r != 0;
 }
 
-// S^T of tile j (a whole warp): pairs as they are stored, each from its slot.
-__device__ __forceinline__ bool issue_s(const Args& a, Shared& s, uint32_t slots, uint32_t q_addr, uint32_t d_tmem,
-                                        int j) {
-    const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
-    for (int i = a.mtiles - 1, slot = 0; i >= 0; --i, slot = slot == kSlots - 1 ? 0 : slot + 1) {
-        const bool ok = __all_sync(0xffffffffu, wait(&s.full[i], j & 1, s, a.status));
-        if (!ok) {
-            // the products already issued end before the CTA frees their memory
-            tc::umma_commit_warp(&s.fin);
-            tc::mbar_wait(&s.fin, 0, kWaitLimit);
-            return false;
-        }
-        tc::tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-            tc::umma_bf16_ta_warp(d_tmem, slots + slot * 64 + kk * 8,
-                                  tc::sdesc_sw128(q_addr + (2 * i + (kk >> 2)) * (kHg * 128) + (kk & 3) * 32, 16, 1024),
-                                  idesc, (i < a.mtiles - 1 || kk) ? 1u : 0u);
-        if (i == kSlots) tc::umma_commit_warp(&s.slot_free);
-    }
-    tc::umma_commit_warp(&s.s_full);
-    return true;
-}
-
-// O^T += of tile j (a whole warp); each pair of blocks goes back to the
-// producers once its product is done, the last first.
-__device__ __forceinline__ bool issue_o(const Args& a, Shared& s, uint32_t kv_addr, uint32_t p_addr, uint32_t d_tmem,
-                                        int j) {
-    const uint32_t idesc = tc::idesc_bf16_f32(128, kHg, 1, 1);
-    if (!__all_sync(0xffffffffu, wait(&s.p_full, j & 1, s, a.status))) return false;
-    tc::tc_fence_after();
-    for (int mt = a.mtiles - 1; mt >= 0; --mt) {
-#pragma unroll
-        for (int ke = 0; ke < kE / 16; ++ke)
-            tc::umma_bf16_warp(d_tmem + mt * kHg,
-                               tc::sdesc_sw128(kv_addr + 2 * mt * kBlockBytes + ke * 2048, kBlockBytes, 1024),
-                               tc::sdesc_sw128(p_addr + ke * 2048, kE * 128, 1024), idesc, (j > 0 || ke > 0) ? 1u : 0u);
-        tc::umma_commit_warp(&s.empty[mt]);
-    }
-    tc::umma_commit_warp(&s.o_done);
-    return true;
-}
-
-// The query block [heads][c], as it lies in memory, to the B operand of S^T:
-// K-major, the channels of each pair in the order in which the expansion
-// leaves them in tensor memory, rows past the last head zero. (It arrives by
-// one bulk copy; loaded through registers, its 64 KB kept the workers 4000
-// cycles at issuing them.)
-__device__ __forceinline__ void arrange_q(const uint8_t* raw, int heads, uint8_t* q_s, int c, int warp, int lane) {
-    for (int h = warp * 4; h < warp * 4 + 4; ++h)
-        for (int p = lane; p < c / 8; p += 32) {
-            const uint4 v = h < heads ? *reinterpret_cast<const uint4*>(raw + (size_t)h * c * 2 + p * 16)
-                                      : make_uint4(0, 0, 0, 0);
-            const int d = (p & 15) * 8, k0 = channel_order(d), k1 = channel_order(d + 4);
-            uint8_t* pair = q_s + (size_t)(p >> 4) * 2 * kHg * 128;
-            *reinterpret_cast<uint2*>(pair + (k0 >> 6) * kHg * 128 + tc::sw128_offset(h, k0 & 63)) = make_uint2(v.x, v.y);
-            *reinterpret_cast<uint2*>(pair + (k1 >> 6) * kHg * 128 + tc::sw128_offset(h, k1 & 63)) = make_uint2(v.z, v.w);
-        }
-}
-
-// v[i] of 32 lanes -> in lane l every lane's v[l / 2] combined (16 shuffles)
+// combines v over the 8 lanes with the same lane % 4
 template <typename Op>
-__device__ __forceinline__ float lanes_reduce16(float* v, int lane, Op op) {
+__device__ __forceinline__ float rows_reduce(float v, Op op) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int o = 16 >> r, n = 8 >> r;
-        const bool upper = (lane & o) != 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (i < n) {
-                const float send = upper ? v[i] : v[i + n];
-                const float keep = upper ? v[i + n] : v[i];
-                v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
-            }
-        }
-    }
-    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+    for (int o = 4; o < 32; o <<= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
 }
 
 // out[i] (4 dims each) for i in [lo, hi): the cluster's staged sums, weighted.
@@ -187,20 +110,20 @@ __device__ __forceinline__ void merge_items(const Args& a, const Shared& s, cons
     constexpr int kB = 8 / kN;
     const uint32_t addr = tc::smem_u32(stage);
     const int own = blockIdx.x;
-    for (int i0 = lo + threadIdx.x; i0 < hi; i0 += kB * kWorkers) {
+    for (int i0 = lo + threadIdx.x; i0 < hi; i0 += kB * kThreads) {
         float4 o[kB][kN];
 #pragma unroll
         for (int u = 0; u < kB; ++u)
 #pragma unroll
             for (int r = 0; r < kN; ++r)
-                if (i0 + u * kWorkers < hi && r < a.nsplit) {
-                    const int i = i0 + u * kWorkers;
+                if (i0 + u * kThreads < hi && r < a.nsplit) {
+                    const int i = i0 + u * kThreads;
                     o[u][r] = r == own ? reinterpret_cast<const float4*>(stage)[i]
                                        : ld_cluster4(tc::mapa(addr + (uint32_t)i * 16, r));
                 }
 #pragma unroll
         for (int u = 0; u < kB; ++u) {
-            const int i = i0 + u * kWorkers, h = i / c4;
+            const int i = i0 + u * kThreads, h = i / c4;
             if (i >= hi) break;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -219,13 +142,14 @@ __device__ __forceinline__ void merge_items(const Args& a, const Shared& s, cons
 }
 
 template <bool kSparse>
-__global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_constant__ Args a,
+                                                              const __grid_constant__ CUtensorMap tmQ) {
     extern __shared__ uint8_t smem_raw[];
     // (an offset, not a rounded pointer: the accesses stay shared-memory ones)
-    uint8_t* kv_s = smem_raw + ((0u - tc::smem_u32(smem_raw)) & 1023u);           // dblocks x 16 KB
-    uint8_t* q_s = kv_s + (size_t)a.dblocks * kBlockBytes;                         // dblocks x 8 KB
-    uint8_t* p_s = q_s + (size_t)a.dblocks * kHg * 128;                            // 128 entries x 64 heads
-    Shared& s = *reinterpret_cast<Shared*>(p_s + kE * 128);
+    uint8_t* kv_s = smem_raw + ((0u - tc::smem_u32(smem_raw)) & 1023u);           // 2 x dblocks x 8 KB
+    uint8_t* q_s = kv_s + (size_t)a.dblocks * 2 * kBlockBytes;                     // dblocks x 8 KB
+    uint8_t* p_s = q_s + (size_t)a.dblocks * kHg * 128;                            // 2 x 64 entries x 64 heads
+    Shared& s = *reinterpret_cast<Shared*>(p_s + 2 * kE * 128);
 
     pdl_wait();
     pdl_launch_next();
@@ -239,127 +163,145 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     const int ntiles = e_end > e_beg ? (int)((e_end - e_beg + kE - 1) / kE) : 0;
 
     if (tid == 0) {
-        for (int i = 0; i < kPairs; ++i) {
-            tc::mbar_init(&s.full[i], 8);            // the warps that share a pair
-            tc::mbar_init(&s.empty[i], 1);
+        for (int b = 0; b < 2; ++b) {
+            for (int i = 0; i < kPairs; ++i) {
+                tc::mbar_init(&s.full[b][i], 8);     // a buffer's producer warps
+                tc::mbar_init(&s.empty[b][i], 1);
+            }
+            tc::mbar_init(&s.s_full[b], 1);
+            tc::mbar_init(&s.p_full[b], kSoftmaxWarps);
+            tc::mbar_init(&s.fin[b], 1);
         }
-        tc::mbar_init(&s.slot_free, 1);
-        tc::mbar_init(&s.s_full, 1);
-        tc::mbar_init(&s.q_raw, 1);
         tc::mbar_init(&s.q_full, 1);
-        tc::mbar_init(&s.peer, 1);
-        tc::mbar_init(&s.p_full, kWorkers / 32);
         tc::mbar_init(&s.o_done, 1);
-        tc::mbar_init(&s.fin, 1);
+        tc::mbar_init(&s.peer, 1);
         tc::fence_mbar_init();
         s.abort = 0;
     }
-    if (warp == 16) {
+    if (warp == kSWarp) {
         tc::tmem_alloc(&s.tmem, kTmemCols);
         tc::tmem_relinquish();
         tc::tc_fence_before();
     }
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tmem_S = __shfl_sync(0xffffffffu, s.tmem, 0), slots = tmem_S + kHg, tmem_O = slots + kSlots * 64;
+    const uint32_t tmem_S = __shfl_sync(0xffffffffu, s.tmem, 0), tmem_O = tmem_S + 2 * kHg;
 
-    if (warp >= 16) {
+    if (warp >= kSWarp) {
         // ------------------------------------------------------------ products
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
-        if (warp == 16 && ntiles > 0) {
+        if (ntiles > 0) {
             const uint32_t kv_addr = __shfl_sync(0xffffffffu, tc::smem_u32(kv_s), 0);
-            const uint32_t q_addr = kv_addr + a.dblocks * kBlockBytes, p_addr = q_addr + a.dblocks * kHg * 128;
-            if (lane == 0) {
-                // (where the tile's last blocks will be)
-                const uint32_t bytes = (uint32_t)(a.H - h0 < kHg ? a.H - h0 : kHg) * a.f.c * 2;
-                tc::mbar_expect_tx(&s.q_raw, bytes);
-                tc::bulk_load(kv_s, a.q + ((int64_t)t * a.H + h0) * a.f.c, bytes, &s.q_raw);
+            const uint32_t tile_bytes = a.dblocks * kBlockBytes;
+            const uint32_t q_addr = kv_addr + 2 * tile_bytes, p_addr = q_addr + a.dblocks * kHg * 128;
+            auto until = [&](uint64_t* bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, wait(bar, parity, s, a.status));
+            };
+            bool ok = true;
+            if (warp == kSWarp) {
+                if (lane == 0) {
+                    tc::mbar_expect_tx(&s.q_full, (uint32_t)a.dblocks * kHg * 128);
+                    for (int b = 0; b < a.dblocks; ++b)
+                        tc::tma_load_2d(q_s + (size_t)b * kHg * 128, &tmQ, &s.q_full, b * 64, t * a.H + h0);
+                }
+                __syncwarp();
+                ok = until(&s.q_full, 0);
+                const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
+                for (int j = 0; ok && j < ntiles; ++j) {
+                    const int b = j & 1;
+                    for (int i = a.mtiles - 1; i >= 0 && (ok = until(&s.full[b][i], (j >> 1) & 1)); --i) {
+                        tc::tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const int blk = 2 * i + (kk >> 2);
+                            tc::umma_bf16_warp(
+                                tmem_S + b * kHg,
+                                tc::sdesc_sw128(kv_addr + b * tile_bytes + blk * kBlockBytes + (kk & 3) * 32, 16, 1024),
+                                tc::sdesc_sw128(q_addr + blk * (kHg * 128) + (kk & 3) * 32, 16, 1024), idesc,
+                                (i < a.mtiles - 1 || kk) ? 1u : 0u);
+                        }
+                    }
+                    if (ok) tc::umma_commit_warp(&s.s_full[b]);
+                }
+                if (!ok) tc::mbar_wait(&s.q_full, 0, kWaitLimit);
+            } else {
+                const uint32_t idesc = tc::idesc_bf16_f32(128, kHg, 1, 1);
+                for (int j = 0; j < ntiles && (ok = until(&s.p_full[j & 1], (j >> 1) & 1)); ++j) {
+                    const int b = j & 1;
+                    tc::tc_fence_after();
+                    for (int mt = a.mtiles - 1; mt >= 0; --mt) {
+#pragma unroll
+                        for (int ke = 0; ke < kE / 16; ++ke)
+                            tc::umma_bf16_warp(
+                                tmem_O + mt * kHg,
+                                tc::sdesc_sw128(kv_addr + b * tile_bytes + 2 * mt * kBlockBytes + ke * 2048, kBlockBytes, 1024),
+                                tc::sdesc_sw128(p_addr + b * (kE * 128) + ke * 2048, kE * 128, 1024), idesc,
+                                (j > 0 || ke > 0) ? 1u : 0u);
+                        tc::umma_commit_warp(&s.empty[b][mt]);
+                    }
+                    tc::umma_commit_warp(&s.o_done);
+                }
             }
-            __syncwarp();
-            bool ok = __all_sync(0xffffffffu, wait(&s.q_raw, 0, s, a.status));
-            ok = __all_sync(0xffffffffu, wait(&s.q_full, 0, s, a.status)) && ok;
-            ok = ok && issue_s(a, s, slots, q_addr, tmem_S, 0);
-            for (int j = 0; ok && j < ntiles; ++j)
-                ok = issue_o(a, s, kv_addr, p_addr, tmem_O, j) &&
-                     (j + 1 == ntiles || issue_s(a, s, slots, q_addr, tmem_S, j + 1));
             // every product issued has ended before the CTA goes on to free the
             // memory it uses (also when a wait ran out)
-            tc::umma_commit_warp(&s.fin);
-            tc::mbar_wait(&s.fin, 0, kWaitLimit);
+            tc::umma_commit_warp(&s.fin[warp - kSWarp]);
+            tc::mbar_wait(&s.fin[warp - kSWarp], 0, kWaitLimit);
         }
-        // the workers' barriers below (code that both ran would have to do
-        // with the fewer registers)
-        __syncthreads();
-        if (a.merge == kCluster) {
-            tc::cluster_sync();
-            __syncthreads();
-            tc::cluster_sync();
-        } else {
-            __syncthreads();
-            __syncthreads();
-        }
-        if (warp == 16) {
-            tc::tc_fence_after();
-            tc::tmem_dealloc(tmem_S, kTmemCols);
-        }
-        return;
-    }
-    // ---------------------------------------------------------------- workers
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
-    {
-        const int quad = warp & 3, g = warp >> 2, hb = g * kGh;
-        const int row = quad * 32 + lane;                 // entry of the tile, TMEM lane
-        const int gth = tid & 127;
+    } else if (warp >= kSoftmaxWarps) {
+        Producer<kSparse>(a, s, kv_s, warp - kSoftmaxWarps, t, (int)e_beg, (int)e_end, ntiles, (ntiles ? seq : 0) * a.Nmax);
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int quad = warp & 3, half = warp >> 2, hb = half * kHalf;
+        const int q4 = lane & 3, ra = quad * 16 + (lane >> 2), rb = ra + 8;   // this thread's entries
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        if (gth < kGh) {
-            s.mref[hb + gth] = s.limit[hb + gth] = -INFINITY;
-            s.mexp[hb + gth] = 0.f;
+        const int hth = tid & 127;
+        if (hth < kHalf) {
+            s.mref[hb + hth] = s.limit[hb + hth] = -INFINITY;
+            s.mexp[hb + hth] = 0.f;
         }
-        Producer<kSparse, true, 2> producer(a, s, kv_s, slots, warp, t, (int)e_beg, (int)e_end, ntiles,
-                                            (ntiles ? seq : 0) * a.Nmax);
-        if (ntiles > 0) {
-            producer.load(0);
-            if (__all_sync(0xffffffffu, wait(&s.q_raw, 0, s, a.status)))
-                arrange_q(kv_s, a.H - h0, q_s, a.f.c, warp, lane);
-            tc::fence_proxy_async_smem();
-            asm volatile("bar.sync 5, %0;" ::"n"(kWorkers) : "memory");   // the tile may overwrite it
-            if (tid == 0) tc::mbar_arrive(&s.q_full);
-        }
-        float lpart[kGh];
+        float lpart[8];                                   // heads hb + 8u + 2 q4 + (0, 1), both entries
 #pragma unroll
-        for (int i = 0; i < kGh; ++i) lpart[i] = 0.f;
-        group_sync(g);
+        for (int i = 0; i < 8; ++i) lpart[i] = 0.f;
+        half_sync(half);
         bool ok = true;
         for (int j = 0; j < ntiles; ++j) {
-            ok = producer.store(j) && ok;
-            const int64_t e = e_beg + (int64_t)j * kE + row;
-            bool valid = e < e_end;
-            if (kSparse && valid) {
+            const int b = j & 1;
+            auto seen = [&](int row) {
+                const int64_t e = e_beg + (int64_t)j * kE + row;
+                if (e >= e_end) return false;
+                if (!kSparse) return true;
                 const int v = __ldg(a.idx + (int64_t)t * a.k + e);
-                valid = v >= 0 && v < a.Nmax;
-            }
-            ok = ok && wait(&s.s_full, j & 1, s, a.status);
+                return v >= 0 && v < a.Nmax;
+            };
+            const bool va = seen(ra), vb = seen(rb);
+            ok = ok && wait(&s.s_full[b], (j >> 1) & 1, s, a.status);
             tc::tc_fence_after();
-            float z[kGh];
+            float z[16];
             auto logits = [&]() {
-                tc::tmem_ld16(tmem_S + lanes + hb, z);
+                tc::tmem_ld_16x32(tmem_S + lanes + b * kHg + hb, z);
                 tc::tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < kGh; ++i) z[i] = valid ? z[i] * a.scale_log2 : -INFINITY;
+                for (int i = 0; i < 16; ++i) z[i] = (i & 2 ? vb : va) ? z[i] * a.scale_log2 : -INFINITY;
             };
             logits();
             bool move = false;
 #pragma unroll
-            for (int i = 0; i < kGh; ++i) move |= z[i] > s.limit[hb + i];
-            if (group_any(g, move || !ok)) {
+            for (int u = 0; u < 4; ++u) {
+                const float2 lim = *reinterpret_cast<const float2*>(&s.limit[hb + 8 * u + 2 * q4]);
+                move |= z[4 * u] > lim.x || z[4 * u + 2] > lim.x || z[4 * u + 1] > lim.y || z[4 * u + 3] > lim.y;
+            }
+            if (half_any(half, move || !ok)) {
                 // all leave together once a wait of one ran out
-                if (group_any(g, !ok)) { ok = false; break; }
-                // (the reduction consumes the logits; they are read again)
-                const float top = lanes_reduce16(z, lane, [](float x, float y) { return fmaxf(x, y); });
-                if (!(lane & 1)) s.red[quad][hb + lane / 2] = top;
-                group_sync(g);
-                if (gth < kGh) {
-                    const int h = hb + gth;
+                if (half_any(half, !ok)) { ok = false; break; }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int u = i >> 1, e = i & 1;
+                    const float top = rows_reduce(fmaxf(z[4 * u + e], z[4 * u + 2 + e]),
+                                                  [](float x, float y) { return fmaxf(x, y); });
+                    if (lane < 4) s.red[quad][hb + 8 * u + 2 * lane + e] = top;
+                }
+                half_sync(half);
+                if (hth < kHalf) {
+                    const int h = hb + hth;
                     const float old = s.mref[h];
                     const float m = fmaxf(fmaxf(fmaxf(s.red[0][h], s.red[1][h]), fmaxf(s.red[2][h], s.red[3][h])), old);
                     s.alpha[h] = old == -INFINITY ? 0.f : ex2(old - m);
@@ -367,56 +309,58 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                     s.limit[h] = m + kMoveLog2;
                     s.mexp[h] = m == -INFINITY ? 0.f : m;
                 }
-                group_sync(g);
+                half_sync(half);
 #pragma unroll
-                for (int i = 0; i < kGh; ++i) lpart[i] *= s.alpha[hb + i];
+                for (int i = 0; i < 8; ++i) lpart[i] *= s.alpha[hb + 8 * (i >> 1) + 2 * q4 + (i & 1)];
                 if (j > 0) {
+                    // rescale O^T (every product before this tile's has ended)
                     ok = wait(&s.o_done, (j - 1) & 1, s, a.status);
                     tc::tc_fence_after();
 #pragma unroll 1
-                    for (int mt = 0; mt < a.mtiles; ++mt) {
-                        float o[kGh];
-                        tc::tmem_ld16(tmem_O + lanes + mt * kHg + hb, o);
+                    for (int n = 0; n < 2 * a.mtiles; ++n) {
+                        const int cc = hb + 16 * (n & 1);
+                        float o[16];
+                        tc::tmem_ld16(tmem_O + lanes + (n >> 1) * kHg + cc, o);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < kGh; ++i) o[i] *= s.alpha[hb + i];
-                        tc::tmem_st16(tmem_O + lanes + mt * kHg + hb, o);
+                        for (int i = 0; i < 16; ++i) o[i] *= s.alpha[cc + i];
+                        tc::tmem_st16(tmem_O + lanes + (n >> 1) * kHg + cc, o);
                     }
                     tc::tmem_st_wait();
                 }
-                logits();
             }
-            uint32_t pk[kGh / 2];
+            // (this tile's S product came after its buffer was free, so the O
+            // product of the tile before last has read this P)
+            uint8_t* p_b = p_s + b * (kE * 128);
 #pragma unroll
-            for (int i = 0; i < kGh; i += 2) {
-                const float p0 = ex2(z[i] - s.mexp[hb + i]), p1 = ex2(z[i + 1] - s.mexp[hb + i + 1]);
-                lpart[i] += p0;
-                lpart[i + 1] += p1;
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
-                pk[i >> 1] = *reinterpret_cast<const uint32_t*>(&b2);
+            for (int u = 0; u < 4; ++u) {
+                const float2 m = *reinterpret_cast<const float2*>(&s.mexp[hb + 8 * u + 2 * q4]);
+                const float p0 = ex2(z[4 * u] - m.x), p1 = ex2(z[4 * u + 1] - m.y);
+                const float p2 = ex2(z[4 * u + 2] - m.x), p3 = ex2(z[4 * u + 3] - m.y);
+                lpart[2 * u] += p0 + p2;
+                lpart[2 * u + 1] += p1 + p3;
+                const __nv_bfloat162 x = __floats2bfloat162_rn(p0, p1), y = __floats2bfloat162_rn(p2, p3);
+                const int piece = ((hb >> 3) + u) ^ (ra & 7);             // (rb & 7 is the same)
+                *reinterpret_cast<__nv_bfloat162*>(p_b + ra * 128 + piece * 16 + q4 * 4) = x;
+                *reinterpret_cast<__nv_bfloat162*>(p_b + rb * 128 + piece * 16 + q4 * 4) = y;
             }
-            // (the previous tile's O product has read P: every pair was free
-            // for this tile, its last included)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                *reinterpret_cast<uint4*>(p_s + row * 128 + (((g * 2 + i) ^ (row & 7)) << 4)) =
-                    make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
             tc::tc_fence_before();                        // S has been read, too
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&s.p_full);
+            if (lane == 0) tc::mbar_arrive(&s.p_full[b]);
         }
         if (ok && ntiles > 0) wait(&s.o_done, (ntiles - 1) & 1, s, a.status);
         __syncwarp();
-        // per-head sums in a fixed order: lanes, then the four warps
-        group_sync(g);                                    // red may still be read
-        {
-            const float sum = lanes_reduce16(lpart, lane, [](float x, float y) { return x + y; });
-            if (!(lane & 1)) s.red[quad][hb + lane / 2] = sum;
+        // per-head sums in a fixed order: entries, lanes, then the four warps
+        half_sync(half);                                  // red may still be read
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float sum = rows_reduce(lpart[i], [](float x, float y) { return x + y; });
+            if (lane < 4) s.red[quad][hb + 8 * (i >> 1) + 2 * lane + (i & 1)] = sum;
         }
-        group_sync(g);
-        if (gth < kGh) {
-            const int h = hb + gth;
+        half_sync(half);
+        if (hth < kHalf) {
+            const int h = hb + hth;
             s.lsum[h] = (s.red[0][h] + s.red[1][h]) + (s.red[2][h] + s.red[3][h]);
             if (a.merge == kDirect) {
                 const float m = s.mref[h], L = s.lsum[h];
@@ -434,38 +378,43 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     }
     // ---------------------------------------------------------------- epilogue
     __syncthreads();
-    {
-        // O^T to shared memory where the tile was, as rows of a head: warp w
-        // has dims 32 (w % 4).. of every M tile and 16 heads
+    const int nh = a.H - h0 < kHg ? a.H - h0 : kHg, c4 = a.f.c / 4;
+    bf16* out = a.out + ((int64_t)t * a.H + h0) * a.f.c;   // this CTA's heads: contiguous rows
+    const int64_t part = ((int64_t)t * a.nsplit + split) * a.H + h0;
+    if (warp < 16) {
+        // warp w has dims 32 (w % 4).. of every M tile and 16 heads, a lane one
+        // dim: written out from the registers, or (a cluster) to shared memory
+        // where the tiles were, as rows of a head
         tc::tc_fence_after();
-        const int hb = (warp >> 2) * kGh, row = (warp & 3) * 32 + lane;
+        const int hb = (warp >> 2) * 16, row = (warp & 3) * 32 + lane;
         const uint32_t addr = tmem_O + ((uint32_t)((warp & 3) * 32) << 16) + hb;
+        const int heads = nh - hb;
 #pragma unroll 1
         for (int mt = 0; mt < a.mtiles; ++mt) {
             const int d = mt * 128 + row;
-            float o[kGh];
+            float o[16];
             if (ntiles > 0) {
                 tc::tmem_ld16(addr + mt * kHg, o);
                 tc::tmem_ld_wait();
             }
             if (a.merge == kDirect) {                     // normalised, bf16
-                bf16* stage = reinterpret_cast<bf16*>(kv_s) + (size_t)hb * a.f.c + d;
+                bf16* dst = out + (int64_t)hb * a.f.c + d;
 #pragma unroll
-                for (int i = 0; i < kGh; ++i) {
+                for (int i = 0; i < 16; ++i) {
                     const float al = s.alpha[hb + i];
-                    stage[(size_t)i * a.f.c] = __float2bfloat16_rn(al != 0.f ? o[i] * al : 0.f);
+                    if (i < heads) dst[i * a.f.c] = __float2bfloat16_rn(al != 0.f ? o[i] * al : 0.f);
                 }
             } else if (ntiles > 0) {
-                float* stage = reinterpret_cast<float*>(kv_s) + (size_t)hb * a.f.c + d;
+                float* dst = a.merge == kCluster ? reinterpret_cast<float*>(kv_s) : a.part_o + part * a.f.c;
+                dst += hb * a.f.c + d;
 #pragma unroll
-                for (int i = 0; i < kGh; ++i) stage[(size_t)i * a.f.c] = o[i];
+                for (int i = 0; i < 16; ++i)
+                    if (i < heads) dst[i * a.f.c] = o[i];
             }
         }
         tc::tc_fence_before();
     }
 
-    const int nh = a.H - h0 < kHg ? a.H - h0 : kHg, c4 = a.f.c / 4;
-    bf16* out = a.out + ((int64_t)t * a.H + h0) * a.f.c;   // this CTA's heads: contiguous rows
     if (a.merge == kCluster) {
         // two splits send each other the half of their sums that the other
         // writes out, one bulk copy to where its queries were; more read their
@@ -512,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             wait(&s.peer, 0, s, a.status);
             const float4* mine = reinterpret_cast<const float4*>(kv_s) + lo;
             const float4* theirs = reinterpret_cast<const float4*>(q_s);
-            for (int i = tid; i < hi - lo; i += kWorkers) {
+            for (int i = tid; i < hi - lo; i += kThreads) {
                 const int h = (lo + i) / c4;
                 const float4 x = mine[i], y = theirs[i];
                 const float w0 = s.coef[split][h], w1 = s.coef[split ^ 1][h];
@@ -529,24 +478,16 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         }
         tc::cluster_sync();                               // no peer still reads this CTA's sums
     } else {
-        __syncthreads();
-        if (a.merge == kDirect) {
-            const uint4* stage = reinterpret_cast<const uint4*>(kv_s);
-            for (int i = tid; i < nh * a.f.c / 8; i += kWorkers) reinterpret_cast<uint4*>(out)[i] = stage[i];
-        } else {
-            const int64_t part = ((int64_t)t * a.nsplit + split) * a.H + h0;
-            if (tid < nh) {
-                const float m = s.mref[tid], L = s.lsum[tid];
-                a.part_ml[(part + tid) * 2] = L == 0.f ? -INFINITY : L != L ? 0.f : m * kLn2;
-                a.part_ml[(part + tid) * 2 + 1] = L;
-            }
-            if (ntiles > 0) {
-                const float4* stage = reinterpret_cast<const float4*>(kv_s);
-                float4* dst = reinterpret_cast<float4*>(a.part_o + part * a.f.c);
-                for (int i = tid; i < nh * c4; i += kWorkers) dst[i] = stage[i];
-            }
+        if (a.merge == kWorkspace && tid < nh) {
+            const float m = s.mref[tid], L = s.lsum[tid];
+            a.part_ml[(part + tid) * 2] = L == 0.f ? -INFINITY : L != L ? 0.f : m * kLn2;
+            a.part_ml[(part + tid) * 2 + 1] = L;
         }
         __syncthreads();
+    }
+    if (warp == kSWarp) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem_S, kTmemCols);
     }
 }
 
@@ -585,7 +526,6 @@ cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {
     Args a{};
     a.qm = QueryMap{x.qs.seq, x.qs.pos, x.qs.pos_base, x.qs.single_seq};
     a.kv4 = x.kv4;
-    a.q = (const bf16*)x.q;
     a.idx = x.idx;
     a.sink = x.sink;
     a.out = (bf16*)x.out;
@@ -606,13 +546,15 @@ cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {
     a.dblocks = x.c / 64;
     a.mtiles = x.c / 128;
     a.scale_log2 = x.scale * kLog2e;
-    const size_t smem = 1024 + (size_t)a.dblocks * (kBlockBytes + kHg * 128) + kE * 128 + sizeof(Shared);
+    CUtensorMap tmQ;
+    if (!make_tmap_bf16_2d(&tmQ, x.q, (uint64_t)x.nq * x.H, x.c, x.c, kHg, 64)) return cudaErrorInvalidValue;
+    const size_t smem = 1024 + (size_t)a.dblocks * (2 * kBlockBytes + kHg * 128) + 2 * kE * 128 + sizeof(Shared);
     auto kern = x.idx ? mqa_fp4_kernel<true> : mqa_fp4_kernel<false>;
     cudaError_t e = smem_ceiling(kern);
     if (e != cudaSuccess) return e;
     CSA_LAUNCH(st, "mqa_fp4",
                e = launch_pdl(kern, dim3(ns, (x.H + kHg - 1) / kHg, x.nq), dim3(kThreads), smem, st,
-                              a.merge == kCluster ? (unsigned)ns : 0u, a));
+                              a.merge == kCluster ? (unsigned)ns : 0u, a, tmQ));
     if (e != cudaSuccess) return e;
     if (a.merge == kWorkspace) {
         e = mqa_combine_bf16(a.part_o, a.part_ml, ns, x.nq, x.H, x.c, x.sink, x.out, x.lse, st);

@@ -2,9 +2,9 @@
 //
 //   weight of s = sum over heads (and queries) of e^{z_s - lse}
 //
-// The logits are the attention's S^T = V_tile . q^T product (128 entries x 64
-// heads, K = c; mqa_fp4.cu) without the second product: entries are the lanes
-// of the result, and a thread sums the weights of its entry over 64 heads.
+// The logits are the attention's S^T = V_tile . q^T product (64 entries x 64
+// heads, K = c; mqa_fp4.cu) without the second product; the four threads that
+// hold an entry's logits sum its weights over the heads.
 // Bound by reading the packed rows; what paces it is expanding them.
 //
 // A CTA walks a run of tiles of one sequence (or of one query's entry list).
@@ -12,9 +12,9 @@
 // its sequence; their q blocks stream through one buffer, refilled in quarters
 // as the product has read them, unless there is only one, which stays. The
 // next tile is expanded as the last query block's product releases the blocks.
-// Every sum has a fixed order: heads, then queries.
+// Every sum has a fixed order: a thread's heads, queries, then the four threads.
 //
-// Warps 0-3: sums; 4-11: producers; 12: products; 13: query loads.
+// Warps 0-3: sums; 4-19: producers; 20: products; 21: query loads.
 #include "fp4_tile.cuh"
 #include "kernels.h"
 #include "tmap.h"
@@ -25,7 +25,7 @@ namespace {
 
 using namespace fp4_tile;
 
-constexpr int kThreads = 448;           // 4 summing warps, 8 producers, products, query loads
+constexpr int kThreads = (4 + kProducerWarps + 2) * 32;   // sums, producers, products, query loads
 
 struct Args : Fp4TileArgs {
     const float* lse;
@@ -64,8 +64,8 @@ template <bool kSparse>
 __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __grid_constant__ Args a,
                                                                         const __grid_constant__ CUtensorMap tmQ) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* kv_s = smem_raw + ((0u - tc::smem_u32(smem_raw)) & 1023u);           // dblocks x 16 KB
-    uint8_t* q_s = kv_s + (size_t)a.dblocks * kBlockBytes;                         // dblocks x 8 KB
+    uint8_t* kv_s = smem_raw + ((0u - tc::smem_u32(smem_raw)) & 1023u);           // 2 x dblocks x 8 KB
+    uint8_t* q_s = kv_s + (size_t)a.dblocks * 2 * kBlockBytes;                     // dblocks x 8 KB
     Shared& s = *reinterpret_cast<Shared*>(q_s + (size_t)a.dblocks * kHg * 128);
 
     pdl_wait();
@@ -78,8 +78,10 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
     const int e_stop = (int64_t)a.run * kE > n_all - e_beg ? n_all : e_beg + a.run * kE;   // this CTA's entries
     if (tid == 0) {
         for (int i = 0; i < kPairs; ++i) {
-            tc::mbar_init(&s.full[i], kProducers / 32);
-            tc::mbar_init(&s.empty[i], 1);
+            for (int b = 0; b < 2; ++b) {
+                tc::mbar_init(&s.full[b][i], 8);         // a buffer's producer warps
+                tc::mbar_init(&s.empty[b][i], 1);
+            }
             tc::mbar_init(&s.q_full[i], 1);
             tc::mbar_init(&s.q_empty[i], 1);
         }
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
         s.abort = 0;
         s.n_max = 0;
     }
-    if (warp == 12) {
+    if (warp == 20) {
         tc::tmem_alloc(&s.tmem, 128);
         tc::tmem_relinquish();
         tc::tc_fence_before();
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
     const uint32_t tmem_S = __shfl_sync(0xffffffffu, s.tmem, 0);
     const bool stay = a.T * a.hgroups == 1;
 
-    if (warp == 13) {
+    if (warp == 21) {
         // ------------------------------------------------------------ query loads
         if (lane == 0) {
             uint32_t n = 0;
@@ -137,11 +139,11 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
                 for (int i = 0; i < a.mtiles; ++i) tc::mbar_wait(&s.q_full[i], (n - 1) & 1, ok ? kWaitLimit : 1u << 16);
         }
         __syncwarp();
-    } else if (warp == 12) {
+    } else if (warp == 20) {
         // ------------------------------------------------------------ products
         if (ntiles > 0) {
             const uint32_t kv_addr = __shfl_sync(0xffffffffu, tc::smem_u32(kv_s), 0);
-            const uint32_t q_addr = kv_addr + a.dblocks * kBlockBytes;
+            const uint32_t tile_bytes = a.dblocks * kBlockBytes, q_addr = kv_addr + 2 * tile_bytes;
             const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
             uint32_t n = 0;
             bool ok = true;
@@ -156,18 +158,18 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
                         for (int o = 0; o < a.mtiles; ++o) {
                             const int i = a.mtiles - 1 - o;               // as they are stored
                             if (!(ok = __all_sync(0xffffffffu, wait(&s.q_full[i], stay ? 0 : n & 1, s, a.status)))) break;
-                            if (first && !(ok = __all_sync(0xffffffffu, wait(&s.full[i], j & 1, s, a.status)))) break;
+                            if (first && !(ok = __all_sync(0xffffffffu, wait(&s.full[j & 1][i], (j >> 1) & 1, s, a.status)))) break;
                             tc::tc_fence_after();
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk) {
                                 const int blk = 2 * i + (kk >> 2);
                                 tc::umma_bf16_warp(tmem_S + sb * kHg,
-                                              tc::sdesc_sw128(kv_addr + blk * kBlockBytes + (kk & 3) * 32, 16, 1024),
+                                              tc::sdesc_sw128(kv_addr + (j & 1) * tile_bytes + blk * kBlockBytes + (kk & 3) * 32, 16, 1024),
                                               tc::sdesc_sw128(q_addr + blk * (kHg * 128) + (kk & 3) * 32, 16, 1024),
                                               idesc, (o | kk) ? 1u : 0u);
                             }
                             if (!stay) tc::umma_commit_warp(&s.q_empty[i]);
-                            if (t == last && g == a.hgroups - 1) tc::umma_commit_warp(&s.empty[i]);
+                            if (t == last && g == a.hgroups - 1) tc::umma_commit_warp(&s.empty[j & 1][i]);
                         }
                         if (ok) tc::umma_commit_warp(&s.s_full[sb]);
                         first = false;
@@ -179,18 +181,16 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
         }
         __syncwarp();
     } else if (warp >= 4) {
-        Producer<kSparse, false, 1> producer(a, s, kv_s, 0, warp - 4, b, e_beg, e_end, ntiles, (int64_t)(ntiles ? seq : 0) * a.Nmax);
-        if (ntiles > 0) producer.load(0);
-        for (int j = 0; j < ntiles; ++j)
-            if (!producer.store(j)) break;
+        Producer<kSparse>(a, s, kv_s, warp - 4, b, e_beg, e_end, ntiles, (int64_t)(ntiles ? seq : 0) * a.Nmax);
     } else {
         // ------------------------------------------------------------ sums
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         uint32_t n = 0;
         bool ok = true;
         for (int j = 0; j < ntiles; ++j) {
-            const int e_tile = e_beg + j * kE, last = blocks.last_query(e_tile), e = e_tile + tid;
-            float w = 0.f;
+            const int e_tile = e_beg + j * kE, last = blocks.last_query(e_tile);
+            const int ea = e_tile + warp * 16 + (lane >> 2), eb = ea + 8;     // this thread's entries
+            float wa = 0.f, wb = 0.f;
             for (int t = 0; t <= last; ++t) {
                 const int seen = blocks.visible(t);
                 if (seen <= e_tile) continue;
@@ -206,35 +206,47 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
                     const uint32_t sb = n & 1;
                     ok = ok && wait(&s.s_full[sb], (n >> 1) & 1, s, a.status);
                     tc::tc_fence_after();
-                    float p = 0.f;
+                    float pa = 0.f, pb = 0.f;
 #pragma unroll
-                    for (int cc = 0; cc < kHg; cc += 16) {
+                    for (int cc = 0; cc < kHg; cc += 32) {
                         float z[16];
-                        tc::tmem_ld16(tmem_S + lanes + sb * kHg + cc, z);
+                        tc::tmem_ld_16x32(tmem_S + lanes + sb * kHg + cc, z);
                         tc::tmem_ld_wait();
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float l = s.lse[warp][cc + i];
-                            p += l == INFINITY ? 0.f : ex2(fmaf(z[i], a.scale_log2, -l));
+                            const float l = s.lse[warp][cc + 8 * (i >> 2) + 2 * (lane & 3) + (i & 1)];
+                            const float p = l == INFINITY ? 0.f : ex2(fmaf(z[i], a.scale_log2, -l));
+                            if (i & 2) pb += p;
+                            else pa += p;
                         }
                     }
                     tc::tc_fence_before();
-                    if (kSparse || e < seen) w += p;
+                    if (kSparse || ea < seen) wa += pa;
+                    if (kSparse || eb < seen) wb += pb;
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&s.s_empty[sb]);
                 }
             }
-            if (e >= e_end) continue;
-            if (kSparse) {
-                const int entry = __ldg(a.idx + (int64_t)b * a.k + e);
-                if (entry < 0 || entry >= a.Nmax) w = 0.f;
-                if (a.weights) a.weights[(int64_t)b * a.k + e] = w;
-                // (entries listed twice add twice the same value, in any order)
-                if (a.acc && entry >= 0 && entry < a.Nmax) atomicAdd(a.acc + (int64_t)seq * a.Nmax + entry, w);
-            } else {
-                const int64_t i = (int64_t)b * a.Nmax + e;
-                a.weights[i] = (a.acc ? a.acc[i] : 0.f) + w;
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                wa += __shfl_xor_sync(0xffffffffu, wa, o);
+                wb += __shfl_xor_sync(0xffffffffu, wb, o);
             }
+            const int e = lane & 1 ? eb : ea;
+            float w = lane & 1 ? wb : wa;
+            if (!(lane & 2) && e < e_end) {
+                if (kSparse) {
+                    const int entry = __ldg(a.idx + (int64_t)b * a.k + e);
+                    if (entry < 0 || entry >= a.Nmax) w = 0.f;
+                    if (a.weights) a.weights[(int64_t)b * a.k + e] = w;
+                    // (entries listed twice add twice the same value, in any order)
+                    if (a.acc && entry >= 0 && entry < a.Nmax) atomicAdd(a.acc + (int64_t)seq * a.Nmax + entry, w);
+                } else {
+                    const int64_t i = (int64_t)b * a.Nmax + e;
+                    a.weights[i] = (a.acc ? a.acc[i] : 0.f) + w;
+                }
+            }
+            __syncwarp();
         }
         // entries that no query sees
         for (int e = (e_end > e_beg ? e_end : e_beg) + tid; e < e_stop; e += 128) {
@@ -248,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
         tc::tc_fence_before();
     }
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 20) {
         tc::tc_fence_after();
         tc::tmem_dealloc(s.tmem, 128);
     }
@@ -288,7 +300,7 @@ cudaError_t entry_weights_fp4(const Fp4WeightArgs& x, cudaStream_t st) {
     CUtensorMap tmQ;
     const uint64_t rows = (uint64_t)x.B * (x.T > 0 ? x.T : 1) * x.H;
     if (!make_tmap_bf16_2d(&tmQ, x.T > 0 ? x.q : x.kv4, rows, x.c, x.c, kHg, 64)) return cudaErrorInvalidValue;
-    const size_t smem = 1024 + (size_t)a.dblocks * (kBlockBytes + kHg * 128) + sizeof(Shared);
+    const size_t smem = 1024 + (size_t)a.dblocks * (2 * kBlockBytes + kHg * 128) + sizeof(Shared);
     auto kern = x.idx ? entry_weights_fp4_kernel<true> : entry_weights_fp4_kernel<false>;
     cudaError_t e = smem_ceiling(kern);
     if (e != cudaSuccess) return e;
