@@ -103,6 +103,14 @@ __device__ __forceinline__ float rows_reduce(float v, Op op) {
     return v;
 }
 
+// 4 matrices of 8 x 8 bf16, transposed: m[i] holds elements (lane / 4, 2 (lane %
+// 4)) and the next of matrix i; column r is written to the 16 bytes that lane
+// 8i + r points to
+__device__ __forceinline__ void stmatrix_trans4(uint32_t dst, const uint32_t (&m)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                 ::"r"(dst), "r"(m[0]), "r"(m[1]), "r"(m[2]), "r"(m[3]) : "memory");
+}
+
 // out[i] (4 dims each) for i in [lo, hi): the cluster's staged sums, weighted.
 template <int kN>
 __device__ __forceinline__ void merge_items(const Args& a, const Shared& s, const uint8_t* stage, bf16* out, int lo,
@@ -141,7 +149,7 @@ __device__ __forceinline__ void merge_items(const Args& a, const Shared& s, cons
     }
 }
 
-template <bool kSparse>
+template <bool kSparse, bool kWide>
 __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_constant__ Args a,
                                                               const __grid_constant__ CUtensorMap tmQ) {
     extern __shared__ uint8_t smem_raw[];
@@ -247,7 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             tc::mbar_wait(&s.fin[warp - kSWarp], 0, kWaitLimit);
         }
     } else if (warp >= kSoftmaxWarps) {
-        Producer<kSparse>(a, s, kv_s, warp - kSoftmaxWarps, t, (int)e_beg, (int)e_end, ntiles, (ntiles ? seq : 0) * a.Nmax);
+        produce<ProducerOf<kSparse, kWide>>(a, s, kv_s, warp - kSoftmaxWarps, t, (int)e_beg, (int)e_end, ntiles,
+                                            (ntiles ? seq : 0) * a.Nmax);
     } else {
         // ------------------------------------------------------------ softmax
         const int quad = warp & 3, half = warp >> 2, hb = half * kHalf;
@@ -381,10 +390,44 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     const int nh = a.H - h0 < kHg ? a.H - h0 : kHg, c4 = a.f.c / 4;
     bf16* out = a.out + ((int64_t)t * a.H + h0) * a.f.c;   // this CTA's heads: contiguous rows
     const int64_t part = ((int64_t)t * a.nsplit + split) * a.H + h0;
-    if (warp < 16) {
-        // warp w has dims 32 (w % 4).. of every M tile and 16 heads, a lane one
-        // dim: written out from the registers, or (a cluster) to shared memory
-        // where the tiles were, as rows of a head
+    // where the output is staged as bf16: rows of 16 more bytes than a head's,
+    // so that 8 rows start in different banks
+    const uint32_t pitch = a.f.c * 2 + 16;
+    if (warp < 16 && a.merge == kDirect) {
+        // normalised, bf16: warp w has dims 32 (w % 4).. of every M tile and 16
+        // heads; the transposing matrix stores write 8 dims of a head at a time
+        tc::tc_fence_after();
+        const int hb = (warp >> 2) * 16;
+        const uint32_t addr = tmem_O + ((uint32_t)((warp & 3) * 32) << 16) + hb;
+        float2 al[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) al[u] = *reinterpret_cast<const float2*>(&s.alpha[hb + 8 * u + 2 * (lane & 3)]);
+        // lane i gives the address of row i % 8 (a head) of matrix i / 8: heads
+        // 8 (i / 16).., dims 8 ((i / 8) % 2)..
+        const uint32_t dst = tc::smem_u32(kv_s) + (hb + (lane >> 4) * 8 + (lane & 7)) * pitch +
+                             ((warp & 3) * 32 + ((lane >> 3) & 1) * 8) * 2;
+#pragma unroll 1
+        for (int n = 0; n < 2 * a.mtiles; ++n) {          // 16 dims at a time
+            float o[8];
+            if (ntiles > 0) {
+                tc::tmem_ld_16x16(addr + (n >> 1) * kHg + ((uint32_t)(16 * (n & 1)) << 16), o);
+                tc::tmem_ld_wait();
+            }
+            uint32_t m[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {                 // heads 8 (i / 2).., dims 8 (i % 2)..
+                const float2 w = al[i >> 1];
+                const __nv_bfloat162 v = __floats2bfloat162_rn(w.x != 0.f ? o[2 * i] * w.x : 0.f,
+                                                               w.y != 0.f ? o[2 * i + 1] * w.y : 0.f);
+                m[i] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            stmatrix_trans4(dst + ((n >> 1) * 128 + (n & 1) * 16) * 2, m);
+        }
+        tc::fence_proxy_async_smem();
+        tc::tc_fence_before();
+    } else if (warp < 16) {
+        // fp32, warp w as above, a lane one dim: to the workspace, or (a
+        // cluster) to shared memory where the tiles were, as rows of a head
         tc::tc_fence_after();
         const int hb = (warp >> 2) * 16, row = (warp & 3) * 32 + lane;
         const uint32_t addr = tmem_O + ((uint32_t)((warp & 3) * 32) << 16) + hb;
@@ -392,19 +435,10 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
 #pragma unroll 1
         for (int mt = 0; mt < a.mtiles; ++mt) {
             const int d = mt * 128 + row;
-            float o[16];
             if (ntiles > 0) {
+                float o[16];
                 tc::tmem_ld16(addr + mt * kHg, o);
                 tc::tmem_ld_wait();
-            }
-            if (a.merge == kDirect) {                     // normalised, bf16
-                bf16* dst = out + (int64_t)hb * a.f.c + d;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float al = s.alpha[hb + i];
-                    if (i < heads) dst[i * a.f.c] = __float2bfloat16_rn(al != 0.f ? o[i] * al : 0.f);
-                }
-            } else if (ntiles > 0) {
                 float* dst = a.merge == kCluster ? reinterpret_cast<float*>(kv_s) : a.part_o + part * a.f.c;
                 dst += hb * a.f.c + d;
 #pragma unroll
@@ -478,7 +512,14 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         }
         tc::cluster_sync();                               // no peer still reads this CTA's sums
     } else {
-        if (a.merge == kWorkspace && tid < nh) {
+        if (a.merge == kDirect) {
+            __syncthreads();
+            if (tid < nh) {
+                tc::bulk_store(out + (int64_t)tid * a.f.c, kv_s + tid * pitch, a.f.c * 2);
+                tc::bulk_commit();
+                tc::bulk_wait_all();
+            }
+        } else if (tid < nh) {
             const float m = s.mref[tid], L = s.lsum[tid];
             a.part_ml[(part + tid) * 2] = L == 0.f ? -INFINITY : L != L ? 0.f : m * kLn2;
             a.part_ml[(part + tid) * 2 + 1] = L;
@@ -549,7 +590,9 @@ cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {
     CUtensorMap tmQ;
     if (!make_tmap_bf16_2d(&tmQ, x.q, (uint64_t)x.nq * x.H, x.c, x.c, kHg, 64)) return cudaErrorInvalidValue;
     const size_t smem = 1024 + (size_t)a.dblocks * (2 * kBlockBytes + kHg * 128) + 2 * kE * 128 + sizeof(Shared);
-    auto kern = x.idx ? mqa_fp4_kernel<true> : mqa_fp4_kernel<false>;
+    const bool wide = wide_rows(a.f, x.kv4);
+    auto kern = x.idx ? (wide ? mqa_fp4_kernel<true, true> : mqa_fp4_kernel<true, false>)
+                      : (wide ? mqa_fp4_kernel<false, true> : mqa_fp4_kernel<false, false>);
     cudaError_t e = smem_ceiling(kern);
     if (e != cudaSuccess) return e;
     CSA_LAUNCH(st, "mqa_fp4",

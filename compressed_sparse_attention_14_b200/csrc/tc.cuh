@@ -72,14 +72,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
     return false;
 }
 
-// ---------------------------------------------------------------- bulk load
-// Global -> shared bulk copy, its bytes counted on `bar`: both addresses
-// 16-byte aligned, size a multiple of 16.
-__device__ __forceinline__ void bulk_load(void* sdst, const void* gsrc, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 :: "r"(smem_u32(sdst)), "l"(gsrc), "r"(bytes), "r"(smem_u32(bar)) : "memory");
-}
-
 // ---------------------------------------------------------------- bulk store
 // Shared -> global bulk copy (async proxy): both addresses 16-byte aligned,
 // size a multiple of 16. The shared data must have been made visible to the
@@ -267,6 +259,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
         : "r"(taddr));
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 16 lanes x 16 columns -> registers, in the order of tmem_ld_16x32.
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 // 16 lanes x 32 columns -> registers: 4u, 4u + 1 are lane (lane / 4), columns
 // 8u + 2 (lane % 4) and the next; 4u + 2, 4u + 3 the same columns 8 lanes on.

@@ -60,7 +60,7 @@ struct Blocks {
     }
 };
 
-template <bool kSparse>
+template <bool kSparse, bool kWide>
 __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __grid_constant__ Args a,
                                                                         const __grid_constant__ CUtensorMap tmQ) {
     extern __shared__ uint8_t smem_raw[];
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
         }
         __syncwarp();
     } else if (warp >= 4) {
-        Producer<kSparse>(a, s, kv_s, warp - 4, b, e_beg, e_end, ntiles, (int64_t)(ntiles ? seq : 0) * a.Nmax);
+        produce<ProducerOf<kSparse, kWide>>(a, s, kv_s, warp - 4, b, e_beg, e_end, ntiles, (int64_t)(ntiles ? seq : 0) * a.Nmax);
     } else {
         // ------------------------------------------------------------ sums
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
@@ -301,7 +301,9 @@ cudaError_t entry_weights_fp4(const Fp4WeightArgs& x, cudaStream_t st) {
     const uint64_t rows = (uint64_t)x.B * (x.T > 0 ? x.T : 1) * x.H;
     if (!make_tmap_bf16_2d(&tmQ, x.T > 0 ? x.q : x.kv4, rows, x.c, x.c, kHg, 64)) return cudaErrorInvalidValue;
     const size_t smem = 1024 + (size_t)a.dblocks * (2 * kBlockBytes + kHg * 128) + sizeof(Shared);
-    auto kern = x.idx ? entry_weights_fp4_kernel<true> : entry_weights_fp4_kernel<false>;
+    const bool wide = wide_rows(a.f, x.kv4);
+    auto kern = x.idx ? (wide ? entry_weights_fp4_kernel<true, true> : entry_weights_fp4_kernel<true, false>)
+                      : (wide ? entry_weights_fp4_kernel<false, true> : entry_weights_fp4_kernel<false, false>);
     cudaError_t e = smem_ceiling(kern);
     if (e != cudaSuccess) return e;
     CSA_LAUNCH(st, "entry_weights_fp4",
