@@ -321,13 +321,15 @@ struct WideProducer {
     }
 };
 
-// All of a producer warp's work (warp: 0 .. 15 of the producers).
-template <typename P>
+// All of a producer warp's work (warp: 0 .. 15 of the producers). ready() is
+// called when the first tile's loads have been issued.
+template <typename P, typename F>
 __device__ __forceinline__ void produce(const Fp4TileArgs& a, Fp4TileShared& s, uint8_t* kv_s, int warp, int t, int e_beg,
-                                        int e_end, int ntiles, int64_t first_row) {
+                                        int e_end, int ntiles, int64_t first_row, F ready) {
     P p(a, s, kv_s, warp, t, e_beg, e_end, ntiles, first_row);
     int j = warp >> 3;
     if (j < ntiles) p.load(j);
+    ready();
     for (; j < ntiles; j += 2) {
         if (!p.store(j)) break;
         if (j + 2 < ntiles) p.load(j + 2);

@@ -170,33 +170,46 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     const int64_t e_end = n_ent < e_beg + a.split_len ? n_ent : e_beg + a.split_len;
     const int ntiles = e_end > e_beg ? (int)((e_end - e_beg + kE - 1) / kE) : 0;
 
-    if (tid == 0) {
-        for (int b = 0; b < 2; ++b) {
-            for (int i = 0; i < kPairs; ++i) {
-                tc::mbar_init(&s.full[b][i], 8);     // a buffer's producer warps
-                tc::mbar_init(&s.empty[b][i], 1);
-            }
-            tc::mbar_init(&s.s_full[b], 1);
-            tc::mbar_init(&s.p_full[b], kSoftmaxWarps);
-            tc::mbar_init(&s.fin[b], 1);
-        }
-        tc::mbar_init(&s.q_full, 1);
-        tc::mbar_init(&s.o_done, 1);
-        tc::mbar_init(&s.peer, 1);
-        tc::fence_mbar_init();
-        s.abort = 0;
-    }
-    if (warp == kSWarp) {
-        tc::tmem_alloc(&s.tmem, kTmemCols);
-        tc::tmem_relinquish();
-        tc::tc_fence_before();
-    }
-    __syncthreads();
-    tc::tc_fence_after();
-    const uint32_t tmem_S = __shfl_sync(0xffffffffu, s.tmem, 0), tmem_O = tmem_S + 2 * kHg;
-
+    // The set-up's barrier stands in each role: what a role can start before it
+    // (the queries' copy, the first tiles' loads) has begun by then.
+    uint32_t tmem_S = 0, tmem_O = 0;
+    auto setup_done = [&]() {
+        __syncthreads();
+        tc::tc_fence_after();
+        tmem_S = __shfl_sync(0xffffffffu, s.tmem, 0);
+        tmem_O = tmem_S + 2 * kHg;
+    };
     if (warp >= kSWarp) {
         // ------------------------------------------------------------ products
+        if (warp == kSWarp) {
+            if (lane == 0) {
+                for (int b = 0; b < 2; ++b) {
+                    for (int i = 0; i < kPairs; ++i) {
+                        tc::mbar_init(&s.full[b][i], 8);     // a buffer's producer warps
+                        tc::mbar_init(&s.empty[b][i], 1);
+                    }
+                    tc::mbar_init(&s.s_full[b], 1);
+                    tc::mbar_init(&s.p_full[b], kSoftmaxWarps);
+                    tc::mbar_init(&s.fin[b], 1);
+                }
+                tc::mbar_init(&s.q_full, 1);
+                tc::mbar_init(&s.o_done, 1);
+                tc::mbar_init(&s.peer, 1);
+                tc::fence_mbar_init();
+                s.abort = 0;
+                if (ntiles > 0) {
+                    tc::mbar_expect_tx(&s.q_full, (uint32_t)a.dblocks * kHg * 128);
+                    for (int b = 0; b < a.dblocks; ++b)
+                        tc::tma_load_2d(q_s + (size_t)b * kHg * 128, &tmQ, &s.q_full, b * 64, t * a.H + h0);
+                }
+            }
+            __syncwarp();
+        } else {
+            tc::tmem_alloc(&s.tmem, kTmemCols);
+            tc::tmem_relinquish();
+            tc::tc_fence_before();
+        }
+        setup_done();
         if (ntiles > 0) {
             const uint32_t kv_addr = __shfl_sync(0xffffffffu, tc::smem_u32(kv_s), 0);
             const uint32_t tile_bytes = a.dblocks * kBlockBytes;
@@ -206,12 +219,6 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             };
             bool ok = true;
             if (warp == kSWarp) {
-                if (lane == 0) {
-                    tc::mbar_expect_tx(&s.q_full, (uint32_t)a.dblocks * kHg * 128);
-                    for (int b = 0; b < a.dblocks; ++b)
-                        tc::tma_load_2d(q_s + (size_t)b * kHg * 128, &tmQ, &s.q_full, b * 64, t * a.H + h0);
-                }
-                __syncwarp();
                 ok = until(&s.q_full, 0);
                 const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
                 for (int j = 0; ok && j < ntiles; ++j) {
@@ -256,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         }
     } else if (warp >= kSoftmaxWarps) {
         produce<ProducerOf<kSparse, kWide>>(a, s, kv_s, warp - kSoftmaxWarps, t, (int)e_beg, (int)e_end, ntiles,
-                                            (ntiles ? seq : 0) * a.Nmax);
+                                            (ntiles ? seq : 0) * a.Nmax, setup_done);
     } else {
         // ------------------------------------------------------------ softmax
         const int quad = warp & 3, half = warp >> 2, hb = half * kHalf;
@@ -270,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         float lpart[8];                                   // heads hb + 8u + 2 q4 + (0, 1), both entries
 #pragma unroll
         for (int i = 0; i < 8; ++i) lpart[i] = 0.f;
-        half_sync(half);
+        setup_done();
         bool ok = true;
         for (int j = 0; j < ntiles; ++j) {
             const int b = j & 1;
@@ -517,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             if (tid < nh) {
                 tc::bulk_store(out + (int64_t)tid * a.f.c, kv_s + tid * pitch, a.f.c * 2);
                 tc::bulk_commit();
-                tc::bulk_wait_all();
+                tc::bulk_wait_read();
             }
         } else if (tid < nh) {
             const float m = s.mref[tid], L = s.lsum[tid];
@@ -526,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         }
         __syncthreads();
     }
-    if (warp == kSWarp) {
+    if (warp == kSWarp + 1) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem_S, kTmemCols);
     }
