@@ -17,7 +17,6 @@ namespace fp4_tile {
 
 constexpr int kProducerWarps = 16;      // 8 to a tile
 constexpr int kE = 64;                  // entries per tile
-constexpr int kHg = 64;                 // heads per CTA
 constexpr int kPairs = CSA_MAX_HEAD_DIM / 128;   // pairs of 64-channel blocks
 constexpr uint32_t kBlockBytes = kE * 128;
 constexpr uint32_t kWaitLimit = 1u << 20;   // (2 us each)

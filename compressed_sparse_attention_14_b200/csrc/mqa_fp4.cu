@@ -46,8 +46,7 @@ using namespace fp4_tile;
 
 constexpr int kSoftmaxWarps = 8, kThreads = (kSoftmaxWarps + kProducerWarps + 2) * 32;
 constexpr int kSWarp = kSoftmaxWarps + kProducerWarps;   // and the next: products
-constexpr int kHalf = kHg / 2;          // heads per softmax warp
-constexpr uint32_t kTmemCols = 512;     // S^T 2 x 64, O^T up to 256
+constexpr int kMaxHg = 64;              // heads per CTA: 64 or 16
 constexpr int kMaxCluster = 8;
 constexpr float kMoveLog2 = 24.0f, kLn2 = 0.6931471805599453f;
 
@@ -67,10 +66,10 @@ struct Args : Fp4TileArgs {
 
 struct Shared : Fp4TileShared {
     // the heads' reference maxima; the same plus the limit; the same, 0 for none
-    float mref[kHg], limit[kHg], mexp[kHg];
-    float alpha[kHg], lsum[kHg];
-    float red[4][kHg];
-    float coef[kMaxCluster][kHg];
+    float mref[kMaxHg], limit[kMaxHg], mexp[kMaxHg];
+    float alpha[kMaxHg], lsum[kMaxHg];
+    float red[4][kMaxHg];
+    float coef[kMaxCluster][kMaxHg];
     uint64_t s_full[2], p_full[2], q_full, o_done, fin[2];
     uint64_t peer;                            // the other split's sums have arrived (clusters of two)
     uint32_t tmem;
@@ -83,7 +82,7 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
     return v;
 }
 
-// barrier (and vote) of the 4 softmax warps that share 32 heads
+// barrier (and vote) of the 4 softmax warps that share half of the heads
 __device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
 __device__ __forceinline__ bool half_any(int half, bool v) {
     uint32_t r;
@@ -149,14 +148,16 @@ __device__ __forceinline__ void merge_items(const Args& a, const Shared& s, cons
     }
 }
 
-template <bool kSparse, bool kWide>
+template <bool kSparse, bool kWide, int kHg>
 __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_constant__ Args a,
                                                               const __grid_constant__ CUtensorMap tmQ) {
+    constexpr int kHalf = kHg / 2, kOct = kHg / 16;       // heads, and groups of 8, per softmax warp
+    constexpr uint32_t kTmemCols = kHg == 64 ? 512 : 128; // S^T 2 x kHg, O^T up to 4 x kHg
     extern __shared__ uint8_t smem_raw[];
     // (an offset, not a rounded pointer: the accesses stay shared-memory ones)
     uint8_t* kv_s = smem_raw + ((0u - tc::smem_u32(smem_raw)) & 1023u);           // 2 x dblocks x 8 KB
     uint8_t* q_s = kv_s + (size_t)a.dblocks * 2 * kBlockBytes;                     // dblocks x 8 KB
-    uint8_t* p_s = q_s + (size_t)a.dblocks * kHg * 128;                            // 2 x 64 entries x 64 heads
+    uint8_t* p_s = q_s + (size_t)a.dblocks * kHg * 128;                            // 2 x 64 entries x 128 bytes
     Shared& s = *reinterpret_cast<Shared*>(p_s + 2 * kE * 128);
 
     pdl_wait();
@@ -274,9 +275,9 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             s.mref[hb + hth] = s.limit[hb + hth] = -INFINITY;
             s.mexp[hb + hth] = 0.f;
         }
-        float lpart[8];                                   // heads hb + 8u + 2 q4 + (0, 1), both entries
+        float lpart[2 * kOct];                            // heads hb + 8u + 2 q4 + (0, 1), both entries
 #pragma unroll
-        for (int i = 0; i < 8; ++i) lpart[i] = 0.f;
+        for (int i = 0; i < 2 * kOct; ++i) lpart[i] = 0.f;
         setup_done();
         bool ok = true;
         for (int j = 0; j < ntiles; ++j) {
@@ -291,17 +292,17 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             const bool va = seen(ra), vb = seen(rb);
             ok = ok && wait(&s.s_full[b], (j >> 1) & 1, s, a.status);
             tc::tc_fence_after();
-            float z[16];
+            float z[4 * kOct];
             auto logits = [&]() {
-                tc::tmem_ld_16x32(tmem_S + lanes + b * kHg + hb, z);
+                tc::tmem_ld_16(tmem_S + lanes + b * kHg + hb, z);
                 tc::tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) z[i] = (i & 2 ? vb : va) ? z[i] * a.scale_log2 : -INFINITY;
+                for (int i = 0; i < 4 * kOct; ++i) z[i] = (i & 2 ? vb : va) ? z[i] * a.scale_log2 : -INFINITY;
             };
             logits();
             bool move = false;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < kOct; ++u) {
                 const float2 lim = *reinterpret_cast<const float2*>(&s.limit[hb + 8 * u + 2 * q4]);
                 move |= z[4 * u] > lim.x || z[4 * u + 2] > lim.x || z[4 * u + 1] > lim.y || z[4 * u + 3] > lim.y;
             }
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                 // all leave together once a wait of one ran out
                 if (half_any(half, !ok)) { ok = false; break; }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < 2 * kOct; ++i) {
                     const int u = i >> 1, e = i & 1;
                     const float top = rows_reduce(fmaxf(z[4 * u + e], z[4 * u + 2 + e]),
                                                   [](float x, float y) { return fmaxf(x, y); });
@@ -327,20 +328,21 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                 }
                 half_sync(half);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) lpart[i] *= s.alpha[hb + 8 * (i >> 1) + 2 * q4 + (i & 1)];
+                for (int i = 0; i < 2 * kOct; ++i) lpart[i] *= s.alpha[hb + 8 * (i >> 1) + 2 * q4 + (i & 1)];
                 if (j > 0) {
                     // rescale O^T (every product before this tile's has ended)
                     ok = wait(&s.o_done, (j - 1) & 1, s, a.status);
                     tc::tc_fence_after();
 #pragma unroll 1
-                    for (int n = 0; n < 2 * a.mtiles; ++n) {
-                        const int cc = hb + 16 * (n & 1);
-                        float o[16];
-                        tc::tmem_ld16(tmem_O + lanes + (n >> 1) * kHg + cc, o);
+                    for (int n = 0; n < 4 * a.mtiles; ++n) {
+                        const int cc = hb + 8 * (n & 3);
+                        if (cc >= hb + kHalf) continue;
+                        float o[8];
+                        tc::tmem_ld8(tmem_O + lanes + (n >> 2) * kHg + cc, o);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] *= s.alpha[cc + i];
-                        tc::tmem_st16(tmem_O + lanes + (n >> 1) * kHg + cc, o);
+                        for (int i = 0; i < 8; ++i) o[i] *= s.alpha[cc + i];
+                        tc::tmem_st8(tmem_O + lanes + (n >> 2) * kHg + cc, o);
                     }
                     tc::tmem_st_wait();
                 }
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             // product of the tile before last has read this P)
             uint8_t* p_b = p_s + b * (kE * 128);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < kOct; ++u) {
                 const float2 m = *reinterpret_cast<const float2*>(&s.mexp[hb + 8 * u + 2 * q4]);
                 const float p0 = ex2(z[4 * u] - m.x), p1 = ex2(z[4 * u + 1] - m.y);
                 const float p2 = ex2(z[4 * u + 2] - m.x), p3 = ex2(z[4 * u + 3] - m.y);
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         // per-head sums in a fixed order: entries, lanes, then the four warps
         half_sync(half);                                  // red may still be read
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 2 * kOct; ++i) {
             const float sum = rows_reduce(lpart[i], [](float x, float y) { return x + y; });
             if (lane < 4) s.red[quad][hb + 8 * (i >> 1) + 2 * lane + (i & 1)] = sum;
         }
@@ -400,24 +402,26 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     // where the output is staged as bf16: rows of 16 more bytes than a head's,
     // so that 8 rows start in different banks
     const uint32_t pitch = a.f.c * 2 + 16;
+    // warp w has dims 32 (w % 4).. of M tiles mt0, mt0 + step, .. and 16 heads
+    constexpr int kStep = 4 / kOct;
+    const int quad = warp & 3, hb = (warp >> 2) % kOct * 16, mt0 = (warp >> 2) / kOct;
+    const uint32_t addr = tmem_O + ((uint32_t)(quad * 32) << 16) + hb;
     if (warp < 16 && a.merge == kDirect) {
-        // normalised, bf16: warp w has dims 32 (w % 4).. of every M tile and 16
-        // heads; the transposing matrix stores write 8 dims of a head at a time
+        // normalised, bf16: the transposing matrix stores write 8 dims of a head
+        // at a time
         tc::tc_fence_after();
-        const int hb = (warp >> 2) * 16;
-        const uint32_t addr = tmem_O + ((uint32_t)((warp & 3) * 32) << 16) + hb;
         float2 al[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) al[u] = *reinterpret_cast<const float2*>(&s.alpha[hb + 8 * u + 2 * (lane & 3)]);
         // lane i gives the address of row i % 8 (a head) of matrix i / 8: heads
         // 8 (i / 16).., dims 8 ((i / 8) % 2)..
         const uint32_t dst = tc::smem_u32(kv_s) + (hb + (lane >> 4) * 8 + (lane & 7)) * pitch +
-                             ((warp & 3) * 32 + ((lane >> 3) & 1) * 8) * 2;
+                             (quad * 32 + ((lane >> 3) & 1) * 8) * 2;
 #pragma unroll 1
-        for (int n = 0; n < 2 * a.mtiles; ++n) {          // 16 dims at a time
+        for (int n = 2 * mt0; n < 2 * a.mtiles; n += n & 1 ? 2 * kStep - 1 : 1) {   // 16 dims at a time
             float o[8];
             if (ntiles > 0) {
-                tc::tmem_ld_16x16(addr + (n >> 1) * kHg + ((uint32_t)(16 * (n & 1)) << 16), o);
+                tc::tmem_ld_16(addr + (n >> 1) * kHg + ((uint32_t)(16 * (n & 1)) << 16), o);
                 tc::tmem_ld_wait();
             }
             uint32_t m[4];
@@ -432,22 +436,23 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         }
         tc::fence_proxy_async_smem();
         tc::tc_fence_before();
-    } else if (warp < 16) {
-        // fp32, warp w as above, a lane one dim: to the workspace, or (a
-        // cluster) to shared memory where the tiles were, as rows of a head
+    } else if (warp < 16 && ntiles > 0) {
+        // fp32, a lane one dim: to the workspace, or (a cluster) to shared memory
+        // where the tiles were, as rows of a head
         tc::tc_fence_after();
-        const int hb = (warp >> 2) * 16, row = (warp & 3) * 32 + lane;
-        const uint32_t addr = tmem_O + ((uint32_t)((warp & 3) * 32) << 16) + hb;
         const int heads = nh - hb;
 #pragma unroll 1
-        for (int mt = 0; mt < a.mtiles; ++mt) {
-            const int d = mt * 128 + row;
-            if (ntiles > 0) {
-                float o[16];
-                tc::tmem_ld16(addr + mt * kHg, o);
-                tc::tmem_ld_wait();
-                float* dst = a.merge == kCluster ? reinterpret_cast<float*>(kv_s) : a.part_o + part * a.f.c;
-                dst += hb * a.f.c + d;
+        for (int mt = mt0; mt < a.mtiles; mt += kStep) {
+            const int64_t at = hb * a.f.c + mt * 128 + quad * 32 + lane;
+            float o[16];
+            tc::tmem_ld16(addr + mt * kHg, o);
+            tc::tmem_ld_wait();
+            if (a.merge == kCluster) {
+                float* dst = reinterpret_cast<float*>(kv_s) + at;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) dst[i * a.f.c] = o[i];
+            } else {
+                float* dst = a.part_o + part * a.f.c + at;
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (i < heads) dst[i * a.f.c] = o[i];
@@ -539,9 +544,16 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     }
 }
 
+// Heads per CTA: 64, so that a query's entries are expanded once for all of
+// them; 16 where four times the CTAs still fit with a tile each. HG_TEXT
+int heads_of(int nq, int H, int64_t max_entries) {
+    const int64_t tiles = (max_entries + kE - 1) / kE;
+    return H <= 16 || (int64_t)nq * ((H + 63) / 64) * tiles * 4 <= 148 ? 16 : 64;
+}
+
 // Splits per query: as many whole tiles per CTA as fill the SMs once.
-int nsplit_of(int nq, int H, int64_t max_entries) {
-    const int64_t ctas = (int64_t)nq * ((H + kHg - 1) / kHg), tiles = (max_entries + kE - 1) / kE;
+int nsplit_of(int64_t ctas, int64_t max_entries) {
+    const int64_t tiles = (max_entries + kE - 1) / kE;
     int64_t ns = ctas > 0 ? 148 / ctas : 1;
     ns = ns > 64 ? 64 : ns;
     ns = ns > tiles ? tiles : ns;
@@ -553,24 +565,37 @@ int nsplit_of(int nq, int H, int64_t max_entries) {
 // How the splits merge. Clusters of n CTAs need n free SMs in one GPC, so
 // fewer of them fit at a time than 148 / n (8: 15, with a CTA per SM);
 // clusters that would take a second wave go through the workspace.
-Merge merge_of(int nq, int H, int ns) {
+Merge merge_of(int64_t ctas, int ns) {
     constexpr int fit[kMaxCluster + 1] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
     if (ns == 1) return kDirect;
-    return ns <= kMaxCluster && (int64_t)nq * ((H + kHg - 1) / kHg) <= fit[ns] ? kCluster : kWorkspace;
+    return ns <= kMaxCluster && ctas <= fit[ns] ? kCluster : kWorkspace;
 }
+
+struct Plan {
+    int hg, groups, ns;
+    Merge merge;
+    Plan(int nq, int H, int64_t max_entries) {
+        hg = heads_of(nq, H, max_entries);
+        groups = (H + hg - 1) / hg;
+        ns = nsplit_of((int64_t)nq * groups, max_entries);
+        merge = merge_of((int64_t)nq * groups, ns);
+    }
+};
 
 }  // namespace
 
 size_t mqa_fp4_workspace_bytes(int nq, int H, int c, int64_t max_entries) {
-    const int ns = nsplit_of(nq, H, max_entries);
-    if (merge_of(nq, H, ns) != kWorkspace) return 0;
+    const Plan plan(nq, H, max_entries);
+    const int ns = plan.ns;
+    if (plan.merge != kWorkspace) return 0;
     return align256((size_t)nq * ns * H * c * sizeof(float)) + align256((size_t)nq * ns * H * 2 * sizeof(float));
 }
 
 cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {
     if (x.nq == 0) return cudaSuccess;
     const int64_t max_entries = x.idx ? x.k : x.Nmax;
-    const int ns = nsplit_of(x.nq, x.H, max_entries);
+    const Plan plan(x.nq, x.H, max_entries);
+    const int ns = plan.ns, hg = plan.hg;
     Args a{};
     a.qm = QueryMap{x.qs.seq, x.qs.pos, x.qs.pos_base, x.qs.single_seq};
     a.kv4 = x.kv4;
@@ -590,20 +615,24 @@ cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {
     a.mp = x.mp;
     a.H = x.H;
     a.nsplit = ns;
-    a.merge = merge_of(x.nq, x.H, ns);
+    a.merge = plan.merge;
     a.dblocks = x.c / 64;
     a.mtiles = x.c / 128;
     a.scale_log2 = x.scale * kLog2e;
     CUtensorMap tmQ;
-    if (!make_tmap_bf16_2d(&tmQ, x.q, (uint64_t)x.nq * x.H, x.c, x.c, kHg, 64)) return cudaErrorInvalidValue;
-    const size_t smem = 1024 + (size_t)a.dblocks * (2 * kBlockBytes + kHg * 128) + 2 * kE * 128 + sizeof(Shared);
+    if (!make_tmap_bf16_2d(&tmQ, x.q, (uint64_t)x.nq * x.H, x.c, x.c, hg, 64)) return cudaErrorInvalidValue;
+    const size_t smem = 1024 + (size_t)a.dblocks * (2 * kBlockBytes + hg * 128) + 2 * kE * 128 + sizeof(Shared);
     const bool wide = wide_rows(a.f, x.kv4);
-    auto kern = x.idx ? (wide ? mqa_fp4_kernel<true, true> : mqa_fp4_kernel<true, false>)
-                      : (wide ? mqa_fp4_kernel<false, true> : mqa_fp4_kernel<false, false>);
+    auto of = [&](auto heads) {
+        constexpr int kHg = decltype(heads)::value;
+        return x.idx ? (wide ? mqa_fp4_kernel<true, true, kHg> : mqa_fp4_kernel<true, false, kHg>)
+                     : (wide ? mqa_fp4_kernel<false, true, kHg> : mqa_fp4_kernel<false, false, kHg>);
+    };
+    auto kern = hg == 16 ? of(std::integral_constant<int, 16>()) : of(std::integral_constant<int, 64>());
     cudaError_t e = smem_ceiling(kern);
     if (e != cudaSuccess) return e;
     CSA_LAUNCH(st, "mqa_fp4",
-               e = launch_pdl(kern, dim3(ns, (x.H + kHg - 1) / kHg, x.nq), dim3(kThreads), smem, st,
+               e = launch_pdl(kern, dim3(ns, plan.groups, x.nq), dim3(kThreads), smem, st,
                               a.merge == kCluster ? (unsigned)ns : 0u, a, tmQ));
     if (e != cudaSuccess) return e;
     if (a.merge == kWorkspace) {

@@ -27,6 +27,8 @@ using namespace fp4_tile;
 
 constexpr int kThreads = (4 + kProducerWarps + 2) * 32;   // sums, producers, products, query loads
 
+constexpr int kHg = 64;                 // heads of a query block
+
 struct Args : Fp4TileArgs {
     const float* lse;
     const int32_t* seq_of_q;
@@ -210,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
 #pragma unroll
                     for (int cc = 0; cc < kHg; cc += 32) {
                         float z[16];
-                        tc::tmem_ld_16x32(tmem_S + lanes + sb * kHg + cc, z);
+                        tc::tmem_ld_16(tmem_S + lanes + sb * kHg + cc, z);
                         tc::tmem_ld_wait();
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
