@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
 // them; 16 where four times the CTAs still fit with a tile each. HG_TEXT
 int heads_of(int nq, int H, int64_t max_entries) {
     const int64_t tiles = (max_entries + kE - 1) / kE;
-    return H <= 16 || (int64_t)nq * ((H + 63) / 64) * tiles * 4 <= 148 ? 16 : 64;
+    return H <= 16 || (int64_t)nq * ((H + 63) / 64) * tiles * 4 <= 2 * 148 ? 16 : 64;
 }
 
 // Splits per query: as many whole tiles per CTA as fill the SMs once.
