@@ -219,7 +219,8 @@ struct Fp4MqaArgs {
 };
 size_t mqa_fp4_workspace_bytes(int nq, int H, int c, int64_t max_entries);
 cudaError_t mqa_fp4(const Fp4MqaArgs& a, void* ws, cudaStream_t st);
-// The attention weight of entries, summed over heads: of idx[t][i] (B queries,
+
+// weights_fp4.cu: the attention weight of entries, summed over heads: of idx[t][i] (B queries,
 // T = 1) into weights [B, k] and added to acc; or of every entry of sequence
 // b over its T queries, weights [B, Nmax] = acc + sum (acc nullable).
 struct Fp4WeightArgs {
@@ -307,9 +308,10 @@ cudaError_t mqa(const void* q, const void* KV, const int32_t* idx, int k, QueryS
                 float* lse, void* ws, ElemType t, cudaStream_t st, RowBlocks kvb = RowBlocks{0, 0});
 
 // mqa.cu: merge of nsplit partial results per query (part_o [nq, nsplit, H, c]
-// scaled by exp(-m), part_ml [nq, nsplit, H, 2] = (m, l); m = -inf: none)
+// scaled by exp(-m), part_ml [nq, nsplit, H, 2] = (m, l); m = -inf: none);
+// nan: an l that is NaN makes lse NaN, not -inf
 cudaError_t mqa_combine_bf16(const float* part_o, const float* part_ml, int nsplit, int nq, int H, int c,
-                             const float* sink, void* out, float* lse, cudaStream_t st);
+                             const float* sink, void* out, float* lse, cudaStream_t st, bool nan = false);
 
 // norm_rope.cu: RMSNorm (gamma != nullptr) then rotary encoding of the last R
 // channels of every row of c channels; row r takes the position of group

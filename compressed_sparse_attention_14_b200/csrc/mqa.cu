@@ -161,7 +161,8 @@ __global__ void __launch_bounds__(256) mqa_partial_ffma_kernel(MqaPartialArgs a)
 // never by multiplying its stale rows. One store per 4 results.
 constexpr int kCombineHeads = 8;
 constexpr int kCombineDims = 128;
-template <typename T>
+// kNan: a sum that is NaN shows in lse, too (otherwise lse = -inf there).
+template <typename T, bool kNan = false>
 __global__ void __launch_bounds__(kCombineHeads * 32) mqa_combine_kernel(const float* __restrict__ part_o,
                                                                          const float* __restrict__ part_ml,
                                                                          int nsplit, int H, int c,
@@ -209,17 +210,17 @@ __global__ void __launch_bounds__(kCombineHeads * 32) mqa_combine_kernel(const f
             M = Mn;
         }
         if (sink && M != -INFINITY) L += expf(z - M);
-        const float inv = (L > 0.f) ? 1.f / L : 0.f;
+        const float inv = (L > 0.f) ? 1.f / L : kNan && L != L ? L : 0.f;
         store4(out + ((int64_t)t * H + h) * c + d, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (lse && blockIdx.z == 0 && j4 == 0) lse[(int64_t)t * H + h] = (L > 0.f) ? M + logf(L) : -INFINITY;
+        if (lse && blockIdx.z == 0 && j4 == 0) lse[(int64_t)t * H + h] = (L > 0.f) ? M + logf(L) : kNan && L != L ? L : -INFINITY;
     }
 }
 
 cudaError_t mqa_combine_bf16(const float* part_o, const float* part_ml, int nsplit, int nq, int H, int c,
-                             const float* sink, void* out, float* lse, cudaStream_t st) {
+                             const float* sink, void* out, float* lse, cudaStream_t st, bool nan) {
     cudaError_t e = cudaSuccess;
     CSA_LAUNCH(st, "mqa_combine",
-               e = launch_pdl(mqa_combine_kernel<bf16>,
+               e = launch_pdl(nan ? mqa_combine_kernel<bf16, true> : mqa_combine_kernel<bf16>,
                               dim3((H + kCombineHeads - 1) / kCombineHeads, nq, (c + kCombineDims - 1) / kCombineDims),
                               dim3(kCombineHeads * 32), 0, st, 0, part_o, part_ml, nsplit, H, c, sink, (bf16*)out, lse));
     return e;

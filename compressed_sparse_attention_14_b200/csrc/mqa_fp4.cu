@@ -636,7 +636,7 @@ cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {
                               a.merge == kCluster ? (unsigned)ns : 0u, a, tmQ));
     if (e != cudaSuccess) return e;
     if (a.merge == kWorkspace) {
-        e = mqa_combine_bf16(a.part_o, a.part_ml, ns, x.nq, x.H, x.c, x.sink, x.out, x.lse, st);
+        e = mqa_combine_bf16(a.part_o, a.part_ml, ns, x.nq, x.H, x.c, x.sink, x.out, x.lse, st, true);
         if (e != cudaSuccess) return e;
     }
     return cudaGetLastError();

@@ -438,7 +438,8 @@ int hca_decode_fp4kv(const void* q, const uint8_t* kv4, const int32_t* ctx_len, 
  *                 exp(scale * q[b][t][h] . v_s - lse[b][t][h])
  *   q [B, T, H, c], lse [B, T, H], pos [B, T], kv4 [B, Nmax, row_bytes], out
  *   [B, Nmax] written in full, acc [B, Nmax] or NULL (0); out == acc is
- *   allowed. Queries are added in order of t.
+ *   allowed. Queries are added in order of t; T <= 2^18 (a longer prompt in
+ *   several calls with acc = out).
  *
  * csa_evict_plan: cuts the first n_ent[b] entries of every sequence to `keep`.
  *   Entries are ordered by (protected, acc descending, index ascending), a NaN
@@ -465,6 +466,7 @@ int hca_decode_fp4kv(const void* q, const uint8_t* kv4, const int32_t* ctx_len, 
  *   acc of the slot becomes 0, its entry_pos i, n_ent counts up to cap. The
  *   entry itself is stored with csa_append_kv_fp4 (or a row copy).
  *
+ * The three eviction calls take Nmax <= 2^30, csa_evict_rows row_bytes <= 2^30.
  * A cache whose entries are no longer in token order is attended with m (or
  * mp) = 1 and pos = ctx_len = n_ent.
  * ------------------------------------------------------------------------ */

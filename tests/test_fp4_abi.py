@@ -80,6 +80,13 @@ def test_weight_refusals():
     assert de(B=0) == 0
 
 
+def test_weights_of_more_queries_than_a_call_takes():
+    def de(T):
+        return L.hca_entry_weights_fp4kv(F, F, F, F, 1, T, 8, 128, 32, 16, 4, 0.0, None, None, None)
+    assert de((1 << 18) + 1) == UNSUP and b"2^18" in L.csa_last_error()
+    assert de(1 << 18) == BAD                                              # (out is missing)
+
+
 def test_eviction_refusals():
     def plan(B=2, N=16, keep=8, pos=None, prot=None, pos_out=None, acc=F, acc_out=F, src=F):
         return L.csa_evict_plan(acc, F, pos, prot, B, N, keep, src, F, F, F, acc_out, pos_out, F * 16, 1 << 30, None)

@@ -170,6 +170,50 @@ def test_sparse_attention(csa, nq, B, N, H, c, R, k, with_sink):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+# heads per CTA 16 and 64; one, two, several and many splits of a query; rows of whole 32-byte pieces and others, at
+# any 16-byte address
+@pytest.mark.parametrize("nq,H,c,R,k,shift", [
+    (64, 64, 512, 64, 512, 0), (64, 64, 512, 64, 512, 16), (64, 40, 384, 64, 500, 0), (30, 64, 512, 64, 512, 0),
+    (20, 65, 256, 64, 600, 0), (20, 33, 384, 96, 640, 16), (36, 64, 512, 64, 1024, 0), (36, 64, 384, 96, 1024, 0),
+    (160, 17, 384, 64, 300, 0), (8, 64, 384, 64, 512, 32), (3, 128, 512, 0, 1024, 0), (150, 16, 512, 64, 700, 16)])
+def test_every_split_and_layout(csa, nq, H, c, R, k, shift):
+    N, rb = 400, csa.csa_fp4_row_bytes(c, R)
+    rows, V = _rows(csa, 3 * N, c, R, 60)
+    flat = torch.zeros(3 * N * rb + 64, dtype=torch.uint8, device=DEV)
+    kv = flat[shift:shift + 3 * N * rb].view(3, N, rb)
+    kv.copy_(rows.view(3, N, rb))
+    g = _gen(nq + k)
+    q = (2 * torch.randn(nq, H, c, generator=g)).to(torch.bfloat16)
+    idx = torch.randint(-N // 8, N, (nq, k), generator=g, dtype=torch.int32)
+    idx[0, 64:] = -1                                                             # later splits see nothing
+    idx[1, :-70] = -1                                                            # and earlier ones
+    idx[2] = -1
+    seq = torch.arange(nq, dtype=torch.int32) % 3
+    sink = torch.randn(H, generator=g)
+    out, lse = csa.csa_sparse_mqa_fp4kv(q.to(DEV), kv, idx.to(DEV), rope_dims=R, sink=sink.to(DEV),
+                                        seq_of_q=seq.to(DEV))
+    ids = idx.numpy().copy()
+    ids[ids < 0] = -1
+    check_attention(out, lse, q, V.reshape(3, N, c), ids, c ** -0.5, sink.double().numpy(), seq.numpy())
+    w = csa.csa_entry_weights_fp4kv(q.to(DEV), lse, kv, idx.to(DEV), rope_dims=R, seq_of_q=seq.to(DEV))
+    ref = oracle.entry_weights(host(q), host(lse), V.reshape(3, N, c), ids, c ** -0.5, seq.numpy())
+    check_weights(w, ref, _logit_slack(host(q), V.reshape(3, N, c), c ** -0.5))
+
+
+@pytest.mark.parametrize("nq,k", [(1, 64), (1, 512), (64, 512), (36, 1024), (160, 256)])
+def test_a_nan_row_shows_however_the_query_is_split(csa, nq, k):
+    N, H, c = 300, 64, 512
+    kv, _ = _rows(csa, N, c, 64, 61)
+    kv[7] = 255
+    g = _gen(k)
+    q = torch.randn(nq, H, c, generator=g).to(torch.bfloat16).to(DEV)
+    idx = torch.randint(8, N, (nq, k), generator=g, dtype=torch.int32)
+    idx[0, k - 2] = 7
+    out, lse = csa.csa_sparse_mqa_fp4kv(q, kv, idx.to(DEV), seq_of_q=torch.zeros(nq, dtype=torch.int32, device=DEV))
+    assert out[0].isnan().all() and lse[0].isnan().all()
+    assert out[1:].isfinite().all() and lse[1:].isfinite().all()
+
+
 def test_sparse_attention_odd_lists(csa):
     # indices past the cache, sequences out of range, logits far apart, a scale of one's own
     B, N, H, c, R, k = 2, 50, 64, 512, 64, 160
