@@ -9,12 +9,13 @@
 //
 // evict_plan: a cluster of up to 8 CTAs per sequence, each with a contiguous
 // part of the entries, their keys in shared memory. The keep-th key is found
-// by radix select, the protected bit and 8 bits, then 8 a pass (local
-// histograms, summed over the cluster through distributed shared memory). Ties stay in index order: every warp
-// owns a contiguous segment and counts it, the counts are scanned over warps
-// and CTAs, and a second walk writes holes and movers at their places without
+// by radix select, the protected bit and 10 bits, then 11 a pass (local
+// histograms, summed over the cluster through distributed shared memory; 4
+// passes of 8 bits took PASSES). Ties stay in index order: every warp owns a
+// contiguous segment and counts it, the counts are scanned over warps and
+// CTAs, and a second walk writes holes and movers at their places without
 // another barrier. Bound by latency: a few passes over some thousand keys per
-// CTA and 7 cluster barriers.
+// CTA and 6 cluster barriers.
 // evict_rows: a thread per 16 bytes, four of them in flight; bound by memory.
 // evict_slot: a CTA per sequence, one reduction.
 #include <type_traits>
@@ -34,14 +35,31 @@ constexpr int kMaxCached = 48 * 1024;      // keys of a CTA's part kept in share
 // NaN counts as -inf
 __device__ __forceinline__ uint32_t weight_key(float w) { return orderable(w != w ? -INFINITY : w); }
 
+__device__ __forceinline__ uint2 ld_cluster_u32x2(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
 
+// inclusive scan over the lanes
+__device__ __forceinline__ int warp_scan(int v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if ((threadIdx.x & 31) >= o) v += u;
+    }
+    return v;
+}
+
+constexpr int kBins = 2048;
+
 struct PlanShared {
-    int hist[512 + 3 * 256];               // one histogram per pass: none is reused
+    int hist[3][kBins];                    // one histogram per pass: none is reused
     int scan[kWarps];
     int count[kWarps][4];                  // per warp: above the keep-th key before / after slot keep, ties likewise
     int total[5];                          // this CTA's sums, and its entries before slot keep
@@ -84,43 +102,55 @@ __global__ void __launch_bounds__(kThreads) evict_plan_kernel(const __grid_const
         const int per_warp = (g1 - g0 + kWarps - 1) / kWarps;
         const int w0 = min(g1, g0 + warp * per_warp), w1 = min(g1, w0 + per_warp);
         uint32_t* prot = keys + per_cta * 32;             // a bit per entry: protected
-        // an entry's key, and the protected bits of its group
-        auto read = [&](int g, uint32_t& k, uint32_t& pm) {
-            const int i = 32 * g + lane;
-            k = i < n ? weight_key(acc[i]) : 0;
-            pm = guard ? __ballot_sync(0xffffffffu, i < n && pos[i] >= from) : 0;
+        // the keys of kG groups and their protected bits, all loads in flight
+        auto read = [&](int g, auto& k, auto& pm) {
+            constexpr int kG = sizeof(k) / sizeof(k[0]);
+            float w[kG];
+            int at[kG];
+#pragma unroll
+            for (int u = 0; u < kG; ++u) {
+                const int i = min(32 * (g + u) + lane, n - 1);
+                w[u] = acc[i];
+                at[u] = guard ? pos[i] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < kG; ++u) {
+                const bool live = 32 * (g + u) + lane < n;
+                k[u] = live ? weight_key(w[u]) : 0;
+                pm[u] = guard ? __ballot_sync(0xffffffffu, live && at[u] >= from) : 0;
+            }
         };
         auto get = [&](int g, uint32_t& k, uint32_t& pm) {
-            if (!cached) return read(g, k, pm);
+            if (!cached) {
+                uint32_t k1[1], pm1[1];
+                read(g, k1, pm1);
+                k = k1[0];
+                pm = pm1[0];
+                return;
+            }
             k = keys[32 * (g - g0) + lane];
             pm = guard ? prot[g - g0] : 0;
         };
-        // one more of this digit for every lane with `in`; equal digits (zero
-        // weights, say) would queue up at one counter
+        // one more of this digit for every lane with `in`, lanes of one digit
+        // together: keys share their leading bits, and would queue up at a counter
         auto tally = [&](int* hist, bool in, uint32_t digit) {
-            const uint32_t m = __ballot_sync(0xffffffffu, in);
-            if (!m) return;
-            const uint32_t lead = __shfl_sync(0xffffffffu, digit, __ffs(m) - 1);
-            const uint32_t same = __ballot_sync(0xffffffffu, in && digit == lead);
-            if (in && digit != lead) atomicAdd(&hist[digit], 1);
-            if (lane == __ffs(m) - 1) atomicAdd(&hist[lead], __popc(same));
+            const uint32_t same = __match_any_sync(0xffffffffu, in ? digit : ~0u);
+            if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
         };
-        for (int i = tid; i < 512 + 3 * 256; i += kThreads) s.hist[i] = 0;
+        for (int i = tid; i < 3 * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
         if (tid < 5) s.total[tid] = 0;
         __syncthreads();
-        // the keep-th key, from the top: protected bit and 8 bits, then 8 a pass
+        // the keep-th key, from the top: protected bit and 10 bits, then 11 a pass
         uint32_t cls = 0, prefix = 0;
         int need = keep;
-#pragma unroll 1
-        for (int d = 0; d < 4; ++d) {
-            int* hist = d == 0 ? s.hist : s.hist + 256 + 256 * d;
-            const int bins = d == 0 ? 512 : 256;
+#pragma unroll
+        for (int d = 0; d < 3; ++d) {
+            int* hist = s.hist[d];
+            const int shift = 22 - 11 * d;
             if (d == 0) {
                 for (int g = w0; g < w1; g += 4) {
-                    uint32_t k[4], pm[4];                 // (four loads in flight)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (g + u < w1) read(g + u, k[u], pm[u]);
+                    uint32_t k[4], pm[4];
+                    read(g, k, pm);
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         if (g + u >= w1) continue;
@@ -128,45 +158,49 @@ __global__ void __launch_bounds__(kThreads) evict_plan_kernel(const __grid_const
                             keys[32 * (g + u - g0) + lane] = k[u];
                             if (lane == 0 && guard) prot[g + u - g0] = pm[u];
                         }
-                        tally(hist, 32 * (g + u) + lane < n, ((pm[u] >> lane) & 1u) << 8 | k[u] >> 24);
+                        tally(hist, 32 * (g + u) + lane < n, ((pm[u] >> lane) & 1u) << 10 | k[u] >> 22);
                     }
                 }
                 __syncwarp();
             } else {
+#pragma unroll 4
                 for (int g = w0; g < w1; ++g) {
                     uint32_t k, pm;
                     get(g, k, pm);
-                    const bool in = 32 * g + lane < n && ((pm >> lane) & 1u) == cls && k >> (32 - 8 * d) == prefix;
-                    tally(hist, in, (k >> (24 - 8 * d)) & 255u);
+                    const bool in = 32 * g + lane < n && ((pm >> lane) & 1u) == cls && k >> (shift + 11) == prefix;
+                    if (in) atomicAdd(&hist[(k >> shift) & (kBins - 1)], 1);
                 }
             }
             sync_all();
-            // entries with this digit, of all CTAs; from the largest digit down
-            int c = 0;
-            if (tid < bins) {
-                int v[kMaxCluster];                       // (all CTAs' loads in flight)
+            // entries with this thread's two digits, of all CTAs; from the largest digit down
+            const int top = kBins - 1 - 2 * tid;
+            uint2 v[kMaxCluster];                         // (all CTAs' loads in flight)
 #pragma unroll
-                for (int r = 0; r < kMaxCluster; ++r) v[r] = r < csize ? peek(hist + bins - 1 - tid, r) : 0;
-#pragma unroll
-                for (int r = 0; r < kMaxCluster; ++r) c += v[r];
+            for (int r = 0; r < kMaxCluster; ++r) {
+                v[r] = make_uint2(0, 0);
+                if (r < csize)
+                    v[r] = csize > 1 ? ld_cluster_u32x2(tc::mapa(tc::smem_u32(hist + top - 1), r))
+                                     : *reinterpret_cast<const uint2*>(hist + top - 1);
             }
-            int sum = c;
+            int c0 = 0, c1 = 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += v;
-            }
+            for (int r = 0; r < kMaxCluster; ++r) { c0 += v[r].y; c1 += v[r].x; }
+            const int sum = warp_scan(c0 + c1);
             if (lane == 31) s.scan[warp] = sum;
             __syncthreads();
-            int above = sum - c;                          // entries with a larger digit
-            for (int w = 0; w < warp; ++w) above += s.scan[w];
-            if (above < need && above + c >= need) {
-                s.digit = bins - 1 - tid;
+            // entries with a larger digit
+            const int warps = warp_scan(s.scan[lane]), before = __shfl_sync(0xffffffffu, warps, max(warp - 1, 0));
+            const int above = (warp ? before : 0) + sum - c0 - c1;
+            if (above < need && above + c0 >= need) {
+                s.digit = top;
                 s.need = need - above;
+            } else if (above + c0 < need && above + c0 + c1 >= need) {
+                s.digit = top - 1;
+                s.need = need - above - c0;
             }
             __syncthreads();
-            if (d == 0) cls = (uint32_t)s.digit >> 8;
-            prefix = (prefix << 8) | ((uint32_t)s.digit & 255u);
+            if (d == 0) cls = (uint32_t)s.digit >> 10;
+            prefix = d == 0 ? (uint32_t)s.digit & 1023u : (prefix << 11) | (uint32_t)s.digit;
             need = s.need;
         }
         // `need` of the entries equal to the keep-th key stay, the first ones
@@ -180,6 +214,7 @@ __global__ void __launch_bounds__(kThreads) evict_plan_kernel(const __grid_const
             eq = __ballot_sync(0xffffffffu, live && p == cls && k == kth);
         };
         int cnt[4] = {0, 0, 0, 0};
+#pragma unroll 4
         for (int g = w0; g < w1; ++g) {
             uint32_t gt, eq;
             compare(g, gt, eq);
@@ -216,11 +251,21 @@ __global__ void __launch_bounds__(kThreads) evict_plan_kernel(const __grid_const
         tie = own_tie;
         hole = own_hole;
         mover = own_mover;
-        for (int w = 0; w < warp; ++w) {
-            const int b0 = min(g1, g0 + w * per_warp), b1 = min(g1, b0 + per_warp);
-            const int v[4] = {s.count[w][0], s.count[w][1], s.count[w][2], s.count[w][3]};
+        {
+            // lane w: warp w's segment
+            const int b0 = min(g1, g0 + lane * per_warp), b1 = min(g1, b0 + per_warp);
+            const int v[4] = {s.count[lane][0], s.count[lane][1], s.count[lane][2], s.count[lane][3]};
+            const int base_hole = hole, base_mover = mover, ties = v[2] + v[3];
+            tie += warp_scan(ties) - ties;
+            const int tie_w = tie;
+            hole = mover = 0;
             pass_over(max(0, min(32 * b1, min(n, keep)) - 32 * b0), v);
+            const int holes = warp_scan(hole) - hole, movers = warp_scan(mover) - mover;
+            tie = __shfl_sync(0xffffffffu, tie_w, warp);
+            hole = base_hole + __shfl_sync(0xffffffffu, holes, warp);
+            mover = base_mover + __shfl_sync(0xffffffffu, movers, warp);
         }
+#pragma unroll 4
         for (int g = w0; g < w1; ++g) {
             const int i = 32 * g + lane;
             uint32_t gt, eq;
