@@ -2,8 +2,10 @@
 // operands: 64 entries x c channels, bf16, in 64-channel blocks of 8 KB with
 // the 128-byte swizzle, two tiles in turn. Producer warps, 8 to each of the two
 // buffers, read the packed rows, expand them (exactly) and store them; blocks
-// are handed to the products and back in pairs (128 channels), so that the
-// next tiles are expanded while the products and the softmax of this one run.
+// are handed to the products and back by halves (256 channels: half 0 is
+// blocks 0 .. 3, half 1 the rest, which goes first), so that the next tiles are
+// expanded while the products and the softmax of this one run. (By pairs of
+// blocks, the products' warps spent as long on barriers as on products.)
 #pragma once
 
 #include <type_traits>
@@ -18,6 +20,7 @@ namespace fp4_tile {
 constexpr int kProducerWarps = 16;      // 8 to a tile
 constexpr int kE = 64;                  // entries per tile
 constexpr int kPairs = CSA_MAX_HEAD_DIM / 128;   // pairs of 64-channel blocks
+constexpr int kHalves = 2;
 constexpr uint32_t kBlockBytes = kE * 128;
 constexpr uint32_t kWaitLimit = 1u << 20;   // (2 us each)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -29,10 +32,13 @@ struct Fp4TileArgs {
     int64_t Nmax;
     Fp4Row f;
     int k, dblocks, mtiles;   // c / 64, c / 128
+    __device__ __forceinline__ int halves() const { return (mtiles + 1) / 2; }
+    // 64-channel blocks of half h
+    __device__ __forceinline__ int blocks(int h) const { return h ? dblocks - 4 : min(dblocks, 4); }
 };
 
 struct Fp4TileShared {
-    uint64_t full[2][kPairs], empty[2][kPairs];   // a pair of blocks of a tile stored / free
+    uint64_t full[2][kHalves], empty[2][kHalves];   // half of a tile stored / free
     int abort;
 };
 
@@ -112,12 +118,11 @@ struct RowScale {
     }
 };
 
-// hands pairs lo .. hi - 1 of a buffer to the products
-__device__ __forceinline__ void hand_over(uint64_t* full, int lo, int hi) {
+// hands half of a buffer to the products
+__device__ __forceinline__ void hand_over(uint64_t* full) {
     tc::fence_proxy_async_smem();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0)
-        for (int i = lo; i < hi; ++i) tc::mbar_arrive(&full[i]);
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(full);
 }
 
 // A producer thread of any layout: of one row, the 32 channels of chunk
@@ -193,8 +198,9 @@ struct Producer {
 #pragma unroll
         for (int i = kPairs - 1; i >= 0; --i) {
             if (i >= a.mtiles || !ok) continue;
-            // the products of the tile before last have read the pair
-            if (j >= 2) ok = __all_sync(0xffffffffu, wait(&s.empty[b][i], ((j >> 1) - 1) & 1, s, a.status));
+            // the products of the tile before last have read the half
+            if (j >= 2 && ((i & 1) || i == a.mtiles - 1))
+                ok = __all_sync(0xffffffffu, wait(&s.empty[b][i >> 1], ((j >> 1) - 1) & 1, s, a.status));
             if (!ok) continue;
             if (4 * i + chunk() < a.f.Q / 32) {
                 const uint32_t S0 = scale.of(two[i] & 255u), S1 = scale.of((two[i] >> 8) & 255u);
@@ -219,7 +225,7 @@ struct Producer {
                     cp_async_wait_all();
                 }
             }
-            hand_over(s.full[b], i, i + 1);
+            if (!(i & 1)) hand_over(&s.full[b][i >> 1]);
         }
         return ok;
     }
@@ -299,9 +305,8 @@ struct WideProducer {
             if (i >= 4 && i == nb) E = w & 255u;
         }
         const RowScale scale(E);
-        // the products of the tile before last have read the pairs (2 is read
-        // after 3, 0 after 1)
-        if (j >= 2 && !__all_sync(0xffffffffu, wait(&s.empty[b][2], parity, s, a.status))) return false;
+        // the products of the tile before last have read the half
+        if (j >= 2 && !__all_sync(0xffffffffu, wait(&s.empty[b][1], parity, s, a.status))) return false;
 #pragma unroll
         for (int n = 1; n < 3; ++n) {
             const int r = 4 * n + q - nb - 1;             // rotary piece
@@ -312,10 +317,10 @@ struct WideProducer {
             }
         }
         if (4 + q < nb) expand_block(raw[1], mine[1], 4 + q, scale);
-        hand_over(s.full[b], 2, a.mtiles);
+        hand_over(&s.full[b][1]);
         if (j >= 2 && !__all_sync(0xffffffffu, wait(&s.empty[b][0], parity, s, a.status))) return false;
         expand_block(raw[0], mine[0], q, scale);
-        hand_over(s.full[b], 0, 2);
+        hand_over(&s.full[b][0]);
         return true;
     }
 };

@@ -21,8 +21,8 @@
 //   warps 0-7   softmax; warp w has entries 16 (w % 4).. and 32 heads, a
 //               thread 2 entries x 8 heads (the 16-lane tensor-memory loads)
 //   warps 8-23  producers (fp4_tile.cuh)
-//   warp 24     S products, pair of blocks by pair as they are stored
-//   warp 25     O products; each hands a pair back to the producers
+//   warp 24     S products, half of the channels by half as they are stored
+//   warp 25     O products, each half of them handed back to the producers
 // One buffer of 128 entries left the four steps of a tile one after another,
 // 8700 cycles for 128 entries, half of them handing over; two of 64 take TWO64.
 // The least is the shared memory's 128 bytes a cycle: 128 entries are written
@@ -70,7 +70,7 @@ struct Shared : Fp4TileShared {
     float alpha[kMaxHg], lsum[kMaxHg];
     float red[4][kMaxHg];
     float coef[kMaxCluster][kMaxHg];
-    uint64_t s_full[2], p_full[2], q_full, o_done, fin[2];
+    uint64_t s_full[2], p_full[2], q_full, fin[2];
     uint64_t peer;                            // the other split's sums have arrived (clusters of two)
     uint32_t tmem;
 };
@@ -185,16 +185,15 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         if (warp == kSWarp) {
             if (lane == 0) {
                 for (int b = 0; b < 2; ++b) {
-                    for (int i = 0; i < kPairs; ++i) {
-                        tc::mbar_init(&s.full[b][i], 8);     // a buffer's producer warps
-                        tc::mbar_init(&s.empty[b][i], 1);
+                    for (int h = 0; h < kHalves; ++h) {
+                        tc::mbar_init(&s.full[b][h], 8);     // a buffer's producer warps
+                        tc::mbar_init(&s.empty[b][h], 1);
                     }
                     tc::mbar_init(&s.s_full[b], 1);
                     tc::mbar_init(&s.p_full[b], kSoftmaxWarps);
                     tc::mbar_init(&s.fin[b], 1);
                 }
                 tc::mbar_init(&s.q_full, 1);
-                tc::mbar_init(&s.o_done, 1);
                 tc::mbar_init(&s.peer, 1);
                 tc::fence_mbar_init();
                 s.abort = 0;
@@ -224,17 +223,18 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                 const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
                 for (int j = 0; ok && j < ntiles; ++j) {
                     const int b = j & 1;
-                    for (int i = a.mtiles - 1; i >= 0 && (ok = until(&s.full[b][i], (j >> 1) & 1)); --i) {
+                    for (int h = a.halves() - 1; h >= 0 && (ok = until(&s.full[b][h], (j >> 1) & 1)); --h) {
                         tc::tc_fence_after();
+                        for (int i = 0; i < a.blocks(h) / 2; ++i)
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) {
-                            const int blk = 2 * i + (kk >> 2);
-                            tc::umma_bf16_warp(
-                                tmem_S + b * kHg,
-                                tc::sdesc_sw128(kv_addr + b * tile_bytes + blk * kBlockBytes + (kk & 3) * 32, 16, 1024),
-                                tc::sdesc_sw128(q_addr + blk * (kHg * 128) + (kk & 3) * 32, 16, 1024), idesc,
-                                (i < a.mtiles - 1 || kk) ? 1u : 0u);
-                        }
+                            for (int kk = 0; kk < 8; ++kk) {
+                                const int blk = 4 * h + 2 * i + (kk >> 2);
+                                tc::umma_bf16_warp(
+                                    tmem_S + b * kHg,
+                                    tc::sdesc_sw128(kv_addr + b * tile_bytes + blk * kBlockBytes + (kk & 3) * 32, 16, 1024),
+                                    tc::sdesc_sw128(q_addr + blk * (kHg * 128) + (kk & 3) * 32, 16, 1024), idesc,
+                                    (h < a.halves() - 1 || i || kk) ? 1u : 0u);
+                            }
                     }
                     if (ok) tc::umma_commit_warp(&s.s_full[b]);
                 }
@@ -252,9 +252,8 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                                 tc::sdesc_sw128(kv_addr + b * tile_bytes + 2 * mt * kBlockBytes + ke * 2048, kBlockBytes, 1024),
                                 tc::sdesc_sw128(p_addr + b * (kE * 128) + ke * 2048, kE * 128, 1024), idesc,
                                 (j > 0 || ke > 0) ? 1u : 0u);
-                        tc::umma_commit_warp(&s.empty[b][mt]);
+                        if (!(mt & 1)) tc::umma_commit_warp(&s.empty[b][mt >> 1]);
                     }
-                    tc::umma_commit_warp(&s.o_done);
                 }
             }
             // every product issued has ended before the CTA goes on to free the
@@ -331,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                 for (int i = 0; i < 2 * kOct; ++i) lpart[i] *= s.alpha[hb + 8 * (i >> 1) + 2 * q4 + (i & 1)];
                 if (j > 0) {
                     // rescale O^T (every product before this tile's has ended)
-                    ok = wait(&s.o_done, (j - 1) & 1, s, a.status);
+                    ok = wait(&s.empty[b ^ 1][0], ((j - 1) >> 1) & 1, s, a.status);
                     tc::tc_fence_after();
 #pragma unroll 1
                     for (int n = 0; n < 4 * a.mtiles; ++n) {
@@ -367,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&s.p_full[b]);
         }
-        if (ok && ntiles > 0) wait(&s.o_done, (ntiles - 1) & 1, s, a.status);
+        if (ok && ntiles > 0) wait(&s.empty[(ntiles - 1) & 1][0], ((ntiles - 1) >> 1) & 1, s, a.status);
         __syncwarp();
         // per-head sums in a fixed order: entries, lanes, then the four warps
         half_sync(half);                                  // red may still be read

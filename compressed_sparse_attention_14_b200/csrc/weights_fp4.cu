@@ -9,7 +9,7 @@
 //
 // A CTA walks a run of tiles of one sequence (or of one query's entry list).
 // Each tile stays in shared memory for all query blocks (query, 64 heads) of
-// its sequence; their q blocks stream through one buffer, refilled in quarters
+// its sequence; their q blocks stream through one buffer, refilled in halves
 // as the product has read them, unless there is only one, which stays. The
 // next tile is expanded as the last query block's product releases the blocks.
 // Every sum has a fixed order: a thread's heads, queries, then the four threads.
@@ -41,7 +41,7 @@ struct Args : Fp4TileArgs {
 
 struct Shared : Fp4TileShared {
     float lse[4][kHg];                        // the query block's, per warp
-    uint64_t q_full[kPairs], q_empty[kPairs], s_full[2], s_empty[2], fin;
+    uint64_t q_full[kHalves], q_empty[kHalves], s_full[2], s_empty[2], fin;
     uint32_t tmem;
     int n_max;
 };
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
     const int e_beg = blockIdx.x * a.run * kE, n_all = kSparse ? a.k : (int)a.Nmax;
     const int e_stop = (int64_t)a.run * kE > n_all - e_beg ? n_all : e_beg + a.run * kE;   // this CTA's entries
     if (tid == 0) {
-        for (int i = 0; i < kPairs; ++i) {
+        for (int i = 0; i < kHalves; ++i) {
             for (int b = 0; b < 2; ++b) {
                 tc::mbar_init(&s.full[b][i], 8);         // a buffer's producer warps
                 tc::mbar_init(&s.empty[b][i], 1);
@@ -126,19 +126,18 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
                 for (int t = 0; ok && t <= blocks.last_query(e_tile); ++t) {
                     if (blocks.visible(t) <= e_tile) continue;
                     for (int g = 0; ok && g < a.hgroups; ++g, ++n)
-                        for (int o = 0; o < a.mtiles; ++o) {
-                            const int i = a.mtiles - 1 - o;               // as they are stored
+                        for (int i = a.halves() - 1; i >= 0; --i) {           // (as they are stored)
                             if (n > 0 && !(ok = wait(&s.q_empty[i], (n - 1) & 1, s, a.status))) break;
-                            tc::mbar_expect_tx(&s.q_full[i], 2 * kHg * 128);
-                            for (int h = 0; h < 2; ++h)
-                                tc::tma_load_2d(q_s + (size_t)(2 * i + h) * kHg * 128, &tmQ, &s.q_full[i],
-                                                (2 * i + h) * 64, (b * a.T + t) * a.H + g * kHg);
+                            tc::mbar_expect_tx(&s.q_full[i], a.blocks(i) * kHg * 128);
+                            for (int blk = 4 * i; blk < 4 * i + a.blocks(i); ++blk)
+                                tc::tma_load_2d(q_s + (size_t)blk * kHg * 128, &tmQ, &s.q_full[i], blk * 64,
+                                                (b * a.T + t) * a.H + g * kHg);
                         }
                 }
             }
-            // the last copies of each pair have landed
+            // the last copies of each half have landed
             if (n > 0)
-                for (int i = 0; i < a.mtiles; ++i) tc::mbar_wait(&s.q_full[i], (n - 1) & 1, ok ? kWaitLimit : 1u << 16);
+                for (int i = 0; i < a.halves(); ++i) tc::mbar_wait(&s.q_full[i], (n - 1) & 1, ok ? kWaitLimit : 1u << 16);
         }
         __syncwarp();
     } else if (warp == 20) {
@@ -147,35 +146,36 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
             const uint32_t kv_addr = __shfl_sync(0xffffffffu, tc::smem_u32(kv_s), 0);
             const uint32_t tile_bytes = a.dblocks * kBlockBytes, q_addr = kv_addr + 2 * tile_bytes;
             const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
+            auto until = [&](uint64_t* bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, wait(bar, parity, s, a.status));
+            };
+            const int per_query = a.hgroups;
             uint32_t n = 0;
             bool ok = true;
             for (int j = 0; ok && j < ntiles; ++j) {
-                const int e_tile = e_beg + j * kE, last = blocks.last_query(e_tile);
-                bool first = true;
-                for (int t = 0; ok && t <= last; ++t) {
-                    if (blocks.visible(t) <= e_tile) continue;
-                    for (int g = 0; ok && g < a.hgroups; ++g, ++n) {
-                        const uint32_t sb = n & 1;
-                        if (n >= 2 && !(ok = __all_sync(0xffffffffu, wait(&s.s_empty[sb], ((n >> 1) - 1) & 1, s, a.status)))) break;
-                        for (int o = 0; o < a.mtiles; ++o) {
-                            const int i = a.mtiles - 1 - o;               // as they are stored
-                            if (!(ok = __all_sync(0xffffffffu, wait(&s.q_full[i], stay ? 0 : n & 1, s, a.status)))) break;
-                            if (first && !(ok = __all_sync(0xffffffffu, wait(&s.full[j & 1][i], (j >> 1) & 1, s, a.status)))) break;
-                            tc::tc_fence_after();
+                const int e_tile = e_beg + j * kE, last = blocks.last_query(e_tile), buf = j & 1;
+                for (int tg = 0; ok && tg < (last + 1) * per_query; ++tg) {
+                    if (blocks.visible(tg / per_query) <= e_tile) continue;
+                    const uint32_t sb = n & 1;
+                    if (n >= 2) ok = until(&s.s_empty[sb], ((n >> 1) - 1) & 1);
+                    for (int h = a.halves() - 1; h >= 0 && (ok = ok && until(&s.q_full[h], stay ? 0 : n & 1) &&
+                                                                   until(&s.full[buf][h], (j >> 1) & 1)); --h) {
+                        tc::tc_fence_after();
+                        for (int i = 0; i < a.blocks(h) / 2; ++i)
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk) {
-                                const int blk = 2 * i + (kk >> 2);
-                                tc::umma_bf16_warp(tmem_S + sb * kHg,
-                                              tc::sdesc_sw128(kv_addr + (j & 1) * tile_bytes + blk * kBlockBytes + (kk & 3) * 32, 16, 1024),
-                                              tc::sdesc_sw128(q_addr + blk * (kHg * 128) + (kk & 3) * 32, 16, 1024),
-                                              idesc, (o | kk) ? 1u : 0u);
+                                const int blk = 4 * h + 2 * i + (kk >> 2);
+                                tc::umma_bf16_warp(
+                                    tmem_S + sb * kHg,
+                                    tc::sdesc_sw128(kv_addr + buf * tile_bytes + blk * kBlockBytes + (kk & 3) * 32, 16, 1024),
+                                    tc::sdesc_sw128(q_addr + blk * (kHg * 128) + (kk & 3) * 32, 16, 1024), idesc,
+                                    (h < a.halves() - 1 || i || kk) ? 1u : 0u);
                             }
-                            if (!stay) tc::umma_commit_warp(&s.q_empty[i]);
-                            if (t == last && g == a.hgroups - 1) tc::umma_commit_warp(&s.empty[j & 1][i]);
-                        }
-                        if (ok) tc::umma_commit_warp(&s.s_full[sb]);
-                        first = false;
+                        if (!stay) tc::umma_commit_warp(&s.q_empty[h]);
+                        if (tg == (last + 1) * per_query - 1) tc::umma_commit_warp(&s.empty[buf][h]);
                     }
+                    if (ok) tc::umma_commit_warp(&s.s_full[sb]);
+                    ++n;
                 }
             }
             tc::umma_commit_warp(&s.fin);
