@@ -3,13 +3,13 @@
 //
 //   z_s = scale * q . v_s,  out = sum_s e^{z_s} v_s / (sum_s e^{z_s} [+ e^{sink}])
 //
-// One CTA serves (query, up to 64 heads, one split of the query's entries)
+// One CTA serves (query, 64 or 16 heads, one split of the query's entries)
 // and walks the split in tiles of 64 entries. Producer warps read the packed
 // rows, expand them to bf16 (exact) and store the tile in shared memory, where
 // ONE copy of it (64-dim blocks, 128-byte swizzle) feeds both products, key
 // and value being the same row:
-//   S^T  = V_tile . q^T         M = 64 entries, N = 64 heads, K = c
-//   O^T += V_tile^T . P^T       M = 128 dims,   N = 64 heads, K = 64 entries
+//   S^T  = V_tile . q^T         M = 64 entries, N = heads, K = c
+//   O^T += V_tile^T . P^T       M = 128 dims,   N = heads, K = 64 entries
 // S^T and O^T live in tensor memory. The softmax keeps a reference maximum per
 // head that moves (O^T and the sums are then rescaled) only when a logit
 // passes it by 2^24; normalisation uses the same reference, so the result does
@@ -18,15 +18,23 @@
 //
 // Two tiles (and two S^T, two P) are in work at a time, so that producers,
 // softmax and products overlap:
-//   warps 0-7   softmax; warp w has entries 16 (w % 4).. and 32 heads, a
-//               thread 2 entries x 8 heads (the 16-lane tensor-memory loads)
+//   warps 0-7   softmax; warp w has entries 16 (w % 4).. and half of the
+//               heads, a thread 2 entries x 8 (2) of them (the 16-lane
+//               tensor-memory loads)
 //   warps 8-23  producers (fp4_tile.cuh)
 //   warp 24     S products, half of the channels by half as they are stored
 //   warp 25     O products, each half of them handed back to the producers
 // One buffer of 128 entries left the four steps of a tile one after another,
-// 8700 cycles for 128 entries, half of them handing over; two of 64 take TWO64.
-// The least is the shared memory's 128 bytes a cycle: 128 entries are written
-// (128 KB) and read by the products (448 KB with q and P), 4600 cycles.
+// 8700 cycles for 128 entries; two of 64 take 3250 a tile, 6500 cycles. What
+// bounds that is a buffer's round: 2100 cycles to expand a tile, 900 more until
+// its logits are there, 1700 for the softmax, 1200 for the O product, over two
+// buffers (a third does not fit beside 64 KB of queries). All 16 producer warps
+// on one tile at a time shorten the first step, but S then starts on whole
+// tiles only: 7% slower. The products alone take 2050 cycles a tile (M = 64, N =
+// 64: 40 cycles each, M = 128: 48, the shared memory's rate), and reading,
+// storing and multiplying through shared memory 2300.
+// 3001 queries x 64 heads over 512 entries: 446 us (297 TFLOP/s, 18% of the
+// dense rate measured on this part); 16 sequences of 8192 entries 44 us.
 //
 // Entries outside the query's set are stored as zeros and get weight 0: no
 // row that the query does not see is read.
@@ -462,9 +470,9 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
 
     if (a.merge == kCluster) {
         // two splits send each other the half of their sums that the other
-        // writes out, one bulk copy to where its queries were; more read their
-        // peers' in place. (A bulk copy moves the 64 KB in SENT us, loads from
-        // the peer in 3.)
+        // writes out, one bulk copy to where its queries were (64 sequences x
+        // 512 entries: 21.2 us a call when it came, 21.6 with loads from the
+        // peer); more read their peers' in place.
         const int items = nh * c4, lo = (int)((int64_t)items * split / a.nsplit);
         const int hi = (int)((int64_t)items * (split + 1) / a.nsplit);
         const bool two = a.nsplit == 2 && items % 2 == 0;
@@ -544,7 +552,12 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
 }
 
 // Heads per CTA: 64, so that a query's entries are expanded once for all of
-// them; 16 where four times the CTAs still fit with a tile each. HG_TEXT
+// them; 16 where four times the CTAs have at most two tiles each, since staging
+// and merging 64 heads' sums takes longer than expanding a few tiles more (one
+// query over 512 entries: 18.5 us with 64, 12.3 with 16; 8 queries 15.3 and
+// 11.6; 8 queries over 1024, four tiles each, 13.7 and 15.6), and for up to 16
+// heads, whose products are shorter (16 heads, 64 x 512 entries: 16.1 and 14.9
+// us, 16 x 8192: 37.7 and 35.4).
 int heads_of(int nq, int H, int64_t max_entries) {
     const int64_t tiles = (max_entries + kE - 1) / kE;
     return H <= 16 || (int64_t)nq * ((H + 63) / 64) * tiles * 4 <= 2 * 148 ? 16 : 64;

@@ -5,7 +5,9 @@
 // The logits are the attention's S^T = V_tile . q^T product (64 entries x 64
 // heads, K = c; mqa_fp4.cu) without the second product; the four threads that
 // hold an entry's logits sum its weights over the heads.
-// Bound by reading the packed rows; what paces it is expanding them.
+// The floor is reading the packed rows; what paces it is the product's barriers
+// and shared-memory reads (16 sequences of 8192 entries x 64 heads: 34 us, 1.2
+// TB/s).
 //
 // A CTA walks a run of tiles of one sequence (or of one query's entry list).
 // Each tile stays in shared memory for all query blocks (query, 64 heads) of
