@@ -752,7 +752,7 @@ static int check_fp4_attn(int nq, int n_seq, int H, int c, int rope_dims, int64_
     CSA_TRY(check_attn_shape(H, c));
     CSA_TRY(check_kv_fp4(c, rope_dims, who));
     CSA_TRY(check_rows(nq, who));
-    if (nq < 0 || Nmax < 0 || n_seq < 1) return fail(CSA_ERR_INVALID_ARG, "%s: bad nq/n_seq/Nmax", who);
+    if (nq < 0 || Nmax < 0 || n_seq < (nq > 0)) return fail(CSA_ERR_INVALID_ARG, "%s: bad nq/n_seq/Nmax", who);
     if (identity && n_seq < nq)
         return fail(CSA_ERR_INVALID_ARG, "%s: seq_of_q is NULL (query t reads sequence t) but n_seq < nq", who);
     return check_cache_rows(n_seq, Nmax);
@@ -818,8 +818,8 @@ int csa_entry_weights_fp4kv(const void* q, const float* lse, const uint8_t* kv4,
     if (seq_of_q && acc)
         return fail(CSA_ERR_INVALID_ARG, "csa_entry_weights_fp4kv: acc needs one query per sequence (seq_of_q NULL): "
                     "the order in which several queries add to one entry would change the sum");
-    if (!weights && !acc) return fail(CSA_ERR_INVALID_ARG, "csa_entry_weights_fp4kv: neither weights nor acc given");
     if (nq == 0) return CSA_OK;
+    if (!weights && !acc) return fail(CSA_ERR_INVALID_ARG, "csa_entry_weights_fp4kv: neither weights nor acc given");
     CSA_TRY(check_ptr(q, "q"));
     CSA_TRY(check_ptr(lse, "lse"));
     CSA_TRY(check_ptr(kv4, "kv4", Nmax > 0));
@@ -875,7 +875,7 @@ int csa_evict_plan(const float* acc, const int32_t* n_ent, const int32_t* entry_
     CSA_TRY(check_evict(B, Nmax, "csa_evict_plan"));
     if (keep < 0 || keep > Nmax)
         return fail(CSA_ERR_INVALID_ARG, "csa_evict_plan: keep=%lld outside [0, Nmax]", (long long)keep);
-    if (protect_from && !entry_pos)
+    if (protect_from && !entry_pos && Nmax > 0)
         return fail(CSA_ERR_INVALID_ARG, "csa_evict_plan: protect_from needs entry_pos");
     if ((entry_pos == nullptr) != (pos_out == nullptr))
         return fail(CSA_ERR_INVALID_ARG, "csa_evict_plan: entry_pos and pos_out go together");

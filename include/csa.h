@@ -456,7 +456,8 @@ int hca_decode_fp4kv(const void* q, const uint8_t* kv4, const int32_t* ctx_len, 
  * csa_evict_rows: carries the moves out on cache [B, Nmax, row_bytes] (any
  *   cache of the sequences: 4-bit or bf16 entries, index keys), in place;
  *   row_bytes a multiple of 16, max_moves = M. A move with a row outside
- *   [0, Nmax) is skipped.
+ *   [0, Nmax) is skipped. The moves run in any order: in lists of one's own no
+ *   row may be in both, nor twice in dst.
  * csa_evict_slot: decode time, one new entry per sequence. A token at pos[b]
  *   closes entry i = (pos+1)/m - 1 when (pos+1) % m == 0 (as
  *   csa_compress_step); otherwise, or for a negative pos, slot[b] = -1 and

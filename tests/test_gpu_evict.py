@@ -189,3 +189,19 @@ def test_a_budgeted_decode_loop(csa):
             held[b][s] = entry
         assert int(n_ent.max()) <= cap
     assert n_ent.tolist() == [cap] * B
+
+
+def test_empty_batches_and_caches(csa):
+    i32 = torch.int32
+    z = lambda *shape, dt=i32: torch.zeros(shape, dtype=dt, device=DEV)
+    assert csa.csa_evict_plan(z(0, 9, dt=torch.float32), z(0), 4)[0].shape == (0, 4)
+    out = csa.csa_evict_plan(z(2, 0, dt=torch.float32), z(2) + 5, 0, entry_pos=z(2, 0), protect_from=z(2))
+    assert out[0].shape == (2, 0) and (out[2] == 0).all() and (out[3] == 0).all()
+    csa.csa_evict_rows(z(2, 0, 32, dt=torch.uint8), z(2, 0), z(2, 0), z(2))
+    assert csa.csa_evict_slot(z(0, 9, dt=torch.float32), z(0), z(0), 4, 3).shape == (0,)
+    # keep nothing, keep everything: no moves either way
+    acc = torch.arange(10, dtype=torch.float32, device=DEV).reshape(2, 5)
+    src, dst, moves, n_out, w, _ = csa.csa_evict_plan(acc, z(2) + 5, 0)
+    assert src.shape == (2, 0) and (moves == 0).all() and (n_out == 0).all() and (w == 0).all()
+    src, dst, moves, n_out, w, _ = csa.csa_evict_plan(acc, z(2) + 5, 5)
+    assert src.shape == (2, 0) and (moves == 0).all() and (n_out == 5).all() and torch.equal(w, acc)

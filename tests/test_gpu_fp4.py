@@ -481,3 +481,81 @@ def test_binding_refusals(csa):
     with pytest.raises(ValueError):
         csa.hca_decode_fp4kv(q, kv[:1], torch.zeros(2, dtype=torch.int32, device=DEV), 4)
     torch.cuda.synchronize()
+
+
+def test_empty_batches_and_caches(csa):
+    z = lambda *shape, dt=torch.bfloat16: torch.zeros(shape, dtype=dt, device=DEV)
+    i32, u8, f32 = torch.int32, torch.uint8, torch.float32
+    assert csa.csa_quantize_kv_fp4(z(0, 512)).shape == (0, 384)
+    assert csa.csa_dequantize_kv_fp4(z(0, 384, dt=u8), 512).shape == (0, 512)
+    csa.csa_append_kv_fp4(z(0, 512), z(0, dt=i32), z(0, 9, 384, dt=u8))
+    csa.csa_append_kv_fp4(z(2, 512), z(2, dt=i32), z(2, 0, 384, dt=u8))
+    out, lse = csa.csa_sparse_mqa_fp4kv(z(0, 4, 512), z(0, 9, 384, dt=u8), z(0, 3, dt=i32))
+    assert out.shape == (0, 4, 512) and lse.shape == (0, 4)
+    assert csa.hca_decode_fp4kv(z(0, 4, 512), z(0, 9, 384, dt=u8), z(0, dt=i32), 4)[0].shape == (0, 4, 512)
+    assert csa.csa_entry_weights_fp4kv(z(0, 4, 512), z(0, 4, dt=f32), z(0, 9, 384, dt=u8), z(0, 3, dt=i32)).shape == (0, 3)
+    assert csa.hca_entry_weights_fp4kv(z(0, 4, 512), z(0, 4, dt=f32), z(0, 9, 384, dt=u8), z(0, dt=i32), 4).shape == (0, 9)
+    # caches without rows: the sink logit, or nothing
+    q, sink = torch.ones(2, 4, 512, dtype=torch.bfloat16, device=DEV), torch.tensor([0.5, -1.0, 2.0, 0.0], device=DEV)
+    for call in (lambda s: csa.csa_sparse_mqa_fp4kv(q, z(2, 0, 384, dt=u8), z(2, 3, dt=i32), sink=s),
+                 lambda s: csa.hca_decode_fp4kv(q, z(2, 0, 384, dt=u8), z(2, dt=i32) + 99, 4, sink=s)):
+        out, lse = call(None)
+        assert (out == 0).all() and lse.isneginf().all()
+        out, lse = call(sink)
+        # the logarithm of e^sink / 1: a logarithm and a product, each within 2^-22 of its value
+        assert (out == 0).all() and ((lse - sink).abs() <= 2.0 ** -21 * (1 + sink.abs())).all()
+    acc = torch.ones(2, 5, device=DEV)
+    no_t = csa.hca_entry_weights_fp4kv(z(2, 0, 4, 512), z(2, 0, 4, dt=f32), z(2, 5, 384, dt=u8), z(2, 0, dt=i32), 4, acc=acc)
+    assert torch.equal(no_t, acc)
+
+
+def test_calls_stay_on_their_stream(csa):
+    # inputs made on a side stream, the call on that stream, the result read on it: no other stream is touched
+    side = torch.cuda.Stream()
+    g = _gen(77)
+    x = torch.randn(4, 600, 512, generator=g).to(torch.bfloat16)
+    q = torch.randn(4, 64, 512, generator=g).to(torch.bfloat16)
+    pos = torch.tensor([600, 1, 0, 599], dtype=torch.int32)
+    want = csa.hca_decode_fp4kv(q.to(DEV), csa.csa_quantize_kv_fp4(x.to(DEV)), pos.to(DEV), 1)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2_000_000)
+            xs = x.pin_memory().to(DEV, non_blocking=True)
+            kv = csa.csa_quantize_kv_fp4(xs)
+            got = csa.hca_decode_fp4kv(q.to(DEV), kv, pos.to(DEV), 1)
+            same = [torch.equal(a, b) for a, b in zip(got, want)]
+        assert all(same)
+
+
+def test_weights_of_a_long_prompt_add_up(csa):
+    # 1500 queries of two sequences in one call, and in three with acc = out
+    B, T, N, H, c, R = 2, 1500, 200, 8, 128, 32
+    kv, V = _rows(csa, B * N, c, R, 90)
+    kv, V = kv.reshape(B, N, -1), V.reshape(B, N, c)
+    g = _gen(91)
+    q = torch.randn(B, T, H, c, generator=g).to(torch.bfloat16)
+    pos = torch.randint(0, 4 * N + 9, (B, T), generator=g, dtype=torch.int32)
+    ref = np.zeros((B, N))
+    lse = np.zeros((B, T, H), np.float32)
+    for b in range(B):
+        z = np.einsum("thc,nc->thn", host(q[b]), V[b]) * c ** -0.5
+        seen = np.arange(N)[None] < np.minimum(N, pos[b].numpy() // 4)[:, None]
+        z = np.where(seen[:, None], z, -np.inf)
+        m = z.max(-1, keepdims=True)
+        m = np.where(np.isfinite(m), m, 0)
+        with np.errstate(divide="ignore"):
+            lse[b] = (m[..., 0] + np.log(np.exp(z - m).sum(-1))).astype(np.float32)
+        ok = np.isfinite(lse[b])
+        ref[b] = np.exp(z - np.where(ok, lse[b], 0)[..., None])[ok].sum(0)
+    dz = _logit_slack(host(q).reshape(B * T, H, c), V, c ** -0.5)
+    args = (q.to(DEV), torch.from_numpy(lse).to(DEV), kv, pos.to(DEV), 4)
+    w = csa.hca_entry_weights_fp4kv(*args, rope_dims=R)
+    # T sums of 64 fp32 terms on top of the single query's bound
+    lim = (math.expm1(dz) + 2.0 ** -18 + (T + H) * 2.0 ** -24) * ref + 1e-37
+    assert (np.abs(host(w) - ref) <= lim).all()
+    acc = torch.zeros(B, N, device=DEV)
+    for a, b in ((0, 700), (700, 701), (701, T)):
+        part = [x[:, a:b].contiguous() for x in (args[0], args[1])] + [kv, args[3][:, a:b].contiguous(), 4]
+        csa.hca_entry_weights_fp4kv(*part, acc=acc, rope_dims=R, out=acc)
+    assert (np.abs(host(acc) - ref) <= lim).all()
