@@ -71,14 +71,19 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Fp4TileShar
 template <bool kSparse>
 struct RowWalk {
     const Fp4TileArgs& a;
+    int row;                          // in the tile
     int row0, t, e0, e_end, ntiles;   // (rows as numbers: n_seq * Nmax is below 2^31)
     int next, cur;                    // entry in two tiles; row in the cache, < 0: none
 
-    // first_row: row of the sequence's entry 0 in the cache
-    __device__ __forceinline__ RowWalk(const Fp4TileArgs& a_, int row, int first, int t_, int e_beg, int e_end_,
-                                       int ntiles_, int64_t first_row)
-        : a(a_), row0((int)first_row), t(t_), e0(e_beg + row), e_end(e_end_), ntiles(ntiles_), cur(-1) {
-        next = entry(first);
+    __device__ __forceinline__ RowWalk(const Fp4TileArgs& a_, int row_) : a(a_), row(row_), ntiles(0), cur(-1) {}
+    // first_row: row of the sequence's entry 0 in the cache; j: this buffer's first tile
+    __device__ __forceinline__ void begin(int t_, int e_beg, int e_end_, int ntiles_, int64_t first_row, int j) {
+        row0 = (int)first_row;
+        t = t_;
+        e0 = e_beg + row;
+        e_end = e_end_;
+        ntiles = ntiles_;
+        next = entry(j);
     }
     // entry index of this row in tile j (outside [0, Nmax): none)
     __device__ __forceinline__ int entry(int j) const {
@@ -146,10 +151,9 @@ struct Producer {
     __device__ __forceinline__ int lane_of(int i) const { return (lane & 0x0E) | ((i >> 1) << 4) | (i & 1); }
 
     // warp: 0 .. 15 of the producers
-    __device__ __forceinline__ Producer(const Fp4TileArgs& a_, Fp4TileShared& s_, uint8_t* kv_s, int warp, int t,
-                                        int e_beg, int e_end, int ntiles, int64_t first_row)
+    __device__ __forceinline__ Producer(const Fp4TileArgs& a_, Fp4TileShared& s_, uint8_t* kv_s, int warp)
         : a(a_), s(s_), lane(threadIdx.x & 31), row((warp & 7) * 8 + ((lane >> 1) & 7)),
-          walk(a_, row, warp >> 3, t, e_beg, e_end, ntiles, first_row),
+          walk(a_, row),
           tile(tc::smem_u32(kv_s) + (warp >> 3) * a_.dblocks * kBlockBytes + row * 128) {}
     // All of a tile's loads, issued together right after the buffer's last
     // tile is stored, and nothing computed from them until the tile is stored: a
@@ -175,7 +179,7 @@ struct Producer {
         if (ok && a.f.R > 64)
             for (int n = 8 + chunk(); n < a.f.R / 8; n += 4) prefetch_l2(p + a.f.rope_off + n * 16);
     }
-    // stores tile j; false when a wait ran out
+    // stores the CTA's j-th tile; false when a wait ran out
     __device__ __forceinline__ bool store(int j) {
         const int nq = a.f.Q / 16, b = j & 1;
         const uint8_t* p = a.kv4 + (int64_t)walk.cur * a.f.bytes;
@@ -257,10 +261,9 @@ struct WideProducer {
     uint32_t tile;            // this thread's row in block 0 of its buffer
     uint32_t raw[3][8];       // pieces lane % 4, + 4, + 8
 
-    __device__ __forceinline__ WideProducer(const Fp4TileArgs& a_, Fp4TileShared& s_, uint8_t* kv_s, int warp, int t,
-                                            int e_beg, int e_end, int ntiles, int64_t first_row)
+    __device__ __forceinline__ WideProducer(const Fp4TileArgs& a_, Fp4TileShared& s_, uint8_t* kv_s, int warp)
         : a(a_), s(s_), lane(threadIdx.x & 31), row((warp & 7) * 8 + (lane >> 2)), nb(a_.f.Q / 64),
-          walk(a_, row, warp >> 3, t, e_beg, e_end, ntiles, first_row),
+          walk(a_, row),
           tile(tc::smem_u32(kv_s) + (warp >> 3) * a_.dblocks * kBlockBytes + row * 128) {}
     // (as above)
     __device__ __forceinline__ void load(int j) {
@@ -326,19 +329,22 @@ struct WideProducer {
     }
 };
 
-// All of a producer warp's work (warp: 0 .. 15 of the producers). ready() is
-// called when the first tile's loads have been issued.
+// A producer warp's part of a run of tiles (warp: 0 .. 15 of the producers, of
+// which 8 have the even and 8 the odd tiles of the CTA; `before` tiles came
+// before this run). ready() is called when the first tile's loads have been
+// issued. False when a wait ran out.
 template <typename P, typename F>
-__device__ __forceinline__ void produce(const Fp4TileArgs& a, Fp4TileShared& s, uint8_t* kv_s, int warp, int t, int e_beg,
-                                        int e_end, int ntiles, int64_t first_row, F ready) {
-    P p(a, s, kv_s, warp, t, e_beg, e_end, ntiles, first_row);
-    int j = warp >> 3;
+__device__ __forceinline__ bool produce(P& p, int warp, int before, int t, int e_beg, int e_end, int ntiles,
+                                        int64_t first_row, F ready) {
+    int j = ((warp >> 3) ^ before) & 1;
+    p.walk.begin(t, e_beg, e_end, ntiles, first_row, j);
     if (j < ntiles) p.load(j);
     ready();
     for (; j < ntiles; j += 2) {
-        if (!p.store(j)) break;
+        if (!p.store(before + j)) return false;
         if (j + 2 < ntiles) p.load(j + 2);
     }
+    return true;
 }
 
 template <bool kSparse, bool kWide>

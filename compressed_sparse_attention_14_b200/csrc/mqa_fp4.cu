@@ -68,7 +68,7 @@ struct Args : Fp4TileArgs {
     float* part_o;
     float* part_ml;
     int64_t split_len;
-    int n_seq, mp, H, nsplit, merge;
+    int n_seq, mp, H, nsplit, merge, groups, items;   // items: queries * head groups
     float scale_log2;
 };
 
@@ -99,6 +99,17 @@ __device__ __forceinline__ bool half_any(int half, bool v) {
                  "bar.red.or.pred p, %2, 128, q;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(r) : "r"((uint32_t)v), "r"(1 + half) : "memory");
+    return r != 0;
+}
+
+// the same of all softmax warps
+__device__ __forceinline__ bool softmax_any(bool v) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "setp.ne.u32 q, %1, 0;\n\t"
+                 "bar.red.or.pred p, 3, 256, q;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r) : "r"((uint32_t)v) : "memory");
     return r != 0;
 }
 
@@ -156,7 +167,7 @@ __device__ __forceinline__ void merge_items(const Args& a, const Shared& s, cons
     }
 }
 
-template <bool kSparse, bool kWide, int kHg>
+template <bool kSparse, bool kWide, int kHg, bool kOne>
 __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_constant__ Args a,
                                                               const __grid_constant__ CUtensorMap tmQ) {
     constexpr int kHalf = kHg / 2, kOct = kHg / 16;       // heads, and groups of 8, per softmax warp
@@ -171,13 +182,30 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     pdl_wait();
     pdl_launch_next();
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // (uniform)
-    const int t = blockIdx.z, h0 = blockIdx.y * kHg, split = blockIdx.x;
-    const int seq = a.qm.seq_of(t);
-    int64_t n_ent = 0;
-    if (seq >= 0 && seq < a.n_seq) n_ent = kSparse ? (int64_t)a.k : visible_entries(a.qm.pos_of(t), a.mp, a.Nmax);
-    const int64_t e_beg = (int64_t)split * a.split_len;
-    const int64_t e_end = n_ent < e_beg + a.split_len ? n_ent : e_beg + a.split_len;
-    const int ntiles = e_end > e_beg ? (int)((e_end - e_beg + kE - 1) / kE) : 0;
+    // What the CTA has to do: one split of a query, or (a query in one split)
+    // every gridDim.x-th of the (query, heads) items, their tiles following one
+    // another through the buffers.
+    struct Item {
+        int t, h0, split, seq, ntiles;
+        int64_t e_beg, e_end;
+    };
+    // (kOne: queries in one split)
+    const int it0 = kOne ? blockIdx.x : 0, it_end = kOne ? a.items : 1, it_step = kOne ? gridDim.x : 1;
+    auto item_of = [&](int it) {
+        Item x;
+        x.t = kOne ? it / a.groups : blockIdx.z;
+        x.h0 = (kOne ? it % a.groups : blockIdx.y) * kHg;
+        x.split = kOne ? 0 : blockIdx.x;
+        x.seq = a.qm.seq_of(x.t);
+        int64_t n_ent = 0;
+        if (x.seq >= 0 && x.seq < a.n_seq) n_ent = kSparse ? (int64_t)a.k : visible_entries(a.qm.pos_of(x.t), a.mp, a.Nmax);
+        x.e_beg = (int64_t)x.split * a.split_len;
+        x.e_end = n_ent < x.e_beg + a.split_len ? n_ent : x.e_beg + a.split_len;
+        x.ntiles = x.e_end > x.e_beg ? (int)((x.e_end - x.e_beg + kE - 1) / kE) : 0;
+        return x;
+    };
+    const Item first = item_of(it0);
+    auto item = [&](int it) { return kOne && it != it0 ? item_of(it) : first; };
 
     // The set-up's barrier stands in each role: what a role can start before it
     // (the queries' copy, the first tiles' loads) has begun by then.
@@ -187,6 +215,11 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         tc::tc_fence_after();
         tmem_S = __shfl_sync(0xffffffffu, s.tmem, 0);
         tmem_O = tmem_S + 2 * kHg;
+    };
+    auto load_q = [&](const Item& x) {
+        tc::mbar_expect_tx(&s.q_full, (uint32_t)a.dblocks * kHg * 128);
+        for (int b = 0; b < a.dblocks; ++b)
+            tc::tma_load_2d(q_s + (size_t)b * kHg * 128, &tmQ, &s.q_full, b * 64, x.t * a.H + x.h0);
     };
     if (warp >= kSWarp) {
         // ------------------------------------------------------------ products
@@ -205,11 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                 tc::mbar_init(&s.peer, 1);
                 tc::fence_mbar_init();
                 s.abort = 0;
-                if (ntiles > 0) {
-                    tc::mbar_expect_tx(&s.q_full, (uint32_t)a.dblocks * kHg * 128);
-                    for (int b = 0; b < a.dblocks; ++b)
-                        tc::tma_load_2d(q_s + (size_t)b * kHg * 128, &tmQ, &s.q_full, b * 64, t * a.H + h0);
-                }
+                if (first.ntiles > 0) load_q(first);
             }
             __syncwarp();
         } else {
@@ -218,18 +247,25 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             tc::tc_fence_before();
         }
         setup_done();
-        if (ntiles > 0) {
-            const uint32_t kv_addr = __shfl_sync(0xffffffffu, tc::smem_u32(kv_s), 0);
-            const uint32_t tile_bytes = a.dblocks * kBlockBytes;
-            const uint32_t q_addr = kv_addr + 2 * tile_bytes, p_addr = q_addr + a.dblocks * kHg * 128;
-            auto until = [&](uint64_t* bar, uint32_t parity) {
-                return __all_sync(0xffffffffu, wait(bar, parity, s, a.status));
-            };
-            bool ok = true;
-            if (warp == kSWarp) {
-                ok = until(&s.q_full, 0);
-                const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
-                for (int j = 0; ok && j < ntiles; ++j) {
+        const uint32_t kv_addr = __shfl_sync(0xffffffffu, tc::smem_u32(kv_s), 0);
+        const uint32_t tile_bytes = a.dblocks * kBlockBytes;
+        const uint32_t q_addr = kv_addr + 2 * tile_bytes, p_addr = q_addr + a.dblocks * kHg * 128;
+        auto until = [&](uint64_t* bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait(bar, parity, s, a.status));
+        };
+        bool ok = true;
+        int before = 0;                                   // tiles of the items before
+        if (warp == kSWarp) {
+            const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
+            uint32_t nq = 0;                              // items that had tiles
+            for (int it = it0; ok && it < it_end; it += it_step) {
+                const Item x = item(it);
+                if (x.ntiles == 0) continue;
+                if (it != it0 && lane == 0) load_q(x);    // (its place is free: see below)
+                __syncwarp();
+                ok = until(&s.q_full, nq++ & 1);
+                const int end = before + x.ntiles;
+                for (int j = before; ok && j < end; ++j) {
                     const int b = j & 1;
                     for (int h = a.halves() - 1; h >= 0 && (ok = until(&s.full[b][h], (j >> 1) & 1)); --h) {
                         tc::tc_fence_after();
@@ -246,10 +282,17 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                     }
                     if (ok) tc::umma_commit_warp(&s.s_full[b]);
                 }
-                if (!ok) tc::mbar_wait(&s.q_full, 0, kWaitLimit);
-            } else {
-                const uint32_t idesc = tc::idesc_bf16_f32(128, kHg, 1, 1);
-                for (int j = 0; j < ntiles && (ok = until(&s.p_full[j & 1], (j >> 1) & 1)); ++j) {
+                before = end;
+                // the products have read this item's queries
+                if (it + it_step < it_end) ok = ok && until(&s.s_full[(end - 1) & 1], ((end - 1) >> 1) & 1);
+                // a copy that was waited for in vain is waited for again below
+                if (!ok) tc::mbar_wait(&s.q_full, (nq - 1) & 1, kWaitLimit);
+            }
+        } else {
+            const uint32_t idesc = tc::idesc_bf16_f32(128, kHg, 1, 1);
+            for (int it = it0; ok && it < it_end; it += it_step) {
+                const int end = before + item(it).ntiles;
+                for (int j = before; j < end && (ok = until(&s.p_full[j & 1], (j >> 1) & 1)); ++j) {
                     const int b = j & 1;
                     tc::tc_fence_after();
                     for (int mt = a.mtiles - 1; mt >= 0; --mt) {
@@ -259,25 +302,38 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                                 tmem_O + mt * kHg,
                                 tc::sdesc_sw128(kv_addr + b * tile_bytes + 2 * mt * kBlockBytes + ke * 2048, kBlockBytes, 1024),
                                 tc::sdesc_sw128(p_addr + b * (kE * 128) + ke * 2048, kE * 128, 1024), idesc,
-                                (j > 0 || ke > 0) ? 1u : 0u);
+                                (j > before || ke > 0) ? 1u : 0u);
                         if (!(mt & 1)) tc::umma_commit_warp(&s.empty[b][mt >> 1]);
                     }
                 }
+                before = end;
             }
-            // every product issued has ended before the CTA goes on to free the
-            // memory it uses (also when a wait ran out)
-            tc::umma_commit_warp(&s.fin[warp - kSWarp]);
-            tc::mbar_wait(&s.fin[warp - kSWarp], 0, kWaitLimit);
         }
+        // every product issued has ended before the CTA goes on to free the
+        // memory it uses (also when a wait ran out)
+        tc::umma_commit_warp(&s.fin[warp - kSWarp]);
+        tc::mbar_wait(&s.fin[warp - kSWarp], 0, kWaitLimit);
     } else if (warp >= kSoftmaxWarps) {
-        produce<ProducerOf<kSparse, kWide>>(a, s, kv_s, warp - kSoftmaxWarps, t, (int)e_beg, (int)e_end, ntiles,
-                                            (ntiles ? seq : 0) * a.Nmax, setup_done);
+        ProducerOf<kSparse, kWide> producer(a, s, kv_s, warp - kSoftmaxWarps);
+        int before = 0;
+        for (int it = it0; it < it_end; it += it_step) {
+            const Item x = item(it);
+            if (!produce(producer, warp - kSoftmaxWarps, before, x.t, (int)x.e_beg, (int)x.e_end, x.ntiles,
+                         (x.ntiles ? x.seq : 0) * a.Nmax, [&]() { if (it == it0) setup_done(); }))
+                break;
+            before += x.ntiles;
+        }
     } else {
         // ------------------------------------------------------------ softmax
         const int quad = warp & 3, half = warp >> 2, hb = half * kHalf;
         const int q4 = lane & 3, ra = quad * 16 + (lane >> 2), rb = ra + 8;   // this thread's entries
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const int hth = tid & 127;
+        bool ok = true;
+        int before = 0;                                   // tiles of the items before
+        for (int it = it0; ok && it < it_end; it += it_step) {
+        const Item x = item(it);
+        const int t = x.t, h0 = x.h0, ntiles = x.ntiles;
         if (hth < kHalf) {
             s.mref[hb + hth] = s.limit[hb + hth] = -INFINITY;
             s.mexp[hb + hth] = 0.f;
@@ -285,13 +341,13 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         float lpart[2 * kOct];                            // heads hb + 8u + 2 q4 + (0, 1), both entries
 #pragma unroll
         for (int i = 0; i < 2 * kOct; ++i) lpart[i] = 0.f;
-        setup_done();
-        bool ok = true;
-        for (int j = 0; j < ntiles; ++j) {
-            const int b = j & 1;
+        if (it == it0) setup_done();
+        else half_sync(half);
+        for (int n = 0; n < ntiles; ++n) {
+            const int j = before + n, b = j & 1;
             auto seen = [&](int row) {
-                const int64_t e = e_beg + (int64_t)j * kE + row;
-                if (e >= e_end) return false;
+                const int64_t e = x.e_beg + (int64_t)n * kE + row;
+                if (e >= x.e_end) return false;
                 if (!kSparse) return true;
                 const int v = __ldg(a.idx + (int64_t)t * a.k + e);
                 return v >= 0 && v < a.Nmax;
@@ -336,20 +392,20 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                 half_sync(half);
 #pragma unroll
                 for (int i = 0; i < 2 * kOct; ++i) lpart[i] *= s.alpha[hb + 8 * (i >> 1) + 2 * q4 + (i & 1)];
-                if (j > 0) {
+                if (n > 0) {
                     // rescale O^T (every product before this tile's has ended)
                     ok = wait(&s.empty[b ^ 1][0], ((j - 1) >> 1) & 1, s, a.status);
                     tc::tc_fence_after();
 #pragma unroll 1
-                    for (int n = 0; n < 4 * a.mtiles; ++n) {
-                        const int cc = hb + 8 * (n & 3);
+                    for (int m = 0; m < 4 * a.mtiles; ++m) {
+                        const int cc = hb + 8 * (m & 3);
                         if (cc >= hb + kHalf) continue;
                         float o[8];
-                        tc::tmem_ld8(tmem_O + lanes + (n >> 2) * kHg + cc, o);
+                        tc::tmem_ld8(tmem_O + lanes + (m >> 2) * kHg + cc, o);
                         tc::tmem_ld_wait();
 #pragma unroll
                         for (int i = 0; i < 8; ++i) o[i] *= s.alpha[cc + i];
-                        tc::tmem_st8(tmem_O + lanes + (n >> 2) * kHg + cc, o);
+                        tc::tmem_st8(tmem_O + lanes + (m >> 2) * kHg + cc, o);
                     }
                     tc::tmem_st_wait();
                 }
@@ -374,7 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&s.p_full[b]);
         }
-        if (ok && ntiles > 0) wait(&s.empty[(ntiles - 1) & 1][0], ((ntiles - 1) >> 1) & 1, s, a.status);
+        before += ntiles;
+        if (ok && ntiles > 0) ok = wait(&s.empty[(before - 1) & 1][0], ((before - 1) >> 1) & 1, s, a.status);
         __syncwarp();
         // per-head sums in a fixed order: entries, lanes, then the four warps
         half_sync(half);                                  // red may still be read
@@ -387,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         if (hth < kHalf) {
             const int h = hb + hth;
             s.lsum[h] = (s.red[0][h] + s.red[1][h]) + (s.red[2][h] + s.red[3][h]);
-            if (a.merge == kDirect) {
+            if (kOne) {
                 const float m = s.mref[h], L = s.lsum[h];
                 const float sk = a.sink && h0 + h < a.H ? a.sink[h0 + h] * kLog2e : -INFINITY;
                 const float M = fmaxf(m, sk);
@@ -399,53 +456,64 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                     a.lse[(int64_t)t * a.H + h0 + h] = Lt == 0.f ? -INFINITY : fmaf(M, kLn2, logf(Lt));
             }
         }
+        if (kOne) {
+            // O^T normalised and written out as bf16, 8 heads x 32 dims at a time:
+            // a transposing matrix store to the warp's part of P's place, then 16
+            // bytes per lane to a head's row
+            ok = !softmax_any(!ok);                       // (also: the sums are known)
+            tc::tc_fence_after();
+            uint8_t* stage = p_s + warp * 1024;
+            bf16* out = a.out + ((int64_t)t * a.H + h0) * a.f.c + quad * 32 + (lane & 3) * 8;
+#pragma unroll 2
+            for (int r = 0; r < kHg / 8; ++r) {
+                const float2 al = *reinterpret_cast<const float2*>(&s.alpha[8 * r + 2 * q4]);
+                const int h = 8 * r + (lane >> 2);
+                for (int mt = half; mt < a.mtiles; mt += 2) {
+                    float o[2][4] = {};
+                    if (ntiles > 0) {
+                        tc::tmem_ld_16(tmem_O + lanes + mt * kHg + 8 * r, o[0]);
+                        tc::tmem_ld_16(tmem_O + lanes + (16u << 16) + mt * kHg + 8 * r, o[1]);
+                        tc::tmem_ld_wait();
+                    }
+                    uint32_t m[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {         // dims 8i .. 8i + 7 of this warp's 32
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(al.x != 0.f ? o[i >> 1][2 * (i & 1)] * al.x : 0.f,
+                                                                       al.y != 0.f ? o[i >> 1][2 * (i & 1) + 1] * al.y : 0.f);
+                        m[i] = *reinterpret_cast<const uint32_t*>(&v);
+                    }
+                    // (two places in turn; rows of 64 bytes, their 16-byte pieces
+                    // turned so that 8 lanes use different banks)
+                    uint8_t* at = stage + (mt >> 1 & 1) * 512;
+                    const int row = lane & 7, piece = lane >> 3;
+                    stmatrix_trans4(tc::smem_u32(at) + row * 64 + ((piece ^ (row >> 1)) & 3) * 16, m);
+                    __syncwarp();
+                    const uint4 v = *reinterpret_cast<const uint4*>(at + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 3)) & 3) * 16);
+                    if (h0 + h < a.H) *reinterpret_cast<uint4*>(out + (int64_t)h * a.f.c + mt * 128) = v;
+                    __syncwarp();
+                }
+            }
+            tc::tc_fence_before();
+            softmax_any(false);                           // P's place and the maxima may be written
+        }
+        }
         tc::tc_fence_before();
     }
-    // ---------------------------------------------------------------- epilogue
+    // ---------------------------------------------------------------- merge
     __syncthreads();
+    if (!kOne) {
+    const Item x = first;
+    const int t = x.t, h0 = x.h0, split = x.split, ntiles = x.ntiles;
     const int nh = a.H - h0 < kHg ? a.H - h0 : kHg, c4 = a.f.c / 4;
     bf16* out = a.out + ((int64_t)t * a.H + h0) * a.f.c;   // this CTA's heads: contiguous rows
     const int64_t part = ((int64_t)t * a.nsplit + split) * a.H + h0;
-    // where the output is staged as bf16: rows of 16 more bytes than a head's,
-    // so that 8 rows start in different banks
-    const uint32_t pitch = a.f.c * 2 + 16;
-    // warp w has dims 32 (w % 4).. of M tiles mt0, mt0 + step, .. and 16 heads
-    constexpr int kStep = 4 / kOct;
-    const int quad = warp & 3, hb = (warp >> 2) % kOct * 16, mt0 = (warp >> 2) / kOct;
-    const uint32_t addr = tmem_O + ((uint32_t)(quad * 32) << 16) + hb;
-    if (warp < 16 && a.merge == kDirect) {
-        // normalised, bf16: the transposing matrix stores write 8 dims of a head
-        // at a time
-        tc::tc_fence_after();
-        float2 al[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) al[u] = *reinterpret_cast<const float2*>(&s.alpha[hb + 8 * u + 2 * (lane & 3)]);
-        // lane i gives the address of row i % 8 (a head) of matrix i / 8: heads
-        // 8 (i / 16).., dims 8 ((i / 8) % 2)..
-        const uint32_t dst = tc::smem_u32(kv_s) + (hb + (lane >> 4) * 8 + (lane & 7)) * pitch +
-                             (quad * 32 + ((lane >> 3) & 1) * 8) * 2;
-#pragma unroll 1
-        for (int n = 2 * mt0; n < 2 * a.mtiles; n += n & 1 ? 2 * kStep - 1 : 1) {   // 16 dims at a time
-            float o[8];
-            if (ntiles > 0) {
-                tc::tmem_ld_16(addr + (n >> 1) * kHg + ((uint32_t)(16 * (n & 1)) << 16), o);
-                tc::tmem_ld_wait();
-            }
-            uint32_t m[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {                 // heads 8 (i / 2).., dims 8 (i % 2)..
-                const float2 w = al[i >> 1];
-                const __nv_bfloat162 v = __floats2bfloat162_rn(w.x != 0.f ? o[2 * i] * w.x : 0.f,
-                                                               w.y != 0.f ? o[2 * i + 1] * w.y : 0.f);
-                m[i] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            stmatrix_trans4(dst + ((n >> 1) * 128 + (n & 1) * 16) * 2, m);
-        }
-        tc::fence_proxy_async_smem();
-        tc::tc_fence_before();
-    } else if (warp < 16 && ntiles > 0) {
-        // fp32, a lane one dim: to the workspace, or (a cluster) to shared memory
-        // where the tiles were, as rows of a head
+    if (warp < 16 && ntiles > 0) {
+        // fp32: to the workspace, or (a cluster) to shared memory where the tiles
+        // were, as rows of a head. Warp w has dims 32 (w % 4).. of M tiles mt0, mt0
+        // + step, .. and 16 heads, a lane one dim
+        constexpr int kStep = 4 / kOct;
+        const int quad = warp & 3, hb = (warp >> 2) % kOct * 16, mt0 = (warp >> 2) / kOct;
+        const uint32_t addr = tmem_O + ((uint32_t)(quad * 32) << 16) + hb;
         tc::tc_fence_after();
         const int heads = nh - hb;
 #pragma unroll 1
@@ -531,19 +599,13 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         }
         tc::cluster_sync();                               // no peer still reads this CTA's sums
     } else {
-        if (a.merge == kDirect) {
-            __syncthreads();
-            if (tid < nh) {
-                tc::bulk_store(out + (int64_t)tid * a.f.c, kv_s + tid * pitch, a.f.c * 2);
-                tc::bulk_commit();
-                tc::bulk_wait_read();
-            }
-        } else if (tid < nh) {
+        if (tid < nh) {
             const float m = s.mref[tid], L = s.lsum[tid];
             a.part_ml[(part + tid) * 2] = L == 0.f ? -INFINITY : L != L ? 0.f : m * kLn2;
             a.part_ml[(part + tid) * 2 + 1] = L;
         }
         __syncthreads();
+    }
     }
     if (warp == kSWarp + 1) {
         tc::tc_fence_after();
@@ -627,6 +689,8 @@ cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {
     a.mp = x.mp;
     a.H = x.H;
     a.nsplit = ns;
+    a.groups = plan.groups;
+    a.items = x.nq * plan.groups;
     a.merge = plan.merge;
     a.dblocks = x.c / 64;
     a.mtiles = x.c / 128;
@@ -635,16 +699,21 @@ cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {
     if (!make_tmap_bf16_2d(&tmQ, x.q, (uint64_t)x.nq * x.H, x.c, x.c, hg, 64)) return cudaErrorInvalidValue;
     const size_t smem = 1024 + (size_t)a.dblocks * (2 * kBlockBytes + hg * 128) + 2 * kE * 128 + sizeof(Shared);
     const bool wide = wide_rows(a.f, x.kv4);
-    auto of = [&](auto heads) {
+    auto of = [&](auto heads, auto one) {
         constexpr int kHg = decltype(heads)::value;
-        return x.idx ? (wide ? mqa_fp4_kernel<true, true, kHg> : mqa_fp4_kernel<true, false, kHg>)
-                     : (wide ? mqa_fp4_kernel<false, true, kHg> : mqa_fp4_kernel<false, false, kHg>);
+        constexpr bool kOne = decltype(one)::value;
+        return x.idx ? (wide ? mqa_fp4_kernel<true, true, kHg, kOne> : mqa_fp4_kernel<true, false, kHg, kOne>)
+                     : (wide ? mqa_fp4_kernel<false, true, kHg, kOne> : mqa_fp4_kernel<false, false, kHg, kOne>);
     };
-    auto kern = hg == 16 ? of(std::integral_constant<int, 16>()) : of(std::integral_constant<int, 64>());
+    auto by_heads = [&](auto one) {
+        return hg == 16 ? of(std::integral_constant<int, 16>(), one) : of(std::integral_constant<int, 64>(), one);
+    };
+    auto kern = a.merge == kDirect ? by_heads(std::true_type()) : by_heads(std::false_type());
     cudaError_t e = smem_ceiling(kern);
     if (e != cudaSuccess) return e;
     CSA_LAUNCH(st, "mqa_fp4",
-               e = launch_pdl(kern, dim3(ns, plan.groups, x.nq), dim3(kThreads), smem, st,
+               e = launch_pdl(kern, a.merge == kDirect ? dim3(a.items < 148 ? a.items : 148) : dim3(ns, plan.groups, x.nq),
+                              dim3(kThreads), smem, st,
                               a.merge == kCluster ? (unsigned)ns : 0u, a, tmQ));
     if (e != cudaSuccess) return e;
     if (a.merge == kWorkspace) {

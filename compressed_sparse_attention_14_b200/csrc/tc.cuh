@@ -84,9 +84,6 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 // waits until every committed bulk store has completed (writes performed)
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// waits until every committed bulk store has read its source
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-
 // ---------------------------------------------------------------- cluster
 // The shared::cluster address of a shared::cta address in CTA `rank` of
 // this cluster.

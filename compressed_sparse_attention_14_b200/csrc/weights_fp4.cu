@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
         }
         __syncwarp();
     } else if (warp >= 4) {
-        produce<ProducerOf<kSparse, kWide>>(a, s, kv_s, warp - 4, b, e_beg, e_end, ntiles, (int64_t)(ntiles ? seq : 0) * a.Nmax, [] {});
+        ProducerOf<kSparse, kWide> producer(a, s, kv_s, warp - 4);
+        produce(producer, warp - 4, 0, b, e_beg, e_end, ntiles, (int64_t)(ntiles ? seq : 0) * a.Nmax, [] {});
     } else {
         // ------------------------------------------------------------ sums
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
