@@ -64,7 +64,10 @@ struct Blocks {
     }
 };
 
-template <bool kSparse, bool kWide>
+// kStay: one query block a sequence, whose queries stay in shared memory (its
+// own instantiation: with loops over queries around them the products are issued
+// half as fast).
+template <bool kSparse, bool kWide, bool kStay>
 __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __grid_constant__ Args a,
                                                                         const __grid_constant__ CUtensorMap tmQ) {
     extern __shared__ uint8_t smem_raw[];
@@ -105,25 +108,32 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
     }
     __syncthreads();
     // the last entry that any query sees
+    int n_max = 0;
     if (seq >= 0 && seq < a.n_seq) {
-        int n = 0;
-        for (int t = tid; t < a.T; t += kThreads) n = max(n, blocks.visible(t));
-        n = __reduce_max_sync(0xffffffffu, n);
-        if (lane == 0 && n > 0) atomicMax(&s.n_max, n);
+        if (kStay) {
+            n_max = blocks.visible(0);
+        } else {
+            int n = 0;
+            for (int t = tid; t < a.T; t += kThreads) n = max(n, blocks.visible(t));
+            n = __reduce_max_sync(0xffffffffu, n);
+            if (lane == 0 && n > 0) atomicMax(&s.n_max, n);
+        }
     }
-    __syncthreads();
+    if (!kStay) {
+        __syncthreads();
+        n_max = s.n_max;
+    }
     tc::tc_fence_after();
-    const int e_end = s.n_max < e_stop ? s.n_max : e_stop;
+    const int e_end = n_max < e_stop ? n_max : e_stop;
     const int ntiles = e_end > e_beg ? (e_end - e_beg + kE - 1) / kE : 0;
     const uint32_t tmem_S = __shfl_sync(0xffffffffu, s.tmem, 0);
-    const bool stay = a.T * a.hgroups == 1;
 
     if (warp == 21) {
         // ------------------------------------------------------------ query loads
         if (lane == 0) {
             uint32_t n = 0;
             bool ok = true;
-            for (int j = 0; ok && j < (stay ? (ntiles > 0 ? 1 : 0) : ntiles); ++j) {
+            for (int j = 0; ok && j < (kStay ? (ntiles > 0 ? 1 : 0) : ntiles); ++j) {
                 const int e_tile = e_beg + j * kE;
                 for (int t = 0; ok && t <= blocks.last_query(e_tile); ++t) {
                     if (blocks.visible(t) <= e_tile) continue;
@@ -151,33 +161,37 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
             auto until = [&](uint64_t* bar, uint32_t parity) {
                 return __all_sync(0xffffffffu, wait(bar, parity, s, a.status));
             };
-            const int per_query = a.hgroups;
-            uint32_t n = 0;
             bool ok = true;
-            for (int j = 0; ok && j < ntiles; ++j) {
-                const int e_tile = e_beg + j * kE, last = blocks.last_query(e_tile), buf = j & 1;
-                for (int tg = 0; ok && tg < (last + 1) * per_query; ++tg) {
-                    if (blocks.visible(tg / per_query) <= e_tile) continue;
-                    const uint32_t sb = n & 1;
-                    if (n >= 2) ok = until(&s.s_empty[sb], ((n >> 1) - 1) & 1);
-                    for (int h = a.halves() - 1; h >= 0 && (ok = ok && until(&s.q_full[h], stay ? 0 : n & 1) &&
-                                                                   until(&s.full[buf][h], (j >> 1) & 1)); --h) {
-                        tc::tc_fence_after();
-                        for (int i = 0; i < a.blocks(h) / 2; ++i)
+            // S of tile j (the n-th of all) and the query block in shared memory
+            auto product = [&](int j, uint32_t n, bool last) {
+                const int buf = j & 1, sb = n & 1;
+                if (n >= 2) ok = until(&s.s_empty[sb], ((n >> 1) - 1) & 1);
+                for (int h = a.halves() - 1; h >= 0 && (ok = ok && until(&s.q_full[h], kStay ? 0 : n & 1) &&
+                                                               until(&s.full[buf][h], (j >> 1) & 1)); --h) {
+                    tc::tc_fence_after();
+                    for (int i = 0; i < a.blocks(h) / 2; ++i)
 #pragma unroll
-                            for (int kk = 0; kk < 8; ++kk) {
-                                const int blk = 4 * h + 2 * i + (kk >> 2);
-                                tc::umma_bf16_warp(
-                                    tmem_S + sb * kHg,
-                                    tc::sdesc_sw128(kv_addr + buf * tile_bytes + blk * kBlockBytes + (kk & 3) * 32, 16, 1024),
-                                    tc::sdesc_sw128(q_addr + blk * (kHg * 128) + (kk & 3) * 32, 16, 1024), idesc,
-                                    (h < a.halves() - 1 || i || kk) ? 1u : 0u);
-                            }
-                        if (!stay) tc::umma_commit_warp(&s.q_empty[h]);
-                        if (tg == (last + 1) * per_query - 1) tc::umma_commit_warp(&s.empty[buf][h]);
-                    }
-                    if (ok) tc::umma_commit_warp(&s.s_full[sb]);
-                    ++n;
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const int blk = 4 * h + 2 * i + (kk >> 2);
+                            tc::umma_bf16_warp(
+                                tmem_S + sb * kHg,
+                                tc::sdesc_sw128(kv_addr + buf * tile_bytes + blk * kBlockBytes + (kk & 3) * 32, 16, 1024),
+                                tc::sdesc_sw128(q_addr + blk * (kHg * 128) + (kk & 3) * 32, 16, 1024), idesc,
+                                (h < a.halves() - 1 || i || kk) ? 1u : 0u);
+                        }
+                    if (!kStay) tc::umma_commit_warp(&s.q_empty[h]);
+                    if (last) tc::umma_commit_warp(&s.empty[buf][h]);
+                }
+                if (ok) tc::umma_commit_warp(&s.s_full[sb]);
+            };
+            if (kStay) {
+                for (int j = 0; ok && j < ntiles; ++j) product(j, j, true);
+            } else {
+                uint32_t n = 0;
+                for (int j = 0; ok && j < ntiles; ++j) {
+                    const int e_tile = e_beg + j * kE, blocks_all = (blocks.last_query(e_tile) + 1) * a.hgroups;
+                    for (int tg = 0; ok && tg < blocks_all; ++tg)
+                        if (blocks.visible(tg / a.hgroups) > e_tile) product(j, n++, tg == blocks_all - 1);
                 }
             }
             tc::umma_commit_warp(&s.fin);
@@ -307,8 +321,12 @@ cudaError_t entry_weights_fp4(const Fp4WeightArgs& x, cudaStream_t st) {
     if (!make_tmap_bf16_2d(&tmQ, x.T > 0 ? x.q : x.kv4, rows, x.c, x.c, kHg, 64)) return cudaErrorInvalidValue;
     const size_t smem = 1024 + (size_t)a.dblocks * (2 * kBlockBytes + kHg * 128) + sizeof(Shared);
     const bool wide = wide_rows(a.f, x.kv4);
-    auto kern = x.idx ? (wide ? entry_weights_fp4_kernel<true, true> : entry_weights_fp4_kernel<true, false>)
-                      : (wide ? entry_weights_fp4_kernel<false, true> : entry_weights_fp4_kernel<false, false>);
+    auto of = [&](auto stay) {
+        constexpr bool kStay = decltype(stay)::value;
+        return x.idx ? (wide ? entry_weights_fp4_kernel<true, true, kStay> : entry_weights_fp4_kernel<true, false, kStay>)
+                     : (wide ? entry_weights_fp4_kernel<false, true, kStay> : entry_weights_fp4_kernel<false, false, kStay>);
+    };
+    auto kern = x.T * a.hgroups == 1 ? of(std::true_type()) : of(std::false_type());
     cudaError_t e = smem_ceiling(kern);
     if (e != cudaSuccess) return e;
     CSA_LAUNCH(st, "entry_weights_fp4",
