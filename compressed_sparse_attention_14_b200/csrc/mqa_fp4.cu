@@ -3,11 +3,14 @@
 //
 //   z_s = scale * q . v_s,  out = sum_s e^{z_s} v_s / (sum_s e^{z_s} [+ e^{sink}])
 //
-// One CTA serves (query, 64 or 16 heads, one split of the query's entries)
-// and walks the split in tiles of 64 entries. Producer warps read the packed
-// rows, expand them to bf16 (exact) and store the tile in shared memory, where
-// ONE copy of it (64-dim blocks, 128-byte swizzle) feeds both products, key
-// and value being the same row:
+// An item of work is (query, 64 or 16 heads, one split of the query's entries).
+// Queries that are split have a CTA per item; where there are enough queries
+// not to split them, a CTA per SM takes every 148th item, and the next item's
+// tiles are expanded while the last one's output is written (3001 queries: 446
+// us with a CTA per item, 390 so). A CTA walks its entries in tiles of 64.
+// Producer warps read the packed rows, expand them to bf16 (exact) and store
+// the tile in shared memory, where ONE copy of it (64-dim blocks, 128-byte
+// swizzle) feeds both products, key and value being the same row:
 //   S^T  = V_tile . q^T         M = 64 entries, N = heads, K = c
 //   O^T += V_tile^T . P^T       M = 128 dims,   N = heads, K = 64 entries
 // S^T and O^T live in tensor memory. The softmax keeps a reference maximum per
@@ -33,8 +36,8 @@
 // tiles only: 7% slower. The products alone take 2050 cycles a tile (M = 64, N =
 // 64: 40 cycles each, M = 128: 48, the shared memory's rate), and reading,
 // storing and multiplying through shared memory 2300.
-// 3001 queries x 64 heads over 512 entries: 446 us (297 TFLOP/s, 18% of the
-// dense rate measured on this part); 16 sequences of 8192 entries 44 us.
+// 3001 queries x 64 heads over 512 entries: 390 us (340 TFLOP/s, 21% of the
+// dense rate measured on this part); 16 sequences of 8192 entries 43 us.
 //
 // Entries outside the query's set are stored as zeros and get weight 0: no
 // row that the query does not see is read.
@@ -332,280 +335,280 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         bool ok = true;
         int before = 0;                                   // tiles of the items before
         for (int it = it0; ok && it < it_end; it += it_step) {
-        const Item x = item(it);
-        const int t = x.t, h0 = x.h0, ntiles = x.ntiles;
-        if (hth < kHalf) {
-            s.mref[hb + hth] = s.limit[hb + hth] = -INFINITY;
-            s.mexp[hb + hth] = 0.f;
-        }
-        float lpart[2 * kOct];                            // heads hb + 8u + 2 q4 + (0, 1), both entries
-#pragma unroll
-        for (int i = 0; i < 2 * kOct; ++i) lpart[i] = 0.f;
-        if (it == it0) setup_done();
-        else half_sync(half);
-        for (int n = 0; n < ntiles; ++n) {
-            const int j = before + n, b = j & 1;
-            auto seen = [&](int row) {
-                const int64_t e = x.e_beg + (int64_t)n * kE + row;
-                if (e >= x.e_end) return false;
-                if (!kSparse) return true;
-                const int v = __ldg(a.idx + (int64_t)t * a.k + e);
-                return v >= 0 && v < a.Nmax;
-            };
-            const bool va = seen(ra), vb = seen(rb);
-            ok = ok && wait(&s.s_full[b], (j >> 1) & 1, s, a.status);
-            tc::tc_fence_after();
-            float z[4 * kOct];
-            auto logits = [&]() {
-                tc::tmem_ld_16(tmem_S + lanes + b * kHg + hb, z);
-                tc::tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 4 * kOct; ++i) z[i] = (i & 2 ? vb : va) ? z[i] * a.scale_log2 : -INFINITY;
-            };
-            logits();
-            bool move = false;
-#pragma unroll
-            for (int u = 0; u < kOct; ++u) {
-                const float2 lim = *reinterpret_cast<const float2*>(&s.limit[hb + 8 * u + 2 * q4]);
-                move |= z[4 * u] > lim.x || z[4 * u + 2] > lim.x || z[4 * u + 1] > lim.y || z[4 * u + 3] > lim.y;
+            const Item x = item(it);
+            const int t = x.t, h0 = x.h0, ntiles = x.ntiles;
+            if (hth < kHalf) {
+                s.mref[hb + hth] = s.limit[hb + hth] = -INFINITY;
+                s.mexp[hb + hth] = 0.f;
             }
-            if (half_any(half, move || !ok)) {
-                // all leave together once a wait of one ran out
-                if (half_any(half, !ok)) { ok = false; break; }
+            float lpart[2 * kOct];                            // heads hb + 8u + 2 q4 + (0, 1), both entries
 #pragma unroll
-                for (int i = 0; i < 2 * kOct; ++i) {
-                    const int u = i >> 1, e = i & 1;
-                    const float top = rows_reduce(fmaxf(z[4 * u + e], z[4 * u + 2 + e]),
-                                                  [](float x, float y) { return fmaxf(x, y); });
-                    if (lane < 4) s.red[quad][hb + 8 * u + 2 * lane + e] = top;
-                }
-                half_sync(half);
-                if (hth < kHalf) {
-                    const int h = hb + hth;
-                    const float old = s.mref[h];
-                    const float m = fmaxf(fmaxf(fmaxf(s.red[0][h], s.red[1][h]), fmaxf(s.red[2][h], s.red[3][h])), old);
-                    s.alpha[h] = old == -INFINITY ? 0.f : ex2(old - m);
-                    s.mref[h] = m;
-                    s.limit[h] = m + kMoveLog2;
-                    s.mexp[h] = m == -INFINITY ? 0.f : m;
-                }
-                half_sync(half);
+            for (int i = 0; i < 2 * kOct; ++i) lpart[i] = 0.f;
+            if (it == it0) setup_done();
+            else half_sync(half);
+            for (int n = 0; n < ntiles; ++n) {
+                const int j = before + n, b = j & 1;
+                auto seen = [&](int row) {
+                    const int64_t e = x.e_beg + (int64_t)n * kE + row;
+                    if (e >= x.e_end) return false;
+                    if (!kSparse) return true;
+                    const int v = __ldg(a.idx + (int64_t)t * a.k + e);
+                    return v >= 0 && v < a.Nmax;
+                };
+                const bool va = seen(ra), vb = seen(rb);
+                ok = ok && wait(&s.s_full[b], (j >> 1) & 1, s, a.status);
+                tc::tc_fence_after();
+                float z[4 * kOct];
+                auto logits = [&]() {
+                    tc::tmem_ld_16(tmem_S + lanes + b * kHg + hb, z);
+                    tc::tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 2 * kOct; ++i) lpart[i] *= s.alpha[hb + 8 * (i >> 1) + 2 * q4 + (i & 1)];
-                if (n > 0) {
-                    // rescale O^T (every product before this tile's has ended)
-                    ok = wait(&s.empty[b ^ 1][0], ((j - 1) >> 1) & 1, s, a.status);
-                    tc::tc_fence_after();
+                    for (int i = 0; i < 4 * kOct; ++i) z[i] = (i & 2 ? vb : va) ? z[i] * a.scale_log2 : -INFINITY;
+                };
+                logits();
+                bool move = false;
+#pragma unroll
+                for (int u = 0; u < kOct; ++u) {
+                    const float2 lim = *reinterpret_cast<const float2*>(&s.limit[hb + 8 * u + 2 * q4]);
+                    move |= z[4 * u] > lim.x || z[4 * u + 2] > lim.x || z[4 * u + 1] > lim.y || z[4 * u + 3] > lim.y;
+                }
+                if (half_any(half, move || !ok)) {
+                    // all leave together once a wait of one ran out
+                    if (half_any(half, !ok)) { ok = false; break; }
+#pragma unroll
+                    for (int i = 0; i < 2 * kOct; ++i) {
+                        const int u = i >> 1, e = i & 1;
+                        const float top = rows_reduce(fmaxf(z[4 * u + e], z[4 * u + 2 + e]),
+                                                      [](float x, float y) { return fmaxf(x, y); });
+                        if (lane < 4) s.red[quad][hb + 8 * u + 2 * lane + e] = top;
+                    }
+                    half_sync(half);
+                    if (hth < kHalf) {
+                        const int h = hb + hth;
+                        const float old = s.mref[h];
+                        const float m = fmaxf(fmaxf(fmaxf(s.red[0][h], s.red[1][h]), fmaxf(s.red[2][h], s.red[3][h])), old);
+                        s.alpha[h] = old == -INFINITY ? 0.f : ex2(old - m);
+                        s.mref[h] = m;
+                        s.limit[h] = m + kMoveLog2;
+                        s.mexp[h] = m == -INFINITY ? 0.f : m;
+                    }
+                    half_sync(half);
+#pragma unroll
+                    for (int i = 0; i < 2 * kOct; ++i) lpart[i] *= s.alpha[hb + 8 * (i >> 1) + 2 * q4 + (i & 1)];
+                    if (n > 0) {
+                        // rescale O^T (every product before this tile's has ended)
+                        ok = wait(&s.empty[b ^ 1][0], ((j - 1) >> 1) & 1, s, a.status);
+                        tc::tc_fence_after();
 #pragma unroll 1
-                    for (int m = 0; m < 4 * a.mtiles; ++m) {
-                        const int cc = hb + 8 * (m & 3);
-                        if (cc >= hb + kHalf) continue;
-                        float o[8];
-                        tc::tmem_ld8(tmem_O + lanes + (m >> 2) * kHg + cc, o);
-                        tc::tmem_ld_wait();
+                        for (int m = 0; m < 4 * a.mtiles; ++m) {
+                            const int cc = hb + 8 * (m & 3);
+                            if (cc >= hb + kHalf) continue;
+                            float o[8];
+                            tc::tmem_ld8(tmem_O + lanes + (m >> 2) * kHg + cc, o);
+                            tc::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] *= s.alpha[cc + i];
-                        tc::tmem_st8(tmem_O + lanes + (m >> 2) * kHg + cc, o);
+                            for (int i = 0; i < 8; ++i) o[i] *= s.alpha[cc + i];
+                            tc::tmem_st8(tmem_O + lanes + (m >> 2) * kHg + cc, o);
+                        }
+                        tc::tmem_st_wait();
                     }
-                    tc::tmem_st_wait();
                 }
-            }
-            // (this tile's S product came after its buffer was free, so the O
-            // product of the tile before last has read this P)
-            uint8_t* p_b = p_s + b * (kE * 128);
+                // (this tile's S product came after its buffer was free, so the O
+                // product of the tile before last has read this P)
+                uint8_t* p_b = p_s + b * (kE * 128);
 #pragma unroll
-            for (int u = 0; u < kOct; ++u) {
-                const float2 m = *reinterpret_cast<const float2*>(&s.mexp[hb + 8 * u + 2 * q4]);
-                const float p0 = ex2(z[4 * u] - m.x), p1 = ex2(z[4 * u + 1] - m.y);
-                const float p2 = ex2(z[4 * u + 2] - m.x), p3 = ex2(z[4 * u + 3] - m.y);
-                lpart[2 * u] += p0 + p2;
-                lpart[2 * u + 1] += p1 + p3;
-                const __nv_bfloat162 x = __floats2bfloat162_rn(p0, p1), y = __floats2bfloat162_rn(p2, p3);
-                const int piece = ((hb >> 3) + u) ^ (ra & 7);             // (rb & 7 is the same)
-                *reinterpret_cast<__nv_bfloat162*>(p_b + ra * 128 + piece * 16 + q4 * 4) = x;
-                *reinterpret_cast<__nv_bfloat162*>(p_b + rb * 128 + piece * 16 + q4 * 4) = y;
+                for (int u = 0; u < kOct; ++u) {
+                    const float2 m = *reinterpret_cast<const float2*>(&s.mexp[hb + 8 * u + 2 * q4]);
+                    const float p0 = ex2(z[4 * u] - m.x), p1 = ex2(z[4 * u + 1] - m.y);
+                    const float p2 = ex2(z[4 * u + 2] - m.x), p3 = ex2(z[4 * u + 3] - m.y);
+                    lpart[2 * u] += p0 + p2;
+                    lpart[2 * u + 1] += p1 + p3;
+                    const __nv_bfloat162 x = __floats2bfloat162_rn(p0, p1), y = __floats2bfloat162_rn(p2, p3);
+                    const int piece = ((hb >> 3) + u) ^ (ra & 7);             // (rb & 7 is the same)
+                    *reinterpret_cast<__nv_bfloat162*>(p_b + ra * 128 + piece * 16 + q4 * 4) = x;
+                    *reinterpret_cast<__nv_bfloat162*>(p_b + rb * 128 + piece * 16 + q4 * 4) = y;
+                }
+                tc::tc_fence_before();                        // S has been read, too
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&s.p_full[b]);
             }
-            tc::tc_fence_before();                        // S has been read, too
-            tc::fence_proxy_async_smem();
+            before += ntiles;
+            if (ok && ntiles > 0) ok = wait(&s.empty[(before - 1) & 1][0], ((before - 1) >> 1) & 1, s, a.status);
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&s.p_full[b]);
-        }
-        before += ntiles;
-        if (ok && ntiles > 0) ok = wait(&s.empty[(before - 1) & 1][0], ((before - 1) >> 1) & 1, s, a.status);
-        __syncwarp();
-        // per-head sums in a fixed order: entries, lanes, then the four warps
-        half_sync(half);                                  // red may still be read
+            // per-head sums in a fixed order: entries, lanes, then the four warps
+            half_sync(half);                                  // red may still be read
 #pragma unroll
-        for (int i = 0; i < 2 * kOct; ++i) {
-            const float sum = rows_reduce(lpart[i], [](float x, float y) { return x + y; });
-            if (lane < 4) s.red[quad][hb + 8 * (i >> 1) + 2 * lane + (i & 1)] = sum;
-        }
-        half_sync(half);
-        if (hth < kHalf) {
-            const int h = hb + hth;
-            s.lsum[h] = (s.red[0][h] + s.red[1][h]) + (s.red[2][h] + s.red[3][h]);
-            if (kOne) {
-                const float m = s.mref[h], L = s.lsum[h];
-                const float sk = a.sink && h0 + h < a.H ? a.sink[h0 + h] * kLog2e : -INFINITY;
-                const float M = fmaxf(m, sk);
-                // (a sum of NaNs has no finite reference: it stays NaN)
-                const float w = L == 0.f ? 0.f : L != L ? L : ex2(m - M);
-                const float Lt = L * w + (sk == -INFINITY ? 0.f : ex2(sk - M));
-                s.alpha[h] = L == 0.f ? 0.f : w / Lt;
-                if (a.lse && h0 + h < a.H)
-                    a.lse[(int64_t)t * a.H + h0 + h] = Lt == 0.f ? -INFINITY : fmaf(M, kLn2, logf(Lt));
+            for (int i = 0; i < 2 * kOct; ++i) {
+                const float sum = rows_reduce(lpart[i], [](float x, float y) { return x + y; });
+                if (lane < 4) s.red[quad][hb + 8 * (i >> 1) + 2 * lane + (i & 1)] = sum;
             }
-        }
-        if (kOne) {
-            // O^T normalised and written out as bf16, 8 heads x 32 dims at a time:
-            // a transposing matrix store to the warp's part of P's place, then 16
-            // bytes per lane to a head's row
-            ok = !softmax_any(!ok);                       // (also: the sums are known)
-            tc::tc_fence_after();
-            uint8_t* stage = p_s + warp * 1024;
-            bf16* out = a.out + ((int64_t)t * a.H + h0) * a.f.c + quad * 32 + (lane & 3) * 8;
-#pragma unroll 2
-            for (int r = 0; r < kHg / 8; ++r) {
-                const float2 al = *reinterpret_cast<const float2*>(&s.alpha[8 * r + 2 * q4]);
-                const int h = 8 * r + (lane >> 2);
-                for (int mt = half; mt < a.mtiles; mt += 2) {
-                    float o[2][4] = {};
-                    if (ntiles > 0) {
-                        tc::tmem_ld_16(tmem_O + lanes + mt * kHg + 8 * r, o[0]);
-                        tc::tmem_ld_16(tmem_O + lanes + (16u << 16) + mt * kHg + 8 * r, o[1]);
-                        tc::tmem_ld_wait();
-                    }
-                    uint32_t m[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {         // dims 8i .. 8i + 7 of this warp's 32
-                        const __nv_bfloat162 v = __floats2bfloat162_rn(al.x != 0.f ? o[i >> 1][2 * (i & 1)] * al.x : 0.f,
-                                                                       al.y != 0.f ? o[i >> 1][2 * (i & 1) + 1] * al.y : 0.f);
-                        m[i] = *reinterpret_cast<const uint32_t*>(&v);
-                    }
-                    // (two places in turn; rows of 64 bytes, their 16-byte pieces
-                    // turned so that 8 lanes use different banks)
-                    uint8_t* at = stage + (mt >> 1 & 1) * 512;
-                    const int row = lane & 7, piece = lane >> 3;
-                    stmatrix_trans4(tc::smem_u32(at) + row * 64 + ((piece ^ (row >> 1)) & 3) * 16, m);
-                    __syncwarp();
-                    const uint4 v = *reinterpret_cast<const uint4*>(at + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 3)) & 3) * 16);
-                    if (h0 + h < a.H) *reinterpret_cast<uint4*>(out + (int64_t)h * a.f.c + mt * 128) = v;
-                    __syncwarp();
+            half_sync(half);
+            if (hth < kHalf) {
+                const int h = hb + hth;
+                s.lsum[h] = (s.red[0][h] + s.red[1][h]) + (s.red[2][h] + s.red[3][h]);
+                if (kOne) {
+                    const float m = s.mref[h], L = s.lsum[h];
+                    const float sk = a.sink && h0 + h < a.H ? a.sink[h0 + h] * kLog2e : -INFINITY;
+                    const float M = fmaxf(m, sk);
+                    // (a sum of NaNs has no finite reference: it stays NaN)
+                    const float w = L == 0.f ? 0.f : L != L ? L : ex2(m - M);
+                    const float Lt = L * w + (sk == -INFINITY ? 0.f : ex2(sk - M));
+                    s.alpha[h] = L == 0.f ? 0.f : w / Lt;
+                    if (a.lse && h0 + h < a.H)
+                        a.lse[(int64_t)t * a.H + h0 + h] = Lt == 0.f ? -INFINITY : fmaf(M, kLn2, logf(Lt));
                 }
             }
-            tc::tc_fence_before();
-            softmax_any(false);                           // P's place and the maxima may be written
-        }
+            if (kOne) {
+                // O^T normalised and written out as bf16, 8 heads x 32 dims at a time:
+                // a transposing matrix store to the warp's part of P's place, then 16
+                // bytes per lane to a head's row
+                ok = !softmax_any(!ok);                       // (also: the sums are known)
+                tc::tc_fence_after();
+                uint8_t* stage = p_s + warp * 1024;
+                bf16* out = a.out + ((int64_t)t * a.H + h0) * a.f.c + quad * 32 + (lane & 3) * 8;
+#pragma unroll 2
+                for (int r = 0; r < kHg / 8; ++r) {
+                    const float2 al = *reinterpret_cast<const float2*>(&s.alpha[8 * r + 2 * q4]);
+                    const int h = 8 * r + (lane >> 2);
+                    for (int mt = half; mt < a.mtiles; mt += 2) {
+                        float o[2][4] = {};
+                        if (ntiles > 0) {
+                            tc::tmem_ld_16(tmem_O + lanes + mt * kHg + 8 * r, o[0]);
+                            tc::tmem_ld_16(tmem_O + lanes + (16u << 16) + mt * kHg + 8 * r, o[1]);
+                            tc::tmem_ld_wait();
+                        }
+                        uint32_t m[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {         // dims 8i .. 8i + 7 of this warp's 32
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(al.x != 0.f ? o[i >> 1][2 * (i & 1)] * al.x : 0.f,
+                                                                           al.y != 0.f ? o[i >> 1][2 * (i & 1) + 1] * al.y : 0.f);
+                            m[i] = *reinterpret_cast<const uint32_t*>(&v);
+                        }
+                        // (two places in turn; rows of 64 bytes, their 16-byte pieces
+                        // turned so that 8 lanes use different banks)
+                        uint8_t* at = stage + (mt >> 1 & 1) * 512;
+                        const int row = lane & 7, piece = lane >> 3;
+                        stmatrix_trans4(tc::smem_u32(at) + row * 64 + ((piece ^ (row >> 1)) & 3) * 16, m);
+                        __syncwarp();
+                        const uint4 v = *reinterpret_cast<const uint4*>(at + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 3)) & 3) * 16);
+                        if (h0 + h < a.H) *reinterpret_cast<uint4*>(out + (int64_t)h * a.f.c + mt * 128) = v;
+                        __syncwarp();
+                    }
+                }
+                tc::tc_fence_before();
+                softmax_any(false);                           // P's place and the maxima may be written
+            }
         }
         tc::tc_fence_before();
     }
     // ---------------------------------------------------------------- merge
     __syncthreads();
     if (!kOne) {
-    const Item x = first;
-    const int t = x.t, h0 = x.h0, split = x.split, ntiles = x.ntiles;
-    const int nh = a.H - h0 < kHg ? a.H - h0 : kHg, c4 = a.f.c / 4;
-    bf16* out = a.out + ((int64_t)t * a.H + h0) * a.f.c;   // this CTA's heads: contiguous rows
-    const int64_t part = ((int64_t)t * a.nsplit + split) * a.H + h0;
-    if (warp < 16 && ntiles > 0) {
-        // fp32: to the workspace, or (a cluster) to shared memory where the tiles
-        // were, as rows of a head. Warp w has dims 32 (w % 4).. of M tiles mt0, mt0
-        // + step, .. and 16 heads, a lane one dim
-        constexpr int kStep = 4 / kOct;
-        const int quad = warp & 3, hb = (warp >> 2) % kOct * 16, mt0 = (warp >> 2) / kOct;
-        const uint32_t addr = tmem_O + ((uint32_t)(quad * 32) << 16) + hb;
-        tc::tc_fence_after();
-        const int heads = nh - hb;
+        const Item x = first;
+        const int t = x.t, h0 = x.h0, split = x.split, ntiles = x.ntiles;
+        const int nh = a.H - h0 < kHg ? a.H - h0 : kHg, c4 = a.f.c / 4;
+        bf16* out = a.out + ((int64_t)t * a.H + h0) * a.f.c;   // this CTA's heads: contiguous rows
+        const int64_t part = ((int64_t)t * a.nsplit + split) * a.H + h0;
+        if (warp < 16 && ntiles > 0) {
+            // fp32: to the workspace, or (a cluster) to shared memory where the tiles
+            // were, as rows of a head. Warp w has dims 32 (w % 4).. of M tiles mt0, mt0
+            // + step, .. and 16 heads, a lane one dim
+            constexpr int kStep = 4 / kOct;
+            const int quad = warp & 3, hb = (warp >> 2) % kOct * 16, mt0 = (warp >> 2) / kOct;
+            const uint32_t addr = tmem_O + ((uint32_t)(quad * 32) << 16) + hb;
+            tc::tc_fence_after();
+            const int heads = nh - hb;
 #pragma unroll 1
-        for (int mt = mt0; mt < a.mtiles; mt += kStep) {
-            const int64_t at = hb * a.f.c + mt * 128 + quad * 32 + lane;
-            float o[16];
-            tc::tmem_ld16(addr + mt * kHg, o);
-            tc::tmem_ld_wait();
-            if (a.merge == kCluster) {
-                float* dst = reinterpret_cast<float*>(kv_s) + at;
+            for (int mt = mt0; mt < a.mtiles; mt += kStep) {
+                const int64_t at = hb * a.f.c + mt * 128 + quad * 32 + lane;
+                float o[16];
+                tc::tmem_ld16(addr + mt * kHg, o);
+                tc::tmem_ld_wait();
+                if (a.merge == kCluster) {
+                    float* dst = reinterpret_cast<float*>(kv_s) + at;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) dst[i * a.f.c] = o[i];
-            } else {
-                float* dst = a.part_o + part * a.f.c + at;
+                    for (int i = 0; i < 16; ++i) dst[i * a.f.c] = o[i];
+                } else {
+                    float* dst = a.part_o + part * a.f.c + at;
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (i < heads) dst[i * a.f.c] = o[i];
-            }
-        }
-        tc::tc_fence_before();
-    }
-
-    if (a.merge == kCluster) {
-        // two splits send each other the half of their sums that the other
-        // writes out, one bulk copy to where its queries were (64 sequences x
-        // 512 entries: 21.2 us a call when it came, 21.6 with loads from the
-        // peer); more read their peers' in place.
-        const int items = nh * c4, lo = (int)((int64_t)items * split / a.nsplit);
-        const int hi = (int)((int64_t)items * (split + 1) / a.nsplit);
-        const bool two = a.nsplit == 2 && items % 2 == 0;
-        if (two && tid == 0) tc::mbar_expect_tx(&s.peer, (uint32_t)(items / 2) * 16);
-        tc::fence_proxy_async_smem();
-        tc::cluster_sync();                               // every split has staged its sums
-        if (two && tid == 0)
-            tc::bulk_copy_to_peer(tc::mapa(tc::smem_u32(q_s), split ^ 1), kv_s + (split ? 0 : (size_t)(items / 2) * 16),
-                                  (uint32_t)(items / 2) * 16, tc::mapa(tc::smem_u32(&s.peer), split ^ 1));
-        if (tid < kHg) {
-            const float sk = a.sink && h0 + tid < a.H ? a.sink[h0 + tid] * kLog2e : -INFINITY;
-            float m[kMaxCluster], L[kMaxCluster], M = sk;
-#pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r) {
-                m[r] = -INFINITY;
-                L[r] = 0.f;
-                if (r < a.nsplit) {
-                    m[r] = tc::ld_cluster_f32(tc::mapa(tc::smem_u32(s.mref + tid), r));
-                    L[r] = tc::ld_cluster_f32(tc::mapa(tc::smem_u32(s.lsum + tid), r));
+                    for (int i = 0; i < 16; ++i)
+                        if (i < heads) dst[i * a.f.c] = o[i];
                 }
-                if (L[r] != 0.f) M = fmaxf(M, m[r]);
             }
-            float Lt = sk == -INFINITY ? 0.f : ex2(sk - M);
-#pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r) {
-                m[r] = L[r] == 0.f ? 0.f : L[r] != L[r] ? L[r] : ex2(m[r] - M);
-                Lt = fmaf(L[r], m[r], Lt);
-            }
-            const float inv = Lt == 0.f ? 0.f : 1.f / Lt;
-#pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r) s.coef[r][tid] = m[r] * inv;
-            if (split == 0 && a.lse && h0 + tid < a.H)
-                a.lse[(int64_t)t * a.H + h0 + tid] = Lt == 0.f ? -INFINITY : fmaf(M, kLn2, logf(Lt));
+            tc::tc_fence_before();
         }
-        __syncthreads();
-        // this split's share of the (head, 4 dims) items, all splits' sums in
-        // split order
-        if (two) {
-            wait(&s.peer, 0, s, a.status);
-            const float4* mine = reinterpret_cast<const float4*>(kv_s) + lo;
-            const float4* theirs = reinterpret_cast<const float4*>(q_s);
-            for (int i = tid; i < hi - lo; i += kThreads) {
-                const int h = (lo + i) / c4;
-                const float4 x = mine[i], y = theirs[i];
-                const float w0 = s.coef[split][h], w1 = s.coef[split ^ 1][h];
-                // (a split without entries has staged nothing)
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (w0 != 0.f) acc = make_float4(w0 * x.x, w0 * x.y, w0 * x.z, w0 * x.w);
-                if (w1 != 0.f) acc = make_float4(fmaf(w1, y.x, acc.x), fmaf(w1, y.y, acc.y), fmaf(w1, y.z, acc.z), fmaf(w1, y.w, acc.w));
-                store4(out + (int64_t)(lo + i) * 4, acc.x, acc.y, acc.z, acc.w);
+
+        if (a.merge == kCluster) {
+            // two splits send each other the half of their sums that the other
+            // writes out, one bulk copy to where its queries were (64 sequences x
+            // 512 entries: 21.2 us a call when it came, 21.6 with loads from the
+            // peer); more read their peers' in place.
+            const int items = nh * c4, lo = (int)((int64_t)items * split / a.nsplit);
+            const int hi = (int)((int64_t)items * (split + 1) / a.nsplit);
+            const bool two = a.nsplit == 2 && items % 2 == 0;
+            if (two && tid == 0) tc::mbar_expect_tx(&s.peer, (uint32_t)(items / 2) * 16);
+            tc::fence_proxy_async_smem();
+            tc::cluster_sync();                               // every split has staged its sums
+            if (two && tid == 0)
+                tc::bulk_copy_to_peer(tc::mapa(tc::smem_u32(q_s), split ^ 1), kv_s + (split ? 0 : (size_t)(items / 2) * 16),
+                                      (uint32_t)(items / 2) * 16, tc::mapa(tc::smem_u32(&s.peer), split ^ 1));
+            if (tid < kHg) {
+                const float sk = a.sink && h0 + tid < a.H ? a.sink[h0 + tid] * kLog2e : -INFINITY;
+                float m[kMaxCluster], L[kMaxCluster], M = sk;
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r) {
+                    m[r] = -INFINITY;
+                    L[r] = 0.f;
+                    if (r < a.nsplit) {
+                        m[r] = tc::ld_cluster_f32(tc::mapa(tc::smem_u32(s.mref + tid), r));
+                        L[r] = tc::ld_cluster_f32(tc::mapa(tc::smem_u32(s.lsum + tid), r));
+                    }
+                    if (L[r] != 0.f) M = fmaxf(M, m[r]);
+                }
+                float Lt = sk == -INFINITY ? 0.f : ex2(sk - M);
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r) {
+                    m[r] = L[r] == 0.f ? 0.f : L[r] != L[r] ? L[r] : ex2(m[r] - M);
+                    Lt = fmaf(L[r], m[r], Lt);
+                }
+                const float inv = Lt == 0.f ? 0.f : 1.f / Lt;
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r) s.coef[r][tid] = m[r] * inv;
+                if (split == 0 && a.lse && h0 + tid < a.H)
+                    a.lse[(int64_t)t * a.H + h0 + tid] = Lt == 0.f ? -INFINITY : fmaf(M, kLn2, logf(Lt));
             }
-        } else if (a.nsplit <= 4) {
-            merge_items<4>(a, s, kv_s, out, lo, hi, c4);
+            __syncthreads();
+            // this split's share of the (head, 4 dims) items, all splits' sums in
+            // split order
+            if (two) {
+                wait(&s.peer, 0, s, a.status);
+                const float4* mine = reinterpret_cast<const float4*>(kv_s) + lo;
+                const float4* theirs = reinterpret_cast<const float4*>(q_s);
+                for (int i = tid; i < hi - lo; i += kThreads) {
+                    const int h = (lo + i) / c4;
+                    const float4 x = mine[i], y = theirs[i];
+                    const float w0 = s.coef[split][h], w1 = s.coef[split ^ 1][h];
+                    // (a split without entries has staged nothing)
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (w0 != 0.f) acc = make_float4(w0 * x.x, w0 * x.y, w0 * x.z, w0 * x.w);
+                    if (w1 != 0.f) acc = make_float4(fmaf(w1, y.x, acc.x), fmaf(w1, y.y, acc.y), fmaf(w1, y.z, acc.z), fmaf(w1, y.w, acc.w));
+                    store4(out + (int64_t)(lo + i) * 4, acc.x, acc.y, acc.z, acc.w);
+                }
+            } else if (a.nsplit <= 4) {
+                merge_items<4>(a, s, kv_s, out, lo, hi, c4);
+            } else {
+                merge_items<8>(a, s, kv_s, out, lo, hi, c4);
+            }
+            tc::cluster_sync();                               // no peer still reads this CTA's sums
         } else {
-            merge_items<8>(a, s, kv_s, out, lo, hi, c4);
+            if (tid < nh) {
+                const float m = s.mref[tid], L = s.lsum[tid];
+                a.part_ml[(part + tid) * 2] = L == 0.f ? -INFINITY : L != L ? 0.f : m * kLn2;
+                a.part_ml[(part + tid) * 2 + 1] = L;
+            }
+            __syncthreads();
         }
-        tc::cluster_sync();                               // no peer still reads this CTA's sums
-    } else {
-        if (tid < nh) {
-            const float m = s.mref[tid], L = s.lsum[tid];
-            a.part_ml[(part + tid) * 2] = L == 0.f ? -INFINITY : L != L ? 0.f : m * kLn2;
-            a.part_ml[(part + tid) * 2 + 1] = L;
-        }
-        __syncthreads();
-    }
     }
     if (warp == kSWarp + 1) {
         tc::tc_fence_after();

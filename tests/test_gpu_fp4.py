@@ -200,6 +200,37 @@ def test_every_split_and_layout(csa, nq, H, c, R, k, shift):
     check_weights(w, ref, _logit_slack(host(q), V.reshape(3, N, c), c ** -0.5))
 
 
+# more queries than SMs: a CTA goes from one query to the next, of any number of tiles
+@pytest.mark.parametrize("nq,B,N,H,c,R", [(700, 3, 150, 72, 256, 64), (500, 2, 330, 20, 512, 64), (401, 4, 70, 64, 384, 64),
+                                          (450, 1, 129, 16, 384, 96)])
+def test_many_queries_of_any_length(csa, nq, B, N, H, c, R):
+    kv, V = _rows(csa, B * N, c, R, 50)
+    kv, V = kv.reshape(B, N, -1), V.reshape(B, N, c)
+    g = _gen(nq)
+    q = (3 * torch.randn(nq, H, c, generator=g)).to(torch.bfloat16)
+    pos = torch.randint(0, 4 * N + 40, (nq,), generator=g, dtype=torch.int32)
+    pos[torch.rand(nq, generator=g) < 0.2] = 3                                   # nothing visible
+    pos[:149] = 0                                                                # a first round of nothing
+    pos[300:] = 4 * N
+    seq = torch.randint(0, B, (nq,), generator=g, dtype=torch.int32)
+    seq[-1] = B                                                                  # no such sequence
+    sink = torch.randn(H, generator=g)
+    out, lse = csa.hca_dense_mqa_fp4kv(q.to(DEV), kv, pos.to(DEV), 4, seq_of_q=seq.to(DEV), sink=sink.to(DEV),
+                                       rope_dims=R)
+    idx = np.full((nq, N), -1, np.int32)
+    for t in range(nq - 1):
+        n = min(N, max(0, int(pos[t])) // 4)
+        idx[t, :n] = np.arange(n)
+    check_attention(out, lse, q, V, idx, c ** -0.5, sink.double().numpy(), np.minimum(seq.numpy(), B - 1))
+    again, lse2 = csa.hca_dense_mqa_fp4kv(q.to(DEV), kv, pos.to(DEV), 4, seq_of_q=seq.to(DEV), sink=sink.to(DEV),
+                                          rope_dims=R)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    # and as a selection
+    lists = torch.from_numpy(idx).to(DEV)
+    sel, lse3 = csa.csa_sparse_mqa_fp4kv(q.to(DEV), kv, lists, seq_of_q=seq.to(DEV), sink=sink.to(DEV), rope_dims=R)
+    check_attention(sel, lse3, q, V, idx, c ** -0.5, sink.double().numpy(), np.minimum(seq.numpy(), B - 1))
+
+
 @pytest.mark.parametrize("nq,k", [(1, 64), (1, 512), (64, 512), (36, 1024), (160, 256)])
 def test_a_nan_row_shows_however_the_query_is_split(csa, nq, k):
     N, H, c = 300, 64, 512
