@@ -35,6 +35,18 @@ __host__ __device__ constexpr Fp4Row fp4_row(int c, int R) {
     return Fp4Row{c, R, Q, so, ro, ro + 2 * R};
 }
 
+// 32 bytes, 32-byte aligned
+__device__ __forceinline__ void ld_global32(uint32_t (&v)[8], const void* p) {
+    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(p));
+}
+__device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // bf16 bits of a block's scale from its byte and the row exponent (E >= 33)
 __device__ __forceinline__ uint32_t fp4_scale_bits(uint32_t s, uint32_t E) {
     return (((E - 31u) << 7) + (s << 4)) & 0xffffu;

@@ -246,12 +246,6 @@ inline bool wide_rows(const Fp4Row& f, const void* kv4) {
     return f.R == 64 && f.Q % 64 == 0 && f.Q >= 256 && f.Q < 512 && (uintptr_t)kv4 % 32 == 0;
 }
 
-__device__ __forceinline__ void ld_global32(uint32_t (&v)[8], const uint8_t* p) {
-    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "l"(p));
-}
-
 template <bool kSparse>
 struct WideProducer {
     const Fp4TileArgs& a;

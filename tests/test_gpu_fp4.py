@@ -118,6 +118,23 @@ def test_any_bytes_read_back(csa):
     np.testing.assert_array_equal(val.double().cpu().numpy(), oracle.dequantize_kv_fp4(rows, c, R))
 
 
+@pytest.mark.parametrize("c,R,n", [(512, 64, 1), (512, 64, 35), (384, 32, 18), (128, 64, 67)])
+@pytest.mark.parametrize("shift", [0, 8, 16])
+def test_rows_at_any_16_byte_address(csa, c, R, n, shift):
+    x = torch.randn(n * c + 32, generator=_gen(n)).to(torch.bfloat16).to(DEV)
+    rows = x[shift:shift + n * c].view(n, c)
+    rb = csa.csa_fp4_row_bytes(c, R)
+    room = torch.full((n * rb + 64,), 9, dtype=torch.uint8, device=DEV)
+    packed = csa.csa_quantize_kv_fp4(rows, rope_dims=R, out=room[2 * shift:2 * shift + n * rb].view(n, rb))
+    ref = oracle.quantize_kv_fp4(rows.double().cpu().numpy(), R)
+    assert np.array_equal(packed.cpu().numpy(), ref)
+    assert (room[:2 * shift] == 9).all() and (room[2 * shift + n * rb:] == 9).all()
+    back = torch.full((n * c + 32,), -3.0, dtype=torch.bfloat16, device=DEV)
+    csa.csa_dequantize_kv_fp4(packed, c, rope_dims=R, out=back[shift:shift + n * c].view(n, c))
+    assert np.array_equal(host(back[shift:shift + n * c].view(n, c)), oracle.dequantize_kv_fp4(ref, c, R))
+    assert (back[:shift] == -3).all() and (back[shift + n * c:] == -3).all()
+
+
 @pytest.mark.parametrize("B,c,R", [(1, 512, 64), (65, 256, 32), (40, 128, 0)])
 def test_append_writes_its_slot_only(csa, B, c, R):
     N = 5
