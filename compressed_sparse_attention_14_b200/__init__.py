@@ -844,7 +844,7 @@ def _arg(t: Optional[torch.Tensor], index: int, dtype: torch.dtype, want: tuple,
     """The pointer of a contiguous tensor of this dtype and shape on device `index` (None: NULL)."""
     if t is None:
         return None
-    if t.dtype is dtype and t.shape == want and t.is_cuda and t.get_device() == index and t.is_contiguous():
+    if t.dtype is dtype and t.shape == want and t.get_device() == index and t.is_contiguous():
         return t.data_ptr()
     if not t.is_cuda or t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")

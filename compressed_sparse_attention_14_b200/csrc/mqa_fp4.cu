@@ -185,14 +185,13 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
     pdl_wait();
     pdl_launch_next();
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // (uniform)
-    // What the CTA has to do: one split of a query, or (a query in one split)
+    // What the CTA has to do: one split of a query, or (kOne: queries in one split)
     // every gridDim.x-th of the (query, heads) items, their tiles following one
     // another through the buffers.
     struct Item {
         int t, h0, split, seq, ntiles;
         int64_t e_beg, e_end;
     };
-    // (kOne: queries in one split)
     const int it0 = kOne ? blockIdx.x : 0, it_end = kOne ? a.items : 1, it_step = kOne ? gridDim.x : 1;
     auto item_of = [&](int it) {
         Item x;
@@ -288,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                 before = end;
                 // the products have read this item's queries
                 if (it + it_step < it_end) ok = ok && until(&s.s_full[(end - 1) & 1], ((end - 1) >> 1) & 1);
-                // a copy that was waited for in vain is waited for again below
+                // (a copy that was waited for in vain must have landed all the same)
                 if (!ok) tc::mbar_wait(&s.q_full, (nq - 1) & 1, kWaitLimit);
             }
         } else {
