@@ -3,7 +3,7 @@
 //
 //   z_s = scale * q . v_s,  out = sum_s e^{z_s} v_s / (sum_s e^{z_s} [+ e^{sink}])
 //
-// An item of work is (query, 64 or 16 heads, one split of the query's entries).
+// An item of work is (query, 64, 32 or 16 heads, one split of the query's entries).
 // Queries that are split have a CTA per item; where there are enough queries
 // not to split them, a CTA per SM takes every 148th item, and the next item's
 // tiles are expanded while the last one's output is written (3001 queries: 446
@@ -22,7 +22,7 @@
 // Two tiles (and two S^T, two P) are in work at a time, so that producers,
 // softmax and products overlap:
 //   warps 0-7   softmax; warp w has entries 16 (w % 4).. and half of the
-//               heads, a thread 2 entries x 8 (2) of them (the 16-lane
+//               heads, a thread 2 entries x 8, 4 or 2 of them (the 16-lane
 //               tensor-memory loads)
 //   warps 8-23  producers (fp4_tile.cuh)
 //   warp 24     S products, half of the channels by half as they are stored
@@ -57,7 +57,7 @@ using namespace fp4_tile;
 
 constexpr int kSoftmaxWarps = 8, kThreads = (kSoftmaxWarps + kProducerWarps + 2) * 32;
 constexpr int kSWarp = kSoftmaxWarps + kProducerWarps;   // and the next: products
-constexpr int kMaxHg = 64;              // heads per CTA: 64 or 16
+constexpr int kMaxHg = 64;              // heads per CTA: 64, 32 or 16
 constexpr int kMaxCluster = 8;
 constexpr float kMoveLog2 = 24.0f, kLn2 = 0.6931471805599453f;
 
@@ -174,7 +174,7 @@ template <bool kSparse, bool kWide, int kHg, bool kOne>
 __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_constant__ Args a,
                                                               const __grid_constant__ CUtensorMap tmQ) {
     constexpr int kHalf = kHg / 2, kOct = kHg / 16;       // heads, and groups of 8, per softmax warp
-    constexpr uint32_t kTmemCols = kHg == 64 ? 512 : 128; // S^T 2 x kHg, O^T up to 4 x kHg
+    constexpr uint32_t kTmemCols = 8 * kHg;               // S^T 2 x kHg, O^T up to 4 x kHg
     extern __shared__ uint8_t smem_raw[];
     // (an offset, not a rounded pointer: the accesses stay shared-memory ones)
     uint8_t* kv_s = smem_raw + ((0u - tc::smem_u32(smem_raw)) & 1023u);           // 2 x dblocks x 8 KB
@@ -616,15 +616,20 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
 }
 
 // Heads per CTA: 64, so that a query's entries are expanded once for all of
-// them; 16 where four times the CTAs have at most two tiles each, since staging
-// and merging 64 heads' sums takes longer than expanding a few tiles more (one
-// query over 512 entries: 18.5 us with 64, 12.3 with 16; 8 queries 15.3 and
-// 11.6; 8 queries over 1024, four tiles each, 13.7 and 15.6), and for up to 16
-// heads, whose products are shorter (16 heads, 64 x 512 entries: 16.1 and 14.9
-// us, 16 x 8192: 37.7 and 35.4).
+// them, unless there are no more. Fewer where the SMs have room and the entries
+// are few, since staging and merging 64 heads' sums takes longer than expanding
+// some tiles again: 16 where four times the CTAs have at most two tiles each (one
+// query over 512 entries: 18.5 us with 64, 12.3 with 16; 8 queries 15.3 and 11.6;
+// 8 queries over 1024, four tiles each, 13.7 and 15.6), 32 up to four tiles (64
+// queries over 128 entries 12.4 us with 64, 9.5 with 32, over 256 13.8 and 12.8,
+// over 512 17.7 and 18.7). Up to 16 and 32 heads the products are shorter, too
+// (16 heads, 64 x 512 entries: 16.1 and 14.9 us, 16 x 8192: 37.7 and 35.4; 32
+// heads 16.1 and 14.5, 36.7 and 31.7).
 int heads_of(int nq, int H, int64_t max_entries) {
     const int64_t tiles = (max_entries + kE - 1) / kE;
-    return H <= 16 || (int64_t)nq * ((H + 63) / 64) * tiles * 4 <= 2 * 148 ? 16 : 64;
+    const int64_t ctas = (int64_t)nq * ((H + 63) / 64);
+    if (H <= 16 || ctas * tiles * 4 <= 2 * 148) return 16;
+    return H <= 32 || (ctas * 2 <= 148 && tiles <= 4) ? 32 : 64;
 }
 
 // Splits per query: as many whole tiles per CTA as fill the SMs once.
@@ -708,7 +713,9 @@ cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {
                      : (wide ? mqa_fp4_kernel<false, true, kHg, kOne> : mqa_fp4_kernel<false, false, kHg, kOne>);
     };
     auto by_heads = [&](auto one) {
-        return hg == 16 ? of(std::integral_constant<int, 16>(), one) : of(std::integral_constant<int, 64>(), one);
+        return hg == 16   ? of(std::integral_constant<int, 16>(), one)
+               : hg == 32 ? of(std::integral_constant<int, 32>(), one)
+                          : of(std::integral_constant<int, 64>(), one);
     };
     auto kern = a.merge == kDirect ? by_heads(std::true_type()) : by_heads(std::false_type());
     cudaError_t e = smem_ceiling(kern);

@@ -260,7 +260,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-// 16 lanes x 8 or 32 columns -> registers: 4u, 4u + 1 are lane (lane / 4),
+// 16 lanes x 8, 16 or 32 columns -> registers: 4u, 4u + 1 are lane (lane / 4),
 // columns 8u + 2 (lane % 4) and the next; 4u + 2, 4u + 3 the same 8 lanes on.
 __device__ __forceinline__ void tmem_ld_16(uint32_t taddr, float (&v)[4]) {
     uint32_t r[4];
@@ -268,6 +268,14 @@ __device__ __forceinline__ void tmem_ld_16(uint32_t taddr, float (&v)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr));
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld_16(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tmem_ld_16(uint32_t taddr, float (&v)[16]) {
     uint32_t r[16];

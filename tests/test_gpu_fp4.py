@@ -217,6 +217,20 @@ def test_every_split_and_layout(csa, nq, H, c, R, k, shift):
     check_weights(w, ref, _logit_slack(host(q), V.reshape(3, N, c), c ** -0.5))
 
 
+# 32 heads per CTA: unsplit, in two, several and many splits, more queries than SMs
+@pytest.mark.parametrize("nq,H,c,R,k,shift", [
+    (60, 64, 512, 64, 200, 0), (30, 64, 512, 64, 256, 16), (20, 100, 256, 32, 256, 0), (21, 128, 384, 64, 130, 0),
+    (5, 24, 512, 64, 1500, 0), (3, 32, 128, 96, 2048, 0), (12, 17, 384, 96, 700, 16), (400, 30, 512, 64, 300, 0),
+    (200, 32, 256, 0, 100, 0)])
+def test_32_heads_a_cta(csa, nq, H, c, R, k, shift):
+    test_every_split_and_layout(csa, nq, H, c, R, k, shift)
+
+
+def test_dense_attention_of_32_heads(csa):
+    test_dense_attention(csa, 9000, 32, 512, 64, [9000, 130], True)
+    test_dense_attention(csa, 500, 20, 384, 96, [500, 0, 64, 65], False)
+
+
 # more queries than SMs: a CTA goes from one query to the next, of any number of tiles
 @pytest.mark.parametrize("nq,B,N,H,c,R", [(700, 3, 150, 72, 256, 64), (500, 2, 330, 20, 512, 64), (401, 4, 70, 64, 384, 64),
                                           (450, 1, 129, 16, 384, 96)])
