@@ -1098,9 +1098,32 @@ def csa_evict_rows(cache, src, dst, n_moves):
     return cache
 
 
+def _check_evictable(cache: torch.Tensor, dev: int, B: int, Nmax: int, name: str) -> None:
+    """What csa_evict_rows asks of a cache of B sequences of Nmax rows, without a launch."""
+    if not cache.is_cuda or cache.get_device() != dev:
+        raise ValueError(f"{name} is on {cache.device}, expected cuda:{dev}")
+    shape = tuple(cache.shape)
+    if shape[:2] != (B, Nmax):
+        raise ValueError(f"{name} has shape {shape}, expected ({B}, {Nmax}, ...)")
+    if not cache.is_contiguous():
+        raise ValueError(f"{name}: libcsa takes contiguous tensors only")
+    row_bytes = math.prod(shape[2:]) * cache.element_size()
+    if row_bytes < 16 or row_bytes % 16 or row_bytes > 1 << 30:
+        raise ValueError(f"{name} has rows of {row_bytes} bytes, expected a positive multiple of 16 (up to 2^30)")
+    if cache.data_ptr() % 16:
+        raise ValueError(f"{name} is not 16-byte aligned")
+
+
 def csa_evict(caches, acc, n_ent, keep: int, entry_pos=None, protect_from=None, ws=None):
     """Cuts every sequence to `keep` entries in place: the plan, then its moves
-    on each cache of `caches`. acc, n_ent and entry_pos are updated in place."""
+    on each cache of `caches` ([B, Nmax, ...], rows of a multiple of 16 bytes).
+    acc, n_ent and entry_pos are updated in place. Every argument is checked
+    before anything is written: a call that raises has changed nothing."""
+    caches = list(caches)
+    dev = _cuda_index(acc)
+    B, Nmax = acc.shape
+    for i, cache in enumerate(caches):
+        _check_evictable(cache, dev, B, Nmax, f"caches[{i}]")
     src, dst, moves, *_ = csa_evict_plan(acc, n_ent, keep, entry_pos, protect_from, n_out=n_ent, acc_out=acc,
                                          pos_out=entry_pos, ws=ws)
     for cache in caches:

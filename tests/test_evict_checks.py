@@ -1,0 +1,83 @@
+"""csa_evict looks at every cache before it writes anything (no GPU: the plan
+and the moves are replaced by records of their calls)."""
+import pytest
+import torch
+
+import compressed_sparse_attention_14_b200 as csa
+
+
+class OnGpu:
+    """The parts of a CUDA tensor that the checks look at."""
+    is_cuda = True
+
+    def __init__(self, *shape, dtype=torch.uint8, device=0, ptr=0x10000, contiguous=True):
+        self.shape, self.dtype, self._dev, self._ptr, self._contiguous = torch.Size(shape), dtype, device, ptr, contiguous
+        self.device = torch.device("cuda", device)
+
+    def get_device(self):
+        return self._dev
+
+    def is_contiguous(self):
+        return self._contiguous
+
+    def data_ptr(self):
+        return self._ptr
+
+    def element_size(self):
+        return torch.empty((), dtype=self.dtype).element_size()
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    seen = []
+    monkeypatch.setattr(csa, "csa_evict_plan", lambda *a, **k: seen.append("plan") or (None,) * 6)
+    monkeypatch.setattr(csa, "csa_evict_rows", lambda cache, *a: seen.append(tuple(cache.shape)))
+    return seen
+
+
+GOOD = OnGpu(2, 64, 384)
+
+
+@pytest.mark.parametrize("bad", [
+    OnGpu(2, 64, dtype=torch.float32),                     # a scale an entry: rows of 4 bytes
+    OnGpu(2, 64, 3, dtype=torch.float32),                  # rows of 12
+    OnGpu(2, 64, 0),
+    OnGpu(2, 63, 384), OnGpu(2, 128, 384), OnGpu(3, 64, 384),   # not the weights' sequences and entries
+    OnGpu(128, 384), OnGpu(64),
+    OnGpu(2, 64, 384, contiguous=False), OnGpu(2, 64, 384, device=1), OnGpu(2, 64, 384, ptr=0x10008),
+    torch.zeros(2, 64, 384, dtype=torch.uint8)])
+def test_a_bad_cache_is_refused_before_the_plan(calls, bad):
+    acc = OnGpu(2, 64, dtype=torch.float32)
+    for caches in ([bad], [GOOD, bad], [bad, GOOD], (x for x in (GOOD, GOOD, bad))):
+        with pytest.raises(ValueError, match="caches"):
+            csa.csa_evict(caches, acc, None, 8)
+        assert calls == []
+
+
+def test_good_caches_move_after_the_plan(calls):
+    keys = OnGpu(2, 64, 8, dtype=torch.bfloat16)
+    csa.csa_evict((x for x in (GOOD, keys)), OnGpu(2, 64, dtype=torch.float32), None, 8)
+    assert calls == ["plan", (2, 64, 384), (2, 64, 8)]
+    csa.csa_evict([], OnGpu(2, 64, dtype=torch.float32), None, 8)
+    assert calls[3:] == ["plan"]
+
+
+@pytest.mark.gpu
+def test_a_refused_eviction_changes_nothing():
+    g = torch.Generator().manual_seed(4)
+    B, N, keep = 3, 80, 30
+    acc = torch.rand(B, N, generator=g).cuda()
+    n_ent = torch.tensor([N, 40, 7], dtype=torch.int32).cuda()
+    pos = torch.arange(N, dtype=torch.int32).repeat(B, 1).cuda()
+    kv4 = torch.randint(0, 256, (B, N, 384), generator=g, dtype=torch.uint8).cuda()
+    state = [acc, n_ent, pos, kv4]
+    before = [t.clone() for t in state]
+    for bad in (torch.ones(B, N, device="cuda"), kv4[:, :N - 1].contiguous(), torch.zeros(B, 2 * N, 384, device="cuda"),
+                torch.zeros(B, N, 768, dtype=torch.uint8, device="cuda")[..., ::2], kv4.cpu()):
+        with pytest.raises(ValueError, match="caches"):
+            csa.csa_evict([kv4, bad], acc, n_ent, keep, entry_pos=pos)
+        assert all(torch.equal(a, b) for a, b in zip(state, before))
+    csa.csa_evict([kv4], acc, n_ent, keep, entry_pos=pos)
+    assert n_ent.tolist() == [30, 30, 7] and not torch.equal(kv4, before[3])
+    for b, n in enumerate((30, 30, 7)):                    # a row is where its position says
+        assert torch.equal(kv4[b, :n], before[3][b, pos[b, :n].long()])
