@@ -223,9 +223,10 @@ def poll_status(reset: bool = True) -> None:
 
 
 def debug_set(wait_limit: int = 0, flags: int = 0) -> None:
-    """Failure-path test hooks (off by default): a shorter bound on the
-    indexer's device waits, and CSA_DEBUG_SKIP_FIRST_TILE to withhold its first
-    key tile so that a wait runs out."""
+    """Failure-path test hooks (off by default): a shorter bound on the device
+    waits of the indexer and the 4-bit attention and weights, and
+    CSA_DEBUG_SKIP_FIRST_TILE to withhold their first tile so that a wait runs
+    out."""
     _check(_lib.csa_debug_set(wait_limit, flags))
 
 

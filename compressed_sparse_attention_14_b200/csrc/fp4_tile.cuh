@@ -12,6 +12,7 @@
 
 #include "csa.h"
 #include "fp4.cuh"
+#include "kernels.h"
 #include "tc.cuh"
 
 namespace csa {
@@ -22,7 +23,7 @@ constexpr int kE = 64;                  // entries per tile
 constexpr int kPairs = CSA_MAX_HEAD_DIM / 128;   // pairs of 64-channel blocks
 constexpr int kHalves = 2;
 constexpr uint32_t kBlockBytes = kE * 128;
-constexpr uint32_t kWaitLimit = 1u << 20;   // (2 us each)
+constexpr uint32_t kWaitLimit = 1u << 20;   // polls before a wait gives up (2 us each)
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Fp4TileArgs {
@@ -32,6 +33,13 @@ struct Fp4TileArgs {
     int64_t Nmax;
     Fp4Row f;
     int k, dblocks, mtiles;   // c / 64, c / 128
+    uint32_t wait_limit;      // polls before a wait gives up (CSA_ERR_TIMEOUT)
+    int skip_first;           // test hook: a CTA's first tile is never stored, so that the waits for it run out
+    // Sets what the process-wide test hooks ask for.
+    void set_hooks() {
+        wait_limit = debug_wait_limit() ? debug_wait_limit() : kWaitLimit;
+        skip_first = (debug_flags() & CSA_DEBUG_SKIP_FIRST_TILE) ? 1 : 0;
+    }
     __device__ __forceinline__ int halves() const { return (mtiles + 1) / 2; }
     // 64-channel blocks of half h
     __device__ __forceinline__ int blocks(int h) const { return h ? dblocks - 4 : min(dblocks, 4); }
@@ -56,15 +64,22 @@ __device__ __forceinline__ void st_shared16(uint32_t dst, uint4 v) {
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // Bounded wait: false once it ran out here or another role gave up.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Fp4TileShared& s, int* status) {
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Fp4TileShared& s, const Fp4TileArgs& a) {
     volatile int* abort = &s.abort;
-    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    for (uint32_t i = 0; i < a.wait_limit; ++i) {
         if (tc::mbar_try_wait_for(bar, parity, 2000)) return true;
         if ((i & 15u) == 15u && *abort) return false;
     }
-    report_device_error(status, CSA_ERR_TIMEOUT);
+    report_device_error(a.status, CSA_ERR_TIMEOUT);
     *abort = 1;
     return false;
+}
+// The wait for a copy in flight into this CTA's memory: it has to land before
+// the CTA may end, whatever became of the other roles.
+__device__ __forceinline__ void wait_copy(uint64_t* bar, uint32_t parity, int* status) {
+    for (uint32_t i = 0; i < kWaitLimit; ++i)
+        if (tc::mbar_try_wait_for(bar, parity, 2000)) return;
+    report_device_error(status, CSA_ERR_TIMEOUT);
 }
 
 // One row of every second tile, followed by the producer lanes that expand it.
@@ -204,7 +219,7 @@ struct Producer {
             if (i >= a.mtiles || !ok) continue;
             // the products of the tile before last have read the half
             if (j >= 2 && ((i & 1) || i == a.mtiles - 1))
-                ok = __all_sync(0xffffffffu, wait(&s.empty[b][i >> 1], ((j >> 1) - 1) & 1, s, a.status));
+                ok = __all_sync(0xffffffffu, wait(&s.empty[b][i >> 1], ((j >> 1) - 1) & 1, s, a));
             if (!ok) continue;
             if (4 * i + chunk() < a.f.Q / 32) {
                 const uint32_t S0 = scale.of(two[i] & 255u), S1 = scale.of((two[i] >> 8) & 255u);
@@ -304,7 +319,7 @@ struct WideProducer {
         }
         const RowScale scale(E);
         // the products of the tile before last have read the half
-        if (j >= 2 && !__all_sync(0xffffffffu, wait(&s.empty[b][1], parity, s, a.status))) return false;
+        if (j >= 2 && !__all_sync(0xffffffffu, wait(&s.empty[b][1], parity, s, a))) return false;
 #pragma unroll
         for (int n = 1; n < 3; ++n) {
             const int r = 4 * n + q - nb - 1;             // rotary piece
@@ -316,7 +331,7 @@ struct WideProducer {
         }
         if (4 + q < nb) expand_block(raw[1], mine[1], 4 + q, scale);
         hand_over(&s.full[b][1]);
-        if (j >= 2 && !__all_sync(0xffffffffu, wait(&s.empty[b][0], parity, s, a.status))) return false;
+        if (j >= 2 && !__all_sync(0xffffffffu, wait(&s.empty[b][0], parity, s, a))) return false;
         expand_block(raw[0], mine[0], q, scale);
         hand_over(&s.full[b][0]);
         return true;
@@ -334,6 +349,7 @@ __device__ __forceinline__ bool produce(P& p, int warp, int before, int t, int e
     p.walk.begin(t, e_beg, e_end, ntiles, first_row, j);
     if (j < ntiles) p.load(j);
     ready();
+    if (p.a.skip_first && before + j == 0) return false;
     for (; j < ntiles; j += 2) {
         if (!p.store(before + j)) return false;
         if (j + 2 < ntiles) p.load(j + 2);

@@ -39,8 +39,9 @@ cudaError_t smem_ceiling(const void* kern) {
 }
 
 // Failure-path test hooks (csa_debug_set): a shorter bound for the device
-// waits of the tensor-core indexer, and flags that withhold one of its copies
-// so that a wait runs out. Both default to off.
+// waits of the tensor-core indexer and the 4-bit attention and weights, and
+// flags that withhold their first tile so that a wait runs out. Both default
+// to off.
 static std::atomic<uint32_t> g_wait_limit{0};
 static std::atomic<uint32_t> g_debug_flags{0};
 

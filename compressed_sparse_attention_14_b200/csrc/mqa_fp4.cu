@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
         const uint32_t tile_bytes = a.dblocks * kBlockBytes;
         const uint32_t q_addr = kv_addr + 2 * tile_bytes, p_addr = q_addr + a.dblocks * kHg * 128;
         auto until = [&](uint64_t* bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, wait(bar, parity, s, a.status));
+            return __all_sync(0xffffffffu, wait(bar, parity, s, a));
         };
         bool ok = true;
         int before = 0;                                   // tiles of the items before
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                 // the products have read this item's queries
                 if (it + it_step < it_end) ok = ok && until(&s.s_full[(end - 1) & 1], ((end - 1) >> 1) & 1);
                 // (a copy that was waited for in vain must have landed all the same)
-                if (!ok) tc::mbar_wait(&s.q_full, (nq - 1) & 1, kWaitLimit);
+                if (!ok) wait_copy(&s.q_full, (nq - 1) & 1, a.status);
             }
         } else {
             const uint32_t idesc = tc::idesc_bf16_f32(128, kHg, 1, 1);
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                     return v >= 0 && v < a.Nmax;
                 };
                 const bool va = seen(ra), vb = seen(rb);
-                ok = ok && wait(&s.s_full[b], (j >> 1) & 1, s, a.status);
+                ok = ok && wait(&s.s_full[b], (j >> 1) & 1, s, a);
                 tc::tc_fence_after();
                 float z[4 * kOct];
                 auto logits = [&]() {
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                     for (int i = 0; i < 2 * kOct; ++i) lpart[i] *= s.alpha[hb + 8 * (i >> 1) + 2 * q4 + (i & 1)];
                     if (n > 0) {
                         // rescale O^T (every product before this tile's has ended)
-                        ok = wait(&s.empty[b ^ 1][0], ((j - 1) >> 1) & 1, s, a.status);
+                        ok = wait(&s.empty[b ^ 1][0], ((j - 1) >> 1) & 1, s, a);
                         tc::tc_fence_after();
 #pragma unroll 1
                         for (int m = 0; m < 4 * a.mtiles; ++m) {
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                 if (lane == 0) tc::mbar_arrive(&s.p_full[b]);
             }
             before += ntiles;
-            if (ok && ntiles > 0) ok = wait(&s.empty[(before - 1) & 1][0], ((before - 1) >> 1) & 1, s, a.status);
+            if (ok && ntiles > 0) ok = wait(&s.empty[(before - 1) & 1][0], ((before - 1) >> 1) & 1, s, a);
             __syncwarp();
             // per-head sums in a fixed order: entries, lanes, then the four warps
             half_sync(half);                                  // red may still be read
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
             // this split's share of the (head, 4 dims) items, all splits' sums in
             // split order
             if (two) {
-                wait(&s.peer, 0, s, a.status);
+                wait_copy(&s.peer, 0, a.status);
                 const float4* mine = reinterpret_cast<const float4*>(kv_s) + lo;
                 const float4* theirs = reinterpret_cast<const float4*>(q_s);
                 for (int i = tid; i < hi - lo; i += kThreads) {
@@ -687,6 +687,7 @@ cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {
     a.part_o = (float*)ws;
     a.part_ml = (float*)((char*)ws + align256((size_t)x.nq * ns * x.H * x.c * sizeof(float)));
     a.status = device_status();
+    a.set_hooks();
     a.Nmax = x.Nmax;
     const int64_t tiles = (max_entries + kE - 1) / kE;
     a.split_len = tiles ? (tiles + ns - 1) / ns * kE : kE;

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
                     if (blocks.visible(t) <= e_tile) continue;
                     for (int g = 0; ok && g < a.hgroups; ++g, ++n)
                         for (int i = a.halves() - 1; i >= 0; --i) {           // (as they are stored)
-                            if (n > 0 && !(ok = wait(&s.q_empty[i], (n - 1) & 1, s, a.status))) break;
+                            if (n > 0 && !(ok = wait(&s.q_empty[i], (n - 1) & 1, s, a))) break;
                             tc::mbar_expect_tx(&s.q_full[i], a.blocks(i) * kHg * 128);
                             for (int blk = 4 * i; blk < 4 * i + a.blocks(i); ++blk)
                                 tc::tma_load_2d(q_s + (size_t)blk * kHg * 128, &tmQ, &s.q_full[i], blk * 64,
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
             const uint32_t tile_bytes = a.dblocks * kBlockBytes, q_addr = kv_addr + 2 * tile_bytes;
             const uint32_t idesc = tc::idesc_bf16_f32(kE, kHg, 0, 0);
             auto until = [&](uint64_t* bar, uint32_t parity) {
-                return __all_sync(0xffffffffu, wait(bar, parity, s, a.status));
+                return __all_sync(0xffffffffu, wait(bar, parity, s, a));
             };
             bool ok = true;
             // S of tile j (the n-th of all) and the query block in shared memory
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
                     }
                     __syncwarp();
                     const uint32_t sb = n & 1;
-                    ok = ok && wait(&s.s_full[sb], (n >> 1) & 1, s, a.status);
+                    ok = ok && wait(&s.s_full[sb], (n >> 1) & 1, s, a);
                     tc::tc_fence_after();
                     float pa = 0.f, pb = 0.f;
 #pragma unroll
@@ -305,6 +305,7 @@ cudaError_t entry_weights_fp4(const Fp4WeightArgs& x, cudaStream_t st) {
     a.kv4 = x.kv4;
     a.idx = x.idx;
     a.status = device_status();
+    a.set_hooks();
     a.Nmax = x.Nmax;
     a.f = fp4_row(x.c, x.R);
     a.k = x.k;

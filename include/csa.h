@@ -91,12 +91,13 @@ int csa_poll_status(void* stream, int reset);
 
 /* Failure-path test hooks (for the tests of the timeout path; leave off in
  * production). csa_debug_set(wait_limit, flags): wait_limit > 0 bounds every
- * device wait of the tensor-core indexer to that many polls (0 restores the
- * built-in bound); flags CSA_DEBUG_SKIP_FIRST_TILE makes the indexer never
- * load its first key tile, so the wait for it runs out: the kernel records
- * CSA_ERR_TIMEOUT in the status word (csa_poll_status), stops every role,
- * drains its copies, frees its tensor memory and returns. Process-wide;
- * affects launches made after the call. */
+ * device wait of the tensor-core indexer, of the attention over 4-bit entries
+ * and of their weights to that many polls (0 restores the built-in bound); flags
+ * CSA_DEBUG_SKIP_FIRST_TILE makes the indexer never load its first key tile
+ * and a CTA of the 4-bit kernels never store its first entries, so the wait for
+ * them runs out: the kernel records CSA_ERR_TIMEOUT in the status word
+ * (csa_poll_status), stops every role, drains its copies, frees its tensor
+ * memory and returns. Process-wide; affects launches made after the call. */
 #define CSA_DEBUG_SKIP_FIRST_TILE 1u
 /* Selection paths of csa_decode, csa_prefill, csa_decode_fp8kv and
  * csa_attend_decode (bf16, contiguous caches). By default the indexer stores
