@@ -135,25 +135,30 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
     if (warp == 21) {
         // ------------------------------------------------------------ query loads
         if (lane == 0) {
-            uint32_t n = 0;
+            uint32_t n = 0, sent[kHalves] = {0, 0};       // query blocks, and copies of each half issued
             bool ok = true;
             for (int j = 0; ok && j < (kStay ? (ntiles > 0 ? 1 : 0) : ntiles); ++j) {
                 const int e_tile = e_beg + j * kE;
                 for (int t = 0; ok && t <= blocks.last_query(e_tile); ++t) {
                     if (blocks.visible(t) <= e_tile) continue;
                     for (int g = 0; ok && g < a.hgroups; ++g, ++n)
-                        for (int i = a.halves() - 1; i >= 0; --i) {           // (as they are stored)
-                            if (n > 0 && !(ok = wait(&s.q_empty[i], (n - 1) & 1, s, a))) break;
+#pragma unroll
+                        for (int i = kHalves - 1; i >= 0; --i) {              // (as they are stored)
+                            if (i >= a.halves()) continue;
+                            ok = ok && (n == 0 || wait(&s.q_empty[i], (n - 1) & 1, s, a));
+                            if (!ok) continue;
                             tc::mbar_expect_tx(&s.q_full[i], a.blocks(i) * kHg * 128);
                             for (int blk = 4 * i; blk < 4 * i + a.blocks(i); ++blk)
                                 tc::tma_load_2d(q_s + (size_t)blk * kHg * 128, &tmQ, &s.q_full[i], blk * 64,
                                                 (b * a.T + t) * a.H + g * kHg);
+                            ++sent[i];
                         }
                 }
             }
-            // the last copies of each half have landed
-            if (n > 0)
-                for (int i = 0; i < a.halves(); ++i) tc::mbar_wait(&s.q_full[i], (n - 1) & 1, ok ? kWaitLimit : 1u << 16);
+            // every copy issued has landed
+#pragma unroll
+            for (int i = 0; i < kHalves; ++i)
+                if (sent[i] > 0) wait_copy(&s.q_full[i], (sent[i] - 1) & 1, a.status);
         }
         __syncwarp();
     } else if (warp == 20) {
@@ -210,11 +215,11 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         uint32_t n = 0;
         bool ok = true;
-        for (int j = 0; j < ntiles; ++j) {
+        for (int j = 0; ok && j < ntiles; ++j) {
             const int e_tile = e_beg + j * kE, last = blocks.last_query(e_tile);
             const int ea = e_tile + warp * 16 + (lane >> 2), eb = ea + 8;     // this thread's entries
             float wa = 0.f, wb = 0.f;
-            for (int t = 0; t <= last; ++t) {
+            for (int t = 0; ok && t <= last; ++t) {
                 const int seen = blocks.visible(t);
                 if (seen <= e_tile) continue;
                 for (int g = 0; g < a.hgroups; ++g, ++n) {
@@ -227,7 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
                     }
                     __syncwarp();
                     const uint32_t sb = n & 1;
-                    ok = ok && wait(&s.s_full[sb], (n >> 1) & 1, s, a);
+                    ok = __all_sync(0xffffffffu, wait(&s.s_full[sb], (n >> 1) & 1, s, a));
+                    if (!ok) break;
                     tc::tc_fence_after();
                     float pa = 0.f, pb = 0.f;
 #pragma unroll
@@ -257,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
                     if (lane == 0) tc::mbar_arrive(&s.s_empty[sb]);
                 }
             }
+            if (!ok) break;                               // (a wait ran out: no sums to write)
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) {
                 wa += __shfl_xor_sync(0xffffffffu, wa, o);
