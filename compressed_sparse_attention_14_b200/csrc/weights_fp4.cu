@@ -138,8 +138,8 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
             uint32_t n = 0, sent[kHalves] = {0, 0};       // query blocks, and copies of each half issued
             bool ok = true;
             for (int j = 0; ok && j < (kStay ? (ntiles > 0 ? 1 : 0) : ntiles); ++j) {
-                const int e_tile = e_beg + j * kE;
-                for (int t = 0; ok && t <= blocks.last_query(e_tile); ++t) {
+                const int e_tile = e_beg + j * kE, last = blocks.last_query(e_tile);
+                for (int t = 0; ok && t <= last; ++t) {
                     if (blocks.visible(t) <= e_tile) continue;
                     for (int g = 0; ok && g < a.hgroups; ++g, ++n)
 #pragma unroll
