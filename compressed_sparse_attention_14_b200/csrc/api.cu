@@ -839,7 +839,7 @@ int hca_entry_weights_fp4kv(const void* q, const float* lse, const uint8_t* kv4,
     CSA_TRY(check_fp4_attn(B, B > 0 ? B : 1, H, c, rope_dims, Nmax, true, "hca_entry_weights_fp4kv"));
     if (T < 0 || mp < 1) return fail(CSA_ERR_INVALID_ARG, "hca_entry_weights_fp4kv: T=%d mp=%d", T, mp);
     if ((int64_t)B * T * H > INT32_MAX) return fail(CSA_ERR_UNSUPPORTED, "query rows B*T*H beyond int32");
-    // (a tile of entries is held while all its queries pass: the kernel's waits are sized for this many)
+    // (every role of the kernel looks through the positions of all queries for each tile)
     if (T > (1 << 18))
         return fail(CSA_ERR_UNSUPPORTED, "hca_entry_weights_fp4kv: T=%d beyond 2^18 queries a call (pass the rest "
                     "with acc = out)", T);

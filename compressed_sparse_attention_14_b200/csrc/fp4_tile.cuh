@@ -48,6 +48,7 @@ struct Fp4TileArgs {
 struct Fp4TileShared {
     uint64_t full[2][kHalves], empty[2][kHalves];   // half of a tile stored / free
     int abort;
+    uint32_t progress;        // changes while a tile is held for many products
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -63,12 +64,20 @@ __device__ __forceinline__ void st_shared16(uint32_t dst, uint4 v) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-// Bounded wait: false once it ran out here or another role gave up.
+// Bounded wait: false once it ran out here or another role gave up. The polls
+// are counted from the last step of progress: a tile of entries may be held while
+// 2^18 queries pass, each in a wait of its own that is bounded.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Fp4TileShared& s, const Fp4TileArgs& a) {
     volatile int* abort = &s.abort;
+    volatile uint32_t* progress = &s.progress;
+    uint32_t last = *progress;
     for (uint32_t i = 0; i < a.wait_limit; ++i) {
         if (tc::mbar_try_wait_for(bar, parity, 2000)) return true;
-        if ((i & 15u) == 15u && *abort) return false;
+        if ((i & 15u) != 15u) continue;
+        if (*abort) return false;
+        const uint32_t now = *progress;
+        if (now != last) i = 0;
+        last = now;
     }
     report_device_error(a.status, CSA_ERR_TIMEOUT);
     *abort = 1;

@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                 tc::mbar_init(&s.peer, 1);
                 tc::fence_mbar_init();
                 s.abort = 0;
+                s.progress = 0;
                 if (first.ntiles > 0) load_q(first);
             }
             __syncwarp();

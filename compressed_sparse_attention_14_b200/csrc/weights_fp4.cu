@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
         tc::mbar_init(&s.fin, 1);
         tc::fence_mbar_init();
         s.abort = 0;
+        s.progress = 0;
         s.n_max = 0;
     }
     if (warp == 20) {
@@ -200,7 +201,11 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
                 for (int j = 0; ok && j < ntiles; ++j) {
                     const int e_tile = e_beg + j * kE, blocks_all = (blocks.last_query(e_tile) + 1) * a.hgroups;
                     for (int tg = 0; ok && tg < blocks_all; ++tg)
-                        if (blocks.visible(tg / a.hgroups) > e_tile) product(j, n++, tg == blocks_all - 1);
+                        if (blocks.visible(tg / a.hgroups) > e_tile) {
+                            product(j, n++, tg == blocks_all - 1);
+                            // (the producers wait for all of a tile's products)
+                            if (lane == 0) *(volatile uint32_t*)&s.progress = n;
+                        }
                 }
             }
             tc::umma_commit_warp(&s.fin);
