@@ -20,6 +20,7 @@
 // evict_rows: a thread per 16 bytes, four of them in flight; bound by memory
 // (8 us for 16 x 8192 to half, rows of 384 bytes).
 // evict_slot: a CTA per sequence, one reduction.
+#include <cstddef>
 #include <type_traits>
 
 #include "common.cuh"
@@ -61,13 +62,15 @@ __device__ __forceinline__ int warp_scan(int v) {
 constexpr int kBins = 2048;
 
 struct PlanShared {
-    int hist[3][kBins];                    // one histogram per pass: none is reused
+    alignas(16) int hist[3][kBins];        // one histogram per pass: none is reused; read in pairs
     int scan[kWarps];
     int count[kWarps][4];                  // per warp: above the keep-th key before / after slot keep, ties likewise
     int total[5];                          // this CTA's sums, and its entries before slot keep
     int all[kMaxCluster][5];               // every CTA's total
     int digit, need;
 };
+static_assert(alignof(PlanShared) % sizeof(uint2) == 0 && offsetof(PlanShared, hist) % sizeof(uint2) == 0 &&
+              sizeof(PlanShared::hist[0]) % sizeof(uint2) == 0, "pairs of counters are read as uint2");
 
 __global__ void __launch_bounds__(kThreads) evict_plan_kernel(const __grid_constant__ EvictPlanArgs a, int csize,
                                                               int cached) {
