@@ -77,8 +77,10 @@ struct Args : Fp4TileArgs {
 
 struct Shared : Fp4TileShared {
     // the heads' reference maxima; the same plus the limit; the same, 0 for none
-    float mref[kMaxHg], limit[kMaxHg], mexp[kMaxHg];
-    float alpha[kMaxHg], lsum[kMaxHg];
+    // (aligned where they are read in pairs)
+    float mref[kMaxHg];
+    alignas(8) float limit[kMaxHg], mexp[kMaxHg], alpha[kMaxHg];
+    float lsum[kMaxHg];
     float red[4][kMaxHg];
     float coef[kMaxCluster][kMaxHg];
     uint64_t s_full[2], p_full[2], q_full, fin[2];
