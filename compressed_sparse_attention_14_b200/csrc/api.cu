@@ -760,7 +760,7 @@ static int check_fp4_attn(int nq, int n_seq, int H, int c, int rope_dims, int64_
 
 size_t csa_sparse_mqa_fp4kv_workspace_size(int nq, int H, int c, int k) {
     if (nq < 0 || H < 1 || c < 1 || k < 1) return 0;
-    return mqa_fp4_workspace_bytes(nq, H, c, k);
+    return mqa_fp4_workspace_bound(nq, H, c, k);
 }
 
 int csa_sparse_mqa_fp4kv(const void* q, const uint8_t* kv4, const int32_t* idx, const int32_t* seq_of_q, int nq,
@@ -777,7 +777,7 @@ int csa_sparse_mqa_fp4kv(const void* q, const uint8_t* kv4, const int32_t* idx, 
     CSA_TRY(check_ptr(out, "out"));
     CSA_TRY(check_ptr(lse, "lse", false));
     CSA_TRY(check_no_alias(out, q, "csa_sparse_mqa_fp4kv"));
-    CSA_TRY(check_ws(ws, ws_bytes, csa_sparse_mqa_fp4kv_workspace_size(nq, H, c, k)));
+    CSA_TRY(check_ws(ws, ws_bytes, mqa_fp4_workspace_bytes(nq, H, c, k)));
     const Fp4MqaArgs a{q, kv4, idx, k, QuerySpec{seq_of_q, nullptr, 0, 0}, 1, nq, n_seq, H, c, rope_dims, Nmax,
                        default_scale(scale, c), sink, out, lse};
     CSA_CUDA(mqa_fp4(a, ws, (cudaStream_t)stream), "csa_sparse_mqa_fp4kv");
@@ -786,7 +786,7 @@ int csa_sparse_mqa_fp4kv(const void* q, const uint8_t* kv4, const int32_t* idx, 
 
 size_t hca_dense_mqa_fp4kv_workspace_size(int nq, int H, int c, int64_t Nmax) {
     if (nq < 0 || H < 1 || c < 1 || Nmax < 0) return 0;
-    return mqa_fp4_workspace_bytes(nq, H, c, Nmax);
+    return mqa_fp4_workspace_bound(nq, H, c, Nmax);
 }
 
 int hca_dense_mqa_fp4kv(const void* q, const uint8_t* kv4, const int32_t* pos, const int32_t* seq_of_q, int nq,
@@ -803,7 +803,7 @@ int hca_dense_mqa_fp4kv(const void* q, const uint8_t* kv4, const int32_t* pos, c
     CSA_TRY(check_ptr(out, "out"));
     CSA_TRY(check_ptr(lse, "lse", false));
     CSA_TRY(check_no_alias(out, q, "hca_dense_mqa_fp4kv"));
-    CSA_TRY(check_ws(ws, ws_bytes, hca_dense_mqa_fp4kv_workspace_size(nq, H, c, Nmax)));
+    CSA_TRY(check_ws(ws, ws_bytes, mqa_fp4_workspace_bytes(nq, H, c, Nmax)));
     const Fp4MqaArgs a{q, kv4, nullptr, 0, QuerySpec{seq_of_q, pos, 0, 0}, mp, nq, n_seq, H, c, rope_dims, Nmax,
                        default_scale(scale, c), sink, out, lse};
     CSA_CUDA(mqa_fp4(a, ws, (cudaStream_t)stream), "hca_dense_mqa_fp4kv");
@@ -1235,7 +1235,7 @@ int csa_decode_fp8kv(const void* qI, const float* w, const void* idx_cache, cons
 size_t csa_decode_fp4kv_workspace_size(int B, int64_t Nmax, int H, int c, int HI, int cI, int k) {
     (void)HI; (void)cI;
     if (B < 0 || Nmax < 0 || k < 1 || H < 1 || c < 1) return 0;
-    return select_bytes(B, Nmax, k) + align256((size_t)B * k * sizeof(int32_t)) + mqa_fp4_workspace_bytes(B, H, c, k);
+    return select_bytes(B, Nmax, k) + align256((size_t)B * k * sizeof(int32_t)) + mqa_fp4_workspace_bound(B, H, c, k);
 }
 
 int csa_decode_fp4kv(const void* qI, const float* w, const void* idx_cache, const void* q, const uint8_t* kv4,
@@ -1259,12 +1259,12 @@ int csa_decode_fp4kv(const void* qI, const float* w, const void* idx_cache, cons
     CSA_TRY(check_ptr(lse, "lse", false));
     CSA_TRY(check_ptr(topk_idx, "topk_idx", false));
     CSA_TRY(check_no_alias(out, q, "csa_decode_fp4kv"));
-    CSA_TRY(check_ws(ws, ws_bytes, csa_decode_fp4kv_workspace_size(B, Nmax, H, c, HI, cI, k)));
     cudaStream_t st = (cudaStream_t)stream;
     Carve cv(ws);
     void* blk = cv.take(select_bytes(B, Nmax, k));
     int32_t* sel = (int32_t*)cv.take((size_t)B * k * sizeof(int32_t));
     void* mws = cv.take(mqa_fp4_workspace_bytes(B, H, c, k));
+    CSA_TRY(check_ws(ws, ws_bytes, cv.off));
     if (topk_idx) sel = topk_idx;
     QuerySpec qs{nullptr, ctx_len, 0, 0};
     const char* step = "indexer";

@@ -217,7 +217,9 @@ struct Fp4MqaArgs {
     void* out;
     float* lse;
 };
+// bytes: what this call needs; bound: what any of at most nq queries over at most max_entries needs
 size_t mqa_fp4_workspace_bytes(int nq, int H, int c, int64_t max_entries);
+size_t mqa_fp4_workspace_bound(int nq, int H, int c, int64_t max_entries);
 cudaError_t mqa_fp4(const Fp4MqaArgs& a, void* ws, cudaStream_t st);
 
 // weights_fp4.cu: the attention weight of entries, summed over heads: of idx[t][i] (B queries,

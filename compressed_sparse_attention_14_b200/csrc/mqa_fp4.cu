@@ -45,6 +45,8 @@
 // Splits of a query: up to 8 form a cluster and merge on chip (each writes a
 // share of the output from all partial sums over distributed shared memory);
 // more go through the workspace and mqa_combine. Either way in split order.
+#include <algorithm>
+
 #include "fp4_tile.cuh"
 #include "kernels.h"
 #include "tmap.h"
@@ -628,11 +630,18 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
 // over 512 17.7 and 18.7). Up to 16 and 32 heads the products are shorter, too
 // (16 heads, 64 x 512 entries: 16.1 and 14.9 us, 16 x 8192: 37.7 and 35.4; 32
 // heads 16.1 and 14.5, 36.7 and 31.7).
+constexpr int kHeadChoices[] = {16, 32, 64};
+// the most tiles of entries that hg heads per CTA are taken for
+int64_t tiles_for(int hg, int nq, int H) {
+    const int64_t ctas = std::max<int64_t>((int64_t)nq * ((H + 63) / 64), 1);
+    if (H <= hg || hg == kMaxHg) return INT64_MAX;
+    return hg == 16 ? 2 * 148 / 4 / ctas : ctas * 2 <= 148 ? 4 : -1;
+}
 int heads_of(int nq, int H, int64_t max_entries) {
     const int64_t tiles = (max_entries + kE - 1) / kE;
-    const int64_t ctas = (int64_t)nq * ((H + 63) / 64);
-    if (H <= 16 || ctas * tiles * 4 <= 2 * 148) return 16;
-    return H <= 32 || (ctas * 2 <= 148 && tiles <= 4) ? 32 : 64;
+    for (int hg : kHeadChoices)
+        if (tiles <= tiles_for(hg, nq, H)) return hg;
+    return kMaxHg;
 }
 
 // Splits per query: as many whole tiles per CTA as fill the SMs once.
@@ -668,11 +677,30 @@ struct Plan {
 
 }  // namespace
 
+static size_t partial_bytes(int nq, int ns, int H, int c) {
+    return align256((size_t)nq * ns * H * c * sizeof(float)) + align256((size_t)nq * ns * H * 2 * sizeof(float));
+}
+
 size_t mqa_fp4_workspace_bytes(int nq, int H, int c, int64_t max_entries) {
     const Plan plan(nq, H, max_entries);
-    const int ns = plan.ns;
-    if (plan.merge != kWorkspace) return 0;
-    return align256((size_t)nq * ns * H * c * sizeof(float)) + align256((size_t)nq * ns * H * 2 * sizeof(float));
+    return plan.merge == kWorkspace ? partial_bytes(nq, plan.ns, H, c) : 0;
+}
+
+// Fewer queries or entries may need more than more of them (24 sequences of
+// 8192 entries are split in 6 and merge through the workspace, 64 are in 2 and
+// merge on chip), so this is the largest need up to these numbers: for every number of
+// queries the most splits that any of them could have.
+size_t mqa_fp4_workspace_bound(int nq, int H, int c, int64_t max_entries) {
+    const int64_t tiles = (max_entries + kE - 1) / kE;
+    size_t most = 0;
+    for (int n = std::min(nq, 148); n > 0; --n)
+        for (int hg : kHeadChoices) {
+            const int64_t ctas = (int64_t)n * ((H + hg - 1) / hg);
+            // (with more splits than these a shorter list would have them, too)
+            const int ns = nsplit_of(ctas, kE * std::min<int64_t>({tiles, tiles_for(hg, n, H), ctas ? 148 / ctas : 1, 64}));
+            if (merge_of(ctas, ns) == kWorkspace) most = std::max(most, partial_bytes(n, ns, H, c));
+        }
+    return most;
 }
 
 cudaError_t mqa_fp4(const Fp4MqaArgs& x, void* ws, cudaStream_t st) {

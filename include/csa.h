@@ -397,6 +397,8 @@ int csa_decode_fp8kv(const void* qI, const float* w, const void* idx_cache, cons
  * that no query sees are not read. Queries without entries give out = 0,
  * lse = -inf (the sink logit with a sink). csa_decode_fp4kv's index keys are
  * bf16 and its selection is csa_decode's. out must not overlap an input.
+ * Workspace: a size asked for with nq (B) queries and k (Nmax) entries also
+ * serves every call of fewer queries and shorter lists with the same H and c.
  * ------------------------------------------------------------------------ */
 size_t csa_fp4_row_bytes(int c, int rope_dims);
 int csa_quantize_kv_fp4(const void* kv, int64_t rows, int c, int rope_dims, uint8_t* out, void* stream);
