@@ -1064,7 +1064,7 @@ def csa_evict_plan(acc, n_ent, keep: int, entry_pos=None, protect_from=None, src
     n_out, acc_out, pos_out): row src[b, i] moves to dst[b, i] for i <
     n_moves[b] (-1 after), n_out entries are left, and acc_out / pos_out hold
     their weights and positions (0 / -1 past them; they may be acc / entry_pos
-    themselves)."""
+    themselves). ws is not used."""
     dev = _cuda_index(acc)
     B, Nmax = acc.shape
     M = max(0, min(keep, Nmax - keep))
@@ -1076,13 +1076,12 @@ def csa_evict_plan(acc, n_ent, keep: int, entry_pos=None, protect_from=None, src
     acc_out = torch.empty_like(acc) if acc_out is None else acc_out
     if entry_pos is not None and pos_out is None:
         pos_out = torch.empty_like(entry_pos)
-    wp, wn, ws = _scratch(_size_of("csa_evict_plan_workspace_size", B, Nmax, keep), dev, ws)
     _run_on(dev, _lib.csa_evict_plan, _arg(acc, dev, _F32, (B, Nmax), "acc"),
             _arg(n_ent, dev, _I32, (B,), "n_ent"), _arg(entry_pos, dev, _I32, (B, Nmax), "entry_pos"),
             _arg(protect_from, dev, _I32, (B,), "protect_from"), B, Nmax, keep, _arg(src, dev, _I32, (B, M), "src"),
             _arg(dst, dev, _I32, (B, M), "dst"), _arg(n_moves, dev, _I32, (B,), "n_moves"),
             _arg(n_out, dev, _I32, (B,), "n_out"), _arg(acc_out, dev, _F32, (B, Nmax), "acc_out"),
-            _arg(pos_out, dev, _I32, (B, Nmax), "pos_out"), wp, wn)
+            _arg(pos_out, dev, _I32, (B, Nmax), "pos_out"), None, 0)
     return src, dst, n_moves, n_out, acc_out, pos_out
 
 
@@ -1119,14 +1118,15 @@ def csa_evict(caches, acc, n_ent, keep: int, entry_pos=None, protect_from=None, 
     """Cuts every sequence to `keep` entries in place: the plan, then its moves
     on each cache of `caches` ([B, Nmax, ...], rows of a multiple of 16 bytes).
     acc, n_ent and entry_pos are updated in place. Every argument is checked
-    before anything is written: a call that raises has changed nothing."""
+    before anything is written: a call that raises has changed nothing. ws is
+    not used."""
     caches = list(caches)
     dev = _cuda_index(acc)
     B, Nmax = acc.shape
     for i, cache in enumerate(caches):
         _check_evictable(cache, dev, B, Nmax, f"caches[{i}]")
     src, dst, moves, *_ = csa_evict_plan(acc, n_ent, keep, entry_pos, protect_from, n_out=n_ent, acc_out=acc,
-                                         pos_out=entry_pos, ws=ws)
+                                         pos_out=entry_pos)
     for cache in caches:
         csa_evict_rows(cache, src, dst, moves)
 

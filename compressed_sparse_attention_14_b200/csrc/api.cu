@@ -865,13 +865,14 @@ static int check_evict(int B, int64_t Nmax, const char* who) {
 }
 
 size_t csa_evict_plan_workspace_size(int B, int64_t Nmax, int64_t keep) {
-    if (B < 0 || Nmax < 0 || keep < 0 || keep > Nmax) return 0;
-    return evict_plan_workspace_bytes(B, Nmax, keep);
+    (void)B; (void)Nmax; (void)keep;
+    return 0;
 }
 
 int csa_evict_plan(const float* acc, const int32_t* n_ent, const int32_t* entry_pos, const int32_t* protect_from,
                    int B, int64_t Nmax, int64_t keep, int32_t* src, int32_t* dst, int32_t* n_moves, int32_t* n_out,
                    float* acc_out, int32_t* pos_out, void* ws, size_t ws_bytes, void* stream) {
+    (void)ws; (void)ws_bytes;
     CSA_TRY(check_evict(B, Nmax, "csa_evict_plan"));
     if (keep < 0 || keep > Nmax)
         return fail(CSA_ERR_INVALID_ARG, "csa_evict_plan: keep=%lld outside [0, Nmax]", (long long)keep);
@@ -891,10 +892,9 @@ int csa_evict_plan(const float* acc, const int32_t* n_ent, const int32_t* entry_
     CSA_TRY(check_ptr(n_out, "n_out"));
     CSA_TRY(check_ptr(acc_out, "acc_out", Nmax > 0));
     CSA_TRY(check_ptr(pos_out, "pos_out", false));
-    CSA_TRY(check_ws(ws, ws_bytes, csa_evict_plan_workspace_size(B, Nmax, keep)));
     const EvictPlanArgs a{acc, n_ent, entry_pos, protect_from, B, Nmax, keep, M, src, dst, n_moves, n_out, acc_out,
                           pos_out};
-    CSA_CUDA(evict_plan(a, ws, (cudaStream_t)stream), "csa_evict_plan");
+    CSA_CUDA(evict_plan(a, (cudaStream_t)stream), "csa_evict_plan");
     return CSA_OK;
 }
 

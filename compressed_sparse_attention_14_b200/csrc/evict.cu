@@ -402,13 +402,7 @@ __global__ void __launch_bounds__(256) evict_slot_kernel(const __grid_constant__
 
 }  // namespace
 
-size_t evict_plan_workspace_bytes(int B, int64_t Nmax, int64_t keep) {
-    (void)B; (void)Nmax; (void)keep;
-    return 0;
-}
-
-cudaError_t evict_plan(const EvictPlanArgs& a, void* ws, cudaStream_t st) {
-    (void)ws;
+cudaError_t evict_plan(const EvictPlanArgs& a, cudaStream_t st) {
     if (a.B == 0) return cudaSuccess;
     // 2048 entries and more per CTA: a part smaller than that costs less than
     // another CTA at the barriers

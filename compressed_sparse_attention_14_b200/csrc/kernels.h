@@ -254,8 +254,7 @@ struct EvictPlanArgs {
     float* acc_out;
     int32_t* pos_out;              // nullable
 };
-size_t evict_plan_workspace_bytes(int B, int64_t Nmax, int64_t keep);
-cudaError_t evict_plan(const EvictPlanArgs& a, void* ws, cudaStream_t st);
+cudaError_t evict_plan(const EvictPlanArgs& a, cudaStream_t st);
 cudaError_t evict_rows(void* cache, int64_t row_bytes, int B, int64_t Nmax, const int32_t* src, const int32_t* dst,
                        const int32_t* n_moves, int64_t M, cudaStream_t st);
 struct EvictSlotArgs {

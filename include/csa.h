@@ -456,6 +456,7 @@ int hca_decode_fp4kv(const void* q, const uint8_t* kv4, const int32_t* ctx_len, 
  *   with entry_pos) are the weights (positions) after the moves, 0 (-1) past
  *   n_out. In place is allowed: acc_out == acc, pos_out == entry_pos, n_out ==
  *   n_ent; other overlap is not. n_ent is clipped to [0, Nmax].
+ *   csa_evict_plan_workspace_size returns 0: ws is not used (may be NULL).
  * csa_evict_rows: carries the moves out on cache [B, Nmax, row_bytes] (any
  *   cache of the sequences: 4-bit or bf16 entries, index keys), in place;
  *   row_bytes a multiple of 16, max_moves = M. A move with a row outside
