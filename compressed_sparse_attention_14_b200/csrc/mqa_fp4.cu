@@ -589,10 +589,11 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_kernel(const __grid_const
                 wait_copy(&s.peer, 0, a.status);
                 const float4* mine = reinterpret_cast<const float4*>(kv_s) + lo;
                 const float4* theirs = reinterpret_cast<const float4*>(q_s);
+                const float4 *first_sums = split ? theirs : mine, *second_sums = split ? mine : theirs;
                 for (int i = tid; i < hi - lo; i += kThreads) {
                     const int h = (lo + i) / c4;
-                    const float4 x = mine[i], y = theirs[i];
-                    const float w0 = s.coef[split][h], w1 = s.coef[split ^ 1][h];
+                    const float4 x = first_sums[i], y = second_sums[i];
+                    const float w0 = s.coef[0][h], w1 = s.coef[1][h];
                     // (a split without entries has staged nothing)
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (w0 != 0.f) acc = make_float4(w0 * x.x, w0 * x.y, w0 * x.z, w0 * x.w);

@@ -81,6 +81,8 @@ def test_equal_logits_count_every_entry(csa, nq, H, c, R, k):
     q = torch.zeros(nq, H, c, dtype=torch.bfloat16)
     seq = torch.zeros(nq, dtype=torch.int32, device=DEV)
     out, lse = csa.csa_sparse_mqa_fp4kv(q.to(DEV), kv, idx.to(DEV), seq_of_q=seq, rope_dims=R)
+    # (one head's reference serves all: their queries are the same)
+    assert torch.equal(out, out[:, :1].expand_as(out)) and torch.equal(lse, lse[:, :1].expand_as(lse))
     bounds.check_attention(host(out[:, :1]), host(lse[:, :1]), host(q[:, :1]), V[None], idx.numpy(), c ** -0.5, None,
                            np.zeros(nq, int))
     w = host(csa.csa_entry_weights_fp4kv(q.to(DEV), lse, kv, idx.to(DEV), seq_of_q=seq, rope_dims=R))
@@ -103,6 +105,7 @@ def test_equal_logits_of_every_visible_entry(csa, lens, N, H, c, R):
     q = torch.zeros(B, H, c, dtype=torch.bfloat16)
     pos = torch.tensor(lens, dtype=torch.int32)
     out, lse = csa.hca_decode_fp4kv(q.to(DEV), kv, pos.to(DEV), 1, rope_dims=R)
+    assert torch.equal(out, out[:, :1].expand_as(out)) and torch.equal(lse, lse[:, :1].expand_as(lse))
     idx = np.where(np.arange(N) < np.array(lens)[:, None], np.arange(N), -1)
     bounds.check_attention(host(out[:, :1]), host(lse[:, :1]), host(q[:, :1]), V, idx, c ** -0.5, None, np.arange(B))
     w = host(csa.hca_entry_weights_fp4kv(q.to(DEV), lse, kv, pos.to(DEV), 1, rope_dims=R))
@@ -134,6 +137,7 @@ def test_a_query_along_every_entry(csa, N, H, c, R):
         t = at[a:a + 64]
         bounds.check_attention(host(out)[t][:, :1], host(lse)[t][:, :1], host(q)[t][:, :1], V[None],
                                np.tile(np.arange(N), (len(t), 1)), c ** -0.5, None, np.zeros(len(t), int))
+    assert torch.equal(out, out[:, :1].expand_as(out))
 
 
 @pytest.mark.parametrize("per,k", [(64, 512), (18, 1029), (8, 513), (4, 2000), (1, 512), (1, 2048)])
@@ -152,6 +156,7 @@ def test_a_query_along_every_edge_of_a_split_list(csa, per, k):
         out, lse = csa.csa_sparse_mqa_fp4kv(q.to(DEV), kv, idx.to(DEV), seq_of_q=seq)
         bounds.check_attention(host(out)[:, :1], host(lse)[:, :1], host(q)[:, :1], V[None], idx.numpy(), c ** -0.5, None,
                                np.zeros(per, int))
+        assert torch.equal(out, out[:, :1].expand_as(out))
 
 
 # ---------------------------------------------------------------- weights
