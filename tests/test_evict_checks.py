@@ -81,3 +81,25 @@ def test_a_refused_eviction_changes_nothing():
     assert n_ent.tolist() == [30, 30, 7] and not torch.equal(kv4, before[3])
     for b, n in enumerate((30, 30, 7)):                    # a row is where its position says
         assert torch.equal(kv4[b, :n], before[3][b, pos[b, :n].long()])
+
+
+@pytest.mark.gpu
+def test_the_newest_entries_by_position_stay_after_slots_were_reused():
+    """A cache whose slots have been reused holds positions far above its slots' numbers: the newest are protected by
+    position, as the readme has it, and the others go by weight."""
+    g = torch.Generator().manual_seed(6)
+    B, N, cap, newest, keep = 2, 64, 50, 12, 30
+    acc = torch.rand(B, N, generator=g).cuda()
+    n_ent = torch.zeros(B, dtype=torch.int32).cuda()
+    pos = torch.full((B, N), -1, dtype=torch.int32).cuda()
+    for step in range(400):
+        csa.csa_evict_slot(acc, n_ent, torch.full((B,), step, dtype=torch.int32).cuda(), 1, cap, entry_pos=pos, recent=20)
+        acc += torch.rand(B, N, generator=g).cuda()
+    weight = {(b, int(pos[b, i])): float(acc[b, i]) for b in range(B) for i in range(cap)}
+    csa.csa_evict([], acc, n_ent, keep, entry_pos=pos, protect_from=pos.amax(1) - (newest - 1))
+    for b in range(B):
+        left = set(pos[b, :keep].tolist())
+        new = set(range(400 - newest, 400))
+        held = {p: w for (x, p), w in weight.items() if x == b and p not in new}
+        assert new <= left and left - new == set(sorted(held, key=held.get)[-(keep - newest):])
+        assert (pos[b, keep:] == -1).all()
