@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) entry_weights_fp4_kernel(const __
             __syncwarp();
         }
         // entries that no query sees
-        for (int e = (e_end > e_beg ? e_end : e_beg) + tid; e < e_stop; e += 128) {
+        for (int64_t e = (int64_t)(e_end > e_beg ? e_end : e_beg) + tid; e < e_stop; e += 128) {
             if (kSparse) {
                 if (a.weights) a.weights[(int64_t)b * a.k + e] = 0.f;
             } else {
