@@ -1,5 +1,6 @@
 """csa_evict looks at every cache before it writes anything (no GPU: the plan
 and the moves are replaced by records of their calls)."""
+import numpy as np
 import pytest
 import torch
 
@@ -103,3 +104,57 @@ def test_the_newest_entries_by_position_stay_after_slots_were_reused():
         held = {p: w for (x, p), w in weight.items() if x == b and p not in new}
         assert new <= left and left - new == set(sorted(held, key=held.get)[-(keep - newest):])
         assert (pos[b, keep:] == -1).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["plain", "ties", "odd"])
+@pytest.mark.parametrize("N,keep", [(393_217, 100_000), (500_003, 499_000), (800_000, 17)])
+def test_plans_of_caches_whose_keys_do_not_fit_on_chip(kind, N, keep):
+    from tests.test_gpu_evict import _expected, _weights
+    acc = _weights(2, N, keep, kind)
+    n_ent = torch.tensor([N, N - 12_345], dtype=torch.int32)
+    pos = torch.argsort(torch.rand(2, N, generator=torch.Generator().manual_seed(N)), 1).int()
+    prot = torch.tensor([N - 9, N // 2], dtype=torch.int32)
+    want = _expected(acc.numpy(), n_ent.numpy(), keep, pos.numpy(), prot.numpy())
+    got = csa.csa_evict_plan(acc.cuda(), n_ent.cuda(), keep, entry_pos=pos.cuda(), protect_from=prot.cuda())
+    for g, w in zip(got, want):
+        np.testing.assert_array_equal(g.cpu().numpy(), w)
+
+
+@pytest.mark.gpu
+def test_a_captured_step_of_a_bounded_cache_replays():
+    """Weights, slot, store and an eviction in one graph, replayed step by step against the eager calls."""
+    B, cap, c, H = 3, 40, 512, 64
+    def start():
+        return [torch.zeros(B, cap).cuda(), torch.zeros(B, dtype=torch.int32).cuda(),
+                torch.full((B, cap), -1, dtype=torch.int32).cuda(), torch.full((B, cap, 384), 255, dtype=torch.uint8).cuda()]
+    q = torch.empty(B, H, c, dtype=torch.bfloat16).cuda()
+    new = torch.empty(B, c, dtype=torch.bfloat16).cuda()
+    pos = torch.zeros(B, dtype=torch.int32).cuda()
+    prot = torch.zeros(B, dtype=torch.int32).cuda()
+
+    def step(acc, n_ent, at, kv):
+        out, lse = csa.hca_decode_fp4kv(q, kv, n_ent, 1)
+        csa.hca_entry_weights_fp4kv(q, lse, kv, n_ent, 1, acc=acc, out=acc)
+        csa.csa_evict([kv], acc, n_ent, cap - 8, entry_pos=at, protect_from=prot)
+        slot = csa.csa_evict_slot(acc, n_ent, pos, 1, cap - 4, entry_pos=at, recent=2)
+        csa.csa_append_kv_fp4(new, slot, kv)
+        return out, lse, slot
+
+    eager, held = start(), start()
+    q.zero_(), new.zero_()
+    step(*start())                                          # (the kernels are loaded)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step(*held)
+    g = torch.Generator().manual_seed(9)
+    for t in range(120):
+        q.copy_(torch.randn(B, H, c, generator=g))
+        new.copy_(torch.randn(B, c, generator=g))
+        pos.fill_(t)
+        prot.fill_(t - 5)
+        want = step(*eager)
+        graph.replay()
+        for a, b in zip((*want, *eager), (*outs, *held)):
+            assert torch.equal(a, b)
+    assert eager[1].tolist() == [cap - 7] * B
