@@ -37,7 +37,8 @@ struct Fp4TileArgs {
     int skip_first;           // test hook: a CTA's first tile is never stored, so that the waits for it run out
     // Sets what the process-wide test hooks ask for.
     void set_hooks() {
-        wait_limit = debug_wait_limit() ? debug_wait_limit() : kWaitLimit;
+        const uint32_t polls = debug_wait_limit();
+        wait_limit = polls ? polls : kWaitLimit;
         skip_first = (debug_flags() & CSA_DEBUG_SKIP_FIRST_TILE) ? 1 : 0;
     }
     __device__ __forceinline__ int halves() const { return (mtiles + 1) / 2; }
