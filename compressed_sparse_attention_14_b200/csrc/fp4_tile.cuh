@@ -268,8 +268,8 @@ struct Producer {
 // with the scales among 4 .. 7: 64 rotary channels and head dims of 384 and
 // 512. The 4 lanes of a row read a whole line at a time, in 3 instructions that
 // touch 3 lines a row; the layout above touches 7 or 8, and issuing them is what
-// paces its tiles (3001 queries over 512 entries 513 us with that, 456 with
-// this; 16 sequences of 8192 entries 56 and 50, their weights 51 and 42).
+// paces its tiles (3001 queries over 512 entries 424 us with that, 383 with
+// this; 16 sequences of 8192 entries 48.2 and 43.5, their weights 33.0 and 29.8).
 inline bool wide_rows(const Fp4Row& f, const void* kv4) {
     return f.R == 64 && f.Q % 64 == 0 && f.Q >= 256 && f.Q < 512 && (uintptr_t)kv4 % 32 == 0;
 }

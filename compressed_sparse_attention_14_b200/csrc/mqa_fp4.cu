@@ -16,8 +16,13 @@
 // S^T and O^T live in tensor memory. The softmax keeps a reference maximum per
 // head that moves (O^T and the sums are then rescaled) only when a logit
 // passes it by 2^24; normalisation uses the same reference, so the result does
-// not depend on when it moves, and the weights' rounding is relative. P is
-// rounded to bf16 for the second product; sums, maxima and O stay fp32.
+// not depend on when it moves, and the weights' rounding is relative. Sums, maxima
+// and O stay fp32. P is rounded to bf16 for the second product (the sums take it
+// unrounded), as in the attention over bf16 entries: a product's two operands have
+// one type, and V's exponents need bf16. It takes an output's relative error from
+// the 0.0016 of its own rounding to 0.0018 .. 0.0023; a second product with the
+// rounding's remainder would add 768 cycles to a tile's 2050 of products and take
+// 16 KB of shared memory that are not there.
 //
 // Two tiles (and two S^T, two P) are in work at a time, so that producers,
 // softmax and products overlap:
@@ -36,8 +41,14 @@
 // tiles only: 7% slower. The products alone take 2050 cycles a tile (M = 64, N =
 // 64: 40 cycles each, M = 128: 48, the shared memory's rate), and reading,
 // storing and multiplying through shared memory 2300.
-// 3001 queries x 64 heads over 512 entries: 390 us (340 TFLOP/s, 21% of the
-// dense rate measured on this part); 16 sequences of 8192 entries 43 us.
+// 3001 queries x 64 heads over 512 entries: 383 us (346 TFLOP/s, 21% of the
+// dense rate measured on this part); 16 sequences of 8192 entries 43.5 us.
+//
+// Splits are equal pieces of what a query could see (k, or the cache's length),
+// not of what it does see: CTAs whose piece lies behind the last visible entry end
+// at once, and the others are as long as in a full cache (16 sequences of 1000
+// entries: 15.6 us in a cache of 1024, 38.9 in one of 8192; 8192 entries: 40.6
+// in a cache of 8192, 214 in one of 65536).
 //
 // Entries outside the query's set are stored as zeros and get weight 0: no
 // row that the query does not see is read.

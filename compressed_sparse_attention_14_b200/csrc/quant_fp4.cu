@@ -15,8 +15,10 @@
 //
 // A lane holds one block (16 channels, 32 bytes of bf16): block maxima need
 // no exchange, the row exponent one warp reduction. c = 512 fills the warp;
-// c = 128 and 256 put 4 and 2 rows in a warp. Bound by memory: 32768 rows of
-// 512 channels are written and read back in 20 us, 4 TB/s.
+// c = 128 and 256 put 4 and 2 rows in a warp. 32768 rows of 512 channels are written
+// in 12.3 us, bound by issuing the instructions (76% of the issue slots used, 26%
+// of the memory's rate, in a cold run), and read back in 6.6 us, bound by its loads'
+// latency; both in a row 20 us, 4 TB/s.
 #include "fp4.cuh"
 #include "kernels.h"
 
@@ -26,7 +28,7 @@ namespace {
 
 __host__ __device__ constexpr int lanes_per_row(int c) { return c <= 128 ? 8 : c <= 256 ? 16 : 32; }
 
-// four signed values -> their e2m1 codes, v[1] v[0] in the low byte
+// the e2m1 codes of 8 channels, as the word that holds them
 __device__ __forceinline__ uint32_t e2m1_word(const float (&v)[8]) {
     // byte i holds nibbles 2i, 2i+1: channels (0, 2), (4, 6), (1, 3), (5, 7)
     uint32_t w;
